@@ -630,6 +630,117 @@ sla_status sla_csr_set_one_group(sla_csr A, int mode);
  */
 sla_status sla_resident_loop_ms(sla_csr A, double* ms_host);
 
+/*
+ * ---------------------------------------------------------------------------
+ * Network operators: what a network that predicts a system's coefficients is
+ * made of, next to the solve it is trained through.  They need no handle and
+ * allocate nothing: the *_work calls give the bytes of the blocks the caller
+ * provides (256-byte aligned, as hipMalloc's are).  Everything is
+ * asynchronous on `stream`, without host synchronisation, and may be captured
+ * into a graph.  Elements are of `type`; sums, statistics and states are
+ * fp32.  Arrays are row-major with contiguous rows; ld* is the distance in
+ * elements from one row (token) to the next.  Outputs are contiguous.  The
+ * same inputs give the same bits.  Errors: SLA_ERR_ARG, SLA_ERR_DEVICE.
+ * ---------------------------------------------------------------------------
+ */
+typedef enum { SLA_F32 = 0, SLA_F16 = 1, SLA_BF16 = 2 } sla_type;
+
+/*
+ * Layer norm over the last axis: y = (x - mean) / sqrt(var + eps) * weight +
+ * bias, x [rows][cols].  weight and bias [cols] (either may be NULL: 1 and 0)
+ * are of wtype: x's type or SLA_F32.  stats [rows][2] (may be NULL) receives
+ * the mean less the row's first element and 1 / sqrt(var + eps), for the
+ * gradient.
+ */
+sla_status sla_layer_norm(const void* x, int64_t ldx, int64_t rows, int64_t cols, sla_type type,
+                          const void* weight, const void* bias, sla_type wtype, double eps,
+                          void* y, float* stats, hipStream_t stream);
+
+/* Workspace bytes of sla_layer_norm_grad. */
+sla_status sla_layer_norm_work(int64_t rows, int64_t cols, sla_type type, int64_t* bytes_host);
+
+/* Gradients of sla_layer_norm from grad_y = dy and the forward pass's stats;
+ * dx, dweight and dbias may each be NULL (not wanted).  With no rows the
+ * weight's and bias's gradients are zero. */
+sla_status sla_layer_norm_grad(const void* dy, int64_t lddy, const void* x, int64_t ldx,
+                               int64_t rows, int64_t cols, sla_type type, const void* weight,
+                               sla_type wtype, const float* stats, void* dx, void* dweight,
+                               void* dbias, void* work, int64_t work_bytes, hipStream_t stream);
+
+/*
+ * Gated feed-forward unit: h = f(x w_gate^T) * (x w_up^T), x [rows][inner],
+ * the weights [outer][inner] contiguous, h [rows][outer].  act: f(a) is
+ * a / (1 + exp(-a)), a (1 + erf(a / sqrt 2)) / 2 or max(a, 0).
+ */
+enum { SLA_ACT_SILU = 0, SLA_ACT_GELU = 1, SLA_ACT_RELU = 2 };
+sla_status sla_gated_ffn(const void* x, int64_t ldx, const void* w_gate, const void* w_up,
+                         int64_t rows, int64_t inner, int64_t outer, sla_type type, int act,
+                         void* h, hipStream_t stream);
+
+/* Workspace bytes of sla_gated_ffn_grad. */
+sla_status sla_gated_ffn_work(int64_t rows, int64_t inner, int64_t outer, sla_type type,
+                              int64_t* bytes_host);
+
+/* Gradients of sla_gated_ffn from dh [rows][outer]; dx may be NULL, and so may
+ * both weights' gradients together (not wanted). */
+sla_status sla_gated_ffn_grad(const void* dh, int64_t lddh, const void* x, int64_t ldx,
+                              const void* w_gate, const void* w_up, int64_t rows, int64_t inner,
+                              int64_t outer, sla_type type, int act, void* dx, void* dw_gate,
+                              void* dw_up, void* work, int64_t work_bytes, hipStream_t stream);
+
+/*
+ * Gated delta rule.  Every sequence and value head has a state S [key_dim]
+ * [value_dim] (fp32); token t turns it into
+ *   S <- exp(g_t) S;  S <- S + k_t (beta_t (v_t - S^T k_t))^T;
+ *   o_t = scale S^T q_t.
+ * q, k [tokens][key_heads][key_dim], v and o [tokens][value_heads]
+ * [value_dim], g and beta fp32 [tokens][value_heads].  Value head h reads key
+ * head h / (value_heads / key_heads).  g <= 0 (a decay) is the meant range:
+ * growth within a chunk of 64 tokens may overflow.
+ * packed == 0: `tokens` are `sequences` sequences of equal length, one after
+ * the other.  packed != 0: sequence i is the tokens offsets[i] ..
+ * offsets[i+1] - 1 (offsets [sequences + 1], int32, device, not falling,
+ * within 0 .. tokens; empty sequences are allowed).  Offsets that fall or
+ * leave the range are raised to their largest predecessor or clamped, never
+ * followed; tokens of no sequence get zeros.
+ * key_dim is 1..128, value_dim 1..4096.
+ */
+typedef struct {
+  int64_t sequences, tokens, key_heads, value_heads, key_dim, value_dim;
+  double scale;
+  sla_type type;
+  int packed;
+} sla_delta_dims;
+
+/* Bytes of the block that sla_delta_rule fills (and its gradient reads), and of
+ * the gradient's workspace; either output may be NULL. */
+sla_status sla_delta_rule_work(const sla_delta_dims* dims, int64_t* kept_bytes_host,
+                               int64_t* grad_bytes_host);
+
+/* The rule over whole sequences.  initial_state and final_state [sequences]
+ * [value_heads][key_dim][value_dim] may be NULL (zeros; not wanted). */
+sla_status sla_delta_rule(const sla_delta_dims* dims, const void* q, int64_t ldq, const void* k,
+                          int64_t ldk, const void* v, int64_t ldv, const float* g,
+                          const float* beta, const int32_t* offsets, const float* initial_state,
+                          void* o, float* final_state, void* kept, int64_t kept_bytes,
+                          hipStream_t stream);
+
+/* Its gradients, from `kept` as the forward call left it.  grad_final_state
+ * may be NULL (zero), and so may every output (not wanted). */
+sla_status sla_delta_rule_grad(const sla_delta_dims* dims, const void* q, int64_t ldq,
+                               const void* k, int64_t ldk, const void* v, int64_t ldv,
+                               const float* g, const float* beta, const void* kept,
+                               int64_t kept_bytes, const void* grad_o, int64_t ldo,
+                               const float* grad_final_state, void* dq, void* dk, void* dv,
+                               float* dg, float* dbeta, float* grad_initial_state, void* work,
+                               int64_t work_bytes, hipStream_t stream);
+
+/* One token of every sequence (tokens == sequences, packed == 0) against the
+ * kept states [sequences][value_heads][key_dim][value_dim], updated in place. */
+sla_status sla_delta_step(const sla_delta_dims* dims, const void* q, int64_t ldq, const void* k,
+                          int64_t ldk, const void* v, int64_t ldv, const float* g,
+                          const float* beta, float* state, void* o, hipStream_t stream);
+
 /* Message of the last failed call on this thread ("" if none): the error
  * reporting of this boundary (not on the pages). */
 const char* sla_last_error(void);

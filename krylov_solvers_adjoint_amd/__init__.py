@@ -32,6 +32,9 @@ __all__ = [
     "sla_solve_list", "sla_adjoint_list", "SparseTensorList",
     "sla_csr_reorder", "sla_csr_ordering", "sla_csr_load_values", "sla_csr_arrays",
     "sla_memory_usage",
+    "layer_norm", "gated_ffn", "gated_delta_rule", "gated_delta_step",
+    "sla_layer_norm", "sla_layer_norm_grad", "sla_gated_ffn", "sla_gated_ffn_grad",
+    "sla_delta_rule", "sla_delta_rule_grad", "sla_delta_step",
     "LIB_PATH", "EXPORTS",
 ]
 
@@ -60,6 +63,9 @@ EXPORTS = [
     "sla_solve_list", "sla_adjoint_list", "sla_csr_reorder", "sla_csr_ordering",
     "sla_csr_set_one_group", "sla_resident_loop_ms", "sla_csr_load_values", "sla_csr_arrays",
     "sla_memory_usage",
+    "sla_layer_norm", "sla_layer_norm_work", "sla_layer_norm_grad",
+    "sla_gated_ffn", "sla_gated_ffn_work", "sla_gated_ffn_grad",
+    "sla_delta_rule_work", "sla_delta_rule", "sla_delta_rule_grad", "sla_delta_step",
     "sla_cg_solve_noalloc", "sla_last_error", "sla_status_string",
 ]
 
@@ -128,6 +134,20 @@ def _bind(lib):
                            ctypes.POINTER(_P)],
         "sla_memory_usage": [ctypes.POINTER(_I64), ctypes.POINTER(_I64), _S],
         "sla_cg_solve_noalloc": [_P, _P, _P, _D, _I64, _U32, _P, _P],
+        "sla_layer_norm": [_P, _I64, _I64, _I64, _S, _P, _P, _S, _D, _P, _P, _P],
+        "sla_layer_norm_work": [_I64, _I64, _S, ctypes.POINTER(_I64)],
+        "sla_layer_norm_grad": [_P, _I64, _P, _I64, _I64, _I64, _S, _P, _S, _P, _P, _P, _P, _P,
+                                _I64, _P],
+        "sla_gated_ffn": [_P, _I64, _P, _P, _I64, _I64, _I64, _S, _S, _P, _P],
+        "sla_gated_ffn_work": [_I64, _I64, _I64, _S, ctypes.POINTER(_I64)],
+        "sla_gated_ffn_grad": [_P, _I64, _P, _I64, _P, _P, _I64, _I64, _I64, _S, _S, _P, _P, _P,
+                               _P, _I64, _P],
+        "sla_delta_rule_work": [_P, _P, _P],
+        "sla_delta_rule": [_P, _P, _I64, _P, _I64, _P, _I64, _P, _P, _P, _P, _P, _P, _P, _I64,
+                           _P],
+        "sla_delta_rule_grad": [_P, _P, _I64, _P, _I64, _P, _I64, _P, _P, _P, _I64, _P, _I64,
+                                _P, _P, _P, _P, _P, _P, _P, _P, _I64, _P],
+        "sla_delta_step": [_P, _P, _I64, _P, _I64, _P, _I64, _P, _P, _P, _P, _P],
     }
     for name, args in sig.items():
         f = getattr(lib, name)
@@ -964,3 +984,8 @@ def solve(A: SparseTensor, b: torch.Tensor, tol: float = 1e-10, maxit: int = 100
           precond: str | None = None, method: str = "cg"):
     """x = A^{-1} b with the adjoint backward pass."""
     return A.solve(b, tol, maxit, precond, method)
+
+
+from .network import (gated_delta_rule, gated_delta_step, gated_ffn, layer_norm,  # noqa: E402
+                      sla_delta_rule, sla_delta_rule_grad, sla_delta_step, sla_gated_ffn,
+                      sla_gated_ffn_grad, sla_layer_norm, sla_layer_norm_grad)

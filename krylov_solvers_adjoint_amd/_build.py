@@ -15,7 +15,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libsla.so")
 SOURCES = ["api.hip", "csr_build.hip", "cg.hip", "lanczos.hip", "bicgstab.hip", "reorder.hip",
-           "noalloc.hip"]
+           "noalloc.hip", "norm.hip", "ffn.hip", "delta.hip"]
 ARCH = os.environ.get("SLA_OFFLOAD_ARCH", "gfx950")
 
 HIPCC_FLAGS = [

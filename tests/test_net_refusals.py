@@ -1,0 +1,158 @@
+"""What the network operators refuse, on the CPU: bad arguments never reach a
+kernel.  The C entries are called with made-up addresses that they must
+reject before any of them is used."""
+import ctypes
+
+import pytest
+import torch
+
+import krylov_solvers_adjoint_amd as K
+from krylov_solvers_adjoint_amd import network as net
+
+lib = K._lib
+P = 256  # an address that is never followed
+
+
+def last():
+    return lib.sla_last_error().decode()
+
+
+def test_layer_norm_refusals():
+    n = K._I64()
+    ok = dict(x=P, ld=8, rows=4, cols=8, t=0, w=P, b=P, wt=0, eps=1e-5, y=P)
+
+    def call(**kw):
+        a = {**ok, **kw}
+        return lib.sla_layer_norm(a["x"], a["ld"], a["rows"], a["cols"], a["t"], a["w"], a["b"],
+                                  a["wt"], a["eps"], a["y"], None, None)
+    for kw in (dict(x=None), dict(y=None), dict(ld=7), dict(rows=-1), dict(rows=1 << 31),
+               dict(cols=0), dict(t=3), dict(t=-1), dict(wt=1), dict(wt=2), dict(eps=-1.0),
+               dict(eps=float("nan"))):
+        assert call(**kw) == K.ERR_ARG, kw
+        assert last().startswith("sla_layer_norm"), kw
+    assert call(rows=0, x=None, y=None) == K.OK  # nothing to do
+    assert lib.sla_layer_norm_work(4, 8, 0, None) == K.ERR_ARG
+    assert lib.sla_layer_norm_work(4, 8, 0, ctypes.byref(n)) == K.OK and n.value > 0
+    # dw wanted, but the workspace is missing or short
+    for work, size in ((None, n.value), (P, n.value - 1)):
+        assert lib.sla_layer_norm_grad(P, 8, P, 8, 4, 8, 0, P, 0, P, P, P, P, work, size,
+                                       None) == K.ERR_ARG
+        assert "workspace" in last()
+    assert lib.sla_layer_norm_grad(None, 8, P, 8, 4, 8, 0, P, 0, P, P, P, P, P, n.value,
+                                   None) == K.ERR_ARG
+    assert lib.sla_layer_norm_grad(P, 7, P, 8, 4, 8, 0, P, 0, P, P, P, P, P, n.value,
+                                   None) == K.ERR_ARG
+
+
+def test_gated_ffn_refusals():
+    def call(x=P, ld=8, wg=P, wu=P, rows=4, inner=8, outer=16, t=0, act=0, h=P):
+        return lib.sla_gated_ffn(x, ld, wg, wu, rows, inner, outer, t, act, h, None)
+    for kw in (dict(x=None), dict(wg=None), dict(wu=None), dict(h=None), dict(ld=7),
+               dict(rows=-1), dict(inner=0), dict(outer=0), dict(t=9), dict(act=3), dict(act=-1),
+               dict(rows=1 << 40), dict(outer=1 << 40)):
+        assert call(**kw) == K.ERR_ARG, kw
+        assert last().startswith("sla_gated_ffn"), kw
+    assert call(rows=0, x=None, h=None) == K.OK
+    n = K._I64()
+    assert lib.sla_gated_ffn_work(4, 8, 16, 2, ctypes.byref(n)) == K.OK
+    # lddh, dh, the workspace, one weight's gradient without the other's
+    good = [P, 16, P, 8, P, P, 4, 8, 16, 2, 0, P, P, P, P, n.value, None]
+    for at, bad in ((0, None), (1, 15), (2, None), (3, 7), (12, None), (14, None),
+                    (15, n.value - 1)):
+        args = list(good)
+        args[at] = bad
+        assert lib.sla_gated_ffn_grad(*args) == K.ERR_ARG, at
+
+
+def dims(**kw):
+    d = dict(sequences=2, tokens=8, key_heads=2, value_heads=4, key_dim=16, value_dim=24,
+             scale=1.0, type=0, packed=0)
+    d.update(kw)
+    return net._DeltaDims(*[d[n] for n, _ in net._DeltaDims._fields_])
+
+
+def test_delta_refusals():
+    n, m = K._I64(), K._I64()
+    for kw in (dict(type=5), dict(sequences=-1), dict(tokens=-1), dict(tokens=9),
+               dict(sequences=0), dict(key_heads=0), dict(value_heads=3), dict(value_heads=0),
+               dict(key_dim=0), dict(key_dim=129), dict(value_dim=0), dict(value_dim=4097),
+               dict(tokens=1 << 31, packed=1)):
+        assert lib.sla_delta_rule_work(ctypes.byref(dims(**kw)), ctypes.byref(n),
+                                       None) == K.ERR_ARG, kw
+    assert lib.sla_delta_rule_work(None, None, None) == K.ERR_ARG
+    d = dims()
+    assert lib.sla_delta_rule_work(ctypes.byref(d), ctypes.byref(n), ctypes.byref(m)) == K.OK
+    good = [ctypes.byref(d), P, 32, P, 32, P, 96, P, P, None, None, P, P, P, n.value, None]
+    for at, bad in ((1, None), (2, 31), (3, None), (4, 31), (5, None), (6, 95), (7, None),
+                    (8, None), (11, None), (13, None), (14, n.value - 1)):
+        args = list(good)
+        args[at] = bad
+        assert lib.sla_delta_rule(*args) == K.ERR_ARG, at
+    packed = dims(packed=1)
+    args = list(good)
+    args[0] = ctypes.byref(packed)
+    args[14] = 1 << 40
+    assert lib.sla_delta_rule(*args) == K.ERR_ARG and "offsets" in last()
+    good = [ctypes.byref(d), P, 32, P, 32, P, 96, P, P, P, n.value, P, 96, None, P, P, P, P, P, P,
+            P, m.value, None]
+    for at, bad in ((1, None), (9, None), (10, n.value - 1), (11, None), (12, 95), (20, None),
+                    (21, m.value - 1)):
+        args = list(good)
+        args[at] = bad
+        assert lib.sla_delta_rule_grad(*args) == K.ERR_ARG, at
+    one = dims(tokens=2)
+    good = [ctypes.byref(one), P, 32, P, 32, P, 96, P, P, P, P, None]
+    for at, bad in ((0, ctypes.byref(dims())), (0, ctypes.byref(dims(tokens=2, packed=1))),
+                    (1, None), (9, None), (10, None), (6, 95)):
+        args = list(good)
+        args[at] = bad
+        assert lib.sla_delta_step(*args) == K.ERR_ARG, at
+    # no sequences: nothing to do
+    assert lib.sla_delta_rule(ctypes.byref(dims(sequences=0, tokens=0)), *([None] * 1), 32, None,
+                              32, None, 96, None, None, None, None, None, None, None, 0,
+                              None) == K.OK
+
+
+def test_cpu_tensors_and_wrong_kinds_are_refused():
+    x = torch.zeros(4, 8)
+    with pytest.raises(ValueError, match="GPU tensor"):
+        K.layer_norm(x)
+    with pytest.raises(TypeError):
+        K.layer_norm([1.0])
+    with pytest.raises(ValueError, match="GPU tensor"):
+        K.gated_ffn(x, x, x)
+    with pytest.raises(ValueError, match="GPU tensor"):
+        K.gated_delta_rule(x, x, x, x, x)
+    with pytest.raises(ValueError, match="GPU tensor"):
+        K.gated_delta_step(x, x, x, x, x, x)
+
+
+@pytest.mark.parametrize("make, tail, ld", [
+    (lambda: torch.zeros(6, 8), 1, 8),
+    (lambda: torch.zeros(6, 20)[:, 4:12], 1, 20),           # part of a wider row
+    (lambda: torch.zeros(2, 3, 20)[..., :8], 1, 20),
+    (lambda: torch.zeros(1, 3, 40)[..., 8:24].unflatten(-1, (2, 8)), 2, 40),
+    (lambda: torch.zeros(1, 8)[:, :3], 1, 8),
+])
+def test_views_with_even_rows_are_taken_as_they_are(make, tail, ld):
+    t = make()
+    u, got = net._rows(t, tail)
+    assert u.data_ptr() == t.data_ptr() and (got == ld or t.shape[0] == 1)
+
+
+@pytest.mark.parametrize("make, tail", [
+    (lambda: torch.zeros(8, 6).t(), 1),                     # rows not contiguous
+    (lambda: torch.zeros(6, 1).expand(6, 8), 1),            # broadcast columns
+    (lambda: torch.zeros(1, 8).expand(6, 8), 1),            # broadcast rows
+    (lambda: torch.zeros(3, 2, 8).transpose(0, 1), 1),      # rows in another order
+    (lambda: torch.zeros(4, 3, 2, 8).transpose(1, 2), 2),   # heads before tokens
+    (lambda: torch.zeros(4, 6, 8)[:, :4], 1),               # gaps between batches
+])
+def test_other_views_are_copied(make, tail):
+    t = make()
+    u, ld = net._rows(t, tail)
+    assert u.is_contiguous() and u.shape == t.shape and torch.equal(u, t)
+    width = 1
+    for n in t.shape[t.dim() - tail:]:
+        width *= n
+    assert ld == width
