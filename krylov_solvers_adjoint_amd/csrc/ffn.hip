@@ -12,6 +12,8 @@
 // type of the products that follow: keeping fp32 would halve nothing and
 // double the bytes, and the 16-bit matrix instructions take 16-bit factors.
 // All sums are fp32.
+#include <type_traits>
+
 #include "net.h"
 
 namespace sla {
@@ -19,7 +21,7 @@ namespace net {
 namespace {
 
 constexpr int kFfnBlock = 256;
-constexpr int kBM = 128, kBN = 128, kBK = 32;
+constexpr int kStepBytes = 128;   // bytes of k a step covers: 64 16-bit values or 32 fp32
 
 enum { EPI_GATE, EPI_GATE_GRAD, EPI_STORE };
 
@@ -45,184 +47,622 @@ struct Product {
   const void *A[2], *B[2];
   int64_t lda, ldb;
   int64_t M, N, K;
-  int parts;
+  int parts, outputs;
   const void* dh;    // EPI_GATE_GRAD [M][N]
   int64_t lddh;
-  void* C[2];        // EPI_GATE: h; EPI_GATE_GRAD: da, db; EPI_STORE: one per blockIdx.z
+  void* C[2];        // EPI_GATE: h; EPI_GATE_GRAD: da, db; EPI_STORE: one per output
   int64_t ldc;
   int act;
+  // filled by the launch
+  int splits;        // of the steps; > 1: fp32 sums go to part [output][split][M][N]
+  float* part;
+  int gx, gy;        // tiles along N and M
 };
 
+// 16 bytes of an operand: a lane's factor of one matrix instruction (8 16-bit
+// values of 32 k) or of four (4 fp32 values of 16 k).
 template <typename T>
-struct Mfma;
-template <>
-struct Mfma<__bf16> {
-  typedef __bf16 Frag __attribute__((ext_vector_type(8)));
-  static constexpr int kPad = 8;
-  static __device__ __forceinline__ f32x4 run(Frag a, Frag b, f32x4 c) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
-  }
-};
-template <>
-struct Mfma<_Float16> {
-  typedef _Float16 Frag __attribute__((ext_vector_type(8)));
-  static constexpr int kPad = 8;
-  static __device__ __forceinline__ f32x4 run(Frag a, Frag b, f32x4 c) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
-  }
-};
-template <>
-struct Mfma<float> {
-  typedef float Frag __attribute__((ext_vector_type(8)));
-  static constexpr int kPad = 4;
-  static __device__ __forceinline__ f32x4 run(Frag a, Frag b, f32x4 c) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[j], b[j], c, 0, 0, 0);
-    return c;
-  }
+struct Unit {
+  static constexpr int kN = 16 / int(sizeof(T));
+  typedef T Vec __attribute__((ext_vector_type(16 / sizeof(T))));
+  typedef typename VecOf<T, 16 / sizeof(T)>::type Loose;
 };
 
-// A kBM (or kBN) x kBK piece of an operand, on its way to LDS through
-// registers: 16 elements a thread, zero outside the matrix.
-template <typename T, bool TRANS>
-struct Piece {
-  typename VecOf<T, 8>::type v[2];
-  __device__ __forceinline__ void fetch(const T* p, int64_t ld, int64_t rows, int64_t k0,
-                                        int64_t K) {
+// acc (4 columns 4 h + r of row l) += rows of `a` times rows of `b`.
+__device__ __forceinline__ void mma16(f32x4& acc, Unit<__bf16>::Vec a, Unit<__bf16>::Vec b) {
+  acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b, a, acc, 0, 0, 0);
+}
+__device__ __forceinline__ void mma16(f32x4& acc, Unit<_Float16>::Vec a, Unit<_Float16>::Vec b) {
+  acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(b, a, acc, 0, 0, 0);
+}
+__device__ __forceinline__ void mma16(f32x4& acc, Unit<float>::Vec a, Unit<float>::Vec b) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int at = threadIdx.x + i * kFfnBlock;
-      int64_t line, along, lines, length;
-      if constexpr (TRANS) {
-        line = k0 + at / 16, along = at % 16 * 8, lines = K, length = rows;
-      } else {
-        line = at / 4, along = k0 + at % 4 * 8, lines = rows, length = K;
-      }
-      const T* q = p + line * ld + along;
-      const int64_t have = line < lines ? length - along : 0;
-      if (have >= 8) {
-        v[i] = *reinterpret_cast<const typename VecOf<T, 8>::type*>(q);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[i][j] = j < have ? q[j] : T(0.f);
-      }
-    }
-  }
-  __device__ __forceinline__ void put(T* lds, int ldl) const {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int at = threadIdx.x + i * kFfnBlock;
-      if constexpr (TRANS) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) lds[(at % 16 * 8 + j) * ldl + at / 16] = v[i][j];
-      } else {
-        T* d = lds + (at / 4) * ldl + at % 4 * 8;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) d[j] = v[i][j];
-      }
-    }
-  }
-};
-
-// 128 x 128 tiles, 4 waves of 64 x 64.  EPI_GATE*: the tile's columns are 64
-// of a and the same 64 of b, half of each in every wave.
-template <typename T, bool AT, bool BT, int EPI>
-__global__ __launch_bounds__(kFfnBlock) void k_ffn_product(Product g) {
-  using MM = Mfma<T>;
-  constexpr bool kGate = EPI != EPI_STORE;
-  constexpr int LD = kBK + MM::kPad, kCols = kGate ? kBN / 2 : kBN;
-  __shared__ __align__(16) T As[kBM * LD];
-  __shared__ __align__(16) T Bs[kBN * LD];
-  const int t = threadIdx.x, w = t / kWave, l = t % 16, h = (t % kWave) / 16;
-  const int wm = w / 2, wn = w % 2;
-  const int64_t m0 = int64_t(blockIdx.y) * kBM, n0 = int64_t(blockIdx.x) * kCols;
-  const int z = blockIdx.z;
-  f32x4 acc[4][4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
-  // row of the B tile of this wave's column tile j
-  auto brow = [&](int j) {
-    return kGate ? (j / 2) * (kBN / 2) + wn * 32 + (j % 2) * 16 : wn * 64 + j * 16;
-  };
-  for (int s = 0; s < g.parts; ++s) {
-    const T* A = (const T*)g.A[kGate ? 0 : s + z] + m0 * (AT ? 1 : g.lda);
-    const T* B0 = (const T*)g.B[kGate ? 0 : s] + n0 * (BT ? 1 : g.ldb);
-    const T* B1 = (const T*)g.B[1] + n0 * g.ldb;  // kGate only
-    for (int64_t k0 = 0; k0 < g.K; k0 += kBK) {
-      Piece<T, AT> pa;
-      Piece<T, BT> pb;
-      pa.fetch(A + k0 * 0, g.lda, g.M - m0, k0, g.K);
-      if constexpr (kGate) {
-        // lines 0..63 from Wg, 64..127 from Wu
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int at = t + i * kFfnBlock;
-          const int64_t line = at / 4 % 64, along = k0 + at % 4 * 8;
-          const T* q = (i ? B1 : B0) + line * g.ldb + along;
-          const int64_t have = n0 + line < g.N ? g.K - along : 0;
-          if (have >= 8) {
-            pb.v[i] = *reinterpret_cast<const typename VecOf<T, 8>::type*>(q);
-          } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) pb.v[i][j] = j < have ? q[j] : T(0.f);
-          }
-        }
-      } else {
-        pb.fetch(B0, g.ldb, g.N - n0, k0, g.K);
-      }
-      __syncthreads();
-      pa.put(As, LD);
-      pb.put(Bs, LD);
-      __syncthreads();
-      typename MM::Frag fa[4], fb[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        fa[i] = *reinterpret_cast<const typename MM::Frag*>(As + (wm * 64 + i * 16 + l) * LD + 8 * h);
-        fb[i] = *reinterpret_cast<const typename MM::Frag*>(Bs + (brow(i) + l) * LD + 8 * h);
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = MM::run(fa[i], fb[j], acc[i][j]);
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int64_t row = m0 + wm * 64 + i * 16 + 4 * h + r;
-      if (row >= g.M) continue;
-#pragma unroll
-      for (int j = 0; j < (kGate ? 2 : 4); ++j) {
-        const int64_t col = n0 + brow(j) + l;
-        if (col >= g.N) continue;
-        if constexpr (EPI == EPI_STORE) {
-          ((T*)g.C[z])[row * g.ldc + col] = T(acc[i][j][r]);
-        } else {
-          float f, df;
-          activation(g.act, acc[i][j][r], f, df);
-          const float b = acc[i][j + 2][r];
-          if constexpr (EPI == EPI_GATE) {
-            ((T*)g.C[0])[row * g.ldc + col] = T(f * b);
-          } else {
-            const float d = float(((const T*)g.dh)[row * g.lddh + col]);
-            ((T*)g.C[0])[row * g.ldc + col] = T(d * b * df);
-            ((T*)g.C[1])[row * g.ldc + col] = T(d * f);
-          }
-        }
-      }
-    }
+  for (int j = 0; j < 4; ++j) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(b[j], a[j], acc, 0, 0, 0);
 }
 
-template <typename T, bool AT, bool BT, int EPI>
-sla_status launch_product(const Product& g, int outputs, hipStream_t stream) {
-  if (g.M == 0 || g.N == 0) return SLA_OK;
-  const int64_t gx = div_up(g.N, EPI == EPI_STORE ? kBN : kBN / 2), gy = div_up(g.M, kBM);
-  SLA_NET_REQUIRE(gx < (int64_t(1) << 31) && gy < 65536, "gated_ffn: a matrix is too large");
-  k_ffn_product<T, AT, BT, EPI><<<dim3(int(gx), int(gy), outputs), kFfnBlock, 0, stream>>>(g);
+typedef __attribute__((address_space(3))) void* LdsPtr;
+typedef __fp16 HalfQuad __attribute__((__vector_size__(8)));
+
+// Four k of one column out of an LDS tile stored [k][row]: the 16 lanes of a
+// group read four lines of 16 values and get a column each.
+template <typename T>
+__device__ __forceinline__ typename VecOf<T, 4>::type read_column(const char* p) {
+  typedef T V4 __attribute__((ext_vector_type(4)));
+  V4 v;
+  if constexpr (std::is_same<T, __bf16>::value)
+    v = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((__attribute__((address_space(3))) V4*)p);
+  else
+    v = __builtin_bit_cast(V4, __builtin_amdgcn_ds_read_tr16_b64_v4f16(
+                                   (__attribute__((address_space(3))) HalfQuad*)p));
+  return v;
+}
+
+// A step's piece of an operand in LDS: W rows by kStepBytes of k, in 16-byte
+// slots.  TRANS: lines of W rows, a line for each k; else lines of k, a line
+// for each row.  Slots are exchanged within their line (by the row, or by the
+// k in groups of 16 rows) so that a wave's fragment read touches every bank
+// evenly; a line's memory is still read whole.
+template <typename T, int W, bool TRANS, int THREADS>
+struct Tile {
+  static constexpr int kBytes = W * kStepBytes;
+  static constexpr int kN = Unit<T>::kN;
+  static constexpr int kLineSlots = TRANS ? W / kN : kStepBytes / 16;
+  static constexpr int kLoads = kBytes / 16 / THREADS;   // slots a thread fills
+  static constexpr int kSteps = kStepBytes / int(sizeof(T));
+  static constexpr int kGroups = W / 16;                   // groups of 16 rows
+  static constexpr int kThreads = THREADS;
+  static constexpr bool kTrans = TRANS;
+  typedef T Element;
+  typedef typename Unit<T>::Vec Vec;
+
+  static __device__ __forceinline__ int twist(int k) {
+    if constexpr (sizeof(T) == 4) return (k >> 2) & 3 & (kGroups - 1);
+    return ((k & 3) | ((k >> 3) & 1) << 2 | ((k >> 2) & 1) << 3) & (kGroups - 1);
+  }
+  // what slot i (of this thread's) holds: line and the first element along it
+  static __device__ __forceinline__ void source(int i, int& line, int& along) {
+    const int s = i * THREADS + int(threadIdx.x);
+    line = s / kLineSlots;
+    const int u = s % kLineSlots;
+    if constexpr (TRANS) {
+      constexpr int G = 16 / kN;  // slots of a group
+      along = ((u / G ^ twist(line)) * G + u % G) * kN;
+    } else {
+      along = (u ^ (line & 7)) * kN;
+    }
+  }
+  // rows base + l (base a multiple of 16), sub-step s (0, 1) of the step
+  static __device__ __forceinline__ Vec read(const char* lds, int base, int s) {
+    const int l = threadIdx.x % 16, h = threadIdx.x % kWave / 16;
+    if constexpr (!TRANS) {
+      return *reinterpret_cast<const Vec*>(lds + (base + l) * kStepBytes +
+                                           (((4 * s + h) ^ (l & 7)) << 4));
+    } else if constexpr (sizeof(T) == 2) {
+      Vec v;
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const int k = 32 * s + 8 * h + 4 * q + (l >> 2);
+        const auto c = read_column<T>(lds + k * W * 2 + ((base / 16 ^ twist(k)) * 32) + (l & 3) * 8);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[4 * q + j] = c[j];
+      }
+      return v;
+    } else {
+      Vec v;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int k = 16 * s + 4 * h + j;
+        v[j] = *reinterpret_cast<const T*>(lds + k * W * 4 + ((base / 16 ^ twist(k)) * 64) + l * 4);
+      }
+      return v;
+    }
+  }
+};
+
+// Where a step's operand lies: its first element, the elements from one line
+// to the next, and how many rows and k there are from it on.
+struct Source {
+  const char* p;
+  int64_t ld, rows, ks;
+};
+
+// Memory to LDS without a register in between, for operands whose lines are
+// whole aligned 16-byte units (the launch checks it).  Rows that do not exist
+// and k behind the end read as zero: their offset lies out of the buffer's
+// range.  `at`: each load's offset from the step's first element, kept from
+// step to step.
+constexpr int kOutside = int(0x80000000u);
+template <typename TI, int FROM, int COUNT>
+__device__ __forceinline__ void stage_offsets(int* at, const Source& s) {
+#pragma unroll
+  for (int i = FROM; i < FROM + COUNT; ++i) {
+    int line, along;
+    TI::source(i, line, along);
+    if (!TI::kTrans) line -= FROM * TI::kThreads / TI::kLineSlots;
+    at[i] = (TI::kTrans ? along : line) < s.rows
+                ? int((line * s.ld + along) * int64_t(16 / TI::kN)) : kOutside;
+  }
+}
+// 16 bytes a lane from p + at to lds + 16 lane (p and lds: one for the wave).
+__device__ __forceinline__ void send(const char* p, int at, char* lds) {
+  const auto rsrc = __builtin_amdgcn_make_buffer_rsrc((void*)p, 0, 0x7fffffff, 0x00020000);
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (LdsPtr)lds, 16, at, 0, 0, 0);
+}
+template <typename TI, int FROM, int COUNT>
+__device__ __forceinline__ void stage(char* lds, const int* at, const Source& s) {
+  const uint64_t p = reinterpret_cast<uint64_t>(s.p);
+  const char* const up = reinterpret_cast<const char*>(
+      uint64_t(uint32_t(__builtin_amdgcn_readfirstlane(int(p >> 32)))) << 32 |
+      uint32_t(__builtin_amdgcn_readfirstlane(int(p))));
+  lds += __builtin_amdgcn_readfirstlane(int(threadIdx.x) / kWave) * 1024;
+  if (s.ks >= TI::kSteps) {
+#pragma unroll
+    for (int i = FROM; i < FROM + COUNT; ++i) send(up, at[i], lds + i * TI::kThreads * 16);
+  } else {
+#pragma unroll
+    for (int i = FROM; i < FROM + COUNT; ++i) {
+      int line, along;
+      TI::source(i, line, along);
+      send(up, (TI::kTrans ? line : along) < s.ks ? at[i] : kOutside, lds + i * TI::kThreads * 16);
+    }
+  }
+}
+
+// ... and by way of registers, for any shape and alignment.
+template <typename TI, int FROM, int COUNT>
+__device__ __forceinline__ void fetch(typename TI::Vec* v, const Source& s) {
+  typedef typename TI::Element T;
+#pragma unroll
+  for (int i = FROM; i < FROM + COUNT; ++i) {
+    int line, along;
+    TI::source(i, line, along);
+    if (!TI::kTrans) line -= FROM * TI::kThreads / TI::kLineSlots;
+    const int64_t have =
+        line < (TI::kTrans ? s.ks : s.rows) ? (TI::kTrans ? s.rows : s.ks) - along : 0;
+    const T* q = (const T*)s.p + line * s.ld + along;
+    if (have >= TI::kN) {
+      const auto u = *reinterpret_cast<const typename Unit<T>::Loose*>(q);
+#pragma unroll
+      for (int j = 0; j < TI::kN; ++j) v[i][j] = u[j];
+    } else {
+#pragma unroll
+      for (int j = 0; j < TI::kN; ++j) v[i][j] = j < have ? q[j] : T(0.f);
+    }
+  }
+}
+
+// The workgroup's tile.  Workgroups go to the 8 XCDs in turn: each XCD gets a
+// run of neighbouring tiles (8 tiles of M by as many of N as it has), whose
+// operands its L2 then holds once.
+struct Where {
+  int m, n, z, split;
+};
+__device__ __forceinline__ Where find_tile(const Product& g) {
+  const int total = gridDim.x, b = blockIdx.x;
+  const int xcd = b % kXcds, q = total / kXcds, r = total % kXcds;
+  int id = xcd * q + (xcd < r ? xcd : r) + b / kXcds;
+  Where w;
+  const int tiles = g.gx * g.gy;
+  const int zs = id / tiles;
+  id -= zs * tiles;
+  w.z = __builtin_amdgcn_readfirstlane(zs / g.splits);
+  w.split = __builtin_amdgcn_readfirstlane(zs % g.splits);
+  const int width = 8 * g.gx, group = id / width;
+  const int rows = g.gy - group * 8 < 8 ? g.gy - group * 8 : 8;
+  id -= group * width;
+  w.m = __builtin_amdgcn_readfirstlane(group * 8 + id % rows);
+  w.n = __builtin_amdgcn_readfirstlane(id / rows);
+  return w;
+}
+
+template <typename T, int EPI>
+__device__ __forceinline__ void leave(const Product& g, int64_t row, int64_t col, int z,
+                                      const f32x4& a, const f32x4& b) {
+  const int64_t have = g.N - col;
+  float u[4], v[4];
+  if constexpr (EPI == EPI_STORE) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) u[r] = a[r];
+    store_f32<4>((T*)g.C[z] + row * g.ldc + col, have, u);
+  } else {
+    float d[4];
+    if constexpr (EPI == EPI_GATE_GRAD) load_f32<4>((const T*)g.dh + row * g.lddh + col, have, d);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      float f, df;
+      activation(g.act, a[r], f, df);
+      if constexpr (EPI == EPI_GATE) {
+        u[r] = f * b[r];
+      } else {
+        u[r] = d[r] * b[r] * df;
+        v[r] = d[r] * f;
+      }
+    }
+    store_f32<4>((T*)g.C[0] + row * g.ldc + col, have, u);
+    if constexpr (EPI == EPI_GATE_GRAD) store_f32<4>((T*)g.C[1] + row * g.ldc + col, have, v);
+  }
+}
+
+// Tiles of B x B in waves of WM x WN.  EPI_GATE*: the tile's columns are B / 2
+// of a and the same B / 2 of b, half of each wave's columns are of either.
+//
+// Two steps' tiles are in LDS.  A wave multiplies a row of 16 x WN at a time
+// and reads the fragments a sub-step ahead of their use, one between the
+// products of each row, so that the matrix cores and the LDS work side by
+// side.  The step's only barrier comes when the last fragment of its tile has
+// been read, NI - 1 rows before its last product: the tile's place is then
+// filled with the step after the next, which has a whole step to arrive.
+template <typename T, int B, int WM, int WN, bool AT, bool BT, int EPI, bool DIRECT>
+__global__ __launch_bounds__(kWave* B* B / WM / WN, 2) void k_ffn_product(Product g) {
+  constexpr bool kGate = EPI != EPI_STORE;
+  constexpr int kThreads = kWave * (B / WM) * (B / WN);
+  constexpr int NI = WM / 16, NJ = WN / 16, kCols = kGate ? B / 2 : B;
+  using TA = Tile<T, B, AT, kThreads>;
+  using TB = Tile<T, B, BT, kThreads>;
+  typedef typename Unit<T>::Vec Vec;
+  extern __shared__ __align__(1024) char smem[];
+  char* const lds0 = smem;
+  char* const lds1 = smem + TA::kBytes + TB::kBytes;
+  const int t = threadIdx.x, l = t % 16, h = t % kWave / 16;
+  const int w = __builtin_amdgcn_readfirstlane(t / kWave), wm = w / (B / WN), wn = w % (B / WN);
+  const Where at = find_tile(g);
+  const int64_t m0 = int64_t(at.m) * B, n0 = int64_t(at.n) * kCols;
+  const int steps = int(div_up(g.K, TA::kSteps)), all = steps * g.parts;
+  const int each = (all + g.splits - 1) / g.splits;
+  const int from = at.split * each, to = from + each < all ? from + each : all;
+  f32x4 acc[NI][NJ];
+#pragma unroll
+  for (int i = 0; i < NI; ++i)
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+
+  auto source_a = [&](int it) {
+    const int seg = it >= steps;
+    const int64_t k0 = int64_t(it - seg * steps) * TA::kSteps;
+    const T* p = (const T*)(kGate || !(seg + at.z) ? g.A[0] : g.A[1]) +
+                 (AT ? k0 * g.lda + m0 : m0 * g.lda + k0);
+    return Source{(const char*)p, g.lda, g.M - m0, g.K - k0};
+  };
+  auto source_b = [&](int it, int which) {
+    const int seg = it >= steps;
+    const int64_t k0 = int64_t(it - seg * steps) * TB::kSteps;
+    const T* p = (const T*)((kGate ? which : seg) ? g.B[1] : g.B[0]) +
+                 (BT ? k0 * g.ldb + n0 : n0 * g.ldb + k0);
+    return Source{(const char*)p, g.ldb, g.N - n0, g.K - k0};
+  };
+  // the wave's rows of the B tile: column tile j
+  auto brow = [&](int j) {
+    return kGate ? (j / (NJ / 2)) * (B / 2) + wn * (WN / 2) + j % (NJ / 2) * 16 : wn * WN + j * 16;
+  };
+  constexpr int HB = TB::kLoads / 2;
+  int ta[DIRECT ? TA::kLoads : 1], tb[DIRECT ? TB::kLoads : 1];
+  if constexpr (DIRECT) {
+    stage_offsets<TA, 0, TA::kLoads>(ta, source_a(0));
+    if constexpr (kGate) {
+      stage_offsets<TB, 0, HB>(tb, source_b(0, 0));
+      stage_offsets<TB, HB, HB>(tb, source_b(0, 0));
+    } else {
+      stage_offsets<TB, 0, TB::kLoads>(tb, source_b(0, 0));
+    }
+  }
+  Vec ra[DIRECT ? 1 : TA::kLoads], rb[DIRECT ? 1 : TB::kLoads];
+  auto begin = [&](char* lds, int it) {   // DIRECT: sends the step's tiles; else loads them
+    if (it >= to) return;
+    if constexpr (DIRECT) {
+      stage<TA, 0, TA::kLoads>(lds, ta, source_a(it));
+      if constexpr (kGate) {
+        stage<TB, 0, HB>(lds + TA::kBytes, tb, source_b(it, 0));
+        stage<TB, HB, HB>(lds + TA::kBytes, tb, source_b(it, 1));
+      } else {
+        stage<TB, 0, TB::kLoads>(lds + TA::kBytes, tb, source_b(it, 0));
+      }
+    } else {
+      fetch<TA, 0, TA::kLoads>(ra, source_a(it));
+      if constexpr (kGate) {
+        fetch<TB, 0, HB>(rb, source_b(it, 0));
+        fetch<TB, HB, HB>(rb, source_b(it, 1));
+      } else {
+        fetch<TB, 0, TB::kLoads>(rb, source_b(it, 0));
+      }
+    }
+  };
+  auto put = [&](char* lds) {
+    if constexpr (!DIRECT) {
+#pragma unroll
+      for (int i = 0; i < TA::kLoads; ++i)
+        *reinterpret_cast<Vec*>(lds + (i * kThreads + t) * 16) = ra[i];
+#pragma unroll
+      for (int i = 0; i < TB::kLoads; ++i)
+        *reinterpret_cast<Vec*>(lds + TA::kBytes + (i * kThreads + t) * 16) = rb[i];
+    }
+  };
+  auto arrive = [&] {
+    if constexpr (DIRECT) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+  };
+  Vec fa[NI], fb[2][NJ];
+  auto read_a = [&](const char* lds, int r) {   // row r of the step's 2 NI
+    fa[r % NI] = TA::read(lds, wm * WM + 16 * (r % NI), r / NI);
+  };
+  auto read_b = [&](const char* lds, int s, int j) {
+    fb[s][j] = TB::read(lds + TA::kBytes, brow(j), s);
+  };
+  if (from < to) {
+    begin(lds0, from);
+    put(lds0);
+    if (from + 1 < to) {
+      begin(lds1, from + 1);
+      put(lds1);
+    }
+    if constexpr (!DIRECT) begin(nullptr, from + 2);
+    arrive();
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) read_b(lds0, 0, j);
+#pragma unroll
+    for (int i = 0; i < NI - 1; ++i) read_a(lds0, i);
+    // behind the last step the fragments read are not used
+    auto step = [&](char* cur, char* nxt, int it) {
+#pragma unroll
+      for (int r = 0; r < 2 * NI; ++r) {
+        constexpr int kTurn = NI + 1;   // from this row on: the next tile's fragments
+        if (r == kTurn) {
+          arrive();
+          if constexpr (DIRECT) {
+            begin(cur, it + 2);
+          } else if (it + 2 < to) {
+            put(cur);
+            begin(nullptr, it + 3);
+          }
+        }
+        if (r < kTurn) read_a(cur, r + NI - 1);
+        else read_a(nxt, r + NI - 1 - 2 * NI);
+        if (r < NJ && r < NI) {
+          read_b(cur, 1, r);
+          if (r == NI - 1)
+            for (int j = NI; j < NJ; ++j) read_b(cur, 1, j);
+        }
+        if (r >= kTurn) {
+          constexpr int kLeft = NI - 1;
+#pragma unroll
+          for (int j = 0; j < NJ; ++j)
+            if (j % kLeft == r - kTurn) read_b(nxt, 0, j);
+        }
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) mma16(acc[r % NI][j], fa[r % NI], fb[r / NI][j]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    };
+    for (int it = from; it < to; it += 2) {
+      step(lds0, lds1, it);
+      if (it + 1 < to) step(lds1, lds0, it + 1);
+    }
+  }
+
+#pragma unroll
+  for (int i = 0; i < NI; ++i) {
+    const int64_t row = m0 + wm * WM + 16 * i + l;
+    if (row >= g.M) continue;
+#pragma unroll
+    for (int j = 0; j < (kGate ? NJ / 2 : NJ); ++j) {
+      const int64_t col = n0 + brow(j) + 4 * h;
+      if (col >= g.N) continue;
+      if (!kGate && g.splits > 1) {
+        float u[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) u[r] = acc[i][j][r];
+        store_f32<4>(g.part + ((int64_t(at.z) * g.splits + at.split) * g.M + row) * g.N + col,
+                     g.N - col, u);
+      } else {
+        leave<T, EPI>(g, row, col, at.z, acc[i][j], acc[i][kGate ? j + NJ / 2 : j]);
+      }
+    }
+  }
+}
+
+// The sums of a split product, in the order of the splits, rounded once.
+template <typename T>
+__global__ __launch_bounds__(kFfnBlock) void k_ffn_join(Product g) {
+  const int64_t size = g.M * g.N, quads = div_up(size, 4);
+  const int64_t i = (int64_t(blockIdx.x) * kFfnBlock + threadIdx.x) * 4;
+  if (i >= quads * 4) return;
+  const float* p = g.part + int64_t(blockIdx.y) * g.splits * size + i;
+  float s[4], u[4];
+  load_f32<4>(p, size - i, s);
+  for (int k = 1; k < g.splits; ++k) {
+    load_f32<4>(p + k * size, size - i, u);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s[j] += u[j];
+  }
+  store_f32<4>((T*)g.C[blockIdx.y] + i, size - i, s);
+}
+
+// The projections of few rows (at most 16 RT): reading the weights is the
+// work.  A workgroup has 16 columns of a and of b; its four waves take turns
+// along k, fragments straight from memory, and are joined through LDS.
+template <typename T, int RT, int EPI>
+__global__ __launch_bounds__(kFfnBlock) void k_ffn_few(Product g) {
+  typedef typename Unit<T>::Vec Vec;
+  constexpr int kN = Unit<T>::kN, kSpan = 4 * kN;   // k of one fragment
+  __shared__ f32x4 sums[4][RT][2][kWave];
+  const int t = threadIdx.x, w = t / kWave, l = t % 16, h = t % kWave / 16;
+  const int64_t n0 = int64_t(blockIdx.x) * 16;
+  auto line = [](const void* p, int64_t ld, int64_t row, int64_t rows) {
+    return (const T*)p + (row < rows ? row : rows - 1) * ld;
+  };
+  const T* b0 = line(g.B[0], g.ldb, n0 + l, g.N);
+  const T* b1 = line(g.B[1], g.ldb, n0 + l, g.N);
+  const T* a[RT];
+#pragma unroll
+  for (int i = 0; i < RT; ++i) a[i] = line(g.A[0], g.lda, 16 * i + l, g.M);
+  const int K = int(g.K);
+  f32x4 acc[RT][2];
+#pragma unroll
+  for (int i = 0; i < RT; ++i) acc[i][0] = acc[i][1] = f32x4{0, 0, 0, 0};
+  // a wave takes two neighbouring spans (128 bytes of a row) at a time
+  auto load = [&](int k, auto whole, Vec (&u)[2][2], Vec (&x)[2][RT]) {
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      const int kk = k + s * kSpan + h * kN;
+      auto unit = [&](const T* p) {
+        Vec v;
+        if constexpr (whole.value) {
+          const auto q = *reinterpret_cast<const typename Unit<T>::Loose*>(p + kk);
+#pragma unroll
+          for (int j = 0; j < kN; ++j) v[j] = q[j];
+        } else {
+#pragma unroll
+          for (int j = 0; j < kN; ++j) v[j] = kk + j < K ? p[kk + j] : T(0.f);
+        }
+        return v;
+      };
+      u[s][0] = unit(b0);
+      u[s][1] = unit(b1);
+#pragma unroll
+      for (int i = 0; i < RT; ++i) x[s][i] = unit(a[i]);
+    }
+  };
+  auto multiply = [&](const Vec (&u)[2][2], const Vec (&x)[2][RT]) {
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int i = 0; i < RT; ++i) {
+        mma16(acc[i][0], x[s][i], u[s][0]);
+        mma16(acc[i][1], x[s][i], u[s][1]);
+      }
+  };
+  constexpr int kStep = 2 * kSpan, kTurn = 4 * kStep;
+  int k = kStep * w;
+  for (; k + 3 * kTurn + kStep <= K; k += 4 * kTurn) {  // four turns' loads travel at once
+    Vec u[4][2][2], x[4][2][RT];
+#pragma unroll
+    for (int n = 0; n < 4; ++n) load(k + n * kTurn, std::true_type(), u[n], x[n]);
+#pragma unroll
+    for (int n = 0; n < 4; ++n) multiply(u[n], x[n]);
+  }
+  for (; k < K; k += kTurn) {
+    Vec u[2][2], x[2][RT];
+    if (k + kStep <= K) load(k, std::true_type(), u, x);
+    else load(k, std::false_type(), u, x);
+    multiply(u, x);
+  }
+#pragma unroll
+  for (int i = 0; i < RT; ++i) {
+    sums[w][i][0][t % kWave] = acc[i][0];
+    sums[w][i][1][t % kWave] = acc[i][1];
+  }
+  __syncthreads();
+  for (int i = w; i < RT; i += 4) {
+    const int64_t row = 16 * i + l, col = n0 + 4 * h;
+    if (row >= g.M || col >= g.N) continue;
+    f32x4 s[2];
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+      s[b] = (sums[0][i][b][t % kWave] + sums[1][i][b][t % kWave]) +
+             (sums[2][i][b][t % kWave] + sums[3][i][b][t % kWave]);
+    leave<T, EPI>(g, row, col, 0, s[0], s[1]);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+
+// Tiles and splits of a product: the pair with the least estimated time.
+struct ProductPlan {
+  int tile, splits;
+};
+ProductPlan plan_product(int64_t M, int64_t N, int64_t K, int parts, int outputs, bool gate,
+                         int es, bool direct) {
+  struct Kind {
+    int tile, slots;       // side; workgroups a CU holds
+    double step, start;    // us of a step with every slot taken; us before and after the steps
+  };
+  static const Kind kind16[] = {{256, 1, 1.10, 6.0}, {128, 2, 0.75, 4.0}, {64, 4, 0.55, 3.0}};
+  static const Kind kind32[] = {{256, 1, 0, 0}, {128, 2, 3.6, 5.0}, {64, 4, 2.0, 4.0}};
+  const Kind* kinds = es == 4 ? kind32 : kind16;
+  const int64_t steps = div_up(K, kStepBytes / es) * parts, cus = device_cus();
+  ProductPlan best{64, 1};
+  double least = 1e30;
+  for (int i = es == 4 || !direct ? 1 : 0; i < 3; ++i) {
+    const Kind& k = kinds[i];
+    const int64_t tiles = div_up(M, k.tile) * div_up(N, gate ? k.tile / 2 : k.tile) * outputs;
+    for (int s = 1; s <= (gate ? 1 : 32) && s <= (steps + 3) / 4; ++s) {
+      const double rounds = double(div_up(tiles * s, cus * k.slots));
+      double time = rounds * (double(div_up(steps, s)) * k.step + k.start);
+      if (s > 1) time += 4.0 + double(s + 1) * double(M * N * outputs) * 4 / 4e6;
+      if (time < least) least = time, best = {k.tile, s};
+    }
+  }
+  return best;
+}
+
+int64_t split_bytes(int64_t M, int64_t N, int64_t K, int parts, int outputs, int es) {
+  int64_t most = 0;
+  for (int direct = 0; direct < 2; ++direct) {
+    const ProductPlan p = plan_product(M, N, K, parts, outputs, false, es, direct);
+    const int64_t b = p.splits > 1 ? p.splits * outputs * M * N * 4 : 0;
+    if (b > most) most = b;
+  }
+  return most;
+}
+
+// Whether an operand's lines are whole aligned 16-byte units that 31 bits of
+// a tile's offsets reach.
+bool whole_units(const void* p, int64_t ld, int64_t along, int es) {
+  const int64_t n = 16 / es;
+  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % n == 0 && along % n == 0 &&
+         ld * es * 256 < (int64_t(1) << 31);
+}
+
+template <typename T, int B, int WM, int WN, bool AT, bool BT, int EPI, bool DIRECT>
+sla_status run_product(Product& g, hipStream_t stream) {
+  constexpr int lds = 2 * 2 * B * kStepBytes;
+  const int64_t gx = div_up(g.N, EPI == EPI_STORE ? B : B / 2), gy = div_up(g.M, B);
+  SLA_NET_REQUIRE(gx * gy * g.outputs * g.splits < (int64_t(1) << 31),
+                  "gated_ffn: a matrix is too large");
+  g.gx = int(gx), g.gy = int(gy);
+  auto* kernel = k_ffn_product<T, B, WM, WN, AT, BT, EPI, DIRECT>;
+  if (lds > 65536)
+    SLA_TRY_HIP(hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                    hipFuncAttributeMaxDynamicSharedMemorySize, lds));
+  kernel<<<int(gx * gy) * g.outputs * g.splits, kWave * (B / WM) * (B / WN), lds, stream>>>(g);
   LAUNCH_CHECK();
+  return SLA_OK;
+}
+
+constexpr int64_t kFewRows = 64;
+
+template <typename T, bool AT, bool BT, int EPI>
+sla_status launch_product(Product& g, hipStream_t stream) {
+  constexpr bool kGate = EPI != EPI_STORE;
+  constexpr int es = int(sizeof(T));
+  if (g.M == 0 || g.N == 0) return SLA_OK;
+  if constexpr (kGate) {
+    if (g.M <= kFewRows) {
+      const int grid = int(div_up(g.N, 16));
+      if (g.M <= 16) k_ffn_few<T, 1, EPI><<<grid, kFfnBlock, 0, stream>>>(g);
+      else if (g.M <= 32) k_ffn_few<T, 2, EPI><<<grid, kFfnBlock, 0, stream>>>(g);
+      else k_ffn_few<T, 4, EPI><<<grid, kFfnBlock, 0, stream>>>(g);
+      LAUNCH_CHECK();
+      return SLA_OK;
+    }
+  }
+  const int64_t ka = AT ? g.M : g.K, kb = BT ? g.N : g.K;
+  const bool direct =
+      es == 2 && whole_units(g.A[0], g.lda, ka, es) && whole_units(g.B[0], g.ldb, kb, es) &&
+      (!g.A[1] || whole_units(g.A[1], g.lda, ka, es)) &&
+      (!g.B[1] || whole_units(g.B[1], g.ldb, kb, es));
+  const ProductPlan p = plan_product(g.M, g.N, g.K, g.parts, g.outputs, kGate, es, direct);
+  g.splits = p.splits;
+  if (p.tile == 64) SLA_TRY((run_product<T, 64, 32, 32, AT, BT, EPI, false>(g, stream)));
+  if (p.tile == 128) SLA_TRY((run_product<T, 128, 64, 64, AT, BT, EPI, false>(g, stream)));
+  if constexpr (es == 2)
+    if (p.tile == 256) SLA_TRY((run_product<T, 256, 128, 64, AT, BT, EPI, true>(g, stream)));
+  if (g.splits > 1) {
+    k_ffn_join<T><<<dim3(int(div_up(g.M * g.N, 4 * kFfnBlock)), g.outputs), kFfnBlock, 0,
+                    stream>>>(g);
+    LAUNCH_CHECK();
+  }
   return SLA_OK;
 }
 
@@ -236,6 +676,17 @@ sla_status ffn_args(const char* who, int64_t rows, int64_t inner, int64_t outer,
                       outer < (int64_t(1) << 22), "%s: inner or outer out of range", who);
   SLA_NET_REQUIRE(ldx >= inner, "%s: row stride below inner", who);
   return SLA_OK;
+}
+
+// The workspace: da, db, then the sums of a split product (dx and the weights'
+// gradients use the same place one after the other).
+int64_t factor_bytes(int64_t rows, int64_t outer, int es) {
+  return div_up(rows * outer * es, 256) * 256;
+}
+int64_t grad_bytes(int64_t rows, int64_t inner, int64_t outer, int es) {
+  const int64_t x = split_bytes(rows, inner, outer, 2, 1, es);
+  const int64_t w = split_bytes(outer, inner, rows, 1, 2, es);
+  return 2 * factor_bytes(rows, outer, es) + (x > w ? x : w);
 }
 
 template <typename F>
@@ -269,11 +720,11 @@ sla_status sla_gated_ffn(const void* x, int64_t ldx, const void* w_gate, const v
     g.B[1] = w_up;
     g.lda = ldx;
     g.ldb = inner;
-    g.M = rows, g.N = outer, g.K = inner, g.parts = 1;
+    g.M = rows, g.N = outer, g.K = inner, g.parts = g.outputs = 1;
     g.C[0] = h;
     g.ldc = outer;
     g.act = act;
-    return launch_product<T, false, false, EPI_GATE>(g, 1, stream);
+    return launch_product<T, false, false, EPI_GATE>(g, stream);
   });
 }
 
@@ -282,7 +733,7 @@ sla_status sla_gated_ffn_work(int64_t rows, int64_t inner, int64_t outer, sla_ty
   clear_error();
   SLA_TRY(ffn_args("sla_gated_ffn_work", rows, inner, outer, inner, type, SLA_ACT_SILU));
   SLA_NET_REQUIRE(bytes_host, "sla_gated_ffn_work: bytes_host is NULL");
-  *bytes_host = 2 * rows * outer * int64_t(type_size(type));
+  *bytes_host = grad_bytes(rows, inner, outer, int(type_size(type)));
   return SLA_OK;
 }
 
@@ -297,8 +748,9 @@ sla_status sla_gated_ffn_grad(const void* dh, int64_t lddh, const void* x, int64
                   "sla_gated_ffn_grad: an argument is NULL");
   SLA_NET_REQUIRE((dw_gate == nullptr) == (dw_up == nullptr),
                   "sla_gated_ffn_grad: both weights' gradients or neither");
-  const int64_t size = rows * outer * int64_t(type_size(type));
-  SLA_NET_REQUIRE(rows == 0 || (work && work_bytes >= 2 * size),
+  const int es = int(type_size(type));
+  const int64_t size = factor_bytes(rows, outer, es);
+  SLA_NET_REQUIRE(rows == 0 || (work && work_bytes >= grad_bytes(rows, inner, outer, es)),
                   "sla_gated_ffn_grad: workspace too small (sla_gated_ffn_work)");
   return with_type(type, [&](auto te) -> sla_status {
     using T = decltype(te);
@@ -308,33 +760,36 @@ sla_status sla_gated_ffn_grad(const void* dh, int64_t lddh, const void* x, int64
     g.B[1] = w_up;
     g.lda = ldx;
     g.ldb = inner;
-    g.M = rows, g.N = outer, g.K = inner, g.parts = 1;
+    g.M = rows, g.N = outer, g.K = inner, g.parts = g.outputs = 1;
     g.dh = dh;
     g.lddh = lddh;
     g.C[0] = work;
     g.C[1] = (char*)work + size;
     g.ldc = outer;
     g.act = act;
-    SLA_TRY((launch_product<T, false, false, EPI_GATE_GRAD>(g, 1, stream)));
+    SLA_TRY((launch_product<T, false, false, EPI_GATE_GRAD>(g, stream)));
+    float* part = (float*)((char*)work + 2 * size);
     if (dx) {
       Product p{};
       p.A[0] = g.C[0], p.A[1] = g.C[1];
       p.B[0] = w_gate, p.B[1] = w_up;
       p.lda = outer, p.ldb = inner;
-      p.M = rows, p.N = inner, p.K = outer, p.parts = 2;
+      p.M = rows, p.N = inner, p.K = outer, p.parts = 2, p.outputs = 1;
+      p.part = part;
       p.C[0] = dx;
       p.ldc = inner;
-      SLA_TRY((launch_product<T, false, true, EPI_STORE>(p, 1, stream)));
+      SLA_TRY((launch_product<T, false, true, EPI_STORE>(p, stream)));
     }
     if (dw_gate) {
       Product p{};
       p.A[0] = g.C[0], p.A[1] = g.C[1];
       p.B[0] = p.B[1] = x;
       p.lda = outer, p.ldb = ldx;
-      p.M = outer, p.N = inner, p.K = rows, p.parts = 1;
+      p.M = outer, p.N = inner, p.K = rows, p.parts = 1, p.outputs = 2;
+      p.part = part;
       p.C[0] = dw_gate, p.C[1] = dw_up;
       p.ldc = inner;
-      SLA_TRY((launch_product<T, true, true, EPI_STORE>(p, 2, stream)));
+      SLA_TRY((launch_product<T, true, true, EPI_STORE>(p, stream)));
     }
     return SLA_OK;
   });
