@@ -25,15 +25,36 @@ constexpr int kStepBytes = 128;   // bytes of k a step covers: 64 16-bit values 
 
 enum { EPI_GATE, EPI_GATE_GRAD, EPI_STORE };
 
+// f(a) and f'(a).  FAST (16-bit tensors): exp and the reciprocal by their
+// instructions (1 ulp each) and erf by the five-term form of Abramowitz and
+// Stegun 7.1.26 (off by at most 1.5e-7), whose errors lie a thousand times
+// below a 16-bit half step; the library's expf, erff and divide took 7 us of
+// a 256 x 256 tile's 41.
+template <bool FAST>
 __device__ __forceinline__ void activation(int act, float a, float& f, float& df) {
+  constexpr float kLog2e = 1.4426950408889634f;
   if (act == SLA_ACT_SILU) {
-    const float s = 1.f / (1.f + expf(-a));
+    float s;
+    if constexpr (FAST) s = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-kLog2e * a));
+    else s = 1.f / (1.f + expf(-a));
     f = a * s;
     df = s * (1.f + a * (1.f - s));
   } else if (act == SLA_ACT_GELU) {
-    const float c = 0.5f * (1.f + erff(a * 0.70710678118654752f));
+    float c, e;   // the normal distribution's integral, exp(-a^2 / 2)
+    if constexpr (FAST) {
+      e = __builtin_amdgcn_exp2f(-0.5f * kLog2e * a * a);
+      const float x = fabsf(a) * 0.70710678118654752f;
+      const float t = __builtin_amdgcn_rcpf(1.f + 0.3275911f * x);
+      const float p = t * (0.254829592f + t * (-0.284496736f + t * (1.421413741f +
+                      t * (-1.453152027f + t * 1.061405429f))));
+      c = 0.5f * p * e;
+      c = a < 0.f ? c : 1.f - c;
+    } else {
+      e = expf(-0.5f * a * a);
+      c = 0.5f * (1.f + erff(a * 0.70710678118654752f));
+    }
     f = a * c;
-    df = c + a * (0.39894228040143268f * expf(-0.5f * a * a));
+    df = c + a * (0.39894228040143268f * e);
   } else {
     f = a > 0.f ? a : a * 0.f;  // NaN stays NaN
     df = a > 0.f ? 1.f : 0.f;
@@ -99,37 +120,54 @@ __device__ __forceinline__ typename VecOf<T, 4>::type read_column(const char* p)
 
 // A step's piece of an operand in LDS: W rows by kStepBytes of k, in 16-byte
 // slots.  TRANS: lines of W rows, a line for each k; else lines of k, a line
-// for each row.  Slots are exchanged within their line (by the row, or by the
-// k in groups of 16 rows) so that a wave's fragment read touches every bank
-// evenly; a line's memory is still read whole.
-template <typename T, int W, bool TRANS, int THREADS>
+// for each row.  So that a wave's fragment read touches every bank evenly the
+// slots of a row's line are exchanged by the row (the offset of a read then
+// depends on the lane alone), and the lines of k are moved apart: a read of 16
+// lines of 32 bytes (16-bit: k = 8 h + r and 4 more) or 4 of 64 (fp32: k = 4 h)
+// finds them at different banks.  Direct loads (PAIR) write 1024 bytes in one
+// piece: there the lines k and k + 32, never read together, are neighbours.
+template <typename T, int W, bool TRANS, int THREADS, bool PAIR>
 struct Tile {
-  static constexpr int kBytes = W * kStepBytes;
   static constexpr int kN = Unit<T>::kN;
   static constexpr int kLineSlots = TRANS ? W / kN : kStepBytes / 16;
-  static constexpr int kLoads = kBytes / 16 / THREADS;   // slots a thread fills
+  static constexpr int kLoads = W * kStepBytes / 16 / THREADS;   // slots a thread fills
   static constexpr int kSteps = kStepBytes / int(sizeof(T));
-  static constexpr int kGroups = W / 16;                   // groups of 16 rows
   static constexpr int kThreads = THREADS;
   static constexpr bool kTrans = TRANS;
   typedef T Element;
   typedef typename Unit<T>::Vec Vec;
+  static_assert(!(TRANS && PAIR) || (W == 256 && sizeof(T) == 2), "a pair of lines a load");
 
-  static __device__ __forceinline__ int twist(int k) {
-    if constexpr (sizeof(T) == 4) return (k >> 2) & 3 & (kGroups - 1);
-    return ((k & 3) | ((k >> 3) & 1) << 2 | ((k >> 2) & 1) << 3) & (kGroups - 1);
+  static constexpr __device__ int line_at(int k) {
+    if (sizeof(T) == 4) return k * W * 4 + 64 * (k >> 2);
+    if (PAIR) return k % 32 * (W * 4 + 32) + 128 * (k % 32 >> 3) + k / 32 * (W * 2);
+    return k * (W * 2 + 32) + 128 * (k >> 3);
   }
+  static constexpr int kBytes =
+      TRANS ? (line_at(kSteps - 1) + W * int(sizeof(T)) + 127) / 128 * 128 : W * kStepBytes;
+
   // what slot i (of this thread's) holds: line and the first element along it
   static __device__ __forceinline__ void source(int i, int& line, int& along) {
     const int s = i * THREADS + int(threadIdx.x);
     line = s / kLineSlots;
     const int u = s % kLineSlots;
     if constexpr (TRANS) {
-      constexpr int G = 16 / kN;  // slots of a group
-      along = ((u / G ^ twist(line)) * G + u % G) * kN;
+      if (PAIR) line = line / 2 + line % 2 * 32;
+      along = u * kN;
     } else {
       along = (u ^ (line & 7)) * kN;
     }
+  }
+  // where the slot lies; for direct loads the place of the wave's first one
+  static __device__ __forceinline__ int place(int i) {
+    const int s = i * THREADS + int(threadIdx.x);
+    if constexpr (!TRANS) return s * 16;
+    else return line_at(s / kLineSlots) + s % kLineSlots * 16;
+  }
+  static __device__ __forceinline__ int place(int i, int wave) {
+    const int n = i * (THREADS / kWave) + wave;
+    if constexpr (!TRANS) return n * 1024;
+    else return line_at(n);
   }
   // rows base + l (base a multiple of 16), sub-step s (0, 1) of the step
   static __device__ __forceinline__ Vec read(const char* lds, int base, int s) {
@@ -139,21 +177,20 @@ struct Tile {
                                            (((4 * s + h) ^ (l & 7)) << 4));
     } else if constexpr (sizeof(T) == 2) {
       Vec v;
+      const char* p = lds + line_at(8 * h + (l >> 2)) + (l & 3) * 8;
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
-        const int k = 32 * s + 8 * h + 4 * q + (l >> 2);
-        const auto c = read_column<T>(lds + k * W * 2 + ((base / 16 ^ twist(k)) * 32) + (l & 3) * 8);
+        const auto c = read_column<T>(p + base * 2 + line_at(32 * s + 4 * q));
 #pragma unroll
         for (int j = 0; j < 4; ++j) v[4 * q + j] = c[j];
       }
       return v;
     } else {
       Vec v;
+      const char* p = lds + line_at(4 * h) + l * 4;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int k = 16 * s + 4 * h + j;
-        v[j] = *reinterpret_cast<const T*>(lds + k * W * 4 + ((base / 16 ^ twist(k)) * 64) + l * 4);
-      }
+      for (int j = 0; j < 4; ++j)
+        v[j] = *reinterpret_cast<const T*>(p + base * 4 + line_at(16 * s + j));
       return v;
     }
   }
@@ -194,16 +231,17 @@ __device__ __forceinline__ void stage(char* lds, const int* at, const Source& s)
   const char* const up = reinterpret_cast<const char*>(
       uint64_t(uint32_t(__builtin_amdgcn_readfirstlane(int(p >> 32)))) << 32 |
       uint32_t(__builtin_amdgcn_readfirstlane(int(p))));
-  lds += __builtin_amdgcn_readfirstlane(int(threadIdx.x) / kWave) * 1024;
+  const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) / kWave);
   if (s.ks >= TI::kSteps) {
 #pragma unroll
-    for (int i = FROM; i < FROM + COUNT; ++i) send(up, at[i], lds + i * TI::kThreads * 16);
+    for (int i = FROM; i < FROM + COUNT; ++i) send(up, at[i], lds + TI::place(i, wave));
   } else {
 #pragma unroll
     for (int i = FROM; i < FROM + COUNT; ++i) {
       int line, along;
       TI::source(i, line, along);
-      send(up, (TI::kTrans ? line : along) < s.ks ? at[i] : kOutside, lds + i * TI::kThreads * 16);
+      send(up, (TI::kTrans ? line : along) < s.ks ? at[i] : kOutside,
+           lds + TI::place(i, wave));
     }
   }
 }
@@ -270,7 +308,7 @@ __device__ __forceinline__ void leave(const Product& g, int64_t row, int64_t col
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       float f, df;
-      activation(g.act, a[r], f, df);
+      activation<sizeof(T) == 2>(g.act, a[r], f, df);
       if constexpr (EPI == EPI_GATE) {
         u[r] = f * b[r];
       } else {
@@ -297,8 +335,8 @@ __global__ __launch_bounds__(kWave* B* B / WM / WN, 2) void k_ffn_product(Produc
   constexpr bool kGate = EPI != EPI_STORE;
   constexpr int kThreads = kWave * (B / WM) * (B / WN);
   constexpr int NI = WM / 16, NJ = WN / 16, kCols = kGate ? B / 2 : B;
-  using TA = Tile<T, B, AT, kThreads>;
-  using TB = Tile<T, B, BT, kThreads>;
+  using TA = Tile<T, B, AT, kThreads, DIRECT>;
+  using TB = Tile<T, B, BT, kThreads, DIRECT>;
   typedef typename Unit<T>::Vec Vec;
   extern __shared__ __align__(1024) char smem[];
   char* const lds0 = smem;
@@ -370,10 +408,10 @@ __global__ __launch_bounds__(kWave* B* B / WM / WN, 2) void k_ffn_product(Produc
     if constexpr (!DIRECT) {
 #pragma unroll
       for (int i = 0; i < TA::kLoads; ++i)
-        *reinterpret_cast<Vec*>(lds + (i * kThreads + t) * 16) = ra[i];
+        *reinterpret_cast<Vec*>(lds + TA::place(i)) = ra[i];
 #pragma unroll
       for (int i = 0; i < TB::kLoads; ++i)
-        *reinterpret_cast<Vec*>(lds + TA::kBytes + (i * kThreads + t) * 16) = rb[i];
+        *reinterpret_cast<Vec*>(lds + TA::kBytes + TB::place(i)) = rb[i];
     }
   };
   auto arrive = [&] {
@@ -616,7 +654,9 @@ bool whole_units(const void* p, int64_t ld, int64_t along, int es) {
 
 template <typename T, int B, int WM, int WN, bool AT, bool BT, int EPI, bool DIRECT>
 sla_status run_product(Product& g, hipStream_t stream) {
-  constexpr int lds = 2 * 2 * B * kStepBytes;
+  constexpr int kThreads = kWave * (B / WM) * (B / WN);
+  constexpr int lds = 2 * (Tile<T, B, AT, kThreads, DIRECT>::kBytes +
+                           Tile<T, B, BT, kThreads, DIRECT>::kBytes);
   const int64_t gx = div_up(g.N, EPI == EPI_STORE ? B : B / 2), gy = div_up(g.M, B);
   SLA_NET_REQUIRE(gx * gy * g.outputs * g.splits < (int64_t(1) << 31),
                   "gated_ffn: a matrix is too large");
@@ -625,7 +665,7 @@ sla_status run_product(Product& g, hipStream_t stream) {
   if (lds > 65536)
     SLA_TRY_HIP(hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
                                     hipFuncAttributeMaxDynamicSharedMemorySize, lds));
-  kernel<<<int(gx * gy) * g.outputs * g.splits, kWave * (B / WM) * (B / WN), lds, stream>>>(g);
+  kernel<<<int(gx * gy) * g.outputs * g.splits, kThreads, lds, stream>>>(g);
   LAUNCH_CHECK();
   return SLA_OK;
 }
