@@ -21,7 +21,14 @@ namespace net {
 namespace {
 
 constexpr int kFfnBlock = 256;
-constexpr int kStepBytes = 128;   // bytes of k a step covers: 64 16-bit values or 32 fp32
+// Bytes of k a step covers (64 bytes: 32 16-bit values or 16 fp32), and the
+// steps in LDS at a time.  Direct loads need the distance: with two steps of
+// 128 bytes (as many bytes in all) every step waited for memory, dx and dW of
+// 16384 x 1024 x 4096 took 316 and 330 us.
+template <bool DIRECT>
+struct Ring {
+  static constexpr int kStep = DIRECT ? 64 : 128, kDepth = DIRECT ? 4 : 2;
+};
 
 enum { EPI_GATE, EPI_GATE_GRAD, EPI_STORE };
 
@@ -30,16 +37,16 @@ enum { EPI_GATE, EPI_GATE_GRAD, EPI_STORE };
 // Stegun 7.1.26 (off by at most 1.5e-7), whose errors lie a thousand times
 // below a 16-bit half step; the library's expf, erff and divide took 7 us of
 // a 256 x 256 tile's 41.
-template <bool FAST>
-__device__ __forceinline__ void activation(int act, float a, float& f, float& df) {
+template <int ACT, bool FAST>
+__device__ __forceinline__ void activation(float a, float& f, float& df) {
   constexpr float kLog2e = 1.4426950408889634f;
-  if (act == SLA_ACT_SILU) {
+  if constexpr (ACT == SLA_ACT_SILU) {
     float s;
     if constexpr (FAST) s = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-kLog2e * a));
     else s = 1.f / (1.f + expf(-a));
     f = a * s;
     df = s * (1.f + a * (1.f - s));
-  } else if (act == SLA_ACT_GELU) {
+  } else if constexpr (ACT == SLA_ACT_GELU) {
     float c, e;   // the normal distribution's integral, exp(-a^2 / 2)
     if constexpr (FAST) {
       e = __builtin_amdgcn_exp2f(-0.5f * kLog2e * a * a);
@@ -118,20 +125,20 @@ __device__ __forceinline__ typename VecOf<T, 4>::type read_column(const char* p)
   return v;
 }
 
-// A step's piece of an operand in LDS: W rows by kStepBytes of k, in 16-byte
+// A step's piece of an operand in LDS: W rows by STEP bytes of k, in 16-byte
 // slots.  TRANS: lines of W rows, a line for each k; else lines of k, a line
 // for each row.  So that a wave's fragment read touches every bank evenly the
 // slots of a row's line are exchanged by the row (the offset of a read then
 // depends on the lane alone), and the lines of k are moved apart: a read of 16
-// lines of 32 bytes (16-bit: k = 8 h + r and 4 more) or 4 of 64 (fp32: k = 4 h)
+// lines of 32 bytes (16-bit: k = 8 h + r, or 4 more) or 4 of 64 (fp32: k = 4 h)
 // finds them at different banks.  Direct loads (PAIR) write 1024 bytes in one
-// piece: there the lines k and k + 32, never read together, are neighbours.
-template <typename T, int W, bool TRANS, int THREADS, bool PAIR>
+// piece: there the lines k and k + 4, never read together, are neighbours.
+template <typename T, int W, bool TRANS, int THREADS, int STEP, bool PAIR>
 struct Tile {
   static constexpr int kN = Unit<T>::kN;
-  static constexpr int kLineSlots = TRANS ? W / kN : kStepBytes / 16;
-  static constexpr int kLoads = W * kStepBytes / 16 / THREADS;   // slots a thread fills
-  static constexpr int kSteps = kStepBytes / int(sizeof(T));
+  static constexpr int kLineSlots = TRANS ? W / kN : STEP / 16;
+  static constexpr int kLoads = W * STEP / 16 / THREADS;   // slots a thread fills
+  static constexpr int kSteps = STEP / int(sizeof(T));
   static constexpr int kThreads = THREADS;
   static constexpr bool kTrans = TRANS;
   typedef T Element;
@@ -140,11 +147,15 @@ struct Tile {
 
   static constexpr __device__ int line_at(int k) {
     if (sizeof(T) == 4) return k * W * 4 + 64 * (k >> 2);
-    if (PAIR) return k % 32 * (W * 4 + 32) + 128 * (k % 32 >> 3) + k / 32 * (W * 2);
+    if (PAIR) return ((k >> 3) * 4 + (k & 3)) * (W * 4 + 32) + (k >> 2 & 1) * (W * 2);
     return k * (W * 2 + 32) + 128 * (k >> 3);
   }
   static constexpr int kBytes =
-      TRANS ? (line_at(kSteps - 1) + W * int(sizeof(T)) + 127) / 128 * 128 : W * kStepBytes;
+      TRANS ? (line_at(kSteps - 1) + W * int(sizeof(T)) + 127) / 128 * 128 : W * STEP;
+  // the slot of a row's line that holds unit u of k
+  static __device__ __forceinline__ int slot_of(int row, int u) {
+    return STEP == 128 ? u ^ (row & 7) : u ^ (row >> 1 & 3);
+  }
 
   // what slot i (of this thread's) holds: line and the first element along it
   static __device__ __forceinline__ void source(int i, int& line, int& along) {
@@ -152,10 +163,10 @@ struct Tile {
     line = s / kLineSlots;
     const int u = s % kLineSlots;
     if constexpr (TRANS) {
-      if (PAIR) line = line / 2 + line % 2 * 32;
+      if (PAIR) line = line / 8 * 8 + line % 2 * 4 + line / 2 % 4;
       along = u * kN;
     } else {
-      along = (u ^ (line & 7)) * kN;
+      along = slot_of(line, u) * kN;
     }
   }
   // where the slot lies; for direct loads the place of the wave's first one
@@ -166,15 +177,13 @@ struct Tile {
   }
   static __device__ __forceinline__ int place(int i, int wave) {
     const int n = i * (THREADS / kWave) + wave;
-    if constexpr (!TRANS) return n * 1024;
-    else return line_at(n);
+    return TRANS ? n * (W * 4 + 32) : n * 1024;
   }
-  // rows base + l (base a multiple of 16), sub-step s (0, 1) of the step
+  // rows base + l (base a multiple of 16), sub-step s (of 64 bytes) of the step
   static __device__ __forceinline__ Vec read(const char* lds, int base, int s) {
     const int l = threadIdx.x % 16, h = threadIdx.x % kWave / 16;
     if constexpr (!TRANS) {
-      return *reinterpret_cast<const Vec*>(lds + (base + l) * kStepBytes +
-                                           (((4 * s + h) ^ (l & 7)) << 4));
+      return *reinterpret_cast<const Vec*>(lds + (base + l) * STEP + slot_of(l, 4 * s + h) * 16);
     } else if constexpr (sizeof(T) == 2) {
       Vec v;
       const char* p = lds + line_at(8 * h + (l >> 2)) + (l & 3) * 8;
@@ -221,29 +230,40 @@ __device__ __forceinline__ void stage_offsets(int* at, const Source& s) {
   }
 }
 // 16 bytes a lane from p + at to lds + 16 lane (p and lds: one for the wave).
+// In assembly, so that the compiler does not take every LDS read behind it for
+// one that has to wait for it; the kernel waits by count (arrive).
 __device__ __forceinline__ void send(const char* p, int at, char* lds) {
-  const auto rsrc = __builtin_amdgcn_make_buffer_rsrc((void*)p, 0, 0x7fffffff, 0x00020000);
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (LdsPtr)lds, 16, at, 0, 0, 0);
+#if defined(__HIP_DEVICE_COMPILE__)
+  typedef int Words __attribute__((ext_vector_type(4)));
+  const uint64_t q = reinterpret_cast<uint64_t>(p);
+  const Words rsrc = {int(q), int(q >> 32) & 0xffff, 0x7fffffff, 0x00020000};
+  const int m0 = int(reinterpret_cast<uintptr_t>((LdsPtr)lds));
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+               :: "s"(m0), "v"(at), "s"(rsrc) : "memory");
+#endif
 }
-template <typename TI, int FROM, int COUNT>
-__device__ __forceinline__ void stage(char* lds, const int* at, const Source& s) {
-  const uint64_t p = reinterpret_cast<uint64_t>(s.p);
-  const char* const up = reinterpret_cast<const char*>(
+// Waits until at most N direct loads are under way and the wave's LDS reads
+// are done, then for the other waves.
+template <int N>
+__device__ __forceinline__ void landed() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" :: "n"(N) : "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+// The wave's first element of a step, in scalar registers.
+__device__ __forceinline__ const char* uniform(const char* q) {
+  const uint64_t p = reinterpret_cast<uint64_t>(q);
+  return reinterpret_cast<const char*>(
       uint64_t(uint32_t(__builtin_amdgcn_readfirstlane(int(p >> 32)))) << 32 |
       uint32_t(__builtin_amdgcn_readfirstlane(int(p))));
+}
+// Load i of a step whose first element is p and that has `ks` k (none: zeros).
+template <typename TI>
+__device__ __forceinline__ void stage(char* lds, const char* p, int at, int i, int ks) {
+  int line, along;
+  TI::source(i, line, along);
   const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) / kWave);
-  if (s.ks >= TI::kSteps) {
-#pragma unroll
-    for (int i = FROM; i < FROM + COUNT; ++i) send(up, at[i], lds + TI::place(i, wave));
-  } else {
-#pragma unroll
-    for (int i = FROM; i < FROM + COUNT; ++i) {
-      int line, along;
-      TI::source(i, line, along);
-      send(up, (TI::kTrans ? line : along) < s.ks ? at[i] : kOutside,
-           lds + TI::place(i, wave));
-    }
-  }
+  send(p, (TI::kTrans ? line : along) < ks ? at : kOutside, lds + TI::place(i, wave));
 }
 
 // ... and by way of registers, for any shape and alignment.
@@ -293,22 +313,31 @@ __device__ __forceinline__ Where find_tile(const Product& g) {
   return w;
 }
 
-template <typename T, int EPI>
-__device__ __forceinline__ void leave(const Product& g, int64_t row, int64_t col, int z,
-                                      const f32x4& a, const f32x4& b) {
-  const int64_t have = g.N - col;
+// f(ACT) with the product's activation as a constant.
+template <int EPI, typename F>
+__device__ __forceinline__ void with_activation(const Product& g, F&& f) {
+  if (EPI == EPI_STORE || g.act == SLA_ACT_SILU) f(std::integral_constant<int, SLA_ACT_SILU>());
+  else if (g.act == SLA_ACT_GELU) f(std::integral_constant<int, SLA_ACT_GELU>());
+  else f(std::integral_constant<int, SLA_ACT_RELU>());
+}
+
+// Four columns of a row leave: at element `at` of C (`dat` of dh), the first
+// `have` of them exist.
+template <typename T, int EPI, int ACT>
+__device__ __forceinline__ void leave(const Product& g, int64_t at, int64_t dat, int64_t have,
+                                      int z, const f32x4& a, const f32x4& b) {
   float u[4], v[4];
   if constexpr (EPI == EPI_STORE) {
 #pragma unroll
     for (int r = 0; r < 4; ++r) u[r] = a[r];
-    store_f32<4>((T*)g.C[z] + row * g.ldc + col, have, u);
+    store_f32<4>((T*)(z ? g.C[1] : g.C[0]) + at, have, u);
   } else {
     float d[4];
-    if constexpr (EPI == EPI_GATE_GRAD) load_f32<4>((const T*)g.dh + row * g.lddh + col, have, d);
+    if constexpr (EPI == EPI_GATE_GRAD) load_f32<4>((const T*)g.dh + dat, have, d);
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       float f, df;
-      activation<sizeof(T) == 2>(g.act, a[r], f, df);
+      activation<ACT, sizeof(T) == 2>(a[r], f, df);
       if constexpr (EPI == EPI_GATE) {
         u[r] = f * b[r];
       } else {
@@ -316,8 +345,8 @@ __device__ __forceinline__ void leave(const Product& g, int64_t row, int64_t col
         v[r] = d[r] * f;
       }
     }
-    store_f32<4>((T*)g.C[0] + row * g.ldc + col, have, u);
-    if constexpr (EPI == EPI_GATE_GRAD) store_f32<4>((T*)g.C[1] + row * g.ldc + col, have, v);
+    store_f32<4>((T*)g.C[0] + at, have, u);
+    if constexpr (EPI == EPI_GATE_GRAD) store_f32<4>((T*)g.C[1] + at, have, v);
   }
 }
 
@@ -335,12 +364,13 @@ __global__ __launch_bounds__(kWave* B* B / WM / WN, 2) void k_ffn_product(Produc
   constexpr bool kGate = EPI != EPI_STORE;
   constexpr int kThreads = kWave * (B / WM) * (B / WN);
   constexpr int NI = WM / 16, NJ = WN / 16, kCols = kGate ? B / 2 : B;
-  using TA = Tile<T, B, AT, kThreads, DIRECT>;
-  using TB = Tile<T, B, BT, kThreads, DIRECT>;
+  constexpr int kStep = Ring<DIRECT>::kStep, kDepth = Ring<DIRECT>::kDepth;
+  constexpr int kRows = kStep / 64 * NI;   // rows of products in a step
+  using TA = Tile<T, B, AT, kThreads, kStep, DIRECT>;
+  using TB = Tile<T, B, BT, kThreads, kStep, DIRECT>;
   typedef typename Unit<T>::Vec Vec;
   extern __shared__ __align__(1024) char smem[];
-  char* const lds0 = smem;
-  char* const lds1 = smem + TA::kBytes + TB::kBytes;
+  auto place = [&](int n) { return smem + n % kDepth * (TA::kBytes + TB::kBytes); };
   const int t = threadIdx.x, l = t % 16, h = t % kWave / 16;
   const int w = __builtin_amdgcn_readfirstlane(t / kWave), wm = w / (B / WN), wn = w % (B / WN);
   const Where at = find_tile(g);
@@ -384,24 +414,38 @@ __global__ __launch_bounds__(kWave* B* B / WM / WN, 2) void k_ffn_product(Produc
     }
   }
   Vec ra[DIRECT ? 1 : TA::kLoads], rb[DIRECT ? 1 : TB::kLoads];
-  auto begin = [&](char* lds, int it) {   // DIRECT: sends the step's tiles; else loads them
-    if (it >= to) return;
+  // DIRECT: the loads of a step, one at a time (the wave's issue would wait
+  // for a burst of them); behind the last step zeros come in their place
+  constexpr int kSends = TA::kLoads + TB::kLoads;
+  const char *pa = nullptr, *pb = nullptr, *pu = nullptr;
+  int ks = 0;
+  auto aim = [&](int it) {
     if constexpr (DIRECT) {
-      stage<TA, 0, TA::kLoads>(lds, ta, source_a(it));
-      if constexpr (kGate) {
-        stage<TB, 0, HB>(lds + TA::kBytes, tb, source_b(it, 0));
-        stage<TB, HB, HB>(lds + TA::kBytes, tb, source_b(it, 1));
-      } else {
-        stage<TB, 0, TB::kLoads>(lds + TA::kBytes, tb, source_b(it, 0));
-      }
+      const bool live = it < to;
+      it = live ? it : from;
+      const Source a = source_a(it);
+      pa = uniform(a.p);
+      pb = uniform(source_b(it, 0).p);
+      if (kGate) pu = uniform(source_b(it, 1).p);
+      ks = live ? int(a.ks < TA::kSteps ? a.ks : TA::kSteps) : 0;
+    }
+  };
+  auto send_one = [&](char* lds, int n) {
+    if (n < TA::kLoads) {
+      stage<TA>(lds, pa, ta[DIRECT ? n : 0], n, ks);
     } else {
-      fetch<TA, 0, TA::kLoads>(ra, source_a(it));
-      if constexpr (kGate) {
-        fetch<TB, 0, HB>(rb, source_b(it, 0));
-        fetch<TB, HB, HB>(rb, source_b(it, 1));
-      } else {
-        fetch<TB, 0, TB::kLoads>(rb, source_b(it, 0));
-      }
+      const int i = n - TA::kLoads;
+      stage<TB>(lds + TA::kBytes, kGate && i >= HB ? pu : pb, tb[DIRECT ? i : 0], i, ks);
+    }
+  };
+  auto load = [&](int it) {   // not DIRECT: the step's tiles into registers
+    if (it >= to) return;
+    fetch<TA, 0, TA::kLoads>(ra, source_a(it));
+    if constexpr (kGate) {
+      fetch<TB, 0, HB>(rb, source_b(it, 0));
+      fetch<TB, HB, HB>(rb, source_b(it, 1));
+    } else {
+      fetch<TB, 0, TB::kLoads>(rb, source_b(it, 0));
     }
   };
   auto put = [&](char* lds) {
@@ -414,87 +458,129 @@ __global__ __launch_bounds__(kWave* B* B / WM / WN, 2) void k_ffn_product(Produc
         *reinterpret_cast<Vec*>(lds + TA::kBytes + TB::place(i)) = rb[i];
     }
   };
-  auto arrive = [&] {
-    if constexpr (DIRECT) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __syncthreads();
-  };
   Vec fa[NI], fb[2][NJ];
-  auto read_a = [&](const char* lds, int r) {   // row r of the step's 2 NI
+  auto read_a = [&](const char* lds, int r) {   // row r of a step
     fa[r % NI] = TA::read(lds, wm * WM + 16 * (r % NI), r / NI);
   };
-  auto read_b = [&](const char* lds, int s, int j) {
-    fb[s][j] = TB::read(lds + TA::kBytes, brow(j), s);
+  auto read_b = [&](const char* lds, int s, int to_s, int j) {
+    fb[to_s][j] = TB::read(lds + TA::kBytes, brow(j), s);
   };
   if (from < to) {
-    begin(lds0, from);
-    put(lds0);
-    if (from + 1 < to) {
-      begin(lds1, from + 1);
-      put(lds1);
+    if constexpr (DIRECT) {
+#pragma unroll
+      for (int d = 0; d < kDepth; ++d) {
+        aim(from + d);
+#pragma unroll
+        for (int n = 0; n < kSends; ++n) send_one(place(d), n);
+      }
+      landed<(kDepth - 1) * kSends>();
+    } else {
+      load(from);
+      put(place(0));
+      if (from + 1 < to) {
+        load(from + 1);
+        put(place(1));
+      }
+      load(from + 2);
+      __syncthreads();
     }
-    if constexpr (!DIRECT) begin(nullptr, from + 2);
-    arrive();
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) read_b(lds0, 0, j);
+    for (int j = 0; j < NJ; ++j) read_b(place(0), 0, 0, j);
 #pragma unroll
-    for (int i = 0; i < NI - 1; ++i) read_a(lds0, i);
-    // behind the last step the fragments read are not used
-    auto step = [&](char* cur, char* nxt, int it) {
+    for (int i = 0; i < NI - 1; ++i) read_a(place(0), i);
+    // Step `it`, whose tiles are at place u; behind the last step the
+    // fragments read are not used.
+    auto step = [&](auto u, int it) {
+      char* const cur = place(u.value);
+      char* const nxt = place(u.value + 1);
+      constexpr int kFlip = kRows == NI ? u.value % 2 : 0;   // which fb the step begins with
+      constexpr int kTurn = kRows - NI + 1;   // from this row on: the next tile's fragments
 #pragma unroll
-      for (int r = 0; r < 2 * NI; ++r) {
-        constexpr int kTurn = NI + 1;   // from this row on: the next tile's fragments
+      for (int r = 0; r < kRows; ++r) {
         if (r == kTurn) {
-          arrive();
+          // the next step's tiles have come (the loads of those behind it may
+          // be under way) and every wave has read this step's
           if constexpr (DIRECT) {
-            begin(cur, it + 2);
-          } else if (it + 2 < to) {
-            put(cur);
-            begin(nullptr, it + 3);
+            landed<(kDepth - 2) * kSends>();
+            aim(it + kDepth);
+          } else {
+            __syncthreads();
+            if (it + 2 < to) {
+              put(cur);
+              load(it + 3);
+            }
           }
         }
         if (r < kTurn) read_a(cur, r + NI - 1);
-        else read_a(nxt, r + NI - 1 - 2 * NI);
-        if (r < NJ && r < NI) {
-          read_b(cur, 1, r);
-          if (r == NI - 1)
-            for (int j = NI; j < NJ; ++j) read_b(cur, 1, j);
+        else read_a(nxt, r + NI - 1 - kRows);
+        if (kRows > NI && r < NI) {
+#pragma unroll
+          for (int j = 0; j < NJ; ++j)
+            if ((j < NI ? j : NI - 1) == r) read_b(cur, 1, 1, j);
         }
         if (r >= kTurn) {
           constexpr int kLeft = NI - 1;
 #pragma unroll
           for (int j = 0; j < NJ; ++j)
-            if (j % kLeft == r - kTurn) read_b(nxt, 0, j);
+            if (j % kLeft == r - kTurn) read_b(nxt, 0, kRows == NI ? kFlip ^ 1 : 0, j);
+          if constexpr (DIRECT) {
+            constexpr int kEach = (kSends + kLeft - 1) / kLeft;
+#pragma unroll
+            for (int n = 0; n < kSends; ++n)
+              if (n / kEach == r - kTurn) send_one(cur, n);
+          }
         }
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) mma16(acc[r % NI][j], fa[r % NI], fb[r / NI][j]);
+        for (int j = 0; j < NJ; ++j)
+          mma16(acc[r % NI][j], fa[r % NI], fb[kRows == NI ? kFlip : r / NI][j]);
         __builtin_amdgcn_sched_barrier(0);
       }
     };
-    for (int it = from; it < to; it += 2) {
-      step(lds0, lds1, it);
-      if (it + 1 < to) step(lds1, lds0, it + 1);
-    }
-  }
-
-#pragma unroll
-  for (int i = 0; i < NI; ++i) {
-    const int64_t row = m0 + wm * WM + 16 * i + l;
-    if (row >= g.M) continue;
-#pragma unroll
-    for (int j = 0; j < (kGate ? NJ / 2 : NJ); ++j) {
-      const int64_t col = n0 + brow(j) + 4 * h;
-      if (col >= g.N) continue;
-      if (!kGate && g.splits > 1) {
-        float u[4];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) u[r] = acc[i][j][r];
-        store_f32<4>(g.part + ((int64_t(at.z) * g.splits + at.split) * g.M + row) * g.N + col,
-                     g.N - col, u);
-      } else {
-        leave<T, EPI>(g, row, col, at.z, acc[i][j], acc[i][kGate ? j + NJ / 2 : j]);
+    for (int it = from; it < to; it += kDepth) {
+      step(std::integral_constant<int, 0>(), it);
+      if (it + 1 < to) step(std::integral_constant<int, 1>(), it + 1);
+      if constexpr (kDepth == 4) {
+        if (it + 2 < to) step(std::integral_constant<int, 2>(), it + 2);
+        if (it + 3 < to) step(std::integral_constant<int, 3>(), it + 3);
       }
     }
+    // the last loads must not come in after the workgroup has given its LDS back
+    if constexpr (DIRECT) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   }
+
+  // the lane's first quad; the others lie 16 rows or 16 columns further
+  const int64_t row0 = m0 + wm * WM + l, col0 = n0 + 4 * h;
+  auto finish = [&](auto act, auto whole) {
+    int64_t at_c = row0 * g.ldc + col0, at_d = row0 * g.lddh + col0;
+    float* part = g.splits > 1 ? g.part + (int64_t(at.z) * g.splits + at.split) * g.M * g.N +
+                                     row0 * g.N + col0 : nullptr;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      if (whole.value || row0 + 16 * i < g.M) {
+#pragma unroll
+        for (int j = 0; j < (kGate ? NJ / 2 : NJ); ++j) {
+          const int64_t have = whole.value ? 4 : g.N - col0 - brow(j);
+          if (!whole.value && have <= 0) continue;
+          if (!kGate && part) {
+            float u[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) u[r] = acc[i][j][r];
+            store_f32<4>(part + brow(j), have, u);
+          } else {
+            leave<T, EPI, act.value>(g, at_c + brow(j), at_d + brow(j), have, at.z, acc[i][j],
+                                     acc[i][kGate ? j + NJ / 2 : j]);
+          }
+        }
+      }
+      at_c += 16 * g.ldc;
+      if (EPI == EPI_GATE_GRAD) at_d += 16 * g.lddh;
+      if (!kGate && part) part += 16 * g.N;
+    }
+  };
+  with_activation<EPI>(g, [&](auto act) {
+    if (m0 + B <= g.M && n0 + kCols <= g.N) finish(act, std::true_type());
+    else finish(act, std::false_type());
+  });
 }
 
 // The sums of a split product, in the order of the splits, rounded once.
@@ -597,7 +683,9 @@ __global__ __launch_bounds__(kFfnBlock) void k_ffn_few(Product g) {
     for (int b = 0; b < 2; ++b)
       s[b] = (sums[0][i][b][t % kWave] + sums[1][i][b][t % kWave]) +
              (sums[2][i][b][t % kWave] + sums[3][i][b][t % kWave]);
-    leave<T, EPI>(g, row, col, 0, s[0], s[1]);
+    with_activation<EPI>(g, [&](auto act) {
+      leave<T, EPI, act.value>(g, row * g.ldc + col, row * g.lddh + col, g.N - col, 0, s[0], s[1]);
+    });
   }
 }
 
@@ -613,12 +701,12 @@ ProductPlan plan_product(int64_t M, int64_t N, int64_t K, int parts, int outputs
                          int es, bool direct) {
   struct Kind {
     int tile, slots;       // side; workgroups a CU holds
-    double step, start;    // us of a step with every slot taken; us before and after the steps
+    double step, start;    // us of 128 bytes of k with every slot taken; us before and after the steps
   };
   static const Kind kind16[] = {{256, 1, 1.10, 6.0}, {128, 2, 0.75, 4.0}, {64, 4, 0.55, 3.0}};
   static const Kind kind32[] = {{256, 1, 0, 0}, {128, 2, 3.6, 5.0}, {64, 4, 2.0, 4.0}};
   const Kind* kinds = es == 4 ? kind32 : kind16;
-  const int64_t steps = div_up(K, kStepBytes / es) * parts, cus = device_cus();
+  const int64_t steps = div_up(K, 128 / es) * parts, cus = device_cus();
   ProductPlan best{64, 1};
   double least = 1e30;
   for (int i = es == 4 || !direct ? 1 : 0; i < 3; ++i) {
@@ -655,8 +743,9 @@ bool whole_units(const void* p, int64_t ld, int64_t along, int es) {
 template <typename T, int B, int WM, int WN, bool AT, bool BT, int EPI, bool DIRECT>
 sla_status run_product(Product& g, hipStream_t stream) {
   constexpr int kThreads = kWave * (B / WM) * (B / WN);
-  constexpr int lds = 2 * (Tile<T, B, AT, kThreads, DIRECT>::kBytes +
-                           Tile<T, B, BT, kThreads, DIRECT>::kBytes);
+  constexpr int kStep = Ring<DIRECT>::kStep;
+  constexpr int lds = Ring<DIRECT>::kDepth * (Tile<T, B, AT, kThreads, kStep, DIRECT>::kBytes +
+                                              Tile<T, B, BT, kThreads, kStep, DIRECT>::kBytes);
   const int64_t gx = div_up(g.N, EPI == EPI_STORE ? B : B / 2), gy = div_up(g.M, B);
   SLA_NET_REQUIRE(gx * gy * g.outputs * g.splits < (int64_t(1) << 31),
                   "gated_ffn: a matrix is too large");
