@@ -321,19 +321,17 @@ __device__ __forceinline__ void with_activation(const Product& g, F&& f) {
   else f(std::integral_constant<int, SLA_ACT_RELU>());
 }
 
-// Four columns of a row leave: at element `at` of C (`dat` of dh), the first
+// Four columns of a row leave (d: dh there) at element `at` of C; the first
 // `have` of them exist.
 template <typename T, int EPI, int ACT>
-__device__ __forceinline__ void leave(const Product& g, int64_t at, int64_t dat, int64_t have,
-                                      int z, const f32x4& a, const f32x4& b) {
+__device__ __forceinline__ void leave(const Product& g, int64_t at, const float (&d)[4],
+                                      int64_t have, int z, const f32x4& a, const f32x4& b) {
   float u[4], v[4];
   if constexpr (EPI == EPI_STORE) {
 #pragma unroll
     for (int r = 0; r < 4; ++r) u[r] = a[r];
     store_f32<4>((T*)(z ? g.C[1] : g.C[0]) + at, have, u);
   } else {
-    float d[4];
-    if constexpr (EPI == EPI_GATE_GRAD) load_f32<4>((const T*)g.dh + dat, have, d);
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       float f, df;
@@ -353,12 +351,12 @@ __device__ __forceinline__ void leave(const Product& g, int64_t at, int64_t dat,
 // Tiles of B x B in waves of WM x WN.  EPI_GATE*: the tile's columns are B / 2
 // of a and the same B / 2 of b, half of each wave's columns are of either.
 //
-// Two steps' tiles are in LDS.  A wave multiplies a row of 16 x WN at a time
-// and reads the fragments a sub-step ahead of their use, one between the
-// products of each row, so that the matrix cores and the LDS work side by
-// side.  The step's only barrier comes when the last fragment of its tile has
-// been read, NI - 1 rows before its last product: the tile's place is then
-// filled with the step after the next, which has a whole step to arrive.
+// A few steps' tiles are in LDS (Ring).  A wave multiplies a row of 16 x WN at
+// a time and reads the fragments some rows ahead of their use, between the
+// products of the rows, so that the matrix cores and the LDS work side by
+// side.  The step's only barrier comes behind the read of its tiles' last
+// fragment, in the middle of its products: from there on the next tiles'
+// fragments are read and this one's place is filled with a later step's.
 template <typename T, int B, int WM, int WN, bool AT, bool BT, int EPI, bool DIRECT>
 __global__ __launch_bounds__(kWave* B* B / WM / WN, 2) void k_ffn_product(Product g) {
   constexpr bool kGate = EPI != EPI_STORE;
@@ -551,29 +549,49 @@ __global__ __launch_bounds__(kWave* B* B / WM / WN, 2) void k_ffn_product(Produc
   // the lane's first quad; the others lie 16 rows or 16 columns further
   const int64_t row0 = m0 + wm * WM + l, col0 = n0 + 4 * h;
   auto finish = [&](auto act, auto whole) {
-    int64_t at_c = row0 * g.ldc + col0, at_d = row0 * g.lddh + col0;
+    int64_t at_c = row0 * g.ldc + col0;
     float* part = g.splits > 1 ? g.part + (int64_t(at.z) * g.splits + at.split) * g.M * g.N +
                                      row0 * g.N + col0 : nullptr;
+    constexpr int kQuads = kGate ? NJ / 2 : NJ;
+    auto has = [&](int j) { return whole.value ? int64_t(4) : g.N - col0 - brow(j); };
+    // dh of all rows is asked for before the first row leaves
+    typename VecOf<T, 4>::type dh[EPI == EPI_GATE_GRAD ? NI : 1][kQuads];
+    if constexpr (EPI == EPI_GATE_GRAD) {
+      const T* p = (const T*)g.dh + row0 * g.lddh + col0;
+#pragma unroll
+      for (int i = 0; i < NI; ++i, p += 16 * g.lddh)
+#pragma unroll
+        for (int j = 0; j < kQuads; ++j) {
+          const int64_t have = whole.value || row0 + 16 * i < g.M ? has(j) : 0;
+          if (have >= 4) {
+            dh[i][j] = *reinterpret_cast<const typename VecOf<T, 4>::type*>(p + brow(j));
+          } else {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) dh[i][j][r] = r < have ? p[brow(j) + r] : T(0.f);
+          }
+        }
+    }
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
       if (whole.value || row0 + 16 * i < g.M) {
 #pragma unroll
-        for (int j = 0; j < (kGate ? NJ / 2 : NJ); ++j) {
-          const int64_t have = whole.value ? 4 : g.N - col0 - brow(j);
+        for (int j = 0; j < kQuads; ++j) {
+          const int64_t have = has(j);
           if (!whole.value && have <= 0) continue;
+          float u[4];
           if (!kGate && part) {
-            float u[4];
 #pragma unroll
             for (int r = 0; r < 4; ++r) u[r] = acc[i][j][r];
             store_f32<4>(part + brow(j), have, u);
           } else {
-            leave<T, EPI, act.value>(g, at_c + brow(j), at_d + brow(j), have, at.z, acc[i][j],
+#pragma unroll
+            for (int r = 0; r < 4; ++r) u[r] = EPI == EPI_GATE_GRAD ? float(dh[i][j][r]) : 0.f;
+            leave<T, EPI, act.value>(g, at_c + brow(j), u, have, at.z, acc[i][j],
                                      acc[i][kGate ? j + NJ / 2 : j]);
           }
         }
       }
       at_c += 16 * g.ldc;
-      if (EPI == EPI_GATE_GRAD) at_d += 16 * g.lddh;
       if (!kGate && part) part += 16 * g.N;
     }
   };
@@ -683,8 +701,11 @@ __global__ __launch_bounds__(kFfnBlock) void k_ffn_few(Product g) {
     for (int b = 0; b < 2; ++b)
       s[b] = (sums[0][i][b][t % kWave] + sums[1][i][b][t % kWave]) +
              (sums[2][i][b][t % kWave] + sums[3][i][b][t % kWave]);
+    float d[4] = {0.f, 0.f, 0.f, 0.f};
+    if constexpr (EPI == EPI_GATE_GRAD)
+      load_f32<4>((const T*)g.dh + row * g.lddh + col, g.N - col, d);
     with_activation<EPI>(g, [&](auto act) {
-      leave<T, EPI, act.value>(g, row * g.ldc + col, row * g.lddh + col, g.N - col, 0, s[0], s[1]);
+      leave<T, EPI, act.value>(g, row * g.ldc + col, d, g.N - col, 0, s[0], s[1]);
     });
   }
 }
