@@ -36,10 +36,27 @@
 // k_delta_adjoint) walks a sequence's chunks, a workgroup for every 32
 // columns of the state, which never mix.
 //
-// Everything is held and multiplied in fp32 whatever the tokens' type: the
-// state, its gradient, dg and dbeta leave in fp32, and a matrix product of
-// rounded 16-bit factors would leave them three digits.  G is summed in
-// fp64: its differences are exponents.
+// Everything is held in fp32 whatever the tokens' type: the state, its
+// gradient, dg and dbeta leave in fp32, and a matrix product of rounded 16-bit
+// factors would leave them three digits.  The products run on the bf16 matrix
+// instructions all the same, 16 times the rate of the fp32 ones: an fp32
+// factor is cut into three bf16 parts of 8 bits each, which hold all its 24
+// (fp16 needs two, bf16 is one), and a product takes the pairs of parts whose
+// orders add up to at most 2: what is left out lies below 2^-24.  Products
+// whose results are only rounded to 16 bits (o, dq, dk) take two parts of
+// their fp32 factors (2^-16 against the half step of 2^-9 or 2^-12).  G is
+// summed in fp64: its differences are exponents.
+//
+// An operand of the 16 x 16 x 32 instruction holds, in lane (l, h) = (lane %
+// 16, lane / 16), eight k of row (column) l; which eight is free as long as
+// both operands agree.  Here they are 4 h .. 4 h + 3 and 16 more, because the
+// results of two instructions, rows 4 h .. 4 h + 3 of column l each, are then
+// an operand of the next one as they stand: a wave that holds all rows of 16
+// columns of the state walks through a chunk in its registers, without a
+// barrier between the products.  Operands stored the other way round are
+// turned by the transposed LDS read.
+#include <type_traits>
+
 #include "net.h"
 
 namespace sla {
@@ -48,9 +65,9 @@ namespace {
 
 constexpr int kChunk = 64;
 constexpr int kDeltaBlock = 256;
-constexpr int kSlice = 32;              // columns of the state per walking workgroup
+constexpr int kSlice = 32;              // columns of the state a parallel kernel takes at a time
 constexpr int kLdC = kChunk + 4;        // LDS row of 64 floats (padded against bank conflicts)
-constexpr int kLdS = kSlice + 4;        // LDS row of a slice
+constexpr int kWalk = 64;               // columns of the state per walking workgroup
 
 struct DeltaShape {
   int64_t total;      // tokens
@@ -76,8 +93,8 @@ struct DeltaKept {
   double* G;   // [64] running sums of g
   float* E;    // [64][64]
   float* P;    // [64][64]
-  float* M;    // [64][dvp]
-  float* S;    // [dk padded][dvp] the state before the chunk
+  float* M;    // [dvp][64], transposed: a lane of the walk has four tokens of a column
+  float* S;    // [dvp][dk padded] the state before the chunk, transposed
 };
 
 struct Place {
@@ -141,31 +158,234 @@ __device__ __forceinline__ void mma(f32x4& acc, const float* A, int lda, const f
   }
 }
 
-// A chunk's rows of `width` elements (zero past `len` rows and `have`
-// columns), 8 elements a load, held in registers between the load and the
-// LDS store so that the next chunk's rows travel while this one is worked on.
+// ---------------------------------------------------------------------------
+// Parts and operands
+// ---------------------------------------------------------------------------
+typedef uint32_t U2 __attribute__((ext_vector_type(2)));
+typedef uint32_t U4 __attribute__((ext_vector_type(4)));
+typedef __bf16 Frag __attribute__((ext_vector_type(8)));
+
+template <typename T>
+constexpr int kParts = sizeof(T) == 4 ? 3 : (std::is_same<T, _Float16>::value ? 2 : 1);
+// Parts of an fp32 factor whose product is rounded to T.
+template <typename T>
+constexpr int kRoundedParts = sizeof(T) == 4 ? 3 : 2;
+
+// The upper halves of two words, a's lowest.
+__device__ __forceinline__ uint32_t upper(uint32_t a, uint32_t b) {
+  return __builtin_amdgcn_perm(b, a, 0x07060302);
+}
+// The parts of n (2, 4 or 8) values, two to a word: each is the value less the
+// ones before, cut off after 8 bits; the differences are exact.
+template <int PARTS, int N>
+__device__ __forceinline__ void split(const float (&x)[N], uint32_t (&p)[PARTS][N / 2]) {
+  float r[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) r[i] = x[i];
+#pragma unroll
+  for (int k = 0; k < PARTS; ++k) {
+#pragma unroll
+    for (int i = 0; i < N; i += 2)
+      p[k][i / 2] = upper(__float_as_uint(r[i]), __float_as_uint(r[i + 1]));
+    if (k + 1 < PARTS) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) r[i] -= __uint_as_float(__float_as_uint(r[i]) & 0xffff0000u);
+    }
+  }
+}
+template <typename T>
+using Eight = typename VecOf<T, 8>::type;
+template <typename T>
+__device__ __forceinline__ void split(const Eight<T>& v, uint32_t (&p)[kParts<T>][4]) {
+  if constexpr (std::is_same<T, __bf16>::value) {
+    const U4 u = __builtin_bit_cast(U4, v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) p[0][i] = u[i];
+  } else {
+    float x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = float(v[i]);
+    split<kParts<T>, 8>(x, p);
+  }
+}
+// An operand's parts.
+template <int PARTS>
+struct Op {
+  Frag f[PARTS];
+};
+__device__ __forceinline__ Frag frag(const uint32_t (&w)[4]) {
+  const U4 u = {w[0], w[1], w[2], w[3]};
+  return __builtin_bit_cast(Frag, u);
+}
+// ... of the results of two instructions (rows 4 h + r of each are the k).
+template <int PARTS>
+__device__ __forceinline__ Op<PARTS> operand(const f32x4& a, const f32x4& b) {
+  const float x[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+  uint32_t p[PARTS][4];
+  split<PARTS, 8>(x, p);
+  Op<PARTS> o;
+#pragma unroll
+  for (int k = 0; k < PARTS; ++k) o.f[k] = frag(p[k]);
+  return o;
+}
+// ... of values that T holds exactly.
+template <typename T>
+__device__ __forceinline__ Op<kParts<T>> operand_of(const f32x4& a, const f32x4& b) {
+  return operand<kParts<T>>(a, b);
+}
+// acc += a b, the small pairs first.
+template <int NA, int NB>
+__device__ __forceinline__ void mul(f32x4& acc, const Op<NA>& a, const Op<NB>& b) {
+  constexpr int kTop = NA + NB - 2 < 2 ? NA + NB - 2 : 2;
+#pragma unroll
+  for (int s = kTop; s >= 0; --s)
+#pragma unroll
+    for (int i = 0; i < NA; ++i)
+      if (s - i >= 0 && s - i < NB)
+        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.f[i], b.f[s - i], acc, 0, 0, 0);
+}
+
+typedef __attribute__((address_space(3))) void* LdsPtr;
+typedef __bf16 Quad __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ Frag join(const Quad& a, const Quad& b) {
+  return Frag{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+}
+// Rows l of an LDS array of rows of k (p: row 0, first of the 32 k; two reads
+// of 8 bytes, free of conflicts if the rows are an odd number of those apart).
+__device__ __forceinline__ Frag row_frag(const char* p, int stride) {
+  const int l = threadIdx.x % 16, h = threadIdx.x % kWave / 16;
+  const char* q = p + l * stride + 8 * h;
+  return join(*reinterpret_cast<const Quad*>(q), *reinterpret_cast<const Quad*>(q + 32));
+}
+// Columns l of 16 lines of k (p: line 0, first of the 16 columns; free of
+// conflicts if the lines are 32 bytes apart modulo 128).
+__device__ __forceinline__ Quad turned(const char* p, int stride) {
+  const int l = threadIdx.x % 16, h = threadIdx.x % kWave / 16;
+  return __builtin_amdgcn_ds_read_tr16_b64_v4bf16(
+      (__attribute__((address_space(3))) Quad*)(p + (4 * h + (l >> 2)) * stride + (l & 3) * 8));
+}
+__device__ __forceinline__ Frag col_frag(const char* p, int stride) {
+  return join(turned(p, stride), turned(p + 16 * stride, stride));
+}
+template <int PARTS>
+__device__ __forceinline__ Op<PARTS> row_op(const char* p, int stride, int part) {
+  Op<PARTS> o;
+#pragma unroll
+  for (int k = 0; k < PARTS; ++k) o.f[k] = row_frag(p + k * part, stride);
+  return o;
+}
+template <int PARTS>
+__device__ __forceinline__ Op<PARTS> col_op(const char* p, int stride, int part) {
+  Op<PARTS> o;
+#pragma unroll
+  for (int k = 0; k < PARTS; ++k) o.f[k] = col_frag(p + k * part, stride);
+  return o;
+}
+
+// A lower triangle of 64 x 64 in 16 x 16 blocks: line i has 16 (i / 16 + 1) columns.
+__device__ __forceinline__ constexpr int tri_stride(int t) {
+  return t == 0 ? 64 : t == 1 ? 96 : 160;
+}
+__device__ __forceinline__ constexpr int tri_at(int t) {   // of line 16 t
+  return t == 0 ? 0 : t == 1 ? 1024 : t == 2 ? 2560 : 5120;
+}
+constexpr int kTri = 7680;   // bytes of a part
+// Operand with rows j = 16 tj + l and k = i = 32 kb .. (the triangle turned).
+template <int PARTS>
+__device__ __forceinline__ Op<PARTS> tri_turned(const char* p, int tj, int kb) {
+  Op<PARTS> o;
+  const Quad zero = {0, 0, 0, 0};
+#pragma unroll
+  for (int k = 0; k < PARTS; ++k) {
+    const char* q = p + k * kTri + 32 * tj;
+    const int t = 2 * kb;
+    o.f[k] = join(t >= tj ? turned(q + tri_at(t), tri_stride(t)) : zero,
+                  t + 1 >= tj ? turned(q + tri_at(t + 1), tri_stride(t + 1)) : zero);
+  }
+  return o;
+}
+// Operand with rows i = 16 ti + l and k = j = 32 kb ...
+template <int PARTS>
+__device__ __forceinline__ Op<PARTS> tri_rows(const char* p, int ti, int kb) {
+  const int l = threadIdx.x % 16, h = threadIdx.x % kWave / 16;
+  Op<PARTS> o;
+  const Quad zero = {0, 0, 0, 0};
+#pragma unroll
+  for (int k = 0; k < PARTS; ++k) {
+    const char* q = p + k * kTri + tri_at(ti) + l * tri_stride(ti) + 64 * kb + 8 * h;
+    o.f[k] = join(2 * kb <= ti ? *reinterpret_cast<const Quad*>(q) : zero,
+                  2 * kb + 1 <= ti ? *reinterpret_cast<const Quad*>(q + 32) : zero);
+  }
+  return o;
+}
+
+// A chunk's rows of WIDTH elements (zero past `len` rows and `have` columns),
+// 8 elements a load, held in registers between the load and the LDS store so
+// that the next chunk's rows travel while this one is worked on.
 template <typename T, int WIDTH>
 struct Rows {
   static constexpr int kLoads = kChunk * WIDTH / 8 / kDeltaBlock;
   static_assert(kLoads >= 1, "a load per thread");
-  float v[kLoads][8];
+  Eight<T> v[kLoads];
   __device__ __forceinline__ void fetch(const T* p, int64_t ld, int len, int have) {
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
       const int at = threadIdx.x + i * kDeltaBlock;
       const int row = at / (WIDTH / 8), col = at % (WIDTH / 8) * 8;
-      load_f32<8>(p + row * ld + col, row < len ? have - col : 0, v[i]);
+      const int n = row < len ? have - col : 0;
+      const T* q = p + row * ld + col;
+      if (n >= 8) {
+        v[i] = *reinterpret_cast<const Eight<T>*>(q);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[i][j] = j < n ? q[j] : T(0.f);
+      }
     }
   }
-  __device__ __forceinline__ void put(float* lds, int ldl) const {
+  // its parts, rows `stride` bytes apart
+  __device__ __forceinline__ void put(char* lds, int stride) const {
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
       const int at = threadIdx.x + i * kDeltaBlock;
-      float* d = lds + (at / (WIDTH / 8)) * ldl + at % (WIDTH / 8) * 8;
+      char* d = lds + (at / (WIDTH / 8)) * stride + at % (WIDTH / 8) * 16;
+      uint32_t p[kParts<T>][4];
+      split<T>(v[i], p);
 #pragma unroll
-      for (int j = 0; j < 8; j += 4)
-        *reinterpret_cast<f32x4*>(d + j) = f32x4{v[i][j], v[i][j + 1], v[i][j + 2], v[i][j + 3]};
+      for (int k = 0; k < kParts<T>; ++k) {
+        *reinterpret_cast<U2*>(d + k * kChunk * stride) = U2{p[k][0], p[k][1]};
+        *reinterpret_cast<U2*>(d + k * kChunk * stride + 8) = U2{p[k][2], p[k][3]};
+      }
     }
+  }
+};
+// A 64 x 64 lower triangle of fp32, four elements a load.
+struct Square {
+  f32x4 v[4];
+  __device__ __forceinline__ void fetch(const float* p) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      v[i] = *reinterpret_cast<const f32x4*>(p + (threadIdx.x + i * kDeltaBlock) * 4);
+  }
+  template <typename F>
+  __device__ __forceinline__ void put(F&& at, int part) const {   // at(row, col): where
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int row = (threadIdx.x + i * kDeltaBlock) / 16, col = threadIdx.x % 16 * 4;
+      const float x[4] = {v[i][0], v[i][1], v[i][2], v[i][3]};
+      uint32_t p[3][2];
+      split<3, 4>(x, p);
+      char* d = at(row, col);
+      if (d) {
+#pragma unroll
+        for (int k = 0; k < 3; ++k) *reinterpret_cast<U2*>(d + k * part) = U2{p[k][0], p[k][1]};
+      }
+    }
+  }
+  __device__ __forceinline__ void put_tri(char* lds) const {
+    put([&](int row, int col) -> char* {
+      const int t = row / 16;
+      return col / 16 <= t ? lds + tri_at(t) + row % 16 * tri_stride(t) + col * 2 : nullptr;
+    }, kTri);
   }
 };
 
@@ -239,15 +459,24 @@ __global__ __launch_bounds__(kDeltaBlock) void k_delta_gaps(const int32_t* tok, 
 //   Z = sum_{J <= K < I} A_IK T_KJ,  E_IJ = Z - E_II (B_I Z),  T_IJ = -B_I E_IJ,
 // a block column per wave, with T = I - B E the inverse so far.
 template <typename T, int DK>
+struct PrepareLds {
+  static constexpr int kStride = 2 * DK + 8;
+  static constexpr int kRow = kParts<T> * kChunk * kStride;
+  static constexpr int kSquare = kChunk * kLdC * 4;
+  static constexpr int kFirst = 2 * kRow > 2 * kSquare ? 2 * kRow : 2 * kSquare;
+  static constexpr int kBytes = kFirst + kSquare + kChunk * 12;
+};
+template <typename T, int DK>
 __global__ __launch_bounds__(kDeltaBlock) void k_delta_prepare(DeltaShape s, DeltaIn<T> in,
                                                                DeltaKept kept) {
-  constexpr int LD = DK + 4;
+  using L = PrepareLds<T, DK>;
+  constexpr int NP = kParts<T>;
   extern __shared__ __align__(16) char smem[];
-  float* kf = (float*)smem;               // [64][LD]
-  float* qf = kf + kChunk * LD;           // [64][LD]
-  float* A = qf + kChunk * LD;            // [64][kLdC]
-  float* E = kf;                          // over k and q once they are used up
-  float* Tm = kf + kChunk * kLdC;
+  char* kf = smem;                        // k's and q's parts
+  char* qf = smem + L::kRow;
+  float* A = (float*)(smem + L::kFirst);  // [64][kLdC]
+  float* E = (float*)smem;                // over k and q once they are used up
+  float* Tm = E + kChunk * kLdC;
   double* G = (double*)(A + kChunk * kLdC);
   float* beta = (float*)(G + kChunk);
   Place p;
@@ -258,8 +487,8 @@ __global__ __launch_bounds__(kDeltaBlock) void k_delta_prepare(DeltaShape s, Del
     Rows<T, DK> kr, qr;
     kr.fetch(in.k + p.tok * in.ldk + int64_t(kh) * s.dk, in.ldk, p.len, s.dk);
     qr.fetch(in.q + p.tok * in.ldq + int64_t(kh) * s.dk, in.ldq, p.len, s.dk);
-    kr.put(kf, LD);
-    qr.put(qf, LD);
+    kr.put(kf, L::kStride);
+    qr.put(qf, L::kStride);
   }
   if (t < kChunk) {
     const int64_t at = (p.tok + t) * s.hv + vh;
@@ -279,8 +508,13 @@ __global__ __launch_bounds__(kDeltaBlock) void k_delta_prepare(DeltaShape s, Del
   for (int J = 0; J < 4; ++J) {
     f32x4 kk = {0, 0, 0, 0}, qk = {0, 0, 0, 0};
     if (J <= w) {
-      mma<DK, false, false>(kk, kf + 16 * w * LD, LD, kf + 16 * J * LD, LD);
-      mma<DK, false, false>(qk, qf + 16 * w * LD, LD, kf + 16 * J * LD, LD);
+#pragma unroll
+      for (int b = 0; b < DK / 32; ++b) {
+        constexpr int part = kChunk * L::kStride;
+        const Op<NP> kj = row_op<NP>(kf + 16 * J * L::kStride + 64 * b, L::kStride, part);
+        mul(kk, row_op<NP>(kf + 16 * w * L::kStride + 64 * b, L::kStride, part), kj);
+        mul(qk, row_op<NP>(qf + 16 * w * L::kStride + 64 * b, L::kStride, part), kj);
+      }
     }
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
@@ -343,22 +577,26 @@ __global__ __launch_bounds__(kDeltaBlock) void k_delta_prepare(DeltaShape s, Del
 }
 
 // Per-token factors of a chunk, computed by its first 64 threads.
-struct Factors {
+struct alignas(16) Factors {
   float beta[kChunk];
   float in[kChunk];    // exp(G)
   float out[kChunk];   // exp(G_L - G)
   float all;           // exp(G_L)
 };
-__device__ __forceinline__ void load_factors(Factors& f, const DeltaShape& s, const double* G,
-                                             const float* beta, const Place& p, int vh) {
+__device__ __forceinline__ void set_factors(Factors& f, double g, double end, float beta) {
   const int t = threadIdx.x;
   if (t < kChunk) {
-    const double g = G[t], end = G[kChunk - 1];
-    f.beta[t] = t < p.len ? beta[(p.tok + t) * s.hv + vh] : 0.f;
+    f.beta[t] = beta;
     f.in[t] = expf(float(g));
     f.out[t] = expf(float(end - g));
     if (t == 0) f.all = expf(float(end));
   }
+}
+__device__ __forceinline__ void set_factors(Factors& f, const DeltaShape& s, const double* G,
+                                            const float* beta, const Place& p, int vh) {
+  const int t = threadIdx.x;
+  if (t < kChunk)
+    set_factors(f, G[t], G[kChunk - 1], t < p.len ? beta[(p.tok + t) * s.hv + vh] : 0.f);
 }
 
 __device__ __forceinline__ Place chunk_of(const DeltaShape& s, int seq, int64_t c) {
@@ -370,478 +608,666 @@ __device__ __forceinline__ Place chunk_of(const DeltaShape& s, int seq, int64_t 
   return p;
 }
 
-// The states' walk forward: M of every chunk and the state before it.
+// A wave's 16 columns of [dk][dv] arrays of a sequence and head, rows 16 a +
+// 4 h + r in f32x4 number a.
+template <int DK>
+__device__ __forceinline__ void load_state(f32x4 (&S)[DK / 16], const float* p, const DeltaShape& s,
+                                           int64_t head, int c0) {
+  const int l = threadIdx.x % 16, h = threadIdx.x % kWave / 16;
+#pragma unroll
+  for (int a = 0; a < DK / 16; ++a)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int row = 16 * a + 4 * h + r, col = c0 + l;
+      S[a][r] = p && row < s.dk && col < s.dv ? p[(head * s.dk + row) * s.dv + col] : 0.f;
+    }
+}
+template <int DK>
+__device__ __forceinline__ void store_state(const f32x4 (&S)[DK / 16], float* p,
+                                            const DeltaShape& s, int64_t head, int c0) {
+  const int l = threadIdx.x % 16, h = threadIdx.x % kWave / 16;
+#pragma unroll
+  for (int a = 0; a < DK / 16; ++a)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int row = 16 * a + 4 * h + r, col = c0 + l;
+      if (row < s.dk && col < s.dv) p[(head * s.dk + row) * s.dv + col] = S[a][r];
+    }
+}
+// A wave's 16 columns of a chunk's [token][dv] rows: tokens 16 i + 4 h + r.
+template <typename T>
+struct Columns {
+  T v[4][4];
+  __device__ __forceinline__ void fetch(const T* p, int64_t ld, int len, int have) {
+    const int l = threadIdx.x % 16, h = threadIdx.x % kWave / 16;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int row = 16 * i + 4 * h + r;
+        v[i][r] = row < len && l < have ? p[row * ld + l] : T(0.f);
+      }
+  }
+  __device__ __forceinline__ f32x4 tile(int i) const {
+    return f32x4{float(v[i][0]), float(v[i][1]), float(v[i][2]), float(v[i][3])};
+  }
+};
+__device__ __forceinline__ f32x4 quad(const float* p, int i) {   // [16 i + 4 h ..]
+  return *reinterpret_cast<const f32x4*>(p + 16 * i + 4 * (threadIdx.x % kWave / 16));
+}
+
+// The states' walk forward: M of every chunk and the state before it.  A
+// workgroup has 64 columns of a sequence and head, a wave 16 of them and all
+// dk rows in registers; k (as rows and turned) and E are shared in LDS.  The
+// next chunk's k, E, v and factors travel while this one is walked.  Bound by
+// the chain of one chunk: 132 matrix instructions of 16 cycles and the cutting
+// of 64 values a lane (bf16, dk = 128).
+template <typename T, int DK>
+struct StatesLds {
+  static constexpr int kRowStride = 2 * DK + 8, kColStride = 2 * DK + 32, kEStride = 136;
+  static constexpr int kRowPart = kChunk * kRowStride, kColPart = kChunk * kColStride;
+  static constexpr int kCol = kParts<T> * kRowPart, kE = kCol + kParts<T> * kColPart;
+  static constexpr int kEPart = kChunk * kEStride;
+  static constexpr int kFactors = kE + 3 * kEPart;
+  static constexpr int kBytes = kFactors + int(sizeof(Factors));
+};
 template <typename T, int DK>
 __global__ __launch_bounds__(kDeltaBlock) void k_delta_states(DeltaShape s, DeltaIn<T> in,
                                                               DeltaKept kept,
                                                               const float* __restrict__ s0,
                                                               float* __restrict__ send) {
-  constexpr int LD = DK + 4, RT = DK / 64;  // 16-row tiles of the state per wave
+  using L = StatesLds<T, DK>;
+  constexpr int NP = kParts<T>, RT = DK / 16, KB = DK / 32;
   extern __shared__ __align__(16) char smem[];
-  float* kf = (float*)smem;              // [64][LD]
-  float* St = kf + kChunk * LD;          // [32][LD]   the state, transposed
-  float* Ef = St + kSlice * LD;          // [64][kLdC]
-  float* Rt = Ef + kChunk * kLdC;        // [32][kLdC] beta R, transposed
-  float* Nt = Rt + kSlice * kLdC;        // [32][kLdC] exp(G_L - G) N, transposed
-  Factors& f = *(Factors*)(Nt + kSlice * kLdC);
-  const int slices = s.dvp / kSlice;
-  const int c0 = blockIdx.x % slices * kSlice;
+  Factors& f = *(Factors*)(smem + L::kFactors);
+  const int slices = int(div_up(s.dvp, kWalk));
+  const int t = threadIdx.x, l = t % 16, h = (t % kWave) / 16;
+  const int w = __builtin_amdgcn_readfirstlane(t / kWave);
+  const int c0 = blockIdx.x % slices * kWalk + 16 * w;
   const int vh = blockIdx.x / slices % s.hv, seq = blockIdx.x / slices / s.hv;
   const int kh = vh / (s.hv / s.hk);
-  const int t = threadIdx.x, w = t / kWave, l = t % 16, h = (t % kWave) / 16;
   const int64_t begin = first_chunk(s, seq), count = first_chunk(s, seq + 1) - begin;
-
-  // this wave's rows of the state: 16 (w RT + a) + 4 h + r, columns c0 + 16 b + l
-  f32x4 S[RT][2];
-#pragma unroll
-  for (int a = 0; a < RT; ++a)
-#pragma unroll
-    for (int b = 0; b < 2; ++b)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int row = 16 * (w * RT + a) + 4 * h + r, col = c0 + 16 * b + l;
-        S[a][b][r] = s0 && row < s.dk && col < s.dv
-                         ? s0[((int64_t(seq) * s.hv + vh) * s.dk + row) * s.dv + col] : 0.f;
-      }
-  for (int64_t c = 0; c < count; ++c) {
+  const int64_t head = int64_t(seq) * s.hv + vh;
+  const bool live = c0 < s.dvp;
+  f32x4 S[RT];
+  load_state<DK>(S, s0, s, head, c0);
+  Rows<T, DK> kr;
+  Square er;
+  Columns<T> vc;
+  double g = 0.0, gend = 0.0;
+  float be = 0.f;
+  auto fetch = [&](int64_t c) {
     const Place p = chunk_of(s, seq, c);
     const int64_t slot = (begin + c) * s.hv + vh;
-    Rows<T, DK> kr;
     kr.fetch(in.k + p.tok * in.ldk + int64_t(kh) * s.dk, in.ldk, p.len, s.dk);
-    Rows<float, kChunk> er;
-    er.fetch(kept.E + slot * kChunk * kChunk, kChunk, kChunk, kChunk);
-    f32x4 v[2];
-#pragma unroll
-    for (int b = 0; b < 2; ++b)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int row = 16 * w + 4 * h + r, col = c0 + 16 * b + l;
-        v[b][r] = row < p.len && col < s.dv
-                      ? float(in.v[(p.tok + row) * in.ldv + int64_t(vh) * s.dv + col]) : 0.f;
-      }
+    er.fetch(kept.E + slot * kChunk * kChunk);
+    vc.fetch(in.v + p.tok * in.ldv + int64_t(vh) * s.dv + c0, in.ldv, p.len, s.dv - c0);
+    if (t < kChunk) {
+      g = kept.G[slot * kChunk + t];
+      gend = kept.G[slot * kChunk + kChunk - 1];
+      be = t < p.len ? in.beta[(p.tok + t) * s.hv + vh] : 0.f;
+    }
+  };
+  if (count > 0) fetch(0);
+  for (int64_t c = 0; c < count; ++c) {
+    const int64_t slot = (begin + c) * s.hv + vh;
     __syncthreads();  // the last chunk's readers are done
-    kr.put(kf, LD);
-    er.put(Ef, kLdC);
-    load_factors(f, s, kept.G + slot * kChunk, in.beta, p, vh);
-    float* Sg = kept.S + slot * DK * s.dvp;
+    kr.put(smem, L::kRowStride);
+    kr.put(smem + L::kCol, L::kColStride);
+    er.put([&](int row, int col) { return smem + L::kE + row * L::kEStride + col * 2; }, L::kEPart);
+    set_factors(f, g, gend, be);
+    f32x4 v[4];
 #pragma unroll
-    for (int a = 0; a < RT; ++a)
-#pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        *reinterpret_cast<f32x4*>(St + (16 * b + l) * LD + 16 * (w * RT + a) + 4 * h) = S[a][b];
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-          Sg[int64_t(16 * (w * RT + a) + 4 * h + r) * s.dvp + c0 + 16 * b + l] = S[a][b][r];
-      }
+    for (int i = 0; i < 4; ++i) v[i] = vc.tile(i);
     __syncthreads();
-    f32x4 R[2];
+    if (c + 1 < count) fetch(c + 1);
+    if (!live) continue;
+    float* Sg = kept.S + (slot * s.dvp + c0 + l) * DK + 4 * h;
+    Op<3> so[KB];
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      f32x4 ks = {0, 0, 0, 0};
-      mma<DK, false, false>(ks, kf + 16 * w * LD, LD, St + 16 * b * LD, LD);
-      f32x4 br;
+    for (int a = 0; a < RT; ++a) *reinterpret_cast<f32x4*>(Sg + 16 * a) = S[a];
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int row = 16 * w + 4 * h + r;
-        R[b][r] = v[b][r] - f.in[row] * ks[r];
-        br[r] = f.beta[row] * R[b][r];
-      }
-      *reinterpret_cast<f32x4*>(Rt + (16 * b + l) * kLdC + 16 * w + 4 * h) = br;
+    for (int b = 0; b < KB; ++b) so[b] = operand<3>(S[2 * b], S[2 * b + 1]);
+    f32x4 R[4], bR[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) R[i] = f32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int b = 0; b < KB; ++b)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        mul(R[i], row_op<NP>(smem + 16 * i * L::kRowStride + 64 * b, L::kRowStride, L::kRowPart),
+            so[b]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      R[i] = v[i] - quad(f.in, i) * R[i];
+      bR[i] = quad(f.beta, i) * R[i];
     }
-    __syncthreads();
-    float* Mg = kept.M + slot * kChunk * s.dvp;
+    Op<3> n[2] = {operand<3>(bR[0], bR[1]), operand<3>(bR[2], bR[3])};
+    float* Mg = kept.M + (slot * s.dvp + c0 + l) * kChunk + 4 * h;
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      f32x4 er2 = {0, 0, 0, 0};
-      mma<kChunk, false, false>(er2, Ef + 16 * w * kLdC, kLdC, Rt + 16 * b * kLdC, kLdC);
-      f32x4 n;
+    for (int i = 0; i < 4; ++i) {
+      f32x4 x = {0, 0, 0, 0};
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int row = 16 * w + 4 * h + r;
-        const float m = R[b][r] - er2[r];
-        Mg[int64_t(row) * s.dvp + c0 + 16 * b + l] = m;
-        n[r] = f.out[row] * (f.beta[row] * m);
-      }
-      *reinterpret_cast<f32x4*>(Nt + (16 * b + l) * kLdC + 16 * w + 4 * h) = n;
+      for (int b = 0; b <= i / 2; ++b)
+        mul(x, row_op<3>(smem + L::kE + 16 * i * L::kEStride + 64 * b, L::kEStride, L::kEPart),
+            n[b]);
+      R[i] -= x;
+      *reinterpret_cast<f32x4*>(Mg + 16 * i) = R[i];
+      bR[i] = quad(f.out, i) * (quad(f.beta, i) * R[i]);
     }
-    __syncthreads();
+    n[0] = operand<3>(bR[0], bR[1]);
+    n[1] = operand<3>(bR[2], bR[3]);
     const float all = f.all;
 #pragma unroll
-    for (int a = 0; a < RT; ++a)
+    for (int a = 0; a < RT; ++a) {
+      S[a] *= all;
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        S[a][b] *= all;
-        mma<kChunk, true, false>(S[a][b], kf + 16 * (w * RT + a), LD, Nt + 16 * b * kLdC, kLdC);
-      }
+      for (int b = 0; b < 2; ++b)
+        mul(S[a], col_op<NP>(smem + L::kCol + 32 * b * L::kColStride + 32 * a, L::kColStride,
+                             L::kColPart), n[b]);
+    }
   }
-  if (!send) return;
-#pragma unroll
-  for (int a = 0; a < RT; ++a)
-#pragma unroll
-    for (int b = 0; b < 2; ++b)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int row = 16 * (w * RT + a) + 4 * h + r, col = c0 + 16 * b + l;
-        if (row < s.dk && col < s.dv)
-          send[((int64_t(seq) * s.hv + vh) * s.dk + row) * s.dv + col] = S[a][b][r];
-      }
+  if (send && live) store_state<DK>(S, send, s, head, c0);
 }
 
 // o = scale exp(G) (q S) + P N, a workgroup per chunk and value head, a slice
-// of the columns at a time.
+// of the columns at a time; a wave has 16 tokens, its rows of q and P stay in
+// registers.
+template <typename T, int DK>
+struct OutLds {
+  static constexpr int NS = kRoundedParts<T>;
+  static constexpr int kSStride = 2 * DK + 8, kNStride = 136;
+  static constexpr int kSPart = kSlice * kSStride, kNPart = kSlice * kNStride;
+  static constexpr int kN = NS * kSPart, kFactors = kN + NS * kNPart;
+  static constexpr int kBytes = kFactors + int(sizeof(Factors));
+};
 template <typename T, int DK>
 __global__ __launch_bounds__(kDeltaBlock) void k_delta_out(DeltaShape s, DeltaIn<T> in,
                                                            DeltaKept kept, T* __restrict__ o) {
-  constexpr int LD = DK + 4;
+  using L = OutLds<T, DK>;
+  constexpr int NP = kParts<T>, NS = L::NS, KB = DK / 32;
   extern __shared__ __align__(16) char smem[];
-  float* qf = (float*)smem;              // [64][LD]
-  float* Pf = qf + kChunk * LD;          // [64][kLdC]
-  float* Sf = Pf + kChunk * kLdC;        // [DK][kLdS]
-  float* Nf = Sf + DK * kLdS;            // [64][kLdS]
-  Factors& f = *(Factors*)(Nf + kChunk * kLdS);
+  Factors& f = *(Factors*)(smem + L::kFactors);
   Place p;
   if (!find_chunk(s, blockIdx.x, p)) return;
   const int vh = blockIdx.y, kh = vh / (s.hv / s.hk);
   const int64_t slot = int64_t(blockIdx.x) * s.hv + vh;
   const int t = threadIdx.x, w = t / kWave, l = t % 16, h = (t % kWave) / 16;
+  set_factors(f, s, kept.G + slot * kChunk, in.beta, p, vh);
+  // rows 16 w + l of q and P; 4 h and 16 more of every 32 columns
+  Op<NP> qo[KB];
+  Op<NS> po[2];
   {
-    Rows<T, DK> qr;
-    qr.fetch(in.q + p.tok * in.ldq + int64_t(kh) * s.dk, in.ldq, p.len, s.dk);
-    Rows<float, kChunk> pr;
-    pr.fetch(kept.P + slot * kChunk * kChunk, kChunk, kChunk, kChunk);
-    qr.put(qf, LD);
-    pr.put(Pf, kLdC);
+    const int row = 16 * w + l;
+    const T* q = in.q + (p.tok + row) * in.ldq + int64_t(kh) * s.dk + 4 * h;
+#pragma unroll
+    for (int b = 0; b < KB; ++b) {
+      float x[2][4];
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+        load_f32<4>(q + 32 * b + 16 * n, row < p.len ? s.dk - 32 * b - 16 * n - 4 * h : 0, x[n]);
+      qo[b] = operand_of<T>(f32x4{x[0][0], x[0][1], x[0][2], x[0][3]},
+                            f32x4{x[1][0], x[1][1], x[1][2], x[1][3]});
+    }
+    const float* P = kept.P + slot * kChunk * kChunk + row * kChunk + 4 * h;
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+      po[b] = operand<NS>(*reinterpret_cast<const f32x4*>(P + 32 * b),
+                          *reinterpret_cast<const f32x4*>(P + 32 * b + 16));
   }
-  load_factors(f, s, kept.G + slot * kChunk, in.beta, p, vh);
-  const float* Sg = kept.S + slot * DK * s.dvp;
-  const float* Mg = kept.M + slot * kChunk * s.dvp;
+  const float* Sg = kept.S + slot * s.dvp * DK;
+  const float* Mg = kept.M + slot * s.dvp * kChunk;
+  constexpr int kLoads = kSlice * DK / 4 / kDeltaBlock;
+  f32x4 sv[kLoads], mv[2];
+  auto fetch = [&](int c0) {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i)
+      sv[i] = *reinterpret_cast<const f32x4*>(Sg + int64_t(c0) * DK + (t + i * kDeltaBlock) * 4);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      mv[i] = *reinterpret_cast<const f32x4*>(Mg + int64_t(c0) * kChunk + (t + i * kDeltaBlock) * 4);
+  };
+  fetch(0);
   for (int c0 = 0; c0 < s.dvp; c0 += kSlice) {
     __syncthreads();
-    for (int i = t; i < DK * kSlice / 4; i += kDeltaBlock) {
-      const int row = i / (kSlice / 4), col = i % (kSlice / 4) * 4;
-      *reinterpret_cast<f32x4*>(Sf + row * kLdS + col) =
-          *reinterpret_cast<const f32x4*>(Sg + int64_t(row) * s.dvp + c0 + col);
+    auto put = [&](const f32x4& x, char* d, int part) {
+      const float y[4] = {x[0], x[1], x[2], x[3]};
+      uint32_t u[NS][2];
+      split<NS, 4>(y, u);
+#pragma unroll
+      for (int k = 0; k < NS; ++k) *reinterpret_cast<U2*>(d + k * part) = U2{u[k][0], u[k][1]};
+    };
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int at = (t + i * kDeltaBlock) * 4;
+      put(sv[i], smem + at / DK * L::kSStride + at % DK * 2, L::kSPart);
     }
-    for (int i = t; i < kChunk * kSlice / 4; i += kDeltaBlock) {
-      const int row = i / (kSlice / 4), col = i % (kSlice / 4) * 4;
-      *reinterpret_cast<f32x4*>(Nf + row * kLdS + col) =
-          *reinterpret_cast<const f32x4*>(Mg + int64_t(row) * s.dvp + c0 + col) * f.beta[row];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int at = (t + i * kDeltaBlock) * 4;
+      put(mv[i] * *reinterpret_cast<const f32x4*>(f.beta + at % kChunk),
+          smem + L::kN + at / kChunk * L::kNStride + at % kChunk * 2, L::kNPart);
     }
     __syncthreads();
+    if (c0 + kSlice < s.dvp) fetch(c0 + kSlice);
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
+    for (int n = 0; n < 2; ++n) {
       f32x4 acc = {0, 0, 0, 0};
-      mma<DK, false, true>(acc, qf + 16 * w * LD, LD, Sf + 16 * b, kLdS);
 #pragma unroll
-      for (int r = 0; r < 4; ++r) acc[r] *= s.scale * f.in[16 * w + 4 * h + r];
-      mma<kChunk, false, true>(acc, Pf + 16 * w * kLdC, kLdC, Nf + 16 * b, kLdS);
+      for (int b = 0; b < KB; ++b)
+        mul(acc, qo[b], row_op<NS>(smem + 16 * n * L::kSStride + 64 * b, L::kSStride, L::kSPart));
+      acc *= s.scale * quad(f.in, w);
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+        if (2 * b <= w)
+          mul(acc, po[b], row_op<NS>(smem + L::kN + 16 * n * L::kNStride + 64 * b, L::kNStride,
+                                     L::kNPart));
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const int row = 16 * w + 4 * h + r, col = c0 + 16 * b + l;
-        if (row < p.len && col < s.dv)
-          o[((p.tok + row) * s.hv + vh) * s.dv + col] = T(acc[r]);
+        const int row = 16 * w + 4 * h + r, col = c0 + 16 * n + l;
+        if (row < p.len && col < s.dv) o[((p.tok + row) * s.hv + vh) * s.dv + col] = T(acc[r]);
       }
     }
   }
 }
 
-// The walk backward: X of every chunk and the gradient of the state behind it.
+// The walk backward: X of every chunk, dv = B X, and the gradient of the
+// state behind it; as the walk forward.  The copy of k as rows is left out
+// where LDS has no place for it (fp32, dk > 64): its reads then meet at the
+// same banks four at a time.
+template <typename T, int DK>
+struct AdjointLds {
+  static constexpr bool kCopy = kParts<T> < 3 || DK == 64;
+  static constexpr int kColStride = 2 * DK + 32, kColPart = kChunk * kColStride;
+  static constexpr int kRowStride = kCopy ? 2 * DK + 8 : kColStride;
+  static constexpr int kRowPart = kChunk * kRowStride;
+  static constexpr int kQ = kParts<T> * kColPart, kE = 2 * kQ, kP = kE + 3 * kTri;
+  static constexpr int kRows = kCopy ? kP + 3 * kTri : 0;
+  static constexpr int kFactors = kP + 3 * kTri + (kCopy ? kParts<T> * kRowPart : 0);
+  static constexpr int kBytes = kFactors + int(sizeof(Factors));
+};
 template <typename T, int DK>
 __global__ __launch_bounds__(kDeltaBlock) void k_delta_adjoint(
     DeltaShape s, DeltaIn<T> in, DeltaKept kept, const T* __restrict__ dout, int64_t ldo,
     const float* __restrict__ dsend, float* __restrict__ X, float* __restrict__ dS,
-    float* __restrict__ ds0) {
-  constexpr int LD = DK + 4, RT = DK / 64;
+    T* __restrict__ dv, float* __restrict__ ds0) {
+  using L = AdjointLds<T, DK>;
+  constexpr int NP = kParts<T>, RT = DK / 16, KB = DK / 32;
   extern __shared__ __align__(16) char smem[];
-  float* kf = (float*)smem;              // [64][LD]
-  float* qf = kf + kChunk * LD;          // [64][LD]
-  float* Dt = qf + kChunk * LD;          // [32][LD] the state's gradient, transposed
-  float* Ef = Dt + kSlice * LD;          // [64][kLdC]
-  float* Pf = Ef + kChunk * kLdC;        // [64][kLdC]
-  float* Ot = Pf + kChunk * kLdC;        // [32][kLdC] do, then scale exp(G) do, transposed
-  float* Yt = Ot + kSlice * kLdC;        // [32][kLdC] beta Y, then -exp(G) beta X, transposed
-  Factors& f = *(Factors*)(Yt + kSlice * kLdC);
-  const int slices = s.dvp / kSlice;
-  const int c0 = blockIdx.x % slices * kSlice;
+  Factors& f = *(Factors*)(smem + L::kFactors);
+  const int slices = int(div_up(s.dvp, kWalk));
+  const int t = threadIdx.x, l = t % 16, h = (t % kWave) / 16;
+  const int w = __builtin_amdgcn_readfirstlane(t / kWave);
+  const int c0 = blockIdx.x % slices * kWalk + 16 * w;
   const int vh = blockIdx.x / slices % s.hv, seq = blockIdx.x / slices / s.hv;
   const int kh = vh / (s.hv / s.hk);
-  const int t = threadIdx.x, w = t / kWave, l = t % 16, h = (t % kWave) / 16;
   const int64_t begin = first_chunk(s, seq), count = first_chunk(s, seq + 1) - begin;
-  f32x4 D[RT][2];
-#pragma unroll
-  for (int a = 0; a < RT; ++a)
-#pragma unroll
-    for (int b = 0; b < 2; ++b)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int row = 16 * (w * RT + a) + 4 * h + r, col = c0 + 16 * b + l;
-        D[a][b][r] = dsend && row < s.dk && col < s.dv
-                         ? dsend[((int64_t(seq) * s.hv + vh) * s.dk + row) * s.dv + col] : 0.f;
-      }
+  const int64_t head = int64_t(seq) * s.hv + vh;
+  const bool live = c0 < s.dvp;
+  f32x4 D[RT];
+  load_state<DK>(D, dsend, s, head, c0);
+  Rows<T, DK> kr, qr;
+  Square er, pr;
+  Columns<T> oc;
+  double g = 0.0, gend = 0.0;
+  float be = 0.f;
+  auto fetch = [&](int64_t c) {
+    const Place p = chunk_of(s, seq, c);
+    const int64_t slot = (begin + c) * s.hv + vh;
+    kr.fetch(in.k + p.tok * in.ldk + int64_t(kh) * s.dk, in.ldk, p.len, s.dk);
+    qr.fetch(in.q + p.tok * in.ldq + int64_t(kh) * s.dk, in.ldq, p.len, s.dk);
+    er.fetch(kept.E + slot * kChunk * kChunk);
+    pr.fetch(kept.P + slot * kChunk * kChunk);
+    oc.fetch(dout + p.tok * ldo + int64_t(vh) * s.dv + c0, ldo, p.len, s.dv - c0);
+    if (t < kChunk) {
+      g = kept.G[slot * kChunk + t];
+      gend = kept.G[slot * kChunk + kChunk - 1];
+      be = t < p.len ? in.beta[(p.tok + t) * s.hv + vh] : 0.f;
+    }
+  };
+  if (count > 0) fetch(count - 1);
   for (int64_t c = count - 1; c >= 0; --c) {
     const Place p = chunk_of(s, seq, c);
     const int64_t slot = (begin + c) * s.hv + vh;
-    f32x4 o[2];
+    __syncthreads();
+    kr.put(smem, L::kColStride);
+    qr.put(smem + L::kQ, L::kColStride);
+    if (L::kCopy) kr.put(smem + L::kRows, L::kRowStride);
+    er.put_tri(smem + L::kE);
+    pr.put_tri(smem + L::kP);
+    set_factors(f, g, gend, be);
+    f32x4 o[4];
 #pragma unroll
-    for (int b = 0; b < 2; ++b)
+    for (int i = 0; i < 4; ++i) o[i] = oc.tile(i);
+    __syncthreads();
+    if (c > 0) fetch(c - 1);
+    if (!live) continue;
+    float* Dg = dS + (slot * s.dvp + c0 + l) * DK + 4 * h;
+    Op<3> so[KB];
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int row = 16 * w + 4 * h + r, col = c0 + 16 * b + l;
-        o[b][r] = row < p.len && col < s.dv
-                      ? float(dout[(p.tok + row) * ldo + int64_t(vh) * s.dv + col]) : 0.f;
+    for (int a = 0; a < RT; ++a) *reinterpret_cast<f32x4*>(Dg + 16 * a) = D[a];
+#pragma unroll
+    for (int b = 0; b < KB; ++b) so[b] = operand<3>(D[2 * b], D[2 * b + 1]);
+    f32x4 Y[4], bY[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) Y[i] = f32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int b = 0; b < KB; ++b)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        mul(Y[i], row_op<NP>(smem + L::kRows + 16 * i * L::kRowStride + 64 * b, L::kRowStride,
+                             L::kRowPart), so[b]);
+    const Op<NP> oo[2] = {operand_of<T>(o[0], o[1]), operand_of<T>(o[2], o[3])};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      Y[i] *= quad(f.out, i);
+#pragma unroll
+      for (int b = i / 2; b < 2; ++b) mul(Y[i], tri_turned<3>(smem + L::kP, i, b), oo[b]);
+      bY[i] = quad(f.beta, i) * Y[i];
+    }
+    Op<3> n[2] = {operand<3>(bY[0], bY[1]), operand<3>(bY[2], bY[3])};
+    float* Xg = X + (slot * s.dvp + c0 + l) * kChunk + 4 * h;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f32x4 x = {0, 0, 0, 0};
+#pragma unroll
+      for (int b = i / 2; b < 2; ++b) mul(x, tri_turned<3>(smem + L::kE, i, b), n[b]);
+      Y[i] -= x;
+      *reinterpret_cast<f32x4*>(Xg + 16 * i) = Y[i];
+      bY[i] = quad(f.beta, i) * Y[i];
+      if (dv && c0 + l < s.dv) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int row = 16 * i + 4 * h + r;
+          if (row < p.len) dv[((p.tok + row) * s.hv + vh) * s.dv + c0 + l] = T(bY[i][r]);
+        }
       }
-    __syncthreads();
-    {
-      Rows<T, DK> kr, qr;
-      kr.fetch(in.k + p.tok * in.ldk + int64_t(kh) * s.dk, in.ldk, p.len, s.dk);
-      qr.fetch(in.q + p.tok * in.ldq + int64_t(kh) * s.dk, in.ldq, p.len, s.dk);
-      Rows<float, kChunk> er, pr;
-      er.fetch(kept.E + slot * kChunk * kChunk, kChunk, kChunk, kChunk);
-      pr.fetch(kept.P + slot * kChunk * kChunk, kChunk, kChunk, kChunk);
-      kr.put(kf, LD);
-      qr.put(qf, LD);
-      er.put(Ef, kLdC);
-      pr.put(Pf, kLdC);
+      const f32x4 ein = quad(f.in, i);
+      bY[i] *= -ein;
+      o[i] *= s.scale * ein;
     }
-    load_factors(f, s, kept.G + slot * kChunk, in.beta, p, vh);
-    float* Dg = dS + slot * DK * s.dvp;
-#pragma unroll
-    for (int a = 0; a < RT; ++a)
-#pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        *reinterpret_cast<f32x4*>(Dt + (16 * b + l) * LD + 16 * (w * RT + a) + 4 * h) = D[a][b];
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-          Dg[int64_t(16 * (w * RT + a) + 4 * h + r) * s.dvp + c0 + 16 * b + l] = D[a][b][r];
-      }
-#pragma unroll
-    for (int b = 0; b < 2; ++b)
-      *reinterpret_cast<f32x4*>(Ot + (16 * b + l) * kLdC + 16 * w + 4 * h) = o[b];
-    __syncthreads();
-    f32x4 Y[2];
-#pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      Y[b] = f32x4{0, 0, 0, 0};
-      mma<DK, false, false>(Y[b], kf + 16 * w * LD, LD, Dt + 16 * b * LD, LD);
-#pragma unroll
-      for (int r = 0; r < 4; ++r) Y[b][r] *= f.out[16 * w + 4 * h + r];
-      mma<kChunk, true, false>(Y[b], Pf + 16 * w, kLdC, Ot + 16 * b * kLdC, kLdC);
-      f32x4 by;
-#pragma unroll
-      for (int r = 0; r < 4; ++r) by[r] = f.beta[16 * w + 4 * h + r] * Y[b][r];
-      *reinterpret_cast<f32x4*>(Yt + (16 * b + l) * kLdC + 16 * w + 4 * h) = by;
-    }
-    __syncthreads();
-    float* Xg = X + slot * kChunk * s.dvp;
-    f32x4 xs[2];
-#pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      f32x4 ey = {0, 0, 0, 0};
-      mma<kChunk, true, false>(ey, Ef + 16 * w, kLdC, Yt + 16 * b * kLdC, kLdC);
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int row = 16 * w + 4 * h + r;
-        const float x = Y[b][r] - ey[r];
-        Xg[int64_t(row) * s.dvp + c0 + 16 * b + l] = x;
-        xs[b][r] = -f.in[row] * (f.beta[row] * x);
-        o[b][r] *= s.scale * f.in[row];
-      }
-    }
-    __syncthreads();
-#pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      *reinterpret_cast<f32x4*>(Yt + (16 * b + l) * kLdC + 16 * w + 4 * h) = xs[b];
-      *reinterpret_cast<f32x4*>(Ot + (16 * b + l) * kLdC + 16 * w + 4 * h) = o[b];
-    }
-    __syncthreads();
+    n[0] = operand<3>(bY[0], bY[1]);
+    n[1] = operand<3>(bY[2], bY[3]);
+    const Op<3> os[2] = {operand<3>(o[0], o[1]), operand<3>(o[2], o[3])};
     const float all = f.all;
 #pragma unroll
-    for (int a = 0; a < RT; ++a)
+    for (int a = 0; a < RT; ++a) {
+      D[a] *= all;
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
-        D[a][b] *= all;
-        mma<kChunk, true, false>(D[a][b], kf + 16 * (w * RT + a), LD, Yt + 16 * b * kLdC, kLdC);
-        mma<kChunk, true, false>(D[a][b], qf + 16 * (w * RT + a), LD, Ot + 16 * b * kLdC, kLdC);
+        const int at = 32 * b * L::kColStride + 32 * a;
+        mul(D[a], col_op<NP>(smem + at, L::kColStride, L::kColPart), n[b]);
+        mul(D[a], col_op<NP>(smem + L::kQ + at, L::kColStride, L::kColPart), os[b]);
       }
+    }
   }
-  if (!ds0) return;
-#pragma unroll
-  for (int a = 0; a < RT; ++a)
-#pragma unroll
-    for (int b = 0; b < 2; ++b)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int row = 16 * (w * RT + a) + 4 * h + r, col = c0 + 16 * b + l;
-        if (row < s.dk && col < s.dv)
-          ds0[((int64_t(seq) * s.hv + vh) * s.dk + row) * s.dv + col] = D[a][b][r];
-      }
+  if (ds0 && live) store_state<DK>(D, ds0, s, head, c0);
 }
 
-// All gradients of a chunk but the state's, a workgroup per chunk and key
-// head: the value heads that share the key head are walked one after the
-// other, so the gradients of q and k are summed in registers, in one order.
+// All gradients of a chunk but the state's and v's, a workgroup per chunk and
+// key head, a wave 16 of its tokens: the value heads that share the key head
+// are walked one after the other, so the gradients of q and k are summed in
+// registers, in one order.  With H = (do N^T) P - (X N^T) (d beta k k^T) element
+// by element, whose row sums come from q.dq + k.u and column sums from k.w,
+//   dG_i = scale exp(G) q.(do S^T) - exp(G) beta k.(X S^T)
+//          - exp(G_L - G) k.(N dS^T) + rows of H - columns of H,
+// so only products of full precision enter dg, and dP and dA, which go on into
+// dq and dk, need no more parts than those are rounded to.
 template <typename T, int DK>
-__global__ __launch_bounds__(kDeltaBlock) void k_delta_grads(
+struct GradsLds {
+  static constexpr int NS = kRoundedParts<T>;
+  // first over the columns of the state, a slice at a time: S (then dS) and
+  // X and N, lines of a column each ...
+  static constexpr int kSStride = 2 * DK + 32, kSPart = kSlice * kSStride;
+  static constexpr int kXStride = 160, kXPart = kSlice * kXStride;
+  static constexpr int kX = 3 * kSPart, kN = kX + 3 * kXPart, kFirst = kN + 3 * kXPart;
+  // ... then over the chunk's tokens
+  static constexpr int kColStride = 2 * DK + 32, kColPart = kChunk * kColStride;
+  static constexpr int kQ = kParts<T> * kColPart, kdP = 2 * kQ, kdA = kdP + NS * kTri;
+  static constexpr int kSecond = kdA + NS * kTri;
+  static constexpr int kFactors = kFirst > kSecond ? kFirst : kSecond;
+  struct Tail {
+    Factors f;
+    double G[kChunk], dG[kChunk];
+    float xm[4][kChunk], cols[4][kChunk], part[8];
+  };
+  static constexpr int kBytes = kFactors + int(sizeof(Tail));
+};
+template <typename T, int DK>
+__global__ __launch_bounds__(kDeltaBlock, kParts<T> == 1 ? 2 : 1) void k_delta_grads(
     DeltaShape s, DeltaIn<T> in, DeltaKept kept, const T* __restrict__ dout, int64_t ldo,
     const float* __restrict__ X, const float* __restrict__ dS, T* __restrict__ dq,
-    T* __restrict__ dk, T* __restrict__ dv, float* __restrict__ dg, float* __restrict__ dbeta) {
-  constexpr int LD = DK + 4, NT = DK / 16;
+    T* __restrict__ dk, float* __restrict__ dg, float* __restrict__ dbeta) {
+  using L = GradsLds<T, DK>;
+  constexpr int NP = kParts<T>, NS = L::NS, NT = DK / 16, KB = DK / 32;
   extern __shared__ __align__(16) char smem[];
-  // first over the columns of the state, a slice at a time ...
-  float* Of = (float*)smem;              // [64][kLdS] do
-  float* Xf = Of + kChunk * kLdS;        // [64][kLdS]
-  float* Nf = Xf + kChunk * kLdS;        // [64][kLdS]
-  float* Sf = Nf + kChunk * kLdS;        // [DK][kLdS]
-  float* Df = Sf + DK * kLdS;            // [DK][kLdS]
-  // ... then over the chunk's tokens
-  float* kf = (float*)smem;              // [64][LD]
-  float* qf = kf + kChunk * LD;          // [64][LD]
-  float* dP = qf + kChunk * LD;          // [64][kLdC]
-  float* dA = dP + kChunk * kLdC;        // [64][kLdC]
-  constexpr int kA = 3 * kChunk * kLdS + 2 * DK * kLdS;
-  constexpr int kB = 2 * kChunk * LD + 2 * kChunk * kLdC;
-  Factors& f = *(Factors*)((float*)smem + (kA > kB ? kA : kB));
-  double* G = (double*)(&f + 1);
-  double* dG = G + kChunk;
-  float* part = (float*)(dG + kChunk);   // [8]
+  typename L::Tail& z = *(typename L::Tail*)(smem + L::kFactors);
   Place p;
   if (!find_chunk(s, blockIdx.x, p)) return;
   const int kh = blockIdx.y, group = s.hv / s.hk;
-  const int t = threadIdx.x, w = t / kWave, l = t % 16, h = (t % kWave) / 16;
+  const int t = threadIdx.x, l = t % 16, h = (t % kWave) / 16;
+  const int w = __builtin_amdgcn_readfirstlane(t / kWave);
   f32x4 aq[NT], ak[NT];  // sums over the group, rows 16 w + 4 h + r, columns 16 n + l
 #pragma unroll
   for (int n = 0; n < NT; ++n) aq[n] = ak[n] = f32x4{0, 0, 0, 0};
 
   for (int vh = kh * group; vh < (kh + 1) * group; ++vh) {
     const int64_t slot = int64_t(blockIdx.x) * s.hv + vh;
-    const float* Sg = kept.S + slot * DK * s.dvp;
-    const float* Dg = dS + slot * DK * s.dvp;
-    const float* Mg = kept.M + slot * kChunk * s.dvp;
-    const float* Xg = X + slot * kChunk * s.dvp;
+    const float* Sg = kept.S + slot * s.dvp * DK;
+    const float* Dg = dS + slot * s.dvp * DK;
+    const float* Mg = kept.M + slot * s.dvp * kChunk;
+    const float* Xg = X + slot * s.dvp * kChunk;
     __syncthreads();
-    load_factors(f, s, kept.G + slot * kChunk, in.beta, p, vh);
-    if (t < kChunk) G[t] = kept.G[slot * kChunk + t];
+    set_factors(z.f, s, kept.G + slot * kChunk, in.beta, p, vh);
+    if (t < kChunk) z.G[t] = kept.G[slot * kChunk + t];
     f32x4 pp[4], pa[4], oS[NT], xS[NT], nD[NT];
 #pragma unroll
     for (int j = 0; j < 4; ++j) pp[j] = pa[j] = f32x4{0, 0, 0, 0};
 #pragma unroll
     for (int n = 0; n < NT; ++n) oS[n] = xS[n] = nD[n] = f32x4{0, 0, 0, 0};
-    float sd = 0.f;   // <S, dS> of this thread's elements
-    float xm = 0.f;   // X . M of row t / 4, a quarter of its columns
-    for (int c0 = 0; c0 < s.dvp; c0 += kSlice) {
-      __syncthreads();
-      {
-        const int row = t / 4, col = t % 4 * 8;
-        float a[8], m[8], x[8];
-        load_f32<8>(dout + (p.tok + row) * ldo + int64_t(vh) * s.dv + c0 + col,
-                    row < p.len ? s.dv - c0 - col : 0, a);
-        load_f32<8>(Mg + int64_t(row) * s.dvp + c0 + col, 8, m);
-        load_f32<8>(Xg + int64_t(row) * s.dvp + c0 + col, 8, x);
-        const float be = f.beta[row];
-        float v[8];
+    float sd = 0.f;                          // <S, dS> of this thread's elements
+    float xm[8] = {0, 0, 0, 0, 0, 0, 0, 0};  // X . M of tokens 8 (t % 8) ..
+    constexpr int kLoads = kSlice * DK / 4 / kDeltaBlock;
+    const T* orow = dout + (p.tok + 16 * w + l) * ldo + int64_t(vh) * s.dv + 4 * h;
+    auto put = [&](const f32x4& x, char* d, int part) {
+      const float y[4] = {x[0], x[1], x[2], x[3]};
+      uint32_t u[3][2];
+      split<3, 4>(y, u);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          xm += x[i] * m[i];
-          v[i] = be * x[i];
-          Of[row * kLdS + col + i] = a[i];
-          Xf[row * kLdS + col + i] = x[i];
-          Nf[row * kLdS + col + i] = be * m[i];
-        }
-        if (dv && row < p.len)
-          store_f32<8>(dv + ((p.tok + row) * s.hv + vh) * s.dv + c0 + col, s.dv - c0 - col, v);
+      for (int k = 0; k < 3; ++k) *reinterpret_cast<U2*>(d + k * part) = U2{u[k][0], u[k][1]};
+    };
+    for (int c0 = 0; c0 < s.dvp; c0 += kSlice) {
+      f32x4 sv[kLoads], dv[kLoads], xv[2], mv[2];
+      float ov[2][4];
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        const int64_t at = int64_t(c0) * DK + (t + i * kDeltaBlock) * 4;
+        sv[i] = *reinterpret_cast<const f32x4*>(Sg + at);
+        dv[i] = *reinterpret_cast<const f32x4*>(Dg + at);
       }
-      for (int i = t; i < DK * kSlice / 4; i += kDeltaBlock) {
-        const int row = i / (kSlice / 4), col = i % (kSlice / 4) * 4;
-        const f32x4 a = *reinterpret_cast<const f32x4*>(Sg + int64_t(row) * s.dvp + c0 + col);
-        const f32x4 b = *reinterpret_cast<const f32x4*>(Dg + int64_t(row) * s.dvp + c0 + col);
-        sd += a[0] * b[0] + a[1] * b[1] + (a[2] * b[2] + a[3] * b[3]);
-        *reinterpret_cast<f32x4*>(Sf + row * kLdS + col) = a;
-        *reinterpret_cast<f32x4*>(Df + row * kLdS + col) = b;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int64_t at = int64_t(c0) * kChunk + t * 8 + 4 * i;
+        xv[i] = *reinterpret_cast<const f32x4*>(Xg + at);
+        mv[i] = *reinterpret_cast<const f32x4*>(Mg + at);
+        load_f32<4>(orow + c0 + 16 * i, 16 * w + l < p.len ? s.dv - c0 - 16 * i - 4 * h : 0, ov[i]);
       }
       __syncthreads();
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        const int at = (t + i * kDeltaBlock) * 4;
+        sd += sv[i][0] * dv[i][0] + sv[i][1] * dv[i][1] +
+              (sv[i][2] * dv[i][2] + sv[i][3] * dv[i][3]);
+        put(sv[i], smem + at / DK * L::kSStride + at % DK * 2, L::kSPart);
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int tok = t % 8 * 8 + 4 * i;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) xm[4 * i + r] += xv[i][r] * mv[i][r];
+        char* d = smem + t / 8 * L::kXStride + tok * 2;
+        put(xv[i], d + L::kX, L::kXPart);
+        put(mv[i] * *reinterpret_cast<const f32x4*>(z.f.beta + tok), d + L::kN, L::kXPart);
+      }
+      __syncthreads();
+      const Op<NP> oo = operand_of<T>(f32x4{ov[0][0], ov[0][1], ov[0][2], ov[0][3]},
+                                      f32x4{ov[1][0], ov[1][1], ov[1][2], ov[1][3]});
+      const Op<3> xo = col_op<3>(smem + L::kX + 32 * w, L::kXStride, L::kXPart);
+      const Op<3> no = col_op<3>(smem + L::kN + 32 * w, L::kXStride, L::kXPart);
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         if (j <= w) {
-          mma<kSlice, false, false>(pp[j], Of + 16 * w * kLdS, kLdS, Nf + 16 * j * kLdS, kLdS);
-          mma<kSlice, false, false>(pa[j], Xf + 16 * w * kLdS, kLdS, Nf + 16 * j * kLdS, kLdS);
+          const Op<3> nj = col_op<3>(smem + L::kN + 32 * j, L::kXStride, L::kXPart);
+          mul(pp[j], oo, nj);
+          mul(pa[j], xo, nj);
         }
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        mma<kSlice, false, false>(oS[n], Of + 16 * w * kLdS, kLdS, Sf + 16 * n * kLdS, kLdS);
-        mma<kSlice, false, false>(xS[n], Xf + 16 * w * kLdS, kLdS, Sf + 16 * n * kLdS, kLdS);
-        mma<kSlice, false, false>(nD[n], Nf + 16 * w * kLdS, kLdS, Df + 16 * n * kLdS, kLdS);
+        const Op<3> sn = col_op<3>(smem + 32 * n, L::kSStride, L::kSPart);
+        mul(oS[n], oo, sn);
+        mul(xS[n], xo, sn);
       }
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        const int at = (t + i * kDeltaBlock) * 4;
+        put(dv[i], smem + at / DK * L::kSStride + at % DK * 2, L::kSPart);
+      }
+      __syncthreads();
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+        mul(nD[n], no, col_op<3>(smem + 32 * n, L::kSStride, L::kSPart));
     }
-    xm = lane_sum<4>(xm);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      xm[i] += __shfl_xor(xm[i], 8, kWave);
+      xm[i] += __shfl_xor(xm[i], 16, kWave);
+      xm[i] += __shfl_xor(xm[i], 32, kWave);
+      if (t % kWave < 8) z.xm[w][t % 8 * 8 + i] = xm[i];
+    }
     sd = lane_sum<kWave>(sd);
+    if (t % kWave == 0) z.part[w] = sd;
     __syncthreads();
-    if (dbeta && t % 4 == 0 && t / 4 < p.len) dbeta[(p.tok + t / 4) * s.hv + vh] = xm;
-    if (t % kWave == 0) part[w] = sd;
+    if (dbeta && t < p.len)
+      dbeta[(p.tok + t) * s.hv + vh] = (z.xm[0][t] + z.xm[1][t]) + (z.xm[2][t] + z.xm[3][t]);
     {
       Rows<T, DK> kr, qr;
       kr.fetch(in.k + p.tok * in.ldk + int64_t(kh) * s.dk, in.ldk, p.len, s.dk);
       qr.fetch(in.q + p.tok * in.ldq + int64_t(kh) * s.dk, in.ldq, p.len, s.dk);
-      kr.put(kf, LD);
-      qr.put(qf, LD);
+      kr.put(smem, L::kColStride);
+      qr.put(smem + L::kQ, L::kColStride);
     }
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int row = 16 * w + 4 * h + r, col = 16 * j + l;
-        const float d = col <= row ? expf(float(G[row] - G[col])) : 0.f;
-        dP[row * kLdC + col] = col <= row ? s.scale * d * pp[j][r] : 0.f;
-        dA[row * kLdC + col] = col < row ? d * f.beta[row] * pa[j][r] : 0.f;
-      }
     __syncthreads();
-    float dgr[4] = {0.f, 0.f, 0.f, 0.f};
+    const f32x4 fin = quad(z.f.in, w), fout = quad(z.f.out, w), fbe = quad(z.f.beta, w);
+    f32x4 row_h = {0, 0, 0, 0};   // the rows' sums of H, this lane's columns
+    const float* Pg = kept.P + slot * kChunk * kChunk;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float col_h = 0.f;
+      if (j <= w) {
+        f32x4 kk = {0, 0, 0, 0};
+#pragma unroll
+        for (int b = 0; b < KB; ++b)
+          mul(kk, row_op<NP>(smem + 16 * w * L::kColStride + 64 * b, L::kColStride, L::kColPart),
+              row_op<NP>(smem + 16 * j * L::kColStride + 64 * b, L::kColStride, L::kColPart));
+        f32x4 dp, da;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int row = 16 * w + 4 * h + r, col = 16 * j + l;
+          const float d = col <= row ? expf(float(z.G[row] - z.G[col])) : 0.f;
+          const float bx = col < row ? d * fbe[r] * pa[j][r] : 0.f;
+          dp[r] = s.scale * d * pp[j][r];
+          da[r] = -bx;
+          const float x = col <= row ? pp[j][r] * Pg[row * kChunk + col] - bx * kk[r] : 0.f;
+          row_h[r] += x;
+          col_h += x;
+        }
+        // element (row 4 h + r, column l) of the block, a column at a time
+        const float y[4] = {dp[0], dp[1], dp[2], dp[3]}, x[4] = {da[0], da[1], da[2], da[3]};
+        uint32_t u[NS][2], v[NS][2];
+        split<NS, 4>(y, u);
+        split<NS, 4>(x, v);
+        char* d = smem + tri_at(w) + 4 * h * tri_stride(w) + 32 * j + 2 * l;
+#pragma unroll
+        for (int k = 0; k < NS; ++k)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            char* e = d + k * kTri + r * tri_stride(w);
+            *reinterpret_cast<uint16_t*>(e + L::kdP) = uint16_t(u[k][r / 2] >> (r % 2 * 16));
+            *reinterpret_cast<uint16_t*>(e + L::kdA) = uint16_t(v[k][r / 2] >> (r % 2 * 16));
+          }
+      }
+      col_h += __shfl_xor(col_h, 16, kWave);
+      col_h += __shfl_xor(col_h, 32, kWave);
+      if (h == 0) z.cols[w][16 * j + l] = col_h;
+    }
+    __syncthreads();
+    // dq = scale exp(G) (do S^T) + dP k and the like, the state's parts first
     float end = 0.f;  // sum over the rows of k_i . exp(G_L - G_i) (N dS^T)_i
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      f32x4 q4, u = {0, 0, 0, 0}, wv = {0, 0, 0, 0}, nd;
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const int row = 16 * w + 4 * h + r;
-        q4[r] = s.scale * f.in[row] * oS[n][r];
-        u[r] = f.in[row] * f.beta[row] * xS[n][r];
-        nd[r] = f.out[row] * nD[n][r];
-      }
-      mma<kChunk, false, true>(q4, dP + 16 * w * kLdC, kLdC, kf + 16 * n, LD);
-      mma<kChunk, false, true>(u, dA + 16 * w * kLdC, kLdC, kf + 16 * n, LD);
-      mma<kChunk, true, true>(wv, dP + 16 * w, kLdC, qf + 16 * n, LD);
-      f32x4 wa = {0, 0, 0, 0};
-      mma<kChunk, true, true>(wa, dA + 16 * w, kLdC, kf + 16 * n, LD);
+        const char* e = smem + (16 * w + 4 * h + r) * L::kColStride + 32 * n + 2 * l;
+        float kv = 0.f, qv = 0.f;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int row = 16 * w + 4 * h + r;
-        const float kv = kf[row * LD + 16 * n + l], qv = qf[row * LD + 16 * n + l];
-        const float away = wv[r] - wa[r] + nd[r];
-        dgr[r] += qv * q4[r] - kv * (u[r] + away);
-        end += kv * nd[r];
-        aq[n][r] += q4[r];
-        ak[n][r] += away - u[r];
+        for (int k = NP - 1; k >= 0; --k) {
+          const char* d = e + k * L::kColPart;
+          kv += __uint_as_float(uint32_t(*reinterpret_cast<const uint16_t*>(d)) << 16);
+          qv += __uint_as_float(uint32_t(*reinterpret_cast<const uint16_t*>(d + L::kQ)) << 16);
+        }
+        oS[n][r] *= s.scale * fin[r];
+        const float u = fin[r] * fbe[r] * xS[n][r], y = fout[r] * nD[n][r];
+        row_h[r] += qv * oS[n][r] - kv * (u + y);
+        end += kv * y;
+        xS[n][r] = y - u;
       }
+    }
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      const Op<NS> pr = tri_rows<NS>(smem + L::kdP, w, b), ar = tri_rows<NS>(smem + L::kdA, w, b);
+      const Op<NS> pc = tri_turned<NS>(smem + L::kdP, w, b), ac = tri_turned<NS>(smem + L::kdA, w, b);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const int at = 32 * b * L::kColStride + 32 * n;
+        const Op<NP> kn = col_op<NP>(smem + at, L::kColStride, L::kColPart);
+        if (2 * b <= w) {
+          mul(oS[n], pr, kn);
+          mul(xS[n], ar, kn);
+        }
+        if (2 * b + 1 >= w) {
+          mul(xS[n], ac, kn);
+          mul(xS[n], pc, col_op<NP>(smem + L::kQ + at, L::kColStride, L::kColPart));
+        }
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      aq[n] += oS[n];
+      ak[n] += xS[n];
     }
     if (dg) {
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        dgr[r] = lane_sum<16>(dgr[r]);
-        if (l == 0) dG[16 * w + 4 * h + r] = double(dgr[r]);
+        const float x = lane_sum<16>(row_h[r]);
+        if (l == 0) z.dG[16 * w + 4 * h + r] = double(x);
       }
       end = lane_sum<kWave>(end);
-      if (t % kWave == 0) part[4 + w] = end;
+      if (t % kWave == 0) z.part[4 + w] = end;
       __syncthreads();
       if (t < kChunk) {
-        double x = dG[kChunk - 1 - t];
+        const int row = kChunk - 1 - t;
+        double x = z.dG[row] - ((double(z.cols[0][row]) + z.cols[1][row]) +
+                                (double(z.cols[2][row]) + z.cols[3][row]));
         if (t == 0)
-          x += double(f.all) * ((double(part[0]) + part[1]) + (double(part[2]) + part[3])) +
-               ((double(part[4]) + part[5]) + (double(part[6]) + part[7]));
+          x += double(z.f.all) * ((double(z.part[0]) + z.part[1]) +
+                                  (double(z.part[2]) + z.part[3])) +
+               ((double(z.part[4]) + z.part[5]) + (double(z.part[6]) + z.part[7]));
 #pragma unroll
         for (int d = 1; d < kWave; d <<= 1) {
           const double u = __shfl_up(x, d, kWave);
           if (t >= d) x += u;
         }
-        const int row = kChunk - 1 - t;
         if (row < p.len) dg[(p.tok + row) * s.hv + vh] = float(x);
       }
     }
@@ -1082,25 +1508,23 @@ sla_status sla_delta_rule(const sla_delta_dims* dims, const void* q, int64_t ldq
   }
   return with_delta(dims, [&](auto te, auto width) -> sla_status {
     using T = decltype(te);
-    constexpr int DK = width.value, LD = DK + 4;
+    constexpr int DK = width.value;
     const DeltaIn<T> in = {(const T*)q, (const T*)k, (const T*)v, ldq, ldk, ldv, g, beta};
     if (z.chunks) {
-      constexpr int lds = (2 * kChunk * LD + kChunk * kLdC) * 4 + kChunk * 12;
+      constexpr int lds = PrepareLds<T, DK>::kBytes;
       SLA_TRY(allow_lds(k_delta_prepare<T, DK>, lds));
       k_delta_prepare<T, DK><<<dim3(int(z.chunks), s.hv), kDeltaBlock, lds, stream>>>(s, in, w);
       LAUNCH_CHECK();
     }
     {
-      constexpr int lds = (kChunk * LD + kSlice * LD + kChunk * kLdC + 2 * kSlice * kLdC) * 4 +
-                          int(sizeof(Factors));
+      constexpr int lds = StatesLds<T, DK>::kBytes;
       SLA_TRY(allow_lds(k_delta_states<T, DK>, lds));
-      k_delta_states<T, DK><<<s.nseq * s.hv * (s.dvp / kSlice), kDeltaBlock, lds, stream>>>(
+      k_delta_states<T, DK><<<s.nseq * s.hv * int(div_up(s.dvp, kWalk)), kDeltaBlock, lds, stream>>>(
           s, in, w, initial_state, final_state);
       LAUNCH_CHECK();
     }
     if (z.chunks) {
-      constexpr int lds = (kChunk * LD + kChunk * kLdC + (DK + kChunk) * kLdS) * 4 +
-                          int(sizeof(Factors));
+      constexpr int lds = OutLds<T, DK>::kBytes;
       SLA_TRY(allow_lds(k_delta_out<T, DK>, lds));
       k_delta_out<T, DK><<<dim3(int(z.chunks), s.hv), kDeltaBlock, lds, stream>>>(s, in, w, (T*)o);
       LAUNCH_CHECK();
@@ -1146,23 +1570,20 @@ sla_status sla_delta_rule_grad(const sla_delta_dims* dims, const void* q, int64_
   }
   return with_delta(dims, [&](auto te, auto width) -> sla_status {
     using T = decltype(te);
-    constexpr int DK = width.value, LD = DK + 4;
+    constexpr int DK = width.value;
     const DeltaIn<T> in = {(const T*)q, (const T*)k, (const T*)v, ldq, ldk, ldv, g, beta};
     {
-      constexpr int lds = (2 * kChunk * LD + kSlice * LD + 2 * kChunk * kLdC +
-                           2 * kSlice * kLdC) * 4 + int(sizeof(Factors));
+      constexpr int lds = AdjointLds<T, DK>::kBytes;
       SLA_TRY(allow_lds(k_delta_adjoint<T, DK>, lds));
-      k_delta_adjoint<T, DK><<<s.nseq * s.hv * (s.dvp / kSlice), kDeltaBlock, lds, stream>>>(
-          s, in, w, (const T*)grad_o, ldo, grad_final_state, X, dS, grad_initial_state);
+      k_delta_adjoint<T, DK><<<s.nseq * s.hv * int(div_up(s.dvp, kWalk)), kDeltaBlock, lds, stream>>>(
+          s, in, w, (const T*)grad_o, ldo, grad_final_state, X, dS, (T*)dv, grad_initial_state);
       LAUNCH_CHECK();
     }
-    if (z.chunks && (dq || dk || dv || dg || dbeta)) {
-      constexpr int a = 3 * kChunk * kLdS + 2 * DK * kLdS;
-      constexpr int b = 2 * kChunk * LD + 2 * kChunk * kLdC;
-      constexpr int lds = (a > b ? a : b) * 4 + int(sizeof(Factors)) + 2 * kChunk * 8 + 32;
+    if (z.chunks && (dq || dk || dg || dbeta)) {
+      constexpr int lds = GradsLds<T, DK>::kBytes;
       SLA_TRY(allow_lds(k_delta_grads<T, DK>, lds));
       k_delta_grads<T, DK><<<dim3(int(z.chunks), s.hk), kDeltaBlock, lds, stream>>>(
-          s, in, w, (const T*)grad_o, ldo, X, dS, (T*)dq, (T*)dk, (T*)dv, dg, dbeta);
+          s, in, w, (const T*)grad_o, ldo, X, dS, (T*)dq, (T*)dk, dg, dbeta);
       LAUNCH_CHECK();
     }
     return SLA_OK;
