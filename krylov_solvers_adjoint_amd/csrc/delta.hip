@@ -250,35 +250,66 @@ typedef __bf16 Quad __attribute__((ext_vector_type(4)));
 __device__ __forceinline__ Frag join(const Quad& a, const Quad& b) {
   return Frag{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
 }
+__device__ __forceinline__ Quad turned(const char* p) {
+  return __builtin_amdgcn_ds_read_tr16_b64_v4bf16((__attribute__((address_space(3))) Quad*)p);
+}
 // Rows l of an LDS array of rows of k (p: row 0, first of the 32 k; two reads
 // of 8 bytes, free of conflicts if the rows are an odd number of those apart).
-__device__ __forceinline__ Frag row_frag(const char* p, int stride) {
+template <int PARTS>
+__device__ __forceinline__ Op<PARTS> row_op(const char* p, int stride, int part) {
   const int l = threadIdx.x % 16, h = threadIdx.x % kWave / 16;
-  const char* q = p + l * stride + 8 * h;
-  return join(*reinterpret_cast<const Quad*>(q), *reinterpret_cast<const Quad*>(q + 32));
+  Op<PARTS> o;
+#pragma unroll
+  for (int k = 0; k < PARTS; ++k) {
+    const char* q = p + k * part + l * stride + 8 * h;
+    o.f[k] = join(*reinterpret_cast<const Quad*>(q), *reinterpret_cast<const Quad*>(q + 32));
+  }
+  return o;
 }
-// Columns l of 16 lines of k (p: line 0, first of the 16 columns; free of
+// Columns l of 32 lines of k (p: line 0, first of the 16 columns; free of
 // conflicts if the lines are 32 bytes apart modulo 128).
 __device__ __forceinline__ Quad turned(const char* p, int stride) {
   const int l = threadIdx.x % 16, h = threadIdx.x % kWave / 16;
-  return __builtin_amdgcn_ds_read_tr16_b64_v4bf16(
-      (__attribute__((address_space(3))) Quad*)(p + (4 * h + (l >> 2)) * stride + (l & 3) * 8));
-}
-__device__ __forceinline__ Frag col_frag(const char* p, int stride) {
-  return join(turned(p, stride), turned(p + 16 * stride, stride));
-}
-template <int PARTS>
-__device__ __forceinline__ Op<PARTS> row_op(const char* p, int stride, int part) {
-  Op<PARTS> o;
-#pragma unroll
-  for (int k = 0; k < PARTS; ++k) o.f[k] = row_frag(p + k * part, stride);
-  return o;
+  return turned(p + (4 * h + (l >> 2)) * stride + (l & 3) * 8);
 }
 template <int PARTS>
 __device__ __forceinline__ Op<PARTS> col_op(const char* p, int stride, int part) {
   Op<PARTS> o;
 #pragma unroll
-  for (int k = 0; k < PARTS; ++k) o.f[k] = col_frag(p + k * part, stride);
+  for (int k = 0; k < PARTS; ++k)
+    o.f[k] = join(turned(p + k * part, stride), turned(p + k * part + 16 * stride, stride));
+  return o;
+}
+// The chunk's rows of k and q are read both ways: their lines are not spread
+// apart, but the 8-byte units of a line are exchanged by key(line), which
+// sends both the same unit of 16 lines and four units of four neighbouring
+// lines to 16 different places modulo 128 bytes.
+__device__ __forceinline__ int key(int line) { return (line & 3) << 2 | (line >> 2 & 3); }
+// Tokens 16 i + l, k = 32 b .. of [64][DK] rows.
+template <int PARTS, int DK>
+__device__ __forceinline__ Op<PARTS> token_rows(const char* p, int i, int b) {
+  const int l = threadIdx.x % 16, h = threadIdx.x % kWave / 16;
+  Op<PARTS> o;
+#pragma unroll
+  for (int k = 0; k < PARTS; ++k) {
+    const char* q = p + k * kChunk * DK * 2 + (16 * i + l) * DK * 2;
+    o.f[k] = join(*reinterpret_cast<const Quad*>(q + ((8 * b + h) ^ key(l)) * 8),
+                  *reinterpret_cast<const Quad*>(q + ((8 * b + 4 + h) ^ key(l)) * 8));
+  }
+  return o;
+}
+// Columns 16 a + l, k = the tokens 32 b ..
+template <int PARTS, int DK>
+__device__ __forceinline__ Op<PARTS> token_cols(const char* p, int a, int b) {
+  const int l = threadIdx.x % 16, h = threadIdx.x % kWave / 16;
+  const int line = 4 * h + (l >> 2);
+  Op<PARTS> o;
+#pragma unroll
+  for (int k = 0; k < PARTS; ++k) {
+    const char* q = p + k * kChunk * DK * 2 + (32 * b + line) * DK * 2 +
+                    ((4 * a + (l & 3)) ^ key(line)) * 8;
+    o.f[k] = join(turned(q), turned(q + 16 * DK * 2));
+  }
   return o;
 }
 
@@ -322,38 +353,51 @@ __device__ __forceinline__ Op<PARTS> tri_rows(const char* p, int ti, int kb) {
 // A chunk's rows of WIDTH elements (zero past `len` rows and `have` columns),
 // 8 elements a load, held in registers between the load and the LDS store so
 // that the next chunk's rows travel while this one is worked on.
-template <typename T, int WIDTH>
+// WHOLE: the columns are a multiple of 8.
+template <typename T, int WIDTH, bool WHOLE>
 struct Rows {
   static constexpr int kLoads = kChunk * WIDTH / 8 / kDeltaBlock;
   static_assert(kLoads >= 1, "a load per thread");
   Eight<T> v[kLoads];
+  uint32_t in;   // load i is of an existing row and column: bit i
+  // No lane branches: a load of what does not exist goes to row 0 instead, and
+  // put() drops it (a branch's join would wait for each load in turn).
   __device__ __forceinline__ void fetch(const T* p, int64_t ld, int len, int have) {
+    in = 0;
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
       const int at = threadIdx.x + i * kDeltaBlock;
       const int row = at / (WIDTH / 8), col = at % (WIDTH / 8) * 8;
-      const int n = row < len ? have - col : 0;
-      const T* q = p + row * ld + col;
-      if (n >= 8) {
-        v[i] = *reinterpret_cast<const Eight<T>*>(q);
+      const bool on = row < len && col < have;
+      in |= uint32_t(on) << i;
+      if constexpr (WHOLE) {
+        v[i] = *reinterpret_cast<const Eight<T>*>(p + (on ? row * ld + col : 0));
       } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[i][j] = j < n ? q[j] : T(0.f);
+        for (int j = 0; j < 8; ++j) {
+          const bool here = on && col + j < have;
+          const T x = p[here ? row * ld + col + j : 0];
+          v[i][j] = here ? x : T(0.f);
+        }
       }
     }
   }
-  // its parts, rows `stride` bytes apart
-  __device__ __forceinline__ void put(char* lds, int stride) const {
+  // its parts, kChunk * WIDTH * 2 bytes each
+  __device__ __forceinline__ void put(char* lds) const {
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
       const int at = threadIdx.x + i * kDeltaBlock;
-      char* d = lds + (at / (WIDTH / 8)) * stride + at % (WIDTH / 8) * 16;
+      const int row = at / (WIDTH / 8), unit = at % (WIDTH / 8) * 2;
       uint32_t p[kParts<T>][4];
       split<T>(v[i], p);
+      const uint32_t keep = 0u - (in >> i & 1u);
 #pragma unroll
       for (int k = 0; k < kParts<T>; ++k) {
-        *reinterpret_cast<U2*>(d + k * kChunk * stride) = U2{p[k][0], p[k][1]};
-        *reinterpret_cast<U2*>(d + k * kChunk * stride + 8) = U2{p[k][2], p[k][3]};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) p[k][j] &= keep;
+        char* d = lds + k * kChunk * WIDTH * 2 + row * WIDTH * 2;
+        *reinterpret_cast<U2*>(d + (unit ^ key(row)) * 8) = U2{p[k][0], p[k][1]};
+        *reinterpret_cast<U2*>(d + (unit + 1 ^ key(row)) * 8) = U2{p[k][2], p[k][3]};
       }
     }
   }
@@ -460,13 +504,12 @@ __global__ __launch_bounds__(kDeltaBlock) void k_delta_gaps(const int32_t* tok, 
 // a block column per wave, with T = I - B E the inverse so far.
 template <typename T, int DK>
 struct PrepareLds {
-  static constexpr int kStride = 2 * DK + 8;
-  static constexpr int kRow = kParts<T> * kChunk * kStride;
+  static constexpr int kRow = kParts<T> * kChunk * DK * 2;
   static constexpr int kSquare = kChunk * kLdC * 4;
   static constexpr int kFirst = 2 * kRow > 2 * kSquare ? 2 * kRow : 2 * kSquare;
   static constexpr int kBytes = kFirst + kSquare + kChunk * 12;
 };
-template <typename T, int DK>
+template <typename T, int DK, bool WHOLE>
 __global__ __launch_bounds__(kDeltaBlock) void k_delta_prepare(DeltaShape s, DeltaIn<T> in,
                                                                DeltaKept kept) {
   using L = PrepareLds<T, DK>;
@@ -484,11 +527,11 @@ __global__ __launch_bounds__(kDeltaBlock) void k_delta_prepare(DeltaShape s, Del
   const int vh = blockIdx.y, kh = vh / (s.hv / s.hk);
   const int t = threadIdx.x, w = t / kWave, l = t % 16, h = (t % kWave) / 16;
   {
-    Rows<T, DK> kr, qr;
+    Rows<T, DK, WHOLE> kr, qr;
     kr.fetch(in.k + p.tok * in.ldk + int64_t(kh) * s.dk, in.ldk, p.len, s.dk);
     qr.fetch(in.q + p.tok * in.ldq + int64_t(kh) * s.dk, in.ldq, p.len, s.dk);
-    kr.put(kf, L::kStride);
-    qr.put(qf, L::kStride);
+    kr.put(kf);
+    qr.put(qf);
   }
   if (t < kChunk) {
     const int64_t at = (p.tok + t) * s.hv + vh;
@@ -510,10 +553,9 @@ __global__ __launch_bounds__(kDeltaBlock) void k_delta_prepare(DeltaShape s, Del
     if (J <= w) {
 #pragma unroll
       for (int b = 0; b < DK / 32; ++b) {
-        constexpr int part = kChunk * L::kStride;
-        const Op<NP> kj = row_op<NP>(kf + 16 * J * L::kStride + 64 * b, L::kStride, part);
-        mul(kk, row_op<NP>(kf + 16 * w * L::kStride + 64 * b, L::kStride, part), kj);
-        mul(qk, row_op<NP>(qf + 16 * w * L::kStride + 64 * b, L::kStride, part), kj);
+        const Op<NP> kj = token_rows<NP, DK>(kf, J, b);
+        mul(kk, token_rows<NP, DK>(kf, w, b), kj);
+        mul(qk, token_rows<NP, DK>(qf, w, b), kj);
       }
     }
 #pragma unroll
@@ -599,11 +641,11 @@ __device__ __forceinline__ void set_factors(Factors& f, const DeltaShape& s, con
     set_factors(f, G[t], G[kChunk - 1], t < p.len ? beta[(p.tok + t) * s.hv + vh] : 0.f);
 }
 
-__device__ __forceinline__ Place chunk_of(const DeltaShape& s, int seq, int64_t c) {
+__device__ __forceinline__ Place chunk_of(int seq, int64_t first, int64_t end, int64_t c) {
   Place p;
   p.seq = seq;
-  p.tok = first_token(s, seq) + c * kChunk;
-  const int64_t left = first_token(s, seq + 1) - p.tok;
+  p.tok = first + c * kChunk;
+  const int64_t left = end - p.tok;
   p.len = left < kChunk ? int(left) : kChunk;
   return p;
 }
@@ -638,18 +680,22 @@ __device__ __forceinline__ void store_state(const f32x4 (&S)[DK / 16], float* p,
 template <typename T>
 struct Columns {
   T v[4][4];
+  int left;   // rows from this lane's first on that exist; 0 if the column does not
   __device__ __forceinline__ void fetch(const T* p, int64_t ld, int len, int have) {
     const int l = threadIdx.x % 16, h = threadIdx.x % kWave / 16;
+    left = l < have ? len - 4 * h : 0;
+    const T* q = p + 4 * h * ld + l;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int row = 16 * i + 4 * h + r;
-        v[i][r] = row < len && l < have ? p[row * ld + l] : T(0.f);
-      }
+      for (int r = 0; r < 4; ++r) v[i][r] = *(16 * i + r < left ? q + (16 * i + r) * ld : any);
   }
+  const T* any;   // an element that exists
   __device__ __forceinline__ f32x4 tile(int i) const {
-    return f32x4{float(v[i][0]), float(v[i][1]), float(v[i][2]), float(v[i][3])};
+    f32x4 x;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) x[r] = 16 * i + r < left ? float(v[i][r]) : 0.f;
+    return x;
   }
 };
 __device__ __forceinline__ f32x4 quad(const float* p, int i) {   // [16 i + 4 h ..]
@@ -664,14 +710,12 @@ __device__ __forceinline__ f32x4 quad(const float* p, int i) {   // [16 i + 4 h 
 // of 64 values a lane (bf16, dk = 128).
 template <typename T, int DK>
 struct StatesLds {
-  static constexpr int kRowStride = 2 * DK + 8, kColStride = 2 * DK + 32, kEStride = 136;
-  static constexpr int kRowPart = kChunk * kRowStride, kColPart = kChunk * kColStride;
-  static constexpr int kCol = kParts<T> * kRowPart, kE = kCol + kParts<T> * kColPart;
+  static constexpr int kE = kParts<T> * kChunk * DK * 2, kEStride = 136;
   static constexpr int kEPart = kChunk * kEStride;
   static constexpr int kFactors = kE + 3 * kEPart;
   static constexpr int kBytes = kFactors + int(sizeof(Factors));
 };
-template <typename T, int DK>
+template <typename T, int DK, bool WHOLE>
 __global__ __launch_bounds__(kDeltaBlock) void k_delta_states(DeltaShape s, DeltaIn<T> in,
                                                               DeltaKept kept,
                                                               const float* __restrict__ s0,
@@ -687,17 +731,19 @@ __global__ __launch_bounds__(kDeltaBlock) void k_delta_states(DeltaShape s, Delt
   const int vh = blockIdx.x / slices % s.hv, seq = blockIdx.x / slices / s.hv;
   const int kh = vh / (s.hv / s.hk);
   const int64_t begin = first_chunk(s, seq), count = first_chunk(s, seq + 1) - begin;
+  const int64_t first = first_token(s, seq), past = first_token(s, seq + 1);
   const int64_t head = int64_t(seq) * s.hv + vh;
   const bool live = c0 < s.dvp;
   f32x4 S[RT];
   load_state<DK>(S, s0, s, head, c0);
-  Rows<T, DK> kr;
+  Rows<T, DK, WHOLE> kr;
   Square er;
   Columns<T> vc;
+  vc.any = in.v;
   double g = 0.0, gend = 0.0;
   float be = 0.f;
   auto fetch = [&](int64_t c) {
-    const Place p = chunk_of(s, seq, c);
+    const Place p = chunk_of(seq, first, past, c);
     const int64_t slot = (begin + c) * s.hv + vh;
     kr.fetch(in.k + p.tok * in.ldk + int64_t(kh) * s.dk, in.ldk, p.len, s.dk);
     er.fetch(kept.E + slot * kChunk * kChunk);
@@ -712,8 +758,7 @@ __global__ __launch_bounds__(kDeltaBlock) void k_delta_states(DeltaShape s, Delt
   for (int64_t c = 0; c < count; ++c) {
     const int64_t slot = (begin + c) * s.hv + vh;
     __syncthreads();  // the last chunk's readers are done
-    kr.put(smem, L::kRowStride);
-    kr.put(smem + L::kCol, L::kColStride);
+    kr.put(smem);
     er.put([&](int row, int col) { return smem + L::kE + row * L::kEStride + col * 2; }, L::kEPart);
     set_factors(f, g, gend, be);
     f32x4 v[4];
@@ -735,8 +780,7 @@ __global__ __launch_bounds__(kDeltaBlock) void k_delta_states(DeltaShape s, Delt
     for (int b = 0; b < KB; ++b)
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        mul(R[i], row_op<NP>(smem + 16 * i * L::kRowStride + 64 * b, L::kRowStride, L::kRowPart),
-            so[b]);
+        mul(R[i], token_rows<NP, DK>(smem, i, b), so[b]);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       R[i] = v[i] - quad(f.in, i) * R[i];
@@ -763,8 +807,7 @@ __global__ __launch_bounds__(kDeltaBlock) void k_delta_states(DeltaShape s, Delt
       S[a] *= all;
 #pragma unroll
       for (int b = 0; b < 2; ++b)
-        mul(S[a], col_op<NP>(smem + L::kCol + 32 * b * L::kColStride + 32 * a, L::kColStride,
-                             L::kColPart), n[b]);
+        mul(S[a], token_cols<NP, DK>(smem, a, b), n[b]);
     }
   }
   if (send && live) store_state<DK>(S, send, s, head, c0);
@@ -872,21 +915,14 @@ __global__ __launch_bounds__(kDeltaBlock) void k_delta_out(DeltaShape s, DeltaIn
 }
 
 // The walk backward: X of every chunk, dv = B X, and the gradient of the
-// state behind it; as the walk forward.  The copy of k as rows is left out
-// where LDS has no place for it (fp32, dk > 64): its reads then meet at the
-// same banks four at a time.
+// state behind it; as the walk forward.
 template <typename T, int DK>
 struct AdjointLds {
-  static constexpr bool kCopy = kParts<T> < 3 || DK == 64;
-  static constexpr int kColStride = 2 * DK + 32, kColPart = kChunk * kColStride;
-  static constexpr int kRowStride = kCopy ? 2 * DK + 8 : kColStride;
-  static constexpr int kRowPart = kChunk * kRowStride;
-  static constexpr int kQ = kParts<T> * kColPart, kE = 2 * kQ, kP = kE + 3 * kTri;
-  static constexpr int kRows = kCopy ? kP + 3 * kTri : 0;
-  static constexpr int kFactors = kP + 3 * kTri + (kCopy ? kParts<T> * kRowPart : 0);
+  static constexpr int kQ = kParts<T> * kChunk * DK * 2, kE = 2 * kQ, kP = kE + 3 * kTri;
+  static constexpr int kFactors = kP + 3 * kTri;
   static constexpr int kBytes = kFactors + int(sizeof(Factors));
 };
-template <typename T, int DK>
+template <typename T, int DK, bool WHOLE>
 __global__ __launch_bounds__(kDeltaBlock) void k_delta_adjoint(
     DeltaShape s, DeltaIn<T> in, DeltaKept kept, const T* __restrict__ dout, int64_t ldo,
     const float* __restrict__ dsend, float* __restrict__ X, float* __restrict__ dS,
@@ -902,17 +938,19 @@ __global__ __launch_bounds__(kDeltaBlock) void k_delta_adjoint(
   const int vh = blockIdx.x / slices % s.hv, seq = blockIdx.x / slices / s.hv;
   const int kh = vh / (s.hv / s.hk);
   const int64_t begin = first_chunk(s, seq), count = first_chunk(s, seq + 1) - begin;
+  const int64_t first = first_token(s, seq), past = first_token(s, seq + 1);
   const int64_t head = int64_t(seq) * s.hv + vh;
   const bool live = c0 < s.dvp;
   f32x4 D[RT];
   load_state<DK>(D, dsend, s, head, c0);
-  Rows<T, DK> kr, qr;
+  Rows<T, DK, WHOLE> kr, qr;
   Square er, pr;
   Columns<T> oc;
+  oc.any = dout;
   double g = 0.0, gend = 0.0;
   float be = 0.f;
   auto fetch = [&](int64_t c) {
-    const Place p = chunk_of(s, seq, c);
+    const Place p = chunk_of(seq, first, past, c);
     const int64_t slot = (begin + c) * s.hv + vh;
     kr.fetch(in.k + p.tok * in.ldk + int64_t(kh) * s.dk, in.ldk, p.len, s.dk);
     qr.fetch(in.q + p.tok * in.ldq + int64_t(kh) * s.dk, in.ldq, p.len, s.dk);
@@ -927,12 +965,11 @@ __global__ __launch_bounds__(kDeltaBlock) void k_delta_adjoint(
   };
   if (count > 0) fetch(count - 1);
   for (int64_t c = count - 1; c >= 0; --c) {
-    const Place p = chunk_of(s, seq, c);
+    const Place p = chunk_of(seq, first, past, c);
     const int64_t slot = (begin + c) * s.hv + vh;
     __syncthreads();
-    kr.put(smem, L::kColStride);
-    qr.put(smem + L::kQ, L::kColStride);
-    if (L::kCopy) kr.put(smem + L::kRows, L::kRowStride);
+    kr.put(smem);
+    qr.put(smem + L::kQ);
     er.put_tri(smem + L::kE);
     pr.put_tri(smem + L::kP);
     set_factors(f, g, gend, be);
@@ -955,8 +992,7 @@ __global__ __launch_bounds__(kDeltaBlock) void k_delta_adjoint(
     for (int b = 0; b < KB; ++b)
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        mul(Y[i], row_op<NP>(smem + L::kRows + 16 * i * L::kRowStride + 64 * b, L::kRowStride,
-                             L::kRowPart), so[b]);
+        mul(Y[i], token_rows<NP, DK>(smem, i, b), so[b]);
     const Op<NP> oo[2] = {operand_of<T>(o[0], o[1]), operand_of<T>(o[2], o[3])};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -995,9 +1031,8 @@ __global__ __launch_bounds__(kDeltaBlock) void k_delta_adjoint(
       D[a] *= all;
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
-        const int at = 32 * b * L::kColStride + 32 * a;
-        mul(D[a], col_op<NP>(smem + at, L::kColStride, L::kColPart), n[b]);
-        mul(D[a], col_op<NP>(smem + L::kQ + at, L::kColStride, L::kColPart), os[b]);
+        mul(D[a], token_cols<NP, DK>(smem, a, b), n[b]);
+        mul(D[a], token_cols<NP, DK>(smem + L::kQ, a, b), os[b]);
       }
     }
   }
@@ -1022,8 +1057,7 @@ struct GradsLds {
   static constexpr int kXStride = 160, kXPart = kSlice * kXStride;
   static constexpr int kX = 3 * kSPart, kN = kX + 3 * kXPart, kFirst = kN + 3 * kXPart;
   // ... then over the chunk's tokens
-  static constexpr int kColStride = 2 * DK + 32, kColPart = kChunk * kColStride;
-  static constexpr int kQ = kParts<T> * kColPart, kdP = 2 * kQ, kdA = kdP + NS * kTri;
+  static constexpr int kQ = kParts<T> * kChunk * DK * 2, kdP = 2 * kQ, kdA = kdP + NS * kTri;
   static constexpr int kSecond = kdA + NS * kTri;
   static constexpr int kFactors = kFirst > kSecond ? kFirst : kSecond;
   struct Tail {
@@ -1033,8 +1067,8 @@ struct GradsLds {
   };
   static constexpr int kBytes = kFactors + int(sizeof(Tail));
 };
-template <typename T, int DK>
-__global__ __launch_bounds__(kDeltaBlock, kParts<T> == 1 ? 2 : 1) void k_delta_grads(
+template <typename T, int DK, bool WHOLE, bool SHARED>
+__global__ __launch_bounds__(kDeltaBlock, kParts<T> == 1 && !SHARED ? 2 : 1) void k_delta_grads(
     DeltaShape s, DeltaIn<T> in, DeltaKept kept, const T* __restrict__ dout, int64_t ldo,
     const float* __restrict__ X, const float* __restrict__ dS, T* __restrict__ dq,
     T* __restrict__ dk, float* __restrict__ dg, float* __restrict__ dbeta) {
@@ -1047,11 +1081,25 @@ __global__ __launch_bounds__(kDeltaBlock, kParts<T> == 1 ? 2 : 1) void k_delta_g
   const int kh = blockIdx.y, group = s.hv / s.hk;
   const int t = threadIdx.x, l = t % 16, h = (t % kWave) / 16;
   const int w = __builtin_amdgcn_readfirstlane(t / kWave);
-  f32x4 aq[NT], ak[NT];  // sums over the group, rows 16 w + 4 h + r, columns 16 n + l
+  // SHARED: sums over the group, rows 16 w + 4 h + r, columns 16 n + l
+  f32x4 aq[SHARED ? NT : 1], ak[SHARED ? NT : 1];
 #pragma unroll
-  for (int n = 0; n < NT; ++n) aq[n] = ak[n] = f32x4{0, 0, 0, 0};
+  for (int n = 0; n < (SHARED ? NT : 1); ++n) aq[n] = ak[n] = f32x4{0, 0, 0, 0};
 
-  for (int vh = kh * group; vh < (kh + 1) * group; ++vh) {
+  auto leave = [&](const f32x4 (&x)[NT], const f32x4 (&y)[NT]) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int row = 16 * w + 4 * h + r, col = 16 * n + l;
+        if (row < p.len && col < s.dk) {
+          const int64_t at = ((p.tok + row) * s.hk + kh) * s.dk + col;
+          if (dq) dq[at] = T(x[n][r]);
+          if (dk) dk[at] = T(y[n][r]);
+        }
+      }
+  };
+  for (int vh = kh * group; vh < (SHARED ? (kh + 1) * group : kh * group + 1); ++vh) {
     const int64_t slot = int64_t(blockIdx.x) * s.hv + vh;
     const float* Sg = kept.S + slot * s.dvp * DK;
     const float* Dg = dS + slot * s.dvp * DK;
@@ -1076,15 +1124,12 @@ __global__ __launch_bounds__(kDeltaBlock, kParts<T> == 1 ? 2 : 1) void k_delta_g
 #pragma unroll
       for (int k = 0; k < 3; ++k) *reinterpret_cast<U2*>(d + k * part) = U2{u[k][0], u[k][1]};
     };
-    for (int c0 = 0; c0 < s.dvp; c0 += kSlice) {
-      f32x4 sv[kLoads], dv[kLoads], xv[2], mv[2];
-      float ov[2][4];
+    f32x4 sv[kLoads], xv[2], mv[2];
+    float ov[2][4];
+    auto fetch = [&](int c0) {
 #pragma unroll
-      for (int i = 0; i < kLoads; ++i) {
-        const int64_t at = int64_t(c0) * DK + (t + i * kDeltaBlock) * 4;
-        sv[i] = *reinterpret_cast<const f32x4*>(Sg + at);
-        dv[i] = *reinterpret_cast<const f32x4*>(Dg + at);
-      }
+      for (int i = 0; i < kLoads; ++i)
+        sv[i] = *reinterpret_cast<const f32x4*>(Sg + int64_t(c0) * DK + (t + i * kDeltaBlock) * 4);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int64_t at = int64_t(c0) * kChunk + t * 8 + 4 * i;
@@ -1092,12 +1137,13 @@ __global__ __launch_bounds__(kDeltaBlock, kParts<T> == 1 ? 2 : 1) void k_delta_g
         mv[i] = *reinterpret_cast<const f32x4*>(Mg + at);
         load_f32<4>(orow + c0 + 16 * i, 16 * w + l < p.len ? s.dv - c0 - 16 * i - 4 * h : 0, ov[i]);
       }
+    };
+    fetch(0);
+    for (int c0 = 0; c0 < s.dvp; c0 += kSlice) {
       __syncthreads();
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
         const int at = (t + i * kDeltaBlock) * 4;
-        sd += sv[i][0] * dv[i][0] + sv[i][1] * dv[i][1] +
-              (sv[i][2] * dv[i][2] + sv[i][3] * dv[i][3]);
         put(sv[i], smem + at / DK * L::kSStride + at % DK * 2, L::kSPart);
       }
 #pragma unroll
@@ -1109,34 +1155,53 @@ __global__ __launch_bounds__(kDeltaBlock, kParts<T> == 1 ? 2 : 1) void k_delta_g
         put(xv[i], d + L::kX, L::kXPart);
         put(mv[i] * *reinterpret_cast<const f32x4*>(z.f.beta + tok), d + L::kN, L::kXPart);
       }
-      __syncthreads();
       const Op<NP> oo = operand_of<T>(f32x4{ov[0][0], ov[0][1], ov[0][2], ov[0][3]},
                                       f32x4{ov[1][0], ov[1][1], ov[1][2], ov[1][3]});
-      const Op<3> xo = col_op<3>(smem + L::kX + 32 * w, L::kXStride, L::kXPart);
-      const Op<3> no = col_op<3>(smem + L::kN + 32 * w, L::kXStride, L::kXPart);
+      __syncthreads();
+      // dS takes S's place next
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (j <= w) {
-          const Op<3> nj = col_op<3>(smem + L::kN + 32 * j, L::kXStride, L::kXPart);
-          mul(pp[j], oo, nj);
-          mul(pa[j], xo, nj);
+      for (int i = 0; i < kLoads; ++i)
+        sv[i] = *reinterpret_cast<const f32x4*>(Dg + int64_t(c0) * DK + (t + i * kDeltaBlock) * 4);
+      {
+        const Op<3> xo = col_op<3>(smem + L::kX + 32 * w, L::kXStride, L::kXPart);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (j <= w) {
+            const Op<3> nj = col_op<3>(smem + L::kN + 32 * j, L::kXStride, L::kXPart);
+            mul(pp[j], oo, nj);
+            mul(pa[j], xo, nj);
+          }
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const Op<3> sn = col_op<3>(smem + 32 * n, L::kSStride, L::kSPart);
+          mul(oS[n], oo, sn);
+          mul(xS[n], xo, sn);
+          if (n % 2) __builtin_amdgcn_sched_barrier(0);   // or all operands are read at once
         }
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const Op<3> sn = col_op<3>(smem + 32 * n, L::kSStride, L::kSPart);
-        mul(oS[n], oo, sn);
-        mul(xS[n], xo, sn);
       }
+      const Op<3> no = col_op<3>(smem + L::kN + 32 * w, L::kXStride, L::kXPart);
       __syncthreads();
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
         const int at = (t + i * kDeltaBlock) * 4;
-        put(dv[i], smem + at / DK * L::kSStride + at % DK * 2, L::kSPart);
+        char* d = smem + at / DK * L::kSStride + at % DK * 2;
+        f32x4 was = {0, 0, 0, 0};   // S there
+#pragma unroll
+        for (int k = 2; k >= 0; --k) {
+          const U2 u = *reinterpret_cast<const U2*>(d + k * L::kSPart);
+          was += f32x4{__uint_as_float(u[0] << 16), __uint_as_float(u[0] & 0xffff0000u),
+                       __uint_as_float(u[1] << 16), __uint_as_float(u[1] & 0xffff0000u)};
+        }
+        sd += was[0] * sv[i][0] + was[1] * sv[i][1] + (was[2] * sv[i][2] + was[3] * sv[i][3]);
+        put(sv[i], d, L::kSPart);
       }
+      if (c0 + kSlice < s.dvp) fetch(c0 + kSlice);
       __syncthreads();
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+      for (int n = 0; n < NT; ++n) {
         mul(nD[n], no, col_op<3>(smem + 32 * n, L::kSStride, L::kSPart));
+        if (n % 2) __builtin_amdgcn_sched_barrier(0);
+      }
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -1151,11 +1216,11 @@ __global__ __launch_bounds__(kDeltaBlock, kParts<T> == 1 ? 2 : 1) void k_delta_g
     if (dbeta && t < p.len)
       dbeta[(p.tok + t) * s.hv + vh] = (z.xm[0][t] + z.xm[1][t]) + (z.xm[2][t] + z.xm[3][t]);
     {
-      Rows<T, DK> kr, qr;
+      Rows<T, DK, WHOLE> kr, qr;
       kr.fetch(in.k + p.tok * in.ldk + int64_t(kh) * s.dk, in.ldk, p.len, s.dk);
       qr.fetch(in.q + p.tok * in.ldq + int64_t(kh) * s.dk, in.ldq, p.len, s.dk);
-      kr.put(smem, L::kColStride);
-      qr.put(smem + L::kQ, L::kColStride);
+      kr.put(smem);
+      qr.put(smem + L::kQ);
     }
     __syncthreads();
     const f32x4 fin = quad(z.f.in, w), fout = quad(z.f.out, w), fbe = quad(z.f.beta, w);
@@ -1168,8 +1233,7 @@ __global__ __launch_bounds__(kDeltaBlock, kParts<T> == 1 ? 2 : 1) void k_delta_g
         f32x4 kk = {0, 0, 0, 0};
 #pragma unroll
         for (int b = 0; b < KB; ++b)
-          mul(kk, row_op<NP>(smem + 16 * w * L::kColStride + 64 * b, L::kColStride, L::kColPart),
-              row_op<NP>(smem + 16 * j * L::kColStride + 64 * b, L::kColStride, L::kColPart));
+          mul(kk, token_rows<NP, DK>(smem, w, b), token_rows<NP, DK>(smem, j, b));
         f32x4 dp, da;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
@@ -1208,11 +1272,12 @@ __global__ __launch_bounds__(kDeltaBlock, kParts<T> == 1 ? 2 : 1) void k_delta_g
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const char* e = smem + (16 * w + 4 * h + r) * L::kColStride + 32 * n + 2 * l;
+        const int row = 16 * w + 4 * h + r, col = 16 * n + l;
+        const char* e = smem + row * DK * 2 + (col / 4 ^ key(row)) * 8 + col % 4 * 2;
         float kv = 0.f, qv = 0.f;
 #pragma unroll
         for (int k = NP - 1; k >= 0; --k) {
-          const char* d = e + k * L::kColPart;
+          const char* d = e + k * kChunk * DK * 2;
           kv += __uint_as_float(uint32_t(*reinterpret_cast<const uint16_t*>(d)) << 16);
           qv += __uint_as_float(uint32_t(*reinterpret_cast<const uint16_t*>(d + L::kQ)) << 16);
         }
@@ -1222,6 +1287,7 @@ __global__ __launch_bounds__(kDeltaBlock, kParts<T> == 1 ? 2 : 1) void k_delta_g
         end += kv * y;
         xS[n][r] = y - u;
       }
+      __builtin_amdgcn_sched_barrier(0);
     }
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
@@ -1229,22 +1295,24 @@ __global__ __launch_bounds__(kDeltaBlock, kParts<T> == 1 ? 2 : 1) void k_delta_g
       const Op<NS> pc = tri_turned<NS>(smem + L::kdP, w, b), ac = tri_turned<NS>(smem + L::kdA, w, b);
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        const int at = 32 * b * L::kColStride + 32 * n;
-        const Op<NP> kn = col_op<NP>(smem + at, L::kColStride, L::kColPart);
-        if (2 * b <= w) {
-          mul(oS[n], pr, kn);
-          mul(xS[n], ar, kn);
-        }
-        if (2 * b + 1 >= w) {
-          mul(xS[n], ac, kn);
-          mul(xS[n], pc, col_op<NP>(smem + L::kQ + at, L::kColStride, L::kColPart));
-        }
+        const Op<NP> kn = token_cols<NP, DK>(smem, n, b);
+        // (the empty blocks' operands are zero: a branch here would have the
+        // compiler move all sums about)
+        mul(oS[n], pr, kn);
+        mul(xS[n], ar, kn);
+        mul(xS[n], ac, kn);
+        mul(xS[n], pc, token_cols<NP, DK>(smem + L::kQ, n, b));
+        if (n % 2) __builtin_amdgcn_sched_barrier(0);
       }
     }
+    if constexpr (SHARED) {
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      aq[n] += oS[n];
-      ak[n] += xS[n];
+      for (int n = 0; n < NT; ++n) {
+        aq[n] += oS[n];
+        ak[n] += xS[n];
+      }
+    } else {
+      leave(oS, xS);
     }
     if (dg) {
 #pragma unroll
@@ -1272,17 +1340,7 @@ __global__ __launch_bounds__(kDeltaBlock, kParts<T> == 1 ? 2 : 1) void k_delta_g
       }
     }
   }
-#pragma unroll
-  for (int n = 0; n < NT; ++n)
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int row = 16 * w + 4 * h + r, col = 16 * n + l;
-      if (row < p.len && col < s.dk) {
-        const int64_t at = ((p.tok + row) * s.hk + kh) * s.dk + col;
-        if (dq) dq[at] = T(aq[n][r]);
-        if (dk) dk[at] = T(ak[n][r]);
-      }
-    }
+  if constexpr (SHARED) leave(aq, ak);
 }
 
 // One token of every sequence, the state updated in place: a workgroup per
@@ -1449,11 +1507,15 @@ sla_status allow_lds(K kernel, int bytes) {
   return SLA_OK;
 }
 
+// f(element, padded dk, whether dk is a multiple of 8).
 template <typename F>
-sla_status with_delta(const sla_delta_dims* d, F&& f) {
+sla_status with_delta(const sla_delta_dims* d, F&& g) {
   using D64 = std::integral_constant<int, 64>;
   using D128 = std::integral_constant<int, 128>;
   const bool small = pad_dk(d->key_dim) == 64;
+  auto f = [&](auto te, auto width) -> sla_status {
+    return d->key_dim % 8 == 0 ? g(te, width, std::true_type()) : g(te, width, std::false_type());
+  };
   if (d->type == SLA_F32) return small ? f(float(), D64()) : f(float(), D128());
   if (d->type == SLA_F16) return small ? f(_Float16(), D64()) : f(_Float16(), D128());
   return small ? f(__bf16(), D64()) : f(__bf16(), D128());
@@ -1506,20 +1568,20 @@ sla_status sla_delta_rule(const sla_delta_dims* dims, const void* q, int64_t ldq
                                                 (int32_t*)s.first, gaps);
     LAUNCH_CHECK();
   }
-  return with_delta(dims, [&](auto te, auto width) -> sla_status {
+  return with_delta(dims, [&](auto te, auto width, auto whole) -> sla_status {
     using T = decltype(te);
     constexpr int DK = width.value;
     const DeltaIn<T> in = {(const T*)q, (const T*)k, (const T*)v, ldq, ldk, ldv, g, beta};
     if (z.chunks) {
       constexpr int lds = PrepareLds<T, DK>::kBytes;
-      SLA_TRY(allow_lds(k_delta_prepare<T, DK>, lds));
-      k_delta_prepare<T, DK><<<dim3(int(z.chunks), s.hv), kDeltaBlock, lds, stream>>>(s, in, w);
+      SLA_TRY(allow_lds(k_delta_prepare<T, DK, whole.value>, lds));
+      k_delta_prepare<T, DK, whole.value><<<dim3(int(z.chunks), s.hv), kDeltaBlock, lds, stream>>>(s, in, w);
       LAUNCH_CHECK();
     }
     {
       constexpr int lds = StatesLds<T, DK>::kBytes;
-      SLA_TRY(allow_lds(k_delta_states<T, DK>, lds));
-      k_delta_states<T, DK><<<s.nseq * s.hv * int(div_up(s.dvp, kWalk)), kDeltaBlock, lds, stream>>>(
+      SLA_TRY(allow_lds(k_delta_states<T, DK, whole.value>, lds));
+      k_delta_states<T, DK, whole.value><<<s.nseq * s.hv * int(div_up(s.dvp, kWalk)), kDeltaBlock, lds, stream>>>(
           s, in, w, initial_state, final_state);
       LAUNCH_CHECK();
     }
@@ -1568,21 +1630,23 @@ sla_status sla_delta_rule_grad(const sla_delta_dims* dims, const void* q, int64_
     k_delta_gaps<<<1, kDeltaBlock, 0, stream>>>(s.tok, s.nseq, s.total, gaps);
     LAUNCH_CHECK();
   }
-  return with_delta(dims, [&](auto te, auto width) -> sla_status {
+  return with_delta(dims, [&](auto te, auto width, auto whole) -> sla_status {
     using T = decltype(te);
     constexpr int DK = width.value;
     const DeltaIn<T> in = {(const T*)q, (const T*)k, (const T*)v, ldq, ldk, ldv, g, beta};
     {
       constexpr int lds = AdjointLds<T, DK>::kBytes;
-      SLA_TRY(allow_lds(k_delta_adjoint<T, DK>, lds));
-      k_delta_adjoint<T, DK><<<s.nseq * s.hv * int(div_up(s.dvp, kWalk)), kDeltaBlock, lds, stream>>>(
+      SLA_TRY(allow_lds(k_delta_adjoint<T, DK, whole.value>, lds));
+      k_delta_adjoint<T, DK, whole.value><<<s.nseq * s.hv * int(div_up(s.dvp, kWalk)), kDeltaBlock, lds, stream>>>(
           s, in, w, (const T*)grad_o, ldo, grad_final_state, X, dS, (T*)dv, grad_initial_state);
       LAUNCH_CHECK();
     }
     if (z.chunks && (dq || dk || dg || dbeta)) {
       constexpr int lds = GradsLds<T, DK>::kBytes;
-      SLA_TRY(allow_lds(k_delta_grads<T, DK>, lds));
-      k_delta_grads<T, DK><<<dim3(int(z.chunks), s.hk), kDeltaBlock, lds, stream>>>(
+      auto* kernel = s.hv > s.hk ? k_delta_grads<T, DK, whole.value, true>
+                                 : k_delta_grads<T, DK, whole.value, false>;
+      SLA_TRY(allow_lds(kernel, lds));
+      kernel<<<dim3(int(z.chunks), s.hk), kDeltaBlock, lds, stream>>>(
           s, in, w, (const T*)grad_o, ldo, X, dS, (T*)dq, (T*)dk, dg, dbeta);
       LAUNCH_CHECK();
     }
@@ -1614,7 +1678,7 @@ sla_status sla_delta_step(const sla_delta_dims* dims, const void* q, int64_t ldq
     LAUNCH_CHECK();
     return SLA_OK;
   };
-  return with_delta(dims, [&](auto te, auto width) {
+  return with_delta(dims, [&](auto te, auto width, auto) {
     return go(te, std::integral_constant<int, width.value / 32>());
   });
 }
