@@ -245,7 +245,22 @@ __device__ __forceinline__ void mul(f32x4& acc, const Op<NA>& a, const Op<NB>& b
         acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.f[i], b.f[s - i], acc, 0, 0, 0);
 }
 
-typedef __attribute__((address_space(3))) void* LdsPtr;
+// The same for N sums with one factor in common, in turns: an instruction on
+// the sum of the one before would wait for it.
+template <int N, int NA, int NB>
+__device__ __forceinline__ void mul_turns(f32x4* acc, const Op<NA> (&a)[N], const Op<NB>& b) {
+  constexpr int kTop = NA + NB - 2 < 2 ? NA + NB - 2 : 2;
+#pragma unroll
+  for (int s = kTop; s >= 0; --s)
+#pragma unroll
+    for (int i = 0; i < NA; ++i)
+      if (s - i >= 0 && s - i < NB) {
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+          acc[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[n].f[i], b.f[s - i], acc[n], 0, 0, 0);
+      }
+}
+
 typedef __bf16 Quad __attribute__((ext_vector_type(4)));
 __device__ __forceinline__ Frag join(const Quad& a, const Quad& b) {
   return Frag{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
@@ -777,10 +792,11 @@ __global__ __launch_bounds__(kDeltaBlock) void k_delta_states(DeltaShape s, Delt
 #pragma unroll
     for (int i = 0; i < 4; ++i) R[i] = f32x4{0, 0, 0, 0};
 #pragma unroll
-    for (int b = 0; b < KB; ++b)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        mul(R[i], token_rows<NP, DK>(smem, i, b), so[b]);
+    for (int b = 0; b < KB; ++b) {
+      const Op<NP> k[4] = {token_rows<NP, DK>(smem, 0, b), token_rows<NP, DK>(smem, 1, b),
+                           token_rows<NP, DK>(smem, 2, b), token_rows<NP, DK>(smem, 3, b)};
+      mul_turns(R, k, so[b]);
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       R[i] = v[i] - quad(f.in, i) * R[i];
@@ -788,14 +804,21 @@ __global__ __launch_bounds__(kDeltaBlock) void k_delta_states(DeltaShape s, Delt
     }
     Op<3> n[2] = {operand<3>(bR[0], bR[1]), operand<3>(bR[2], bR[3])};
     float* Mg = kept.M + (slot * s.dvp + c0 + l) * kChunk + 4 * h;
+    f32x4 x[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = f32x4{0, 0, 0, 0};
+    {
+      auto e = [&](int i, int b) {
+        return row_op<3>(smem + L::kE + 16 * i * L::kEStride + 64 * b, L::kEStride, L::kEPart);
+      };
+      const Op<3> e0[4] = {e(0, 0), e(1, 0), e(2, 0), e(3, 0)};
+      mul_turns(x, e0, n[0]);
+      const Op<3> e1[2] = {e(2, 1), e(3, 1)};
+      mul_turns(x + 2, e1, n[1]);
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      f32x4 x = {0, 0, 0, 0};
-#pragma unroll
-      for (int b = 0; b <= i / 2; ++b)
-        mul(x, row_op<3>(smem + L::kE + 16 * i * L::kEStride + 64 * b, L::kEStride, L::kEPart),
-            n[b]);
-      R[i] -= x;
+      R[i] -= x[i];
       *reinterpret_cast<f32x4*>(Mg + 16 * i) = R[i];
       bR[i] = quad(f.out, i) * (quad(f.beta, i) * R[i]);
     }
@@ -803,11 +826,15 @@ __global__ __launch_bounds__(kDeltaBlock) void k_delta_states(DeltaShape s, Delt
     n[1] = operand<3>(bR[2], bR[3]);
     const float all = f.all;
 #pragma unroll
-    for (int a = 0; a < RT; ++a) {
-      S[a] *= all;
+    for (int a = 0; a < RT; a += 4) {
 #pragma unroll
-      for (int b = 0; b < 2; ++b)
-        mul(S[a], token_cols<NP, DK>(smem, a, b), n[b]);
+      for (int i = 0; i < 4; ++i) S[a + i] *= all;
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const Op<NP> k[4] = {token_cols<NP, DK>(smem, a, b), token_cols<NP, DK>(smem, a + 1, b),
+                             token_cols<NP, DK>(smem, a + 2, b), token_cols<NP, DK>(smem, a + 3, b)};
+        mul_turns(S + a, k, n[b]);
+      }
     }
   }
   if (send && live) store_state<DK>(S, send, s, head, c0);
@@ -989,26 +1016,33 @@ __global__ __launch_bounds__(kDeltaBlock) void k_delta_adjoint(
 #pragma unroll
     for (int i = 0; i < 4; ++i) Y[i] = f32x4{0, 0, 0, 0};
 #pragma unroll
-    for (int b = 0; b < KB; ++b)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        mul(Y[i], token_rows<NP, DK>(smem, i, b), so[b]);
-    const Op<NP> oo[2] = {operand_of<T>(o[0], o[1]), operand_of<T>(o[2], o[3])};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      Y[i] *= quad(f.out, i);
-#pragma unroll
-      for (int b = i / 2; b < 2; ++b) mul(Y[i], tri_turned<3>(smem + L::kP, i, b), oo[b]);
-      bY[i] = quad(f.beta, i) * Y[i];
+    for (int b = 0; b < KB; ++b) {
+      const Op<NP> k[4] = {token_rows<NP, DK>(smem, 0, b), token_rows<NP, DK>(smem, 1, b),
+                           token_rows<NP, DK>(smem, 2, b), token_rows<NP, DK>(smem, 3, b)};
+      mul_turns(Y, k, so[b]);
     }
+    // (the triangle p turned) times (b0, b1)
+    auto turn = [&](f32x4* y, const char* p, const auto& b0, const auto& b1) {
+      const Op<3> p1[4] = {tri_turned<3>(p, 0, 1), tri_turned<3>(p, 1, 1), tri_turned<3>(p, 2, 1),
+                           tri_turned<3>(p, 3, 1)};
+      mul_turns(y, p1, b1);
+      const Op<3> p0[2] = {tri_turned<3>(p, 0, 0), tri_turned<3>(p, 1, 0)};
+      mul_turns(y, p0, b0);
+    };
+#pragma unroll
+    for (int i = 0; i < 4; ++i) Y[i] *= quad(f.out, i);
+    turn(Y, smem + L::kP, operand_of<T>(o[0], o[1]), operand_of<T>(o[2], o[3]));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) bY[i] = quad(f.beta, i) * Y[i];
     Op<3> n[2] = {operand<3>(bY[0], bY[1]), operand<3>(bY[2], bY[3])};
     float* Xg = X + (slot * s.dvp + c0 + l) * kChunk + 4 * h;
+    f32x4 x[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = f32x4{0, 0, 0, 0};
+    turn(x, smem + L::kE, n[0], n[1]);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      f32x4 x = {0, 0, 0, 0};
-#pragma unroll
-      for (int b = i / 2; b < 2; ++b) mul(x, tri_turned<3>(smem + L::kE, i, b), n[b]);
-      Y[i] -= x;
+      Y[i] -= x[i];
       *reinterpret_cast<f32x4*>(Xg + 16 * i) = Y[i];
       bY[i] = quad(f.beta, i) * Y[i];
       if (dv && c0 + l < s.dv) {
@@ -1027,12 +1061,18 @@ __global__ __launch_bounds__(kDeltaBlock) void k_delta_adjoint(
     const Op<3> os[2] = {operand<3>(o[0], o[1]), operand<3>(o[2], o[3])};
     const float all = f.all;
 #pragma unroll
-    for (int a = 0; a < RT; ++a) {
-      D[a] *= all;
+    for (int a = 0; a < RT; a += 4) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) D[a + i] *= all;
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
-        mul(D[a], token_cols<NP, DK>(smem, a, b), n[b]);
-        mul(D[a], token_cols<NP, DK>(smem + L::kQ, a, b), os[b]);
+        auto cols = [&](const char* p, const Op<3>& y) {
+          const Op<NP> k[4] = {token_cols<NP, DK>(p, a, b), token_cols<NP, DK>(p, a + 1, b),
+                               token_cols<NP, DK>(p, a + 2, b), token_cols<NP, DK>(p, a + 3, b)};
+          mul_turns(D + a, k, y);
+        };
+        cols(smem + L::kQ, os[b]);
+        cols(smem, n[b]);
       }
     }
   }
