@@ -381,7 +381,7 @@ struct Rows {
     in = 0;
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
-      const int at = threadIdx.x + i * kDeltaBlock;
+      const int at = threadIdx.x % kDeltaBlock + i * kDeltaBlock;
       const int row = at / (WIDTH / 8), col = at % (WIDTH / 8) * 8;
       const bool on = row < len && col < have;
       in |= uint32_t(on) << i;
@@ -401,7 +401,7 @@ struct Rows {
   __device__ __forceinline__ void put(char* lds) const {
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
-      const int at = threadIdx.x + i * kDeltaBlock;
+      const int at = threadIdx.x % kDeltaBlock + i * kDeltaBlock;
       const int row = at / (WIDTH / 8), unit = at % (WIDTH / 8) * 2;
       uint32_t p[kParts<T>][4];
       split<T>(v[i], p);
@@ -423,13 +423,13 @@ struct Square {
   __device__ __forceinline__ void fetch(const float* p) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      v[i] = *reinterpret_cast<const f32x4*>(p + (threadIdx.x + i * kDeltaBlock) * 4);
+      v[i] = *reinterpret_cast<const f32x4*>(p + (threadIdx.x % kDeltaBlock + i * kDeltaBlock) * 4);
   }
   template <typename F>
   __device__ __forceinline__ void put(F&& at, int part) const {   // at(row, col): where
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int row = (threadIdx.x + i * kDeltaBlock) / 16, col = threadIdx.x % 16 * 4;
+      const int row = (threadIdx.x % kDeltaBlock + i * kDeltaBlock) / 16, col = threadIdx.x % 16 * 4;
       const float x[4] = {v[i][0], v[i][1], v[i][2], v[i][3]};
       uint32_t p[3][2];
       split<3, 4>(x, p);
@@ -641,7 +641,7 @@ struct alignas(16) Factors {
   float all;           // exp(G_L)
 };
 __device__ __forceinline__ void set_factors(Factors& f, double g, double end, float beta) {
-  const int t = threadIdx.x;
+  const int t = threadIdx.x % kDeltaBlock;
   if (t < kChunk) {
     f.beta[t] = beta;
     f.in[t] = expf(float(g));
@@ -717,71 +717,128 @@ __device__ __forceinline__ f32x4 quad(const float* p, int i) {   // [16 i + 4 h 
   return *reinterpret_cast<const f32x4*>(p + 16 * i + 4 * (threadIdx.x % kWave / 16));
 }
 
+// The walks' workgroups: four waves that walk, 16 columns each, and four that
+// bring k, E and the like of the next chunk into LDS, so that neither memory's
+// latency nor the cutting of k and E lies in the chain from chunk to chunk.
+// Two chunks' worth where LDS holds them; else the bringing waves keep the next
+// chunk in registers and store it when the walking ones have read this one's.
+constexpr int kWalkBlock = 2 * kDeltaBlock;
+template <int SLOT>
+constexpr int kWalkDepth = 2 * SLOT <= 160 * 1024 ? 2 : 1;
+// All LDS accesses of the wave are done, then those of the others; loads and
+// stores of memory go on.
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+template <int DEPTH, typename F, typename P>
+__device__ __forceinline__ void bring(int64_t count, F&& fetch, P&& put) {
+  if (count == 0) return;
+  fetch(0);
+  if constexpr (DEPTH == 2) {
+    put(0);
+    if (count > 1) fetch(1);
+    lds_barrier();
+    for (int64_t c = 0; c < count; ++c) {
+      if (c + 1 < count) put(int(c + 1) & 1);
+      if (c + 2 < count) fetch(c + 2);
+      lds_barrier();
+    }
+  } else {
+    for (int64_t c = 0; c < count; ++c) {
+      lds_barrier();
+      put(0);
+      lds_barrier();
+      if (c + 1 < count) fetch(c + 1);
+    }
+  }
+}
+template <int DEPTH, typename F>
+__device__ __forceinline__ void walk(int64_t count, F&& chunk) {   // chunk(c, slot)
+  if (DEPTH == 2 && count > 0) lds_barrier();
+  for (int64_t c = 0; c < count; ++c) {
+    if constexpr (DEPTH == 1) {
+      lds_barrier();
+      lds_barrier();
+    }
+    chunk(c, DEPTH == 2 ? int(c) & 1 : 0);
+    if constexpr (DEPTH == 2) lds_barrier();
+  }
+}
+
 // The states' walk forward: M of every chunk and the state before it.  A
 // workgroup has 64 columns of a sequence and head, a wave 16 of them and all
-// dk rows in registers; k (as rows and turned) and E are shared in LDS.  The
-// next chunk's k, E, v and factors travel while this one is walked.  Bound by
-// the chain of one chunk: 132 matrix instructions of 16 cycles and the cutting
-// of 64 values a lane (bf16, dk = 128).
+// dk rows in registers; k and E are shared in LDS.  Bound by the chain of one
+// chunk: 132 matrix instructions of 16 cycles and the cutting of 64 values a
+// lane (bf16, dk = 128).
 template <typename T, int DK>
 struct StatesLds {
   static constexpr int kE = kParts<T> * kChunk * DK * 2, kEStride = 136;
   static constexpr int kEPart = kChunk * kEStride;
   static constexpr int kFactors = kE + 3 * kEPart;
-  static constexpr int kBytes = kFactors + int(sizeof(Factors));
+  static constexpr int kSlot = kFactors + int(sizeof(Factors));
+  static constexpr int kDepth = kWalkDepth<kSlot>, kBytes = kDepth * kSlot;
 };
 template <typename T, int DK, bool WHOLE>
-__global__ __launch_bounds__(kDeltaBlock) void k_delta_states(DeltaShape s, DeltaIn<T> in,
-                                                              DeltaKept kept,
-                                                              const float* __restrict__ s0,
-                                                              float* __restrict__ send) {
+__global__ __launch_bounds__(kWalkBlock) void k_delta_states(DeltaShape s, DeltaIn<T> in,
+                                                             DeltaKept kept,
+                                                             const float* __restrict__ s0,
+                                                             float* __restrict__ send) {
   using L = StatesLds<T, DK>;
   constexpr int NP = kParts<T>, RT = DK / 16, KB = DK / 32;
-  extern __shared__ __align__(16) char smem[];
-  Factors& f = *(Factors*)(smem + L::kFactors);
+  extern __shared__ __align__(16) char lds[];
   const int slices = int(div_up(s.dvp, kWalk));
-  const int t = threadIdx.x, l = t % 16, h = (t % kWave) / 16;
-  const int w = __builtin_amdgcn_readfirstlane(t / kWave);
-  const int c0 = blockIdx.x % slices * kWalk + 16 * w;
+  const int t = threadIdx.x % kDeltaBlock, l = t % 16, h = (t % kWave) / 16;
+  const int w = __builtin_amdgcn_readfirstlane(int(threadIdx.x) / kWave);
   const int vh = blockIdx.x / slices % s.hv, seq = blockIdx.x / slices / s.hv;
   const int kh = vh / (s.hv / s.hk);
   const int64_t begin = first_chunk(s, seq), count = first_chunk(s, seq + 1) - begin;
   const int64_t first = first_token(s, seq), past = first_token(s, seq + 1);
   const int64_t head = int64_t(seq) * s.hv + vh;
+  if (w >= 4) {
+    Rows<T, DK, WHOLE> kr;
+    Square er;
+    double g = 0.0, gend = 0.0;
+    float be = 0.f;
+    bring<L::kDepth>(count, [&](int64_t c) {
+      const Place p = chunk_of(seq, first, past, c);
+      const int64_t slot = (begin + c) * s.hv + vh;
+      kr.fetch(in.k + p.tok * in.ldk + int64_t(kh) * s.dk, in.ldk, p.len, s.dk);
+      er.fetch(kept.E + slot * kChunk * kChunk);
+      if (t < kChunk) {
+        g = kept.G[slot * kChunk + t];
+        gend = kept.G[slot * kChunk + kChunk - 1];
+        be = t < p.len ? in.beta[(p.tok + t) * s.hv + vh] : 0.f;
+      }
+    }, [&](int n) {
+      char* const d = lds + n * L::kSlot;
+      kr.put(d);
+      er.put([&](int row, int col) { return d + L::kE + row * L::kEStride + col * 2; }, L::kEPart);
+      set_factors(*(Factors*)(d + L::kFactors), g, gend, be);
+    });
+    return;
+  }
+  const int c0 = blockIdx.x % slices * kWalk + 16 * w;
   const bool live = c0 < s.dvp;
   f32x4 S[RT];
   load_state<DK>(S, s0, s, head, c0);
-  Rows<T, DK, WHOLE> kr;
-  Square er;
   Columns<T> vc;
   vc.any = in.v;
-  double g = 0.0, gend = 0.0;
-  float be = 0.f;
-  auto fetch = [&](int64_t c) {
+  auto fetch_v = [&](int64_t c) {
     const Place p = chunk_of(seq, first, past, c);
-    const int64_t slot = (begin + c) * s.hv + vh;
-    kr.fetch(in.k + p.tok * in.ldk + int64_t(kh) * s.dk, in.ldk, p.len, s.dk);
-    er.fetch(kept.E + slot * kChunk * kChunk);
     vc.fetch(in.v + p.tok * in.ldv + int64_t(vh) * s.dv + c0, in.ldv, p.len, s.dv - c0);
-    if (t < kChunk) {
-      g = kept.G[slot * kChunk + t];
-      gend = kept.G[slot * kChunk + kChunk - 1];
-      be = t < p.len ? in.beta[(p.tok + t) * s.hv + vh] : 0.f;
-    }
   };
-  if (count > 0) fetch(0);
-  for (int64_t c = 0; c < count; ++c) {
+  if (count > 0) fetch_v(0);
+  walk<L::kDepth>(count, [&](int64_t c, int n_) {
+    if (!live) return;
+    const char* const smem = lds + n_ * L::kSlot;
+    const Factors& f = *(const Factors*)(smem + L::kFactors);
     const int64_t slot = (begin + c) * s.hv + vh;
-    __syncthreads();  // the last chunk's readers are done
-    kr.put(smem);
-    er.put([&](int row, int col) { return smem + L::kE + row * L::kEStride + col * 2; }, L::kEPart);
-    set_factors(f, g, gend, be);
     f32x4 v[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = vc.tile(i);
-    __syncthreads();
-    if (c + 1 < count) fetch(c + 1);
-    if (!live) continue;
+    if (c + 1 < count) fetch_v(c + 1);
     float* Sg = kept.S + (slot * s.dvp + c0 + l) * DK + 4 * h;
     Op<3> so[KB];
 #pragma unroll
@@ -836,7 +893,7 @@ __global__ __launch_bounds__(kDeltaBlock) void k_delta_states(DeltaShape s, Delt
         mul_turns(S + a, k, n[b]);
       }
     }
-  }
+  });
   if (send && live) store_state<DK>(S, send, s, head, c0);
 }
 
@@ -947,65 +1004,71 @@ template <typename T, int DK>
 struct AdjointLds {
   static constexpr int kQ = kParts<T> * kChunk * DK * 2, kE = 2 * kQ, kP = kE + 3 * kTri;
   static constexpr int kFactors = kP + 3 * kTri;
-  static constexpr int kBytes = kFactors + int(sizeof(Factors));
+  static constexpr int kSlot = kFactors + int(sizeof(Factors));
+  static constexpr int kDepth = kWalkDepth<kSlot>, kBytes = kDepth * kSlot;
 };
 template <typename T, int DK, bool WHOLE>
-__global__ __launch_bounds__(kDeltaBlock) void k_delta_adjoint(
+__global__ __launch_bounds__(kWalkBlock) void k_delta_adjoint(
     DeltaShape s, DeltaIn<T> in, DeltaKept kept, const T* __restrict__ dout, int64_t ldo,
     const float* __restrict__ dsend, float* __restrict__ X, float* __restrict__ dS,
     T* __restrict__ dv, float* __restrict__ ds0) {
   using L = AdjointLds<T, DK>;
   constexpr int NP = kParts<T>, RT = DK / 16, KB = DK / 32;
-  extern __shared__ __align__(16) char smem[];
-  Factors& f = *(Factors*)(smem + L::kFactors);
+  extern __shared__ __align__(16) char lds[];
   const int slices = int(div_up(s.dvp, kWalk));
-  const int t = threadIdx.x, l = t % 16, h = (t % kWave) / 16;
-  const int w = __builtin_amdgcn_readfirstlane(t / kWave);
-  const int c0 = blockIdx.x % slices * kWalk + 16 * w;
+  const int t = threadIdx.x % kDeltaBlock, l = t % 16, h = (t % kWave) / 16;
+  const int w = __builtin_amdgcn_readfirstlane(int(threadIdx.x) / kWave);
   const int vh = blockIdx.x / slices % s.hv, seq = blockIdx.x / slices / s.hv;
   const int kh = vh / (s.hv / s.hk);
   const int64_t begin = first_chunk(s, seq), count = first_chunk(s, seq + 1) - begin;
   const int64_t first = first_token(s, seq), past = first_token(s, seq + 1);
   const int64_t head = int64_t(seq) * s.hv + vh;
+  if (w >= 4) {
+    Rows<T, DK, WHOLE> kr, qr;
+    Square er, pr;
+    double g = 0.0, gend = 0.0;
+    float be = 0.f;
+    bring<L::kDepth>(count, [&](int64_t i) {
+      const int64_t c = count - 1 - i;
+      const Place p = chunk_of(seq, first, past, c);
+      const int64_t slot = (begin + c) * s.hv + vh;
+      kr.fetch(in.k + p.tok * in.ldk + int64_t(kh) * s.dk, in.ldk, p.len, s.dk);
+      qr.fetch(in.q + p.tok * in.ldq + int64_t(kh) * s.dk, in.ldq, p.len, s.dk);
+      er.fetch(kept.E + slot * kChunk * kChunk);
+      pr.fetch(kept.P + slot * kChunk * kChunk);
+      if (t < kChunk) {
+        g = kept.G[slot * kChunk + t];
+        gend = kept.G[slot * kChunk + kChunk - 1];
+        be = t < p.len ? in.beta[(p.tok + t) * s.hv + vh] : 0.f;
+      }
+    }, [&](int n) {
+      char* const d = lds + n * L::kSlot;
+      kr.put(d);
+      qr.put(d + L::kQ);
+      er.put_tri(d + L::kE);
+      pr.put_tri(d + L::kP);
+      set_factors(*(Factors*)(d + L::kFactors), g, gend, be);
+    });
+    return;
+  }
+  const int c0 = blockIdx.x % slices * kWalk + 16 * w;
   const bool live = c0 < s.dvp;
   f32x4 D[RT];
   load_state<DK>(D, dsend, s, head, c0);
-  Rows<T, DK, WHOLE> kr, qr;
-  Square er, pr;
   Columns<T> oc;
   oc.any = dout;
-  double g = 0.0, gend = 0.0;
-  float be = 0.f;
-  auto fetch = [&](int64_t c) {
+  auto fetch_o = [&](int64_t c) {
     const Place p = chunk_of(seq, first, past, c);
-    const int64_t slot = (begin + c) * s.hv + vh;
-    kr.fetch(in.k + p.tok * in.ldk + int64_t(kh) * s.dk, in.ldk, p.len, s.dk);
-    qr.fetch(in.q + p.tok * in.ldq + int64_t(kh) * s.dk, in.ldq, p.len, s.dk);
-    er.fetch(kept.E + slot * kChunk * kChunk);
-    pr.fetch(kept.P + slot * kChunk * kChunk);
     oc.fetch(dout + p.tok * ldo + int64_t(vh) * s.dv + c0, ldo, p.len, s.dv - c0);
-    if (t < kChunk) {
-      g = kept.G[slot * kChunk + t];
-      gend = kept.G[slot * kChunk + kChunk - 1];
-      be = t < p.len ? in.beta[(p.tok + t) * s.hv + vh] : 0.f;
-    }
   };
-  if (count > 0) fetch(count - 1);
-  for (int64_t c = count - 1; c >= 0; --c) {
+  if (count > 0) fetch_o(count - 1);
+  walk<L::kDepth>(count, [&](int64_t i_, int n_) {
+    if (!live) return;
+    const int64_t c = count - 1 - i_;
+    const char* const smem = lds + n_ * L::kSlot;
+    const Factors& f = *(const Factors*)(smem + L::kFactors);
     const Place p = chunk_of(seq, first, past, c);
     const int64_t slot = (begin + c) * s.hv + vh;
-    __syncthreads();
-    kr.put(smem);
-    qr.put(smem + L::kQ);
-    er.put_tri(smem + L::kE);
-    pr.put_tri(smem + L::kP);
-    set_factors(f, g, gend, be);
-    f32x4 o[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] = oc.tile(i);
-    __syncthreads();
-    if (c > 0) fetch(c - 1);
-    if (!live) continue;
     float* Dg = dS + (slot * s.dvp + c0 + l) * DK + 4 * h;
     Op<3> so[KB];
 #pragma unroll
@@ -1021,25 +1084,32 @@ __global__ __launch_bounds__(kDeltaBlock) void k_delta_adjoint(
                            token_rows<NP, DK>(smem, 2, b), token_rows<NP, DK>(smem, 3, b)};
       mul_turns(Y, k, so[b]);
     }
+    __builtin_amdgcn_sched_barrier(0);   // the operands of one step at a time
     // (the triangle p turned) times (b0, b1)
     auto turn = [&](f32x4* y, const char* p, const auto& b0, const auto& b1) {
-      const Op<3> p1[4] = {tri_turned<3>(p, 0, 1), tri_turned<3>(p, 1, 1), tri_turned<3>(p, 2, 1),
-                           tri_turned<3>(p, 3, 1)};
-      mul_turns(y, p1, b1);
+#pragma unroll
+      for (int i = 0; i < 4; i += 2) {
+        const Op<3> p1[2] = {tri_turned<3>(p, i, 1), tri_turned<3>(p, i + 1, 1)};
+        mul_turns(y + i, p1, b1);
+        __builtin_amdgcn_sched_barrier(0);
+      }
       const Op<3> p0[2] = {tri_turned<3>(p, 0, 0), tri_turned<3>(p, 1, 0)};
       mul_turns(y, p0, b0);
     };
 #pragma unroll
     for (int i = 0; i < 4; ++i) Y[i] *= quad(f.out, i);
-    turn(Y, smem + L::kP, operand_of<T>(o[0], o[1]), operand_of<T>(o[2], o[3]));
+    turn(Y, smem + L::kP, operand_of<T>(oc.tile(0), oc.tile(1)),
+         operand_of<T>(oc.tile(2), oc.tile(3)));
 #pragma unroll
     for (int i = 0; i < 4; ++i) bY[i] = quad(f.beta, i) * Y[i];
+    __builtin_amdgcn_sched_barrier(0);
     Op<3> n[2] = {operand<3>(bY[0], bY[1]), operand<3>(bY[2], bY[3])};
     float* Xg = X + (slot * s.dvp + c0 + l) * kChunk + 4 * h;
     f32x4 x[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) x[i] = f32x4{0, 0, 0, 0};
     turn(x, smem + L::kE, n[0], n[1]);
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       Y[i] -= x[i];
@@ -1052,14 +1122,15 @@ __global__ __launch_bounds__(kDeltaBlock) void k_delta_adjoint(
           if (row < p.len) dv[((p.tok + row) * s.hv + vh) * s.dv + c0 + l] = T(bY[i][r]);
         }
       }
-      const f32x4 ein = quad(f.in, i);
-      bY[i] *= -ein;
-      o[i] *= s.scale * ein;
+      bY[i] *= -quad(f.in, i);
     }
     n[0] = operand<3>(bY[0], bY[1]);
     n[1] = operand<3>(bY[2], bY[3]);
-    const Op<3> os[2] = {operand<3>(o[0], o[1]), operand<3>(o[2], o[3])};
+    auto so_of = [&](int i) { return s.scale * quad(f.in, i) * oc.tile(i); };
+    const Op<3> os[2] = {operand<3>(so_of(0), so_of(1)), operand<3>(so_of(2), so_of(3))};
+    if (c > 0) fetch_o(c - 1);
     const float all = f.all;
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int a = 0; a < RT; a += 4) {
 #pragma unroll
@@ -1073,9 +1144,10 @@ __global__ __launch_bounds__(kDeltaBlock) void k_delta_adjoint(
         };
         cols(smem + L::kQ, os[b]);
         cols(smem, n[b]);
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
-  }
+  });
   if (ds0 && live) store_state<DK>(D, ds0, s, head, c0);
 }
 
@@ -1621,7 +1693,7 @@ sla_status sla_delta_rule(const sla_delta_dims* dims, const void* q, int64_t ldq
     {
       constexpr int lds = StatesLds<T, DK>::kBytes;
       SLA_TRY(allow_lds(k_delta_states<T, DK, whole.value>, lds));
-      k_delta_states<T, DK, whole.value><<<s.nseq * s.hv * int(div_up(s.dvp, kWalk)), kDeltaBlock, lds, stream>>>(
+      k_delta_states<T, DK, whole.value><<<s.nseq * s.hv * int(div_up(s.dvp, kWalk)), kWalkBlock, lds, stream>>>(
           s, in, w, initial_state, final_state);
       LAUNCH_CHECK();
     }
@@ -1677,7 +1749,7 @@ sla_status sla_delta_rule_grad(const sla_delta_dims* dims, const void* q, int64_
     {
       constexpr int lds = AdjointLds<T, DK>::kBytes;
       SLA_TRY(allow_lds(k_delta_adjoint<T, DK, whole.value>, lds));
-      k_delta_adjoint<T, DK, whole.value><<<s.nseq * s.hv * int(div_up(s.dvp, kWalk)), kDeltaBlock, lds, stream>>>(
+      k_delta_adjoint<T, DK, whole.value><<<s.nseq * s.hv * int(div_up(s.dvp, kWalk)), kWalkBlock, lds, stream>>>(
           s, in, w, (const T*)grad_o, ldo, grad_final_state, X, dS, (T*)dv, grad_initial_state);
       LAUNCH_CHECK();
     }
