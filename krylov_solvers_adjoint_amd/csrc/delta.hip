@@ -328,14 +328,15 @@ __device__ __forceinline__ Op<PARTS> token_cols(const char* p, int a, int b) {
   return o;
 }
 
-// A lower triangle of 64 x 64 in 16 x 16 blocks: line i has 16 (i / 16 + 1) columns.
+// A lower triangle of 64 x 64 in 16 x 16 blocks: line i has 16 (i / 16 + 1)
+// columns, and the lines are an odd number of 32 bytes apart.
 __device__ __forceinline__ constexpr int tri_stride(int t) {
-  return t == 0 ? 64 : t == 1 ? 96 : 160;
+  return t == 0 ? 32 : t == 3 ? 160 : 96;
 }
 __device__ __forceinline__ constexpr int tri_at(int t) {   // of line 16 t
-  return t == 0 ? 0 : t == 1 ? 1024 : t == 2 ? 2560 : 5120;
+  return t == 0 ? 0 : t == 1 ? 512 : t == 2 ? 2048 : 3584;
 }
-constexpr int kTri = 7680;   // bytes of a part
+constexpr int kTri = 6144;   // bytes of a part
 // Operand with rows j = 16 tj + l and k = i = 32 kb .. (the triangle turned).
 template <int PARTS>
 __device__ __forceinline__ Op<PARTS> tri_turned(const char* p, int tj, int kb) {
@@ -691,25 +692,53 @@ __device__ __forceinline__ void store_state(const f32x4 (&S)[DK / 16], float* p,
       if (row < s.dk && col < s.dv) p[(head * s.dk + row) * s.dv + col] = S[a][r];
     }
 }
-// A wave's 16 columns of a chunk's [token][dv] rows: tokens 16 i + 4 h + r.
+// A chunk's rows of 64 columns of v or do, as they are, in LDS.
 template <typename T>
-struct Columns {
-  T v[4][4];
-  int left;   // rows from this lane's first on that exist; 0 if the column does not
-  __device__ __forceinline__ void fetch(const T* p, int64_t ld, int len, int have) {
-    const int l = threadIdx.x % 16, h = threadIdx.x % kWave / 16;
-    left = l < have ? len - 4 * h : 0;
-    const T* q = p + 4 * h * ld + l;
+struct Values {
+  static constexpr int kBytes = kChunk * kWalk * int(sizeof(T));
+  static constexpr int kLoads = kChunk * kWalk / 8 / kDeltaBlock;
+  Eight<T> v[kLoads];
+  // have: columns from the first on; whole: a multiple of 8 of them
+  __device__ __forceinline__ void fetch(const T* p, int64_t ld, int len, int have, bool whole) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < kLoads; ++i) {
+      const int at = threadIdx.x % kDeltaBlock + i * kDeltaBlock;
+      const int row = at / (kWalk / 8), col = at % (kWalk / 8) * 8;
+      const bool on = row < len && col < have;
+      if (whole) {
+        const Eight<T> x = *reinterpret_cast<const Eight<T>*>(p + (on ? row * ld + col : 0));
 #pragma unroll
-      for (int r = 0; r < 4; ++r) v[i][r] = *(16 * i + r < left ? q + (16 * i + r) * ld : any);
+        for (int j = 0; j < 8; ++j) v[i][j] = on ? x[j] : T(0.f);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const bool here = on && col + j < have;
+          const T x = p[here ? row * ld + col + j : 0];
+          v[i][j] = here ? x : T(0.f);
+        }
+      }
+    }
   }
-  const T* any;   // an element that exists
-  __device__ __forceinline__ f32x4 tile(int i) const {
-    f32x4 x;
+  __device__ __forceinline__ void put(char* lds) const {
 #pragma unroll
-    for (int r = 0; r < 4; ++r) x[r] = 16 * i + r < left ? float(v[i][r]) : 0.f;
+    for (int i = 0; i < kLoads; ++i)
+      *reinterpret_cast<Eight<T>*>(lds + (threadIdx.x % kDeltaBlock + i * kDeltaBlock) * 8 *
+                                             int(sizeof(T))) = v[i];
+  }
+  // tokens 16 i + 4 h + r of columns col + l
+  static __device__ __forceinline__ f32x4 tile(const char* lds, int col, int i) {
+    const int l = threadIdx.x % 16, h = threadIdx.x % kWave / 16;
+    f32x4 x;
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        x[r] = *reinterpret_cast<const T*>(lds + ((16 * i + 4 * h + r) * kWalk + col + l) * 4);
+    } else {
+      typedef T V4 __attribute__((ext_vector_type(4)));
+      const V4 v = __builtin_bit_cast(V4, turned(lds + 16 * i * kWalk * 2 + col * 2, kWalk * 2));
+#pragma unroll
+      for (int r = 0; r < 4; ++r) x[r] = float(v[r]);
+    }
     return x;
   }
 };
@@ -767,6 +796,31 @@ __device__ __forceinline__ void walk(int64_t count, F&& chunk) {   // chunk(c, s
   }
 }
 
+// N products whose operands come from LDS, each read while the one before is
+// multiplied: first holds those of product 0; behind the last, next() may
+// read ahead.  (The fences keep the reads where they are; left alone the
+// compiler puts each in front of its use and the wave waits for it.)
+template <int N, typename O, typename L, typename U, typename X>
+__device__ __forceinline__ void pipe(O (&first), L&& load, U&& use, X&& next) {
+  O o[2];
+  o[0] = first;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    if (i + 1 < N) o[(i + 1) % 2] = load(i + 1);
+    else next();
+    __builtin_amdgcn_sched_barrier(0);
+    use(i, o[i % 2]);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+}
+template <int PARTS, int N>
+struct Ops {
+  Op<PARTS> o[N];
+};
+// The tiles a step of a product with the tokens' rows takes.
+template <typename T>
+constexpr int kTilesAStep = kParts<T> == 1 ? 4 : 2;
+
 // The states' walk forward: M of every chunk and the state before it.  A
 // workgroup has 64 columns of a sequence and head, a wave 16 of them and all
 // dk rows in registers; k and E are shared in LDS.  Bound by the chain of one
@@ -776,7 +830,7 @@ template <typename T, int DK>
 struct StatesLds {
   static constexpr int kE = kParts<T> * kChunk * DK * 2, kEStride = 136;
   static constexpr int kEPart = kChunk * kEStride;
-  static constexpr int kFactors = kE + 3 * kEPart;
+  static constexpr int kV = kE + 3 * kEPart, kFactors = kV + Values<T>::kBytes;
   static constexpr int kSlot = kFactors + int(sizeof(Factors));
   static constexpr int kDepth = kWalkDepth<kSlot>, kBytes = kDepth * kSlot;
 };
@@ -796,9 +850,12 @@ __global__ __launch_bounds__(kWalkBlock) void k_delta_states(DeltaShape s, Delta
   const int64_t begin = first_chunk(s, seq), count = first_chunk(s, seq + 1) - begin;
   const int64_t first = first_token(s, seq), past = first_token(s, seq + 1);
   const int64_t head = int64_t(seq) * s.hv + vh;
+  const int c0 = blockIdx.x % slices * kWalk + 16 * (w % 4);
   if (w >= 4) {
     Rows<T, DK, WHOLE> kr;
     Square er;
+    Values<T> vr;
+    const int col = blockIdx.x % slices * kWalk;
     double g = 0.0, gend = 0.0;
     float be = 0.f;
     bring<L::kDepth>(count, [&](int64_t c) {
@@ -806,6 +863,8 @@ __global__ __launch_bounds__(kWalkBlock) void k_delta_states(DeltaShape s, Delta
       const int64_t slot = (begin + c) * s.hv + vh;
       kr.fetch(in.k + p.tok * in.ldk + int64_t(kh) * s.dk, in.ldk, p.len, s.dk);
       er.fetch(kept.E + slot * kChunk * kChunk);
+      vr.fetch(in.v + p.tok * in.ldv + int64_t(vh) * s.dv + col, in.ldv, p.len, s.dv - col,
+               s.dv % 8 == 0);
       if (t < kChunk) {
         g = kept.G[slot * kChunk + t];
         gend = kept.G[slot * kChunk + kChunk - 1];
@@ -815,48 +874,57 @@ __global__ __launch_bounds__(kWalkBlock) void k_delta_states(DeltaShape s, Delta
       char* const d = lds + n * L::kSlot;
       kr.put(d);
       er.put([&](int row, int col) { return d + L::kE + row * L::kEStride + col * 2; }, L::kEPart);
+      vr.put(d + L::kV);
       set_factors(*(Factors*)(d + L::kFactors), g, gend, be);
     });
     return;
   }
-  const int c0 = blockIdx.x % slices * kWalk + 16 * w;
   const bool live = c0 < s.dvp;
   f32x4 S[RT];
   load_state<DK>(S, s0, s, head, c0);
-  Columns<T> vc;
-  vc.any = in.v;
-  auto fetch_v = [&](int64_t c) {
-    const Place p = chunk_of(seq, first, past, c);
-    vc.fetch(in.v + p.tok * in.ldv + int64_t(vh) * s.dv + c0, in.ldv, p.len, s.dv - c0);
-  };
-  if (count > 0) fetch_v(0);
   walk<L::kDepth>(count, [&](int64_t c, int n_) {
     if (!live) return;
     const char* const smem = lds + n_ * L::kSlot;
     const Factors& f = *(const Factors*)(smem + L::kFactors);
     const int64_t slot = (begin + c) * s.hv + vh;
-    f32x4 v[4];
+    constexpr int GT = kTilesAStep<T>, kSide = 4 / GT;
+    typedef Ops<NP, GT> Tokens;
+    auto rows = [&](int i) {   // step i of k S
+      Tokens o;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = vc.tile(i);
-    if (c + 1 < count) fetch_v(c + 1);
+      for (int n = 0; n < GT; ++n) o.o[n] = token_rows<NP, DK>(smem, i % kSide * GT + n, i / kSide);
+      return o;
+    };
+    auto cols = [&](int i) {   // step i of k^T N
+      Tokens o;
+#pragma unroll
+      for (int n = 0; n < GT; ++n) o.o[n] = token_cols<NP, DK>(smem, i / 2 * GT + n, i % 2);
+      return o;
+    };
+    auto tri = [&](int i) {    // rows 0 and 1, 2 and 3 of E's first half, 2 and 3 of its second
+      Ops<3, 2> o;
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+        o.o[n] = row_op<3>(smem + L::kE + 16 * ((i ? 2 : 0) + n) * L::kEStride + i / 2 * 64,
+                           L::kEStride, L::kEPart);
+      return o;
+    };
     float* Sg = kept.S + (slot * s.dvp + c0 + l) * DK + 4 * h;
-    Op<3> so[KB];
+    Tokens k0 = rows(0);
+    Op<3> so;
 #pragma unroll
     for (int a = 0; a < RT; ++a) *reinterpret_cast<f32x4*>(Sg + 16 * a) = S[a];
-#pragma unroll
-    for (int b = 0; b < KB; ++b) so[b] = operand<3>(S[2 * b], S[2 * b + 1]);
     f32x4 R[4], bR[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) R[i] = f32x4{0, 0, 0, 0};
-#pragma unroll
-    for (int b = 0; b < KB; ++b) {
-      const Op<NP> k[4] = {token_rows<NP, DK>(smem, 0, b), token_rows<NP, DK>(smem, 1, b),
-                           token_rows<NP, DK>(smem, 2, b), token_rows<NP, DK>(smem, 3, b)};
-      mul_turns(R, k, so[b]);
-    }
+    Ops<3, 2> e0;
+    pipe<KB * kSide>(k0, rows, [&](int i, const Tokens& o) {
+      if (i % kSide == 0) so = operand<3>(S[2 * (i / kSide)], S[2 * (i / kSide) + 1]);
+      mul_turns(R + i % kSide * GT, o.o, so);
+    }, [&] { e0 = tri(0); });
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      R[i] = v[i] - quad(f.in, i) * R[i];
+      R[i] = Values<T>::tile(smem + L::kV, 16 * w, i) - quad(f.in, i) * R[i];
       bR[i] = quad(f.beta, i) * R[i];
     }
     Op<3> n[2] = {operand<3>(bR[0], bR[1]), operand<3>(bR[2], bR[3])};
@@ -864,15 +932,9 @@ __global__ __launch_bounds__(kWalkBlock) void k_delta_states(DeltaShape s, Delta
     f32x4 x[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) x[i] = f32x4{0, 0, 0, 0};
-    {
-      auto e = [&](int i, int b) {
-        return row_op<3>(smem + L::kE + 16 * i * L::kEStride + 64 * b, L::kEStride, L::kEPart);
-      };
-      const Op<3> e0[4] = {e(0, 0), e(1, 0), e(2, 0), e(3, 0)};
-      mul_turns(x, e0, n[0]);
-      const Op<3> e1[2] = {e(2, 1), e(3, 1)};
-      mul_turns(x + 2, e1, n[1]);
-    }
+    pipe<3>(e0, tri, [&](int i, const Ops<3, 2>& o) {
+      mul_turns(x + (i ? 2 : 0), o.o, n[i / 2]);
+    }, [&] { k0 = cols(0); });
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       R[i] -= x[i];
@@ -883,16 +945,10 @@ __global__ __launch_bounds__(kWalkBlock) void k_delta_states(DeltaShape s, Delta
     n[1] = operand<3>(bR[2], bR[3]);
     const float all = f.all;
 #pragma unroll
-    for (int a = 0; a < RT; a += 4) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) S[a + i] *= all;
-#pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        const Op<NP> k[4] = {token_cols<NP, DK>(smem, a, b), token_cols<NP, DK>(smem, a + 1, b),
-                             token_cols<NP, DK>(smem, a + 2, b), token_cols<NP, DK>(smem, a + 3, b)};
-        mul_turns(S + a, k, n[b]);
-      }
-    }
+    for (int a = 0; a < RT; ++a) S[a] *= all;
+    pipe<RT / GT * 2>(k0, cols, [&](int i, const Tokens& o) {
+      mul_turns(S + i / 2 * GT, o.o, n[i % 2]);
+    }, [] {});
   });
   if (send && live) store_state<DK>(S, send, s, head, c0);
 }
@@ -1003,7 +1059,7 @@ __global__ __launch_bounds__(kDeltaBlock) void k_delta_out(DeltaShape s, DeltaIn
 template <typename T, int DK>
 struct AdjointLds {
   static constexpr int kQ = kParts<T> * kChunk * DK * 2, kE = 2 * kQ, kP = kE + 3 * kTri;
-  static constexpr int kFactors = kP + 3 * kTri;
+  static constexpr int kO = kP + 3 * kTri, kFactors = kO + Values<T>::kBytes;
   static constexpr int kSlot = kFactors + int(sizeof(Factors));
   static constexpr int kDepth = kWalkDepth<kSlot>, kBytes = kDepth * kSlot;
 };
@@ -1023,9 +1079,12 @@ __global__ __launch_bounds__(kWalkBlock) void k_delta_adjoint(
   const int64_t begin = first_chunk(s, seq), count = first_chunk(s, seq + 1) - begin;
   const int64_t first = first_token(s, seq), past = first_token(s, seq + 1);
   const int64_t head = int64_t(seq) * s.hv + vh;
+  const int c0 = blockIdx.x % slices * kWalk + 16 * (w % 4);
   if (w >= 4) {
     Rows<T, DK, WHOLE> kr, qr;
     Square er, pr;
+    Values<T> orow;
+    const int col = blockIdx.x % slices * kWalk;
     double g = 0.0, gend = 0.0;
     float be = 0.f;
     bring<L::kDepth>(count, [&](int64_t i) {
@@ -1036,6 +1095,8 @@ __global__ __launch_bounds__(kWalkBlock) void k_delta_adjoint(
       qr.fetch(in.q + p.tok * in.ldq + int64_t(kh) * s.dk, in.ldq, p.len, s.dk);
       er.fetch(kept.E + slot * kChunk * kChunk);
       pr.fetch(kept.P + slot * kChunk * kChunk);
+      orow.fetch(dout + p.tok * ldo + int64_t(vh) * s.dv + col, ldo, p.len, s.dv - col,
+                 s.dv % 8 == 0);
       if (t < kChunk) {
         g = kept.G[slot * kChunk + t];
         gend = kept.G[slot * kChunk + kChunk - 1];
@@ -1047,21 +1108,14 @@ __global__ __launch_bounds__(kWalkBlock) void k_delta_adjoint(
       qr.put(d + L::kQ);
       er.put_tri(d + L::kE);
       pr.put_tri(d + L::kP);
+      orow.put(d + L::kO);
       set_factors(*(Factors*)(d + L::kFactors), g, gend, be);
     });
     return;
   }
-  const int c0 = blockIdx.x % slices * kWalk + 16 * w;
   const bool live = c0 < s.dvp;
   f32x4 D[RT];
   load_state<DK>(D, dsend, s, head, c0);
-  Columns<T> oc;
-  oc.any = dout;
-  auto fetch_o = [&](int64_t c) {
-    const Place p = chunk_of(seq, first, past, c);
-    oc.fetch(dout + p.tok * ldo + int64_t(vh) * s.dv + c0, ldo, p.len, s.dv - c0);
-  };
-  if (count > 0) fetch_o(count - 1);
   walk<L::kDepth>(count, [&](int64_t i_, int n_) {
     if (!live) return;
     const int64_t c = count - 1 - i_;
@@ -1069,47 +1123,73 @@ __global__ __launch_bounds__(kWalkBlock) void k_delta_adjoint(
     const Factors& f = *(const Factors*)(smem + L::kFactors);
     const Place p = chunk_of(seq, first, past, c);
     const int64_t slot = (begin + c) * s.hv + vh;
+    constexpr int GT = kTilesAStep<T>, kSide = 4 / GT;
+    typedef Ops<NP, GT> Tokens;
+    auto rows = [&](int i) {   // step i of k dS
+      Tokens o;
+#pragma unroll
+      for (int n = 0; n < GT; ++n) o.o[n] = token_rows<NP, DK>(smem, i % kSide * GT + n, i / kSide);
+      return o;
+    };
+    auto cols = [&](const char* p, int i) {
+      Tokens o;
+#pragma unroll
+      for (int n = 0; n < GT; ++n) o.o[n] = token_cols<NP, DK>(p, i / 2 * GT + n, i % 2);
+      return o;
+    };
+    auto q_cols = [&](int i) { return cols(smem + L::kQ, i); };   // step i of q^T do
+    auto k_cols = [&](int i) { return cols(smem, i); };           // step i of k^T (B X)
+    // rows 0 and 1, 2 and 3 of a turned triangle's second half, 0 and 1 of its first
+    auto tri_step = [&](const char* p, int i) {
+      Ops<3, 2> o;
+#pragma unroll
+      for (int n = 0; n < 2; ++n) o.o[n] = tri_turned<3>(p, (i == 1 ? 2 : 0) + n, i < 2);
+      return o;
+    };
+    auto tri_p = [&](int i) { return tri_step(smem + L::kP, i); };
+    auto tri_e = [&](int i) { return tri_step(smem + L::kE, i); };
     float* Dg = dS + (slot * s.dvp + c0 + l) * DK + 4 * h;
-    Op<3> so[KB];
+    Tokens k0 = rows(0);
+    Op<3> so;
 #pragma unroll
     for (int a = 0; a < RT; ++a) *reinterpret_cast<f32x4*>(Dg + 16 * a) = D[a];
-#pragma unroll
-    for (int b = 0; b < KB; ++b) so[b] = operand<3>(D[2 * b], D[2 * b + 1]);
     f32x4 Y[4], bY[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) Y[i] = f32x4{0, 0, 0, 0};
-#pragma unroll
-    for (int b = 0; b < KB; ++b) {
-      const Op<NP> k[4] = {token_rows<NP, DK>(smem, 0, b), token_rows<NP, DK>(smem, 1, b),
-                           token_rows<NP, DK>(smem, 2, b), token_rows<NP, DK>(smem, 3, b)};
-      mul_turns(Y, k, so[b]);
-    }
-    __builtin_amdgcn_sched_barrier(0);   // the operands of one step at a time
-    // (the triangle p turned) times (b0, b1)
-    auto turn = [&](f32x4* y, const char* p, const auto& b0, const auto& b1) {
-#pragma unroll
-      for (int i = 0; i < 4; i += 2) {
-        const Op<3> p1[2] = {tri_turned<3>(p, i, 1), tri_turned<3>(p, i + 1, 1)};
-        mul_turns(y + i, p1, b1);
-        __builtin_amdgcn_sched_barrier(0);
-      }
-      const Op<3> p0[2] = {tri_turned<3>(p, 0, 0), tri_turned<3>(p, 1, 0)};
-      mul_turns(y, p0, b0);
-    };
+    Ops<3, 2> t0;
+    pipe<KB * kSide>(k0, rows, [&](int i, const Tokens& o) {
+      if (i % kSide == 0) so = operand<3>(D[2 * (i / kSide)], D[2 * (i / kSide) + 1]);
+      mul_turns(Y + i % kSide * GT, o.o, so);
+    }, [&] { t0 = tri_p(0); });
+    auto out_grad = [&](int i) { return Values<T>::tile(smem + L::kO, 16 * w, i); };
+    const Op<NP> oo[2] = {operand_of<T>(out_grad(0), out_grad(1)),
+                          operand_of<T>(out_grad(2), out_grad(3))};
 #pragma unroll
     for (int i = 0; i < 4; ++i) Y[i] *= quad(f.out, i);
-    turn(Y, smem + L::kP, operand_of<T>(oc.tile(0), oc.tile(1)),
-         operand_of<T>(oc.tile(2), oc.tile(3)));
+    pipe<3>(t0, tri_p, [&](int i, const Ops<3, 2>& o) {
+      mul_turns(Y + (i == 1 ? 2 : 0), o.o, oo[i < 2]);
+    }, [&] { k0 = q_cols(0); });
+    {
+      auto read_o = [&](int i) { return s.scale * quad(f.in, i) * out_grad(i); };
+      const Op<3> os[2] = {operand<3>(read_o(0), read_o(1)), operand<3>(read_o(2), read_o(3))};
+      const float all = f.all;
+#pragma unroll
+      for (int a = 0; a < RT; ++a) D[a] *= all;
+      pipe<RT / GT * 2>(k0, q_cols, [&](int i, const Tokens& o) {
+        mul_turns(D + i / 2 * GT, o.o, os[i % 2]);
+      }, [&] { t0 = tri_e(0); });
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i) bY[i] = quad(f.beta, i) * Y[i];
-    __builtin_amdgcn_sched_barrier(0);
     Op<3> n[2] = {operand<3>(bY[0], bY[1]), operand<3>(bY[2], bY[3])};
     float* Xg = X + (slot * s.dvp + c0 + l) * kChunk + 4 * h;
+    T* const dvp = dv + ((p.tok + 4 * h) * s.hv + vh) * s.dv + c0 + l;
     f32x4 x[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) x[i] = f32x4{0, 0, 0, 0};
-    turn(x, smem + L::kE, n[0], n[1]);
-    __builtin_amdgcn_sched_barrier(0);
+    pipe<3>(t0, tri_e, [&](int i, const Ops<3, 2>& o) {
+      mul_turns(x + (i == 1 ? 2 : 0), o.o, n[i < 2]);
+    }, [&] { k0 = k_cols(0); });
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       Y[i] -= x[i];
@@ -1117,36 +1197,17 @@ __global__ __launch_bounds__(kWalkBlock) void k_delta_adjoint(
       bY[i] = quad(f.beta, i) * Y[i];
       if (dv && c0 + l < s.dv) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int row = 16 * i + 4 * h + r;
-          if (row < p.len) dv[((p.tok + row) * s.hv + vh) * s.dv + c0 + l] = T(bY[i][r]);
-        }
+        for (int r = 0; r < 4; ++r)
+          if (p.len == kChunk || 16 * i + 4 * h + r < p.len)
+            dvp[int64_t(16 * i + r) * s.hv * s.dv] = T(bY[i][r]);
       }
       bY[i] *= -quad(f.in, i);
     }
     n[0] = operand<3>(bY[0], bY[1]);
     n[1] = operand<3>(bY[2], bY[3]);
-    auto so_of = [&](int i) { return s.scale * quad(f.in, i) * oc.tile(i); };
-    const Op<3> os[2] = {operand<3>(so_of(0), so_of(1)), operand<3>(so_of(2), so_of(3))};
-    if (c > 0) fetch_o(c - 1);
-    const float all = f.all;
-    __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-    for (int a = 0; a < RT; a += 4) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) D[a + i] *= all;
-#pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        auto cols = [&](const char* p, const Op<3>& y) {
-          const Op<NP> k[4] = {token_cols<NP, DK>(p, a, b), token_cols<NP, DK>(p, a + 1, b),
-                               token_cols<NP, DK>(p, a + 2, b), token_cols<NP, DK>(p, a + 3, b)};
-          mul_turns(D + a, k, y);
-        };
-        cols(smem + L::kQ, os[b]);
-        cols(smem, n[b]);
-        __builtin_amdgcn_sched_barrier(0);
-      }
-    }
+    pipe<RT / GT * 2>(k0, k_cols, [&](int i, const Tokens& o) {
+      mul_turns(D + i / 2 * GT, o.o, n[i % 2]);
+    }, [] {});
   });
   if (ds0 && live) store_state<DK>(D, ds0, s, head, c0);
 }
