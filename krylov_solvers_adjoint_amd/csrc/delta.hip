@@ -93,8 +93,11 @@ struct DeltaKept {
   double* G;   // [64] running sums of g
   float* E;    // [64][64]
   float* P;    // [64][64]
-  float* M;    // [dvp][64], transposed: a lane of the walk has four tokens of a column
-  float* S;    // [dvp][dk padded] the state before the chunk, transposed
+  // As the walk's waves hold them, so that a store is 1 KB in one piece: for
+  // every 16 columns and every 16 rows (tokens; rows of the state) 64 lanes by
+  // 4, lane (l, h) rows 4 h .. 4 h + 3 of column l.
+  float* M;    // [dvp / 16][4][64][4]
+  float* S;    // [dvp / 16][dk padded / 16][64][4] the state before the chunk
 };
 
 struct Place {
@@ -909,11 +912,11 @@ __global__ __launch_bounds__(kWalkBlock) void k_delta_states(DeltaShape s, Delta
                            L::kEStride, L::kEPart);
       return o;
     };
-    float* Sg = kept.S + (slot * s.dvp + c0 + l) * DK + 4 * h;
+    float* Sg = kept.S + (slot * s.dvp + c0) * DK + t % kWave * 4;
     Tokens k0 = rows(0);
     Op<3> so;
 #pragma unroll
-    for (int a = 0; a < RT; ++a) *reinterpret_cast<f32x4*>(Sg + 16 * a) = S[a];
+    for (int a = 0; a < RT; ++a) *reinterpret_cast<f32x4*>(Sg + 256 * a) = S[a];
     f32x4 R[4], bR[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) R[i] = f32x4{0, 0, 0, 0};
@@ -928,7 +931,7 @@ __global__ __launch_bounds__(kWalkBlock) void k_delta_states(DeltaShape s, Delta
       bR[i] = quad(f.beta, i) * R[i];
     }
     Op<3> n[2] = {operand<3>(bR[0], bR[1]), operand<3>(bR[2], bR[3])};
-    float* Mg = kept.M + (slot * s.dvp + c0 + l) * kChunk + 4 * h;
+    float* Mg = kept.M + (slot * s.dvp + c0) * kChunk + t % kWave * 4;
     f32x4 x[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) x[i] = f32x4{0, 0, 0, 0};
@@ -938,7 +941,7 @@ __global__ __launch_bounds__(kWalkBlock) void k_delta_states(DeltaShape s, Delta
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       R[i] -= x[i];
-      *reinterpret_cast<f32x4*>(Mg + 16 * i) = R[i];
+      *reinterpret_cast<f32x4*>(Mg + 256 * i) = R[i];
       bR[i] = quad(f.out, i) * (quad(f.beta, i) * R[i]);
     }
     n[0] = operand<3>(bR[0], bR[1]);
@@ -968,7 +971,7 @@ template <typename T, int DK>
 __global__ __launch_bounds__(kDeltaBlock) void k_delta_out(DeltaShape s, DeltaIn<T> in,
                                                            DeltaKept kept, T* __restrict__ o) {
   using L = OutLds<T, DK>;
-  constexpr int NP = kParts<T>, NS = L::NS, KB = DK / 32;
+  constexpr int NP = kParts<T>, NS = L::NS, KB = DK / 32, NT = DK / 16;
   extern __shared__ __align__(16) char smem[];
   Factors& f = *(Factors*)(smem + L::kFactors);
   Place p;
@@ -1022,15 +1025,13 @@ __global__ __launch_bounds__(kDeltaBlock) void k_delta_out(DeltaShape s, DeltaIn
     };
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
-      const int at = (t + i * kDeltaBlock) * 4;
-      put(sv[i], smem + at / DK * L::kSStride + at % DK * 2, L::kSPart);
+      const int n = 4 * i + w;   // of the slice's blocks of 16 columns by 16 rows
+      put(sv[i], smem + (n / NT * 16 + l) * L::kSStride + (n % NT * 16 + 4 * h) * 2, L::kSPart);
     }
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int at = (t + i * kDeltaBlock) * 4;
-      put(mv[i] * *reinterpret_cast<const f32x4*>(f.beta + at % kChunk),
-          smem + L::kN + at / kChunk * L::kNStride + at % kChunk * 2, L::kNPart);
-    }
+    for (int i = 0; i < 2; ++i)
+      put(mv[i] * quad(f.beta, w),
+          smem + L::kN + (16 * i + l) * L::kNStride + (16 * w + 4 * h) * 2, L::kNPart);
     __syncthreads();
     if (c0 + kSlice < s.dvp) fetch(c0 + kSlice);
 #pragma unroll
@@ -1148,11 +1149,11 @@ __global__ __launch_bounds__(kWalkBlock) void k_delta_adjoint(
     };
     auto tri_p = [&](int i) { return tri_step(smem + L::kP, i); };
     auto tri_e = [&](int i) { return tri_step(smem + L::kE, i); };
-    float* Dg = dS + (slot * s.dvp + c0 + l) * DK + 4 * h;
+    float* Dg = dS + (slot * s.dvp + c0) * DK + t % kWave * 4;
     Tokens k0 = rows(0);
     Op<3> so;
 #pragma unroll
-    for (int a = 0; a < RT; ++a) *reinterpret_cast<f32x4*>(Dg + 16 * a) = D[a];
+    for (int a = 0; a < RT; ++a) *reinterpret_cast<f32x4*>(Dg + 256 * a) = D[a];
     f32x4 Y[4], bY[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) Y[i] = f32x4{0, 0, 0, 0};
@@ -1182,7 +1183,7 @@ __global__ __launch_bounds__(kWalkBlock) void k_delta_adjoint(
 #pragma unroll
     for (int i = 0; i < 4; ++i) bY[i] = quad(f.beta, i) * Y[i];
     Op<3> n[2] = {operand<3>(bY[0], bY[1]), operand<3>(bY[2], bY[3])};
-    float* Xg = X + (slot * s.dvp + c0 + l) * kChunk + 4 * h;
+    float* Xg = X + (slot * s.dvp + c0) * kChunk + t % kWave * 4;
     T* const dvp = dv + ((p.tok + 4 * h) * s.hv + vh) * s.dv + c0 + l;
     f32x4 x[4];
 #pragma unroll
@@ -1193,7 +1194,7 @@ __global__ __launch_bounds__(kWalkBlock) void k_delta_adjoint(
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       Y[i] -= x[i];
-      *reinterpret_cast<f32x4*>(Xg + 16 * i) = Y[i];
+      *reinterpret_cast<f32x4*>(Xg + 256 * i) = Y[i];
       bY[i] = quad(f.beta, i) * Y[i];
       if (dv && c0 + l < s.dv) {
 #pragma unroll
@@ -1236,7 +1237,7 @@ struct GradsLds {
   struct Tail {
     Factors f;
     double G[kChunk], dG[kChunk];
-    float xm[4][kChunk], cols[4][kChunk], part[8];
+    float cols[4][kChunk], part[8];
   };
   static constexpr int kBytes = kFactors + int(sizeof(Tail));
 };
@@ -1287,7 +1288,7 @@ __global__ __launch_bounds__(kDeltaBlock, kParts<T> == 1 && !SHARED ? 2 : 1) voi
 #pragma unroll
     for (int n = 0; n < NT; ++n) oS[n] = xS[n] = nD[n] = f32x4{0, 0, 0, 0};
     float sd = 0.f;                          // <S, dS> of this thread's elements
-    float xm[8] = {0, 0, 0, 0, 0, 0, 0, 0};  // X . M of tokens 8 (t % 8) ..
+    f32x4 xm = {0, 0, 0, 0};                 // X . M of tokens 16 w + 4 h .., this lane's columns
     constexpr int kLoads = kSlice * DK / 4 / kDeltaBlock;
     const T* orow = dout + (p.tok + 16 * w + l) * ldo + int64_t(vh) * s.dv + 4 * h;
     auto put = [&](const f32x4& x, char* d, int part) {
@@ -1305,28 +1306,30 @@ __global__ __launch_bounds__(kDeltaBlock, kParts<T> == 1 && !SHARED ? 2 : 1) voi
         sv[i] = *reinterpret_cast<const f32x4*>(Sg + int64_t(c0) * DK + (t + i * kDeltaBlock) * 4);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int64_t at = int64_t(c0) * kChunk + t * 8 + 4 * i;
+        const int64_t at = int64_t(c0) * kChunk + (t + i * kDeltaBlock) * 4;
         xv[i] = *reinterpret_cast<const f32x4*>(Xg + at);
         mv[i] = *reinterpret_cast<const f32x4*>(Mg + at);
         load_f32<4>(orow + c0 + 16 * i, 16 * w + l < p.len ? s.dv - c0 - 16 * i - 4 * h : 0, ov[i]);
       }
+    };
+    // this thread's load i of a slice: a quad of column l of one of its blocks
+    auto state_at = [&](int i) {
+      const int n = 4 * i + w;
+      return (n / NT * 16 + l) * L::kSStride + (n % NT * 16 + 4 * h) * 2;
     };
     fetch(0);
     for (int c0 = 0; c0 < s.dvp; c0 += kSlice) {
       __syncthreads();
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
-        const int at = (t + i * kDeltaBlock) * 4;
-        put(sv[i], smem + at / DK * L::kSStride + at % DK * 2, L::kSPart);
+        put(sv[i], smem + state_at(i), L::kSPart);
       }
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int tok = t % 8 * 8 + 4 * i;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) xm[4 * i + r] += xv[i][r] * mv[i][r];
-        char* d = smem + t / 8 * L::kXStride + tok * 2;
+        xm += xv[i] * mv[i];
+        char* d = smem + (16 * i + l) * L::kXStride + (16 * w + 4 * h) * 2;
         put(xv[i], d + L::kX, L::kXPart);
-        put(mv[i] * *reinterpret_cast<const f32x4*>(z.f.beta + tok), d + L::kN, L::kXPart);
+        put(mv[i] * quad(z.f.beta, w), d + L::kN, L::kXPart);
       }
       const Op<NP> oo = operand_of<T>(f32x4{ov[0][0], ov[0][1], ov[0][2], ov[0][3]},
                                       f32x4{ov[1][0], ov[1][1], ov[1][2], ov[1][3]});
@@ -1356,8 +1359,7 @@ __global__ __launch_bounds__(kDeltaBlock, kParts<T> == 1 && !SHARED ? 2 : 1) voi
       __syncthreads();
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
-        const int at = (t + i * kDeltaBlock) * 4;
-        char* d = smem + at / DK * L::kSStride + at % DK * 2;
+        char* d = smem + state_at(i);
         f32x4 was = {0, 0, 0, 0};   // S there
 #pragma unroll
         for (int k = 2; k >= 0; --k) {
@@ -1377,17 +1379,14 @@ __global__ __launch_bounds__(kDeltaBlock, kParts<T> == 1 && !SHARED ? 2 : 1) voi
       }
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      xm[i] += __shfl_xor(xm[i], 8, kWave);
-      xm[i] += __shfl_xor(xm[i], 16, kWave);
-      xm[i] += __shfl_xor(xm[i], 32, kWave);
-      if (t % kWave < 8) z.xm[w][t % 8 * 8 + i] = xm[i];
+    for (int r = 0; r < 4; ++r) {
+      const float x = lane_sum<16>(xm[r]);
+      const int row = 16 * w + 4 * h + r;
+      if (dbeta && l == 0 && row < p.len) dbeta[(p.tok + row) * s.hv + vh] = x;
     }
     sd = lane_sum<kWave>(sd);
     if (t % kWave == 0) z.part[w] = sd;
     __syncthreads();
-    if (dbeta && t < p.len)
-      dbeta[(p.tok + t) * s.hv + vh] = (z.xm[0][t] + z.xm[1][t]) + (z.xm[2][t] + z.xm[3][t]);
     {
       Rows<T, DK, WHOLE> kr, qr;
       kr.fetch(in.k + p.tok * in.ldk + int64_t(kh) * s.dk, in.ldk, p.len, s.dk);
