@@ -108,6 +108,22 @@ __device__ __forceinline__ void mma16(f32x4& acc, Unit<float>::Vec a, Unit<float
   for (int j = 0; j < 4; ++j) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(b[j], a[j], acc, 0, 0, 0);
 }
 
+// A row of sums; fp32's four instructions a factor in turns over the sums: one
+// on the sum of the one before would wait for it.
+template <int NJ, typename V>
+__device__ __forceinline__ void mma_row(f32x4 (&acc)[NJ], const V& a, const V (&b)[NJ]) {
+  if constexpr (sizeof(a[0]) == 4) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+        acc[j] = __builtin_amdgcn_mfma_f32_16x16x4f32(b[j][k], a[k], acc[j], 0, 0, 0);
+  } else {
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) mma16(acc[j], a, b[j]);
+  }
+}
+
 typedef __attribute__((address_space(3))) void* LdsPtr;
 typedef __fp16 HalfQuad __attribute__((__vector_size__(8)));
 
@@ -139,7 +155,7 @@ struct Tile {
   static constexpr int kLineSlots = TRANS ? W / kN : STEP / 16;
   static constexpr int kLoads = W * STEP / 16 / THREADS;   // slots a thread fills
   static constexpr int kSteps = STEP / int(sizeof(T));
-  static constexpr int kThreads = THREADS;
+  static constexpr int kThreads = THREADS, kRows = W;
   static constexpr bool kTrans = TRANS;
   typedef T Element;
   typedef typename Unit<T>::Vec Vec;
@@ -206,10 +222,11 @@ struct Tile {
 };
 
 // Where a step's operand lies: its first element, the elements from one line
-// to the next, and how many rows and k there are from it on.
+// to the next, how many rows and k there are from it on, and the length of a
+// whole line.
 struct Source {
   const char* p;
-  int64_t ld, rows, ks;
+  int64_t ld, rows, ks, line;
 };
 
 // Memory to LDS without a register in between, for operands whose lines are
@@ -266,26 +283,67 @@ __device__ __forceinline__ void stage(char* lds, const char* p, int at, int i, i
   send(p, (TI::kTrans ? line : along) < ks ? at : kOutside, lds + TI::place(i, wave));
 }
 
-// ... and by way of registers, for any shape and alignment.
+// ... and by way of registers, for any shape and alignment.  No lane branches
+// (the join of one would wait for its load): a unit that passes the end of its
+// line is read from further in front, a line that does not exist is another
+// one, and mend() puts that right when the loads have come.
 template <typename TI, int FROM, int COUNT>
 __device__ __forceinline__ void fetch(typename TI::Vec* v, const Source& s) {
   typedef typename TI::Element T;
+  const int64_t length = TI::kTrans ? s.rows : s.ks, lines = TI::kTrans ? s.ks : s.rows;
+  const bool units = s.line >= TI::kN;
 #pragma unroll
   for (int i = FROM; i < FROM + COUNT; ++i) {
     int line, along;
     TI::source(i, line, along);
     if (!TI::kTrans) line -= FROM * TI::kThreads / TI::kLineSlots;
-    const int64_t have =
-        line < (TI::kTrans ? s.ks : s.rows) ? (TI::kTrans ? s.rows : s.ks) - along : 0;
-    const T* q = (const T*)s.p + line * s.ld + along;
-    if (have >= TI::kN) {
-      const auto u = *reinterpret_cast<const typename Unit<T>::Loose*>(q);
+    const T* q = (const T*)s.p + (line < lines ? line : lines - 1) * s.ld;
+    if (units) {
+      const int64_t last = length - TI::kN;
+      const auto u = *reinterpret_cast<const typename Unit<T>::Loose*>(
+          q + (along < last ? int64_t(along) : last));
 #pragma unroll
       for (int j = 0; j < TI::kN; ++j) v[i][j] = u[j];
     } else {
 #pragma unroll
-      for (int j = 0; j < TI::kN; ++j) v[i][j] = j < have ? q[j] : T(0.f);
+      for (int j = 0; j < TI::kN; ++j) {
+        const T x = q[along + j < length ? along + j : 0];
+        v[i][j] = along + j < length ? x : T(0.f);
+      }
     }
+  }
+}
+// What fetch() read in place of what does not exist becomes zero; for a step
+// that lies inside its operand nothing is to be done.  Rows that do not exist
+// may hold anything: nobody stores what is made of them.
+template <typename TI, int FROM, int COUNT>
+__device__ __forceinline__ void mend(typename TI::Vec* v, const Source& s) {
+  typedef uint32_t Words __attribute__((ext_vector_type(4)));
+  const int64_t length = TI::kTrans ? s.rows : s.ks;
+  constexpr int64_t kWhole = TI::kTrans ? int64_t(TI::kRows) : int64_t(TI::kSteps);
+  if (length >= kWhole && s.ks >= TI::kSteps) return;
+  const int over = int((TI::kN - length % TI::kN) % TI::kN);   // elements a cut unit was moved by
+  const bool units = s.line >= TI::kN;
+#pragma unroll
+  for (int i = FROM; i < FROM + COUNT; ++i) {
+    int line, along;
+    TI::source(i, line, along);
+    Words w = __builtin_bit_cast(Words, v[i]);
+    if (units) {
+      // down by `over` elements
+      constexpr int kWord = 4 / int(sizeof(typename TI::Element));
+      Words m = w;
+      if (over / kWord & 1) m = Words{m[1], m[2], m[3], 0};
+      if (over / kWord & 2) m = Words{m[2], m[3], 0, 0};
+      if (over % kWord)
+        m = Words{m[0] >> 16 | m[1] << 16, m[1] >> 16 | m[2] << 16, m[2] >> 16 | m[3] << 16,
+                  m[3] >> 16};
+      const bool cut = along < length && along + TI::kN > length, past = along >= length;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[j] = past ? 0u : cut ? m[j] : w[j];
+    }
+    if (TI::kTrans && line >= s.ks) w = Words{0, 0, 0, 0};
+    v[i] = __builtin_bit_cast(typename TI::Vec, w);
   }
 }
 
@@ -387,14 +445,14 @@ __global__ __launch_bounds__(kWave* B* B / WM / WN, 2) void k_ffn_product(Produc
     const int64_t k0 = int64_t(it - seg * steps) * TA::kSteps;
     const T* p = (const T*)(kGate || !(seg + at.z) ? g.A[0] : g.A[1]) +
                  (AT ? k0 * g.lda + m0 : m0 * g.lda + k0);
-    return Source{(const char*)p, g.lda, g.M - m0, g.K - k0};
+    return Source{(const char*)p, g.lda, g.M - m0, g.K - k0, AT ? g.M : g.K};
   };
   auto source_b = [&](int it, int which) {
     const int seg = it >= steps;
     const int64_t k0 = int64_t(it - seg * steps) * TB::kSteps;
     const T* p = (const T*)((kGate ? which : seg) ? g.B[1] : g.B[0]) +
                  (BT ? k0 * g.ldb + n0 : n0 * g.ldb + k0);
-    return Source{(const char*)p, g.ldb, g.N - n0, g.K - k0};
+    return Source{(const char*)p, g.ldb, g.N - n0, g.K - k0, BT ? g.N : g.K};
   };
   // the wave's rows of the B tile: column tile j
   auto brow = [&](int j) {
@@ -446,8 +504,15 @@ __global__ __launch_bounds__(kWave* B* B / WM / WN, 2) void k_ffn_product(Produc
       fetch<TB, 0, TB::kLoads>(rb, source_b(it, 0));
     }
   };
-  auto put = [&](char* lds) {
+  auto put = [&](char* lds, int it) {
     if constexpr (!DIRECT) {
+      mend<TA, 0, TA::kLoads>(ra, source_a(it));
+      if constexpr (kGate) {
+        mend<TB, 0, HB>(rb, source_b(it, 0));
+        mend<TB, HB, HB>(rb, source_b(it, 1));
+      } else {
+        mend<TB, 0, TB::kLoads>(rb, source_b(it, 0));
+      }
 #pragma unroll
       for (int i = 0; i < TA::kLoads; ++i)
         *reinterpret_cast<Vec*>(lds + TA::place(i)) = ra[i];
@@ -474,10 +539,10 @@ __global__ __launch_bounds__(kWave* B* B / WM / WN, 2) void k_ffn_product(Produc
       landed<(kDepth - 1) * kSends>();
     } else {
       load(from);
-      put(place(0));
+      put(place(0), from);
       if (from + 1 < to) {
         load(from + 1);
-        put(place(1));
+        put(place(1), from + 1);
       }
       load(from + 2);
       __syncthreads();
@@ -504,7 +569,7 @@ __global__ __launch_bounds__(kWave* B* B / WM / WN, 2) void k_ffn_product(Produc
           } else {
             __syncthreads();
             if (it + 2 < to) {
-              put(cur);
+              put(cur, it + 2);
               load(it + 3);
             }
           }
@@ -528,9 +593,7 @@ __global__ __launch_bounds__(kWave* B* B / WM / WN, 2) void k_ffn_product(Produc
               if (n / kEach == r - kTurn) send_one(cur, n);
           }
         }
-#pragma unroll
-        for (int j = 0; j < NJ; ++j)
-          mma16(acc[r % NI][j], fa[r % NI], fb[kRows == NI ? kFlip : r / NI][j]);
+        mma_row(acc[r % NI], fa[r % NI], fb[kRows == NI ? kFlip : r / NI]);
         __builtin_amdgcn_sched_barrier(0);
       }
     };
