@@ -777,18 +777,27 @@ __global__ __launch_bounds__(kFfnBlock) void k_ffn_few(Product g) {
 // Host side
 // ---------------------------------------------------------------------------
 
-// Tiles and splits of a product: the pair with the least estimated time.
+// Tiles and splits of a product: the pair with the least estimated time.  With
+// n workgroups on a CU, at most `slots` of them at once, a step of 128 bytes of
+// k takes wait (per round of slots) + n share, as measured from n = 1 to 6:
+//   fp32     64: 0.93, 1.37, 1.89, 2.37, 3.07, 3.57 us   128: 2.53, 4.19, -, 8.44
+//   16 bit   64: 0.60, 0.66, 0.78, 0.94, 1.32, 1.47 us   128: 1.07, 1.31, 2.20, 2.53
+//           256: 1.54, 3.00, 4.63, 6.01 us
+// so the large tile wins as soon as it fills the card, the small one where
+// there is little to do; a split costs the writing and reading of its sums.
 struct ProductPlan {
   int tile, splits;
 };
 ProductPlan plan_product(int64_t M, int64_t N, int64_t K, int parts, int outputs, bool gate,
                          int es, bool direct) {
   struct Kind {
-    int tile, slots;       // side; workgroups a CU holds
-    double step, start;    // us of 128 bytes of k with every slot taken; us before and after the steps
+    int tile, slots;
+    double wait, share, start;   // us; start: before and behind the steps
   };
-  static const Kind kind16[] = {{256, 1, 1.10, 6.0}, {128, 2, 0.75, 4.0}, {64, 4, 0.55, 3.0}};
-  static const Kind kind32[] = {{256, 1, 0, 0}, {128, 2, 3.6, 5.0}, {64, 4, 2.0, 4.0}};
+  static const Kind kind16[] = {{256, 1, 0.0, 1.5, 8.0}, {128, 2, 0.83, 0.24, 5.5},
+                                {64, 4, 0.48, 0.115, 4.0}};
+  static const Kind kind32[] = {{256, 1, 0, 0, 0}, {128, 2, 0.87, 1.66, 5.0},
+                                {64, 4, 0.42, 0.5, 5.0}};
   const Kind* kinds = es == 4 ? kind32 : kind16;
   const int64_t steps = div_up(K, 128 / es) * parts, cus = device_cus();
   ProductPlan best{64, 1};
@@ -797,9 +806,11 @@ ProductPlan plan_product(int64_t M, int64_t N, int64_t K, int parts, int outputs
     const Kind& k = kinds[i];
     const int64_t tiles = div_up(M, k.tile) * div_up(N, gate ? k.tile / 2 : k.tile) * outputs;
     for (int s = 1; s <= (gate ? 1 : 32) && s <= (steps + 3) / 4; ++s) {
-      const double rounds = double(div_up(tiles * s, cus * k.slots));
-      double time = rounds * (double(div_up(steps, s)) * k.step + k.start);
-      if (s > 1) time += 4.0 + double(s + 1) * double(M * N * outputs) * 4 / 4e6;
+      const int64_t n = div_up(tiles * s, cus);
+      const double rounds = double(div_up(n, k.slots));
+      double time = double(div_up(steps, s)) * (rounds * k.wait + double(n) * k.share) +
+                    rounds * k.start;
+      if (s > 1) time += 5.0 + double(s + 1) * double(M * N * outputs) * 4 / 4e6;
       if (time < least) least = time, best = {k.tile, s};
     }
   }
