@@ -18,12 +18,13 @@ and states in float32.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import _I64, _check, _lib, _stream
+from . import _I64, _check, _lib
 
 F32, F16, BF16 = 0, 1, 2
 _TYPES = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
@@ -43,14 +44,30 @@ def _tensor(t, name: str, like: torch.Tensor | None = None, dtypes=None) -> torc
     if not t.is_cuda:
         raise ValueError(f"{name}: expected a GPU tensor (the library has no CPU path)")
     if like is None:
-        if t.device.index != torch.cuda.current_device():
+        if t.get_device() != torch._C._cuda_getDevice():
             raise ValueError(f"{name}: is on {t.device}, which is not the current device")
-    elif t.device != like.device:
+    elif t.get_device() != like.get_device():
         raise ValueError(f"{name}: is on {t.device}, the other tensors on {like.device}")
     if t.dtype not in (dtypes or _TYPES):
         raise TypeError(f"{name}: expected {' or '.join(str(d) for d in dtypes or _TYPES)}, "
                         f"got {t.dtype}")
     return t
+
+
+def _stream(stream, like: torch.Tensor) -> int:
+    """The raw stream: `stream`, or the current one of like's device.  (The
+    stream object of torch.cuda costs as much as a launch.)"""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(like.get_device())
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+@functools.lru_cache(maxsize=1024)
+def _work_bytes(entry: str, *args) -> int:
+    """What a workspace call says; the sizes alone decide it."""
+    n = _I64()
+    _check(getattr(_lib, entry)(*args, ctypes.byref(n)))
+    return n.value
 
 
 def _sized(t: torch.Tensor, shape: tuple, name: str):
@@ -92,7 +109,11 @@ def _ptr(t):
 
 
 def _wants(*tensors) -> bool:
-    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
+    if torch.is_grad_enabled():
+        for t in tensors:
+            if t is not None and t.requires_grad:
+                return True
+    return False
 
 
 def _block(nbytes: int, like: torch.Tensor) -> torch.Tensor:
@@ -113,7 +134,7 @@ def sla_layer_norm(x, weight, bias, eps: float, want_stats: bool = False, stream
     par = weight if weight is not None else bias
     _check(_lib.sla_layer_norm(x.data_ptr(), ld, rows, cols, _TYPES[x.dtype], _ptr(weight),
                                _ptr(bias), _TYPES[par.dtype if par is not None else x.dtype],
-                               eps, y.data_ptr(), _ptr(stats), _stream(stream)))
+                               eps, y.data_ptr(), _ptr(stats), _stream(stream, x)))
     return y, stats
 
 
@@ -130,14 +151,12 @@ def sla_layer_norm_grad(dy, x, weight, stats, want_x=True, want_weight=True, wan
     db = torch.empty(cols, dtype=wtype, device=x.device) if want_bias else None
     work, size = None, 0
     if want_weight or want_bias:
-        n = _I64()
-        _check(_lib.sla_layer_norm_work(rows, cols, _TYPES[x.dtype], ctypes.byref(n)))
-        size = n.value
+        size = _work_bytes("sla_layer_norm_work", rows, cols, _TYPES[x.dtype])
         work = _block(size, x)
     _check(_lib.sla_layer_norm_grad(dy.data_ptr(), lddy, x.data_ptr(), ldx, rows, cols,
                                     _TYPES[x.dtype], _ptr(weight), _TYPES[wtype],
                                     stats.data_ptr(), _ptr(dx), _ptr(dw), _ptr(db), _ptr(work),
-                                    size, _stream(stream)))
+                                    size, _stream(stream, x)))
     return dx, dw, db
 
 
@@ -194,7 +213,7 @@ def sla_gated_ffn(x, w_gate, w_up, act: int, stream=None):
     h = torch.empty((*x.shape[:-1], outer), dtype=x.dtype, device=x.device)
     _check(_lib.sla_gated_ffn(x.data_ptr(), ld, w_gate.data_ptr(), w_up.data_ptr(),
                               x.numel() // inner, inner, outer, _TYPES[x.dtype], act,
-                              h.data_ptr(), _stream(stream)))
+                              h.data_ptr(), _stream(stream, x)))
     return h
 
 
@@ -207,13 +226,12 @@ def sla_gated_ffn_grad(dh, x, w_gate, w_up, act: int, want_x=True, want_w=True, 
     dx = torch.empty(x.shape, dtype=x.dtype, device=x.device) if want_x else None
     dwg = torch.empty_like(w_gate) if want_w else None
     dwu = torch.empty_like(w_up) if want_w else None
-    n = _I64()
-    _check(_lib.sla_gated_ffn_work(rows, inner, outer, _TYPES[x.dtype], ctypes.byref(n)))
-    work = _block(n.value, x)
+    size = _work_bytes("sla_gated_ffn_work", rows, inner, outer, _TYPES[x.dtype])
+    work = _block(size, x)
     _check(_lib.sla_gated_ffn_grad(dh.data_ptr(), lddh, x.data_ptr(), ldx, w_gate.data_ptr(),
                                    w_up.data_ptr(), rows, inner, outer, _TYPES[x.dtype], act,
-                                   _ptr(dx), _ptr(dwg), _ptr(dwu), work.data_ptr(), n.value,
-                                   _stream(stream)))
+                                   _ptr(dx), _ptr(dwg), _ptr(dwu), work.data_ptr(), size,
+                                   _stream(stream, x)))
     return dx, dwg, dwu
 
 
@@ -261,12 +279,21 @@ def gated_ffn(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor,
 # ---------------------------------------------------------------------------
 # The gated delta rule
 # ---------------------------------------------------------------------------
+@functools.lru_cache(maxsize=1024)
+def _dims(*args):
+    """(the C structure, its address, the bytes that sla_delta_rule_work says)"""
+    d = _DeltaDims(*args)
+    kept, grad = _I64(), _I64()
+    _check(_lib.sla_delta_rule_work(ctypes.byref(d), ctypes.byref(kept), ctypes.byref(grad)))
+    return d, ctypes.byref(d), kept.value, grad.value
+
+
 def _delta_dims(q, v, sequences, scale, packed):
     tokens = 1
     for n in q.shape[:-2]:
         tokens *= n
-    return _DeltaDims(sequences, tokens, q.shape[-2], v.shape[-2], q.shape[-1], v.shape[-1],
-                      scale, _TYPES[q.dtype], int(packed))
+    return _dims(sequences, tokens, q.shape[-2], v.shape[-2], q.shape[-1], v.shape[-1],
+                 scale, _TYPES[q.dtype], int(packed))
 
 
 def _states(dims, like):
@@ -277,37 +304,33 @@ def _states(dims, like):
 def sla_delta_rule(q, k, v, g, beta, offsets, initial_state, sequences: int, scale: float,
                    want_state: bool = True, stream=None):
     """(o, final_state or None, kept): kept is what the gradient reads."""
-    dims = _delta_dims(q, v, sequences, scale, offsets is not None)
+    dims, at, size, _ = _delta_dims(q, v, sequences, scale, offsets is not None)
     (q, ldq), (k, ldk), (v, ldv) = _rows(q, 2), _rows(k, 2), _rows(v, 2)
-    n = _I64()
-    _check(_lib.sla_delta_rule_work(ctypes.byref(dims), ctypes.byref(n), None))
-    kept = _block(n.value, q)
+    kept = _block(size, q)
     o = torch.empty(v.shape, dtype=v.dtype, device=v.device)
     state = _states(dims, q) if want_state else None
-    _check(_lib.sla_delta_rule(ctypes.byref(dims), q.data_ptr(), ldq, k.data_ptr(), ldk,
+    _check(_lib.sla_delta_rule(at, q.data_ptr(), ldq, k.data_ptr(), ldk,
                                v.data_ptr(), ldv, g.data_ptr(), beta.data_ptr(), _ptr(offsets),
                                _ptr(initial_state), o.data_ptr(), _ptr(state), kept.data_ptr(),
-                               n.value, _stream(stream)))
+                               size, _stream(stream, q)))
     return o, state, kept
 
 
 def sla_delta_rule_grad(q, k, v, g, beta, kept, grad_o, grad_state, sequences: int, scale: float,
                         packed: bool, want_initial: bool = True, stream=None):
     """(dq, dk, dv, dg, dbeta, grad of the initial state or None)."""
-    dims = _delta_dims(q, v, sequences, scale, packed)
+    dims, at, _, size = _delta_dims(q, v, sequences, scale, packed)
     (q, ldq), (k, ldk), (v, ldv) = _rows(q, 2), _rows(k, 2), _rows(v, 2)
     grad_o, ldo = _rows(grad_o, 2)
-    n = _I64()
-    _check(_lib.sla_delta_rule_work(ctypes.byref(dims), None, ctypes.byref(n)))
-    work = _block(n.value, q)
+    work = _block(size, q)
     dq, dk, dv, dg, dbeta = (torch.empty(t.shape, dtype=t.dtype, device=t.device)
                              for t in (q, k, v, g, beta))
     ds0 = _states(dims, q) if want_initial else None
     _check(_lib.sla_delta_rule_grad(
-        ctypes.byref(dims), q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv, g.data_ptr(),
+        at, q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv, g.data_ptr(),
         beta.data_ptr(), kept.data_ptr(), kept.numel(), grad_o.data_ptr(), ldo, _ptr(grad_state),
         dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), dg.data_ptr(), dbeta.data_ptr(), _ptr(ds0),
-        work.data_ptr(), n.value, _stream(stream)))
+        work.data_ptr(), size, _stream(stream, q)))
     return dq, dk, dv, dg, dbeta, ds0
 
 
@@ -414,12 +437,12 @@ def gated_delta_rule(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch
 
 def sla_delta_step(q, k, v, g, beta, state, scale: float, stream=None):
     """o [sequences, value_heads, dv]; state is updated in place."""
-    dims = _delta_dims(q, v, q.shape[0], scale, False)
+    at = _delta_dims(q, v, q.shape[0], scale, False)[1]
     (q, ldq), (k, ldk), (v, ldv) = _rows(q, 2), _rows(k, 2), _rows(v, 2)
     o = torch.empty(v.shape, dtype=v.dtype, device=v.device)
-    _check(_lib.sla_delta_step(ctypes.byref(dims), q.data_ptr(), ldq, k.data_ptr(), ldk,
+    _check(_lib.sla_delta_step(at, q.data_ptr(), ldq, k.data_ptr(), ldk,
                                v.data_ptr(), ldv, g.data_ptr(), beta.data_ptr(),
-                               state.data_ptr(), o.data_ptr(), _stream(stream)))
+                               state.data_ptr(), o.data_ptr(), _stream(stream, q)))
     return o
 
 
