@@ -331,6 +331,21 @@ __device__ __forceinline__ Op<PARTS> token_cols(const char* p, int a, int b) {
   return o;
 }
 
+// ... as they are: columns 16 a + l of the tokens 16 i + 4 h + r.
+template <int PARTS, int DK>
+__device__ __forceinline__ f32x4 token_tile(const char* p, int a, int i) {
+  const int l = threadIdx.x % 16, h = threadIdx.x % kWave / 16;
+  const int line = 4 * h + (l >> 2);
+  f32x4 x = {0, 0, 0, 0};
+#pragma unroll
+  for (int k = PARTS - 1; k >= 0; --k) {
+    const Quad v = turned(p + k * kChunk * DK * 2 + (16 * i + line) * DK * 2 +
+                          ((4 * a + (l & 3)) ^ key(line)) * 8);
+    x += f32x4{float(v[0]), float(v[1]), float(v[2]), float(v[3])};
+  }
+  return x;
+}
+
 // A lower triangle of 64 x 64 in 16 x 16 blocks: line i has 16 (i / 16 + 1)
 // columns, and the lines are an odd number of 32 bytes apart.
 __device__ __forceinline__ constexpr int tri_stride(int t) {
@@ -354,17 +369,37 @@ __device__ __forceinline__ Op<PARTS> tri_turned(const char* p, int tj, int kb) {
   }
   return o;
 }
+// The same triangle stored turned, line j with its 64 - 16 (j / 16) rows i:
+// what a wave holds of a block, four rows of a column a lane, is 8 bytes of it.
+__device__ __forceinline__ constexpr int upper_stride(int t) { return tri_stride(3 - t); }
+__device__ __forceinline__ constexpr int upper_at(int t) {   // of line 16 t
+  return t == 0 ? 0 : t == 1 ? 2560 : t == 2 ? 4096 : 5632;
+}
 // Operand with rows i = 16 ti + l and k = j = 32 kb ...
 template <int PARTS>
-__device__ __forceinline__ Op<PARTS> tri_rows(const char* p, int ti, int kb) {
+__device__ __forceinline__ Op<PARTS> upper_rows(const char* p, int ti, int kb) {
+  Op<PARTS> o;
+  const Quad zero = {0, 0, 0, 0};
+#pragma unroll
+  for (int k = 0; k < PARTS; ++k) {
+    const int t = 2 * kb;
+    const char* q = p + k * kTri + 32 * (ti - t);
+    o.f[k] = join(t <= ti ? turned(q + upper_at(t), upper_stride(t)) : zero,
+                  t + 1 <= ti ? turned(q + upper_at(t + 1) - 32, upper_stride(t + 1)) : zero);
+  }
+  return o;
+}
+// Operand with rows j = 16 tj + l and k = i = 32 kb ...
+template <int PARTS>
+__device__ __forceinline__ Op<PARTS> upper_turned(const char* p, int tj, int kb) {
   const int l = threadIdx.x % 16, h = threadIdx.x % kWave / 16;
   Op<PARTS> o;
   const Quad zero = {0, 0, 0, 0};
 #pragma unroll
   for (int k = 0; k < PARTS; ++k) {
-    const char* q = p + k * kTri + tri_at(ti) + l * tri_stride(ti) + 64 * kb + 8 * h;
-    o.f[k] = join(2 * kb <= ti ? *reinterpret_cast<const Quad*>(q) : zero,
-                  2 * kb + 1 <= ti ? *reinterpret_cast<const Quad*>(q + 32) : zero);
+    const char* q = p + k * kTri + upper_at(tj) + l * upper_stride(tj) + 32 * (2 * kb - tj) + 8 * h;
+    o.f[k] = join(2 * kb >= tj ? *reinterpret_cast<const Quad*>(q) : zero,
+                  2 * kb + 1 >= tj ? *reinterpret_cast<const Quad*>(q + 32) : zero);
   }
   return o;
 }
@@ -1317,8 +1352,8 @@ __global__ __launch_bounds__(kDeltaBlock, kParts<T> == 1 && !SHARED ? 2 : 1) voi
       const int n = 4 * i + w;
       return (n / NT * 16 + l) * L::kSStride + (n % NT * 16 + 4 * h) * 2;
     };
-    fetch(0);
     for (int c0 = 0; c0 < s.dvp; c0 += kSlice) {
+      fetch(c0);
       __syncthreads();
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
@@ -1370,7 +1405,6 @@ __global__ __launch_bounds__(kDeltaBlock, kParts<T> == 1 && !SHARED ? 2 : 1) voi
         sd += was[0] * sv[i][0] + was[1] * sv[i][1] + (was[2] * sv[i][2] + was[3] * sv[i][3]);
         put(sv[i], d, L::kSPart);
       }
-      if (c0 + kSlice < s.dvp) fetch(c0 + kSlice);
       __syncthreads();
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
@@ -1418,20 +1452,17 @@ __global__ __launch_bounds__(kDeltaBlock, kParts<T> == 1 && !SHARED ? 2 : 1) voi
           row_h[r] += x;
           col_h += x;
         }
-        // element (row 4 h + r, column l) of the block, a column at a time
+        // line 16 j + l, rows 16 w + 4 h .. of the turned triangle
         const float y[4] = {dp[0], dp[1], dp[2], dp[3]}, x[4] = {da[0], da[1], da[2], da[3]};
         uint32_t u[NS][2], v[NS][2];
         split<NS, 4>(y, u);
         split<NS, 4>(x, v);
-        char* d = smem + tri_at(w) + 4 * h * tri_stride(w) + 32 * j + 2 * l;
+        char* d = smem + upper_at(j) + l * upper_stride(j) + 32 * (w - j) + 8 * h;
 #pragma unroll
-        for (int k = 0; k < NS; ++k)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            char* e = d + k * kTri + r * tri_stride(w);
-            *reinterpret_cast<uint16_t*>(e + L::kdP) = uint16_t(u[k][r / 2] >> (r % 2 * 16));
-            *reinterpret_cast<uint16_t*>(e + L::kdA) = uint16_t(v[k][r / 2] >> (r % 2 * 16));
-          }
+        for (int k = 0; k < NS; ++k) {
+          *reinterpret_cast<U2*>(d + L::kdP + k * kTri) = U2{u[k][0], u[k][1]};
+          *reinterpret_cast<U2*>(d + L::kdA + k * kTri) = U2{v[k][0], v[k][1]};
+        }
       }
       col_h += __shfl_xor(col_h, 16, kWave);
       col_h += __shfl_xor(col_h, 32, kWave);
@@ -1442,29 +1473,23 @@ __global__ __launch_bounds__(kDeltaBlock, kParts<T> == 1 && !SHARED ? 2 : 1) voi
     float end = 0.f;  // sum over the rows of k_i . exp(G_L - G_i) (N dS^T)_i
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
+      const f32x4 kv = token_tile<NP, DK>(smem, n, w), qv = token_tile<NP, DK>(smem + L::kQ, n, w);
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const int row = 16 * w + 4 * h + r, col = 16 * n + l;
-        const char* e = smem + row * DK * 2 + (col / 4 ^ key(row)) * 8 + col % 4 * 2;
-        float kv = 0.f, qv = 0.f;
-#pragma unroll
-        for (int k = NP - 1; k >= 0; --k) {
-          const char* d = e + k * kChunk * DK * 2;
-          kv += __uint_as_float(uint32_t(*reinterpret_cast<const uint16_t*>(d)) << 16);
-          qv += __uint_as_float(uint32_t(*reinterpret_cast<const uint16_t*>(d + L::kQ)) << 16);
-        }
         oS[n][r] *= s.scale * fin[r];
         const float u = fin[r] * fbe[r] * xS[n][r], y = fout[r] * nD[n][r];
-        row_h[r] += qv * oS[n][r] - kv * (u + y);
-        end += kv * y;
+        row_h[r] += qv[r] * oS[n][r] - kv[r] * (u + y);
+        end += kv[r] * y;
         xS[n][r] = y - u;
       }
       __builtin_amdgcn_sched_barrier(0);
     }
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
-      const Op<NS> pr = tri_rows<NS>(smem + L::kdP, w, b), ar = tri_rows<NS>(smem + L::kdA, w, b);
-      const Op<NS> pc = tri_turned<NS>(smem + L::kdP, w, b), ac = tri_turned<NS>(smem + L::kdA, w, b);
+      const Op<NS> pr = upper_rows<NS>(smem + L::kdP, w, b);
+      const Op<NS> ar = upper_rows<NS>(smem + L::kdA, w, b);
+      const Op<NS> pc = upper_turned<NS>(smem + L::kdP, w, b);
+      const Op<NS> ac = upper_turned<NS>(smem + L::kdA, w, b);
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         const Op<NP> kn = token_cols<NP, DK>(smem, n, b);
