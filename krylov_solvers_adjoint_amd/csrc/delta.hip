@@ -420,7 +420,7 @@ struct Rows {
     in = 0;
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
-      const int at = threadIdx.x % kDeltaBlock + i * kDeltaBlock;
+      const int at = threadIdx.x + i * kDeltaBlock;
       const int row = at / (WIDTH / 8), col = at % (WIDTH / 8) * 8;
       const bool on = row < len && col < have;
       in |= uint32_t(on) << i;
@@ -440,7 +440,7 @@ struct Rows {
   __device__ __forceinline__ void put(char* lds) const {
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
-      const int at = threadIdx.x % kDeltaBlock + i * kDeltaBlock;
+      const int at = threadIdx.x + i * kDeltaBlock;
       const int row = at / (WIDTH / 8), unit = at % (WIDTH / 8) * 2;
       uint32_t p[kParts<T>][4];
       split<T>(v[i], p);
@@ -462,13 +462,13 @@ struct Square {
   __device__ __forceinline__ void fetch(const float* p) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      v[i] = *reinterpret_cast<const f32x4*>(p + (threadIdx.x % kDeltaBlock + i * kDeltaBlock) * 4);
+      v[i] = *reinterpret_cast<const f32x4*>(p + (threadIdx.x + i * kDeltaBlock) * 4);
   }
   template <typename F>
   __device__ __forceinline__ void put(F&& at, int part) const {   // at(row, col): where
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int row = (threadIdx.x % kDeltaBlock + i * kDeltaBlock) / 16, col = threadIdx.x % 16 * 4;
+      const int row = (threadIdx.x + i * kDeltaBlock) / 16, col = threadIdx.x % 16 * 4;
       const float x[4] = {v[i][0], v[i][1], v[i][2], v[i][3]};
       uint32_t p[3][2];
       split<3, 4>(x, p);
@@ -680,7 +680,7 @@ struct alignas(16) Factors {
   float all;           // exp(G_L)
 };
 __device__ __forceinline__ void set_factors(Factors& f, double g, double end, float beta) {
-  const int t = threadIdx.x % kDeltaBlock;
+  const int t = threadIdx.x;
   if (t < kChunk) {
     f.beta[t] = beta;
     f.in[t] = expf(float(g));
@@ -740,7 +740,7 @@ struct Values {
   __device__ __forceinline__ void fetch(const T* p, int64_t ld, int len, int have, bool whole) {
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
-      const int at = threadIdx.x % kDeltaBlock + i * kDeltaBlock;
+      const int at = threadIdx.x + i * kDeltaBlock;
       const int row = at / (kWalk / 8), col = at % (kWalk / 8) * 8;
       const bool on = row < len && col < have;
       if (whole) {
@@ -760,7 +760,7 @@ struct Values {
   __device__ __forceinline__ void put(char* lds) const {
 #pragma unroll
     for (int i = 0; i < kLoads; ++i)
-      *reinterpret_cast<Eight<T>*>(lds + (threadIdx.x % kDeltaBlock + i * kDeltaBlock) * 8 *
+      *reinterpret_cast<Eight<T>*>(lds + (threadIdx.x + i * kDeltaBlock) * 8 *
                                              int(sizeof(T))) = v[i];
   }
   // tokens 16 i + 4 h + r of columns col + l
@@ -784,12 +784,12 @@ __device__ __forceinline__ f32x4 quad(const float* p, int i) {   // [16 i + 4 h 
   return *reinterpret_cast<const f32x4*>(p + 16 * i + 4 * (threadIdx.x % kWave / 16));
 }
 
-// The walks' workgroups: four waves that walk, 16 columns each, and four that
-// bring k, E and the like of the next chunk into LDS, so that neither memory's
+// The walks' workgroups: four waves that bring k, E and the like of the next
+// chunk into LDS, and behind them waves that walk, 16 columns each, so that neither memory's
 // latency nor the cutting of k and E lies in the chain from chunk to chunk.
 // Two chunks' worth where LDS holds them; else the bringing waves keep the next
 // chunk in registers and store it when the walking ones have read this one's.
-constexpr int kWalkBlock = 2 * kDeltaBlock;
+constexpr int kWalkBlock = kDeltaBlock + kWalk / 16 * kWave;
 template <int SLOT>
 constexpr int kWalkDepth = 2 * SLOT <= 160 * 1024 ? 2 : 1;
 // All LDS accesses of the wave are done, then those of the others; loads and
@@ -881,15 +881,15 @@ __global__ __launch_bounds__(kWalkBlock) void k_delta_states(DeltaShape s, Delta
   constexpr int NP = kParts<T>, RT = DK / 16, KB = DK / 32;
   extern __shared__ __align__(16) char lds[];
   const int slices = int(div_up(s.dvp, kWalk));
-  const int t = threadIdx.x % kDeltaBlock, l = t % 16, h = (t % kWave) / 16;
+  const int t = threadIdx.x;
   const int w = __builtin_amdgcn_readfirstlane(int(threadIdx.x) / kWave);
   const int vh = blockIdx.x / slices % s.hv, seq = blockIdx.x / slices / s.hv;
   const int kh = vh / (s.hv / s.hk);
   const int64_t begin = first_chunk(s, seq), count = first_chunk(s, seq + 1) - begin;
   const int64_t first = first_token(s, seq), past = first_token(s, seq + 1);
   const int64_t head = int64_t(seq) * s.hv + vh;
-  const int c0 = blockIdx.x % slices * kWalk + 16 * (w % 4);
-  if (w >= 4) {
+  const int wc = 16 * (w - 4), c0 = blockIdx.x % slices * kWalk + wc;
+  if (w < 4) {
     Rows<T, DK, WHOLE> kr;
     Square er;
     Values<T> vr;
@@ -962,7 +962,7 @@ __global__ __launch_bounds__(kWalkBlock) void k_delta_states(DeltaShape s, Delta
     }, [&] { e0 = tri(0); });
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      R[i] = Values<T>::tile(smem + L::kV, 16 * w, i) - quad(f.in, i) * R[i];
+      R[i] = Values<T>::tile(smem + L::kV, wc, i) - quad(f.in, i) * R[i];
       bR[i] = quad(f.beta, i) * R[i];
     }
     Op<3> n[2] = {operand<3>(bR[0], bR[1]), operand<3>(bR[2], bR[3])};
@@ -1108,15 +1108,15 @@ __global__ __launch_bounds__(kWalkBlock) void k_delta_adjoint(
   constexpr int NP = kParts<T>, RT = DK / 16, KB = DK / 32;
   extern __shared__ __align__(16) char lds[];
   const int slices = int(div_up(s.dvp, kWalk));
-  const int t = threadIdx.x % kDeltaBlock, l = t % 16, h = (t % kWave) / 16;
+  const int t = threadIdx.x, l = t % 16, h = (t % kWave) / 16;
   const int w = __builtin_amdgcn_readfirstlane(int(threadIdx.x) / kWave);
   const int vh = blockIdx.x / slices % s.hv, seq = blockIdx.x / slices / s.hv;
   const int kh = vh / (s.hv / s.hk);
   const int64_t begin = first_chunk(s, seq), count = first_chunk(s, seq + 1) - begin;
   const int64_t first = first_token(s, seq), past = first_token(s, seq + 1);
   const int64_t head = int64_t(seq) * s.hv + vh;
-  const int c0 = blockIdx.x % slices * kWalk + 16 * (w % 4);
-  if (w >= 4) {
+  const int wc = 16 * (w - 4), c0 = blockIdx.x % slices * kWalk + wc;
+  if (w < 4) {
     Rows<T, DK, WHOLE> kr, qr;
     Square er, pr;
     Values<T> orow;
@@ -1197,7 +1197,7 @@ __global__ __launch_bounds__(kWalkBlock) void k_delta_adjoint(
       if (i % kSide == 0) so = operand<3>(D[2 * (i / kSide)], D[2 * (i / kSide) + 1]);
       mul_turns(Y + i % kSide * GT, o.o, so);
     }, [&] { t0 = tri_p(0); });
-    auto out_grad = [&](int i) { return Values<T>::tile(smem + L::kO, 16 * w, i); };
+    auto out_grad = [&](int i) { return Values<T>::tile(smem + L::kO, wc, i); };
     const Op<NP> oo[2] = {operand_of<T>(out_grad(0), out_grad(1)),
                           operand_of<T>(out_grad(2), out_grad(3))};
 #pragma unroll
