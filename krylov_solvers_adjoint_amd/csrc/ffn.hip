@@ -23,8 +23,8 @@ namespace {
 constexpr int kFfnBlock = 256;
 // Bytes of k a step covers (64 bytes: 32 16-bit values or 16 fp32), and the
 // steps in LDS at a time.  Direct loads need the distance: with two steps of
-// 128 bytes (as many bytes in all) every step waited for memory, dx and dW of
-// 16384 x 1024 x 4096 took 316 and 330 us.
+// 128 bytes (as many bytes in all) every step waited for memory: dx and dW of
+// 16384 x 1024 x 4096 took 316 and 330 us, and take 256 each.
 template <bool DIRECT>
 struct Ring {
   static constexpr int kStep = DIRECT ? 64 : 128, kDepth = DIRECT ? 4 : 2;
@@ -410,11 +410,16 @@ __device__ __forceinline__ void leave(const Product& g, int64_t at, const float 
 // of a and the same B / 2 of b, half of each wave's columns are of either.
 //
 // A few steps' tiles are in LDS (Ring).  A wave multiplies a row of 16 x WN at
-// a time and reads the fragments some rows ahead of their use, between the
+// a time and reads the fragments NI - 1 rows ahead of their use, between the
 // products of the rows, so that the matrix cores and the LDS work side by
 // side.  The step's only barrier comes behind the read of its tiles' last
-// fragment, in the middle of its products: from there on the next tiles'
-// fragments are read and this one's place is filled with a later step's.
+// fragment: from there on the next tiles' fragments are read and this one's
+// place is filled with a later step's.
+//
+// Bound by the matrix cores at the card's power limit (the same products of
+// zeros take three quarters of the time) and, for tiles of 256, by the LDS
+// reads beside them: 8192 x 2048 x 2 x 8192 bf16 482 us, 1.14 PFLOP/s, where
+// the instructions alone reach 1.8 on such data; fp32 85 % of its 0.154.
 template <typename T, int B, int WM, int WN, bool AT, bool BT, int EPI, bool DIRECT>
 __global__ __launch_bounds__(kWave* B* B / WM / WN, 2) void k_ffn_product(Product g) {
   constexpr bool kGate = EPI != EPI_STORE;
@@ -683,7 +688,8 @@ __global__ __launch_bounds__(kFfnBlock) void k_ffn_join(Product g) {
 
 // The projections of few rows (at most 16 RT): reading the weights is the
 // work.  A workgroup has 16 columns of a and of b; its four waves take turns
-// along k, fragments straight from memory, and are joined through LDS.
+// along k, fragments straight from memory, and are joined through LDS.  4 x
+// 1024 x 2 x 4096 bf16: 5.4 us (16.8 MB), against 36 us with tiles of 128.
 template <typename T, int RT, int EPI>
 __global__ __launch_bounds__(kFfnBlock) void k_ffn_few(Product g) {
   typedef typename Unit<T>::Vec Vec;
@@ -785,11 +791,13 @@ __global__ __launch_bounds__(kFfnBlock) void k_ffn_few(Product g) {
 //           256: 1.54, 3.00, 4.63, 6.01 us
 // so the large tile wins as soon as it fills the card, the small one where
 // there is little to do; a split costs the writing and reading of its sums.
+// fp32 operands stored [k][row] (`turned` of the two) are read from LDS a word
+// at a time: 2.0 us instead of 1.37 with both of them (64, n = 2).
 struct ProductPlan {
   int tile, splits;
 };
 ProductPlan plan_product(int64_t M, int64_t N, int64_t K, int parts, int outputs, bool gate,
-                         int es, bool direct) {
+                         int turned, int es, bool direct) {
   struct Kind {
     int tile, slots;
     double wait, share, start;   // us; start: before and behind the steps
@@ -808,7 +816,8 @@ ProductPlan plan_product(int64_t M, int64_t N, int64_t K, int parts, int outputs
     for (int s = 1; s <= (gate ? 1 : 32) && s <= (steps + 3) / 4; ++s) {
       const int64_t n = div_up(tiles * s, cus);
       const double rounds = double(div_up(n, k.slots));
-      double time = double(div_up(steps, s)) * (rounds * k.wait + double(n) * k.share) +
+      const double wait = k.wait + (es == 4 ? 0.3 * turned : 0.0);
+      double time = double(div_up(steps, s)) * (rounds * wait + double(n) * k.share) +
                     rounds * k.start;
       if (s > 1) time += 5.0 + double(s + 1) * double(M * N * outputs) * 4 / 4e6;
       if (time < least) least = time, best = {k.tile, s};
@@ -817,10 +826,10 @@ ProductPlan plan_product(int64_t M, int64_t N, int64_t K, int parts, int outputs
   return best;
 }
 
-int64_t split_bytes(int64_t M, int64_t N, int64_t K, int parts, int outputs, int es) {
+int64_t split_bytes(int64_t M, int64_t N, int64_t K, int parts, int outputs, int turned, int es) {
   int64_t most = 0;
   for (int direct = 0; direct < 2; ++direct) {
-    const ProductPlan p = plan_product(M, N, K, parts, outputs, false, es, direct);
+    const ProductPlan p = plan_product(M, N, K, parts, outputs, false, turned, es, direct);
     const int64_t b = p.splits > 1 ? p.splits * outputs * M * N * 4 : 0;
     if (b > most) most = b;
   }
@@ -876,7 +885,8 @@ sla_status launch_product(Product& g, hipStream_t stream) {
       es == 2 && whole_units(g.A[0], g.lda, ka, es) && whole_units(g.B[0], g.ldb, kb, es) &&
       (!g.A[1] || whole_units(g.A[1], g.lda, ka, es)) &&
       (!g.B[1] || whole_units(g.B[1], g.ldb, kb, es));
-  const ProductPlan p = plan_product(g.M, g.N, g.K, g.parts, g.outputs, kGate, es, direct);
+  const ProductPlan p = plan_product(g.M, g.N, g.K, g.parts, g.outputs, kGate, int(AT) + int(BT),
+                                     es, direct);
   g.splits = p.splits;
   if (p.tile == 64) SLA_TRY((run_product<T, 64, 32, 32, AT, BT, EPI, false>(g, stream)));
   if (p.tile == 128) SLA_TRY((run_product<T, 128, 64, 64, AT, BT, EPI, false>(g, stream)));
@@ -908,8 +918,8 @@ int64_t factor_bytes(int64_t rows, int64_t outer, int es) {
   return div_up(rows * outer * es, 256) * 256;
 }
 int64_t grad_bytes(int64_t rows, int64_t inner, int64_t outer, int es) {
-  const int64_t x = split_bytes(rows, inner, outer, 2, 1, es);
-  const int64_t w = split_bytes(outer, inner, rows, 1, 2, es);
+  const int64_t x = split_bytes(rows, inner, outer, 2, 1, 1, es);
+  const int64_t w = split_bytes(outer, inner, rows, 1, 2, 2, es);
   return 2 * factor_bytes(rows, outer, es) + (x > w ? x : w);
 }
 
@@ -932,6 +942,7 @@ extern "C" {
 sla_status sla_gated_ffn(const void* x, int64_t ldx, const void* w_gate, const void* w_up,
                          int64_t rows, int64_t inner, int64_t outer, sla_type type, int act,
                          void* h, hipStream_t stream) {
+  SLA_NET_BEGIN
   clear_error();
   SLA_TRY(ffn_args("sla_gated_ffn", rows, inner, outer, ldx, type, act));
   if (rows == 0) return SLA_OK;
@@ -950,21 +961,25 @@ sla_status sla_gated_ffn(const void* x, int64_t ldx, const void* w_gate, const v
     g.act = act;
     return launch_product<T, false, false, EPI_GATE>(g, stream);
   });
+  SLA_NET_END
 }
 
 sla_status sla_gated_ffn_work(int64_t rows, int64_t inner, int64_t outer, sla_type type,
                               int64_t* bytes_host) {
+  SLA_NET_BEGIN
   clear_error();
   SLA_TRY(ffn_args("sla_gated_ffn_work", rows, inner, outer, inner, type, SLA_ACT_SILU));
   SLA_NET_REQUIRE(bytes_host, "sla_gated_ffn_work: bytes_host is NULL");
   *bytes_host = grad_bytes(rows, inner, outer, int(type_size(type)));
   return SLA_OK;
+  SLA_NET_END
 }
 
 sla_status sla_gated_ffn_grad(const void* dh, int64_t lddh, const void* x, int64_t ldx,
                               const void* w_gate, const void* w_up, int64_t rows, int64_t inner,
                               int64_t outer, sla_type type, int act, void* dx, void* dw_gate,
                               void* dw_up, void* work, int64_t work_bytes, hipStream_t stream) {
+  SLA_NET_BEGIN
   clear_error();
   SLA_TRY(ffn_args("sla_gated_ffn_grad", rows, inner, outer, ldx, type, act));
   SLA_NET_REQUIRE(lddh >= outer, "sla_gated_ffn_grad: row stride of dh below outer");
@@ -1017,6 +1032,7 @@ sla_status sla_gated_ffn_grad(const void* dh, int64_t lddh, const void* x, int64
     }
     return SLA_OK;
   });
+  SLA_NET_END
 }
 
 }  // extern "C"

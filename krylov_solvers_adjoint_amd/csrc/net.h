@@ -3,6 +3,8 @@
 // access, cross-lane sums.
 #pragma once
 
+#include <new>
+
 #include "common.h"
 
 // Products and sums of these operators may be fused (one rounding instead of
@@ -79,3 +81,16 @@ inline bool valid_type(sla_type t) { return t == SLA_F32 || t == SLA_F16 || t ==
       return SLA_ERR_ARG;                                                      \
     }                                                                          \
   } while (0)
+
+// No exception leaves a C entry.
+#define SLA_NET_BEGIN try {
+#define SLA_NET_END                                                            \
+  }                                                                            \
+  catch (const std::bad_alloc&) {                                              \
+    ::sla::set_error("host out of memory");                                    \
+    return SLA_ERR_OOM;                                                        \
+  }                                                                            \
+  catch (...) {                                                                \
+    ::sla::set_error("internal error");                                        \
+    return SLA_ERR_DEVICE;                                                     \
+  }

@@ -17,6 +17,9 @@
 // rounding of a plain mean would pass for a deviation (constant rows of 1e18
 // came out as +-1).  The mean that is kept is less x_0 too.
 //
+// Measured: 10^6 x 64 fp32 forward 92 us (5.6 TB/s) and backward 152 + 5 (5.1
+// TB/s); 16384 x 1024 bf16 17 and 22 + 4.5 us.
+//
 // The weight's gradient: every thread keeps its columns' sums over all the
 // rows its workgroup walks, the teams of a workgroup are joined through LDS,
 // and a second kernel sums the workgroups' partials in a fixed order: no
@@ -386,6 +389,7 @@ extern "C" {
 sla_status sla_layer_norm(const void* x, int64_t ldx, int64_t rows, int64_t cols, sla_type type,
                           const void* weight, const void* bias, sla_type wtype, double eps,
                           void* y, float* stats, hipStream_t stream) {
+  SLA_NET_BEGIN
   clear_error();
   SLA_TRY(norm_args("sla_layer_norm", rows, cols, ldx, type, wtype));
   SLA_NET_REQUIRE(eps >= 0 && eps < 1e30, "sla_layer_norm: eps must be non-negative");
@@ -411,20 +415,24 @@ sla_status sla_layer_norm(const void* x, int64_t ldx, int64_t rows, int64_t cols
       return SLA_OK;
     });
   });
+  SLA_NET_END
 }
 
 sla_status sla_layer_norm_work(int64_t rows, int64_t cols, sla_type type, int64_t* bytes_host) {
+  SLA_NET_BEGIN
   clear_error();
   SLA_TRY(norm_args("sla_layer_norm_work", rows, cols, cols, type, type));
   SLA_NET_REQUIRE(bytes_host, "sla_layer_norm_work: bytes_host is NULL");
   *bytes_host = 2 * int64_t(norm_slabs(rows, cols, int(16 / type_size(type)))) * cols * 4;
   return SLA_OK;
+  SLA_NET_END
 }
 
 sla_status sla_layer_norm_grad(const void* dy, int64_t lddy, const void* x, int64_t ldx,
                                int64_t rows, int64_t cols, sla_type type, const void* weight,
                                sla_type wtype, const float* stats, void* dx, void* dweight,
                                void* dbias, void* work, int64_t work_bytes, hipStream_t stream) {
+  SLA_NET_BEGIN
   clear_error();
   SLA_TRY(norm_args("sla_layer_norm_grad", rows, cols, ldx < lddy ? ldx : lddy, type, wtype));
   const bool sums = dweight || dbias;
@@ -465,6 +473,7 @@ sla_status sla_layer_norm_grad(const void* dy, int64_t lddy, const void* x, int6
     }
     return SLA_OK;
   });
+  SLA_NET_END
 }
 
 }  // extern "C"
