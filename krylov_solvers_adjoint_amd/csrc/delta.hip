@@ -940,7 +940,8 @@ __global__ __launch_bounds__(kWalkBlock) void k_delta_states(DeltaShape s, Delta
     auto cols = [&](int i) {   // step i of k^T N
       Tokens o;
 #pragma unroll
-      for (int n = 0; n < GT; ++n) o.o[n] = token_cols<NP, DK>(smem, i / 2 * GT + n, i % 2);
+      for (int n = 0; n < GT; ++n)
+        o.o[n] = token_cols<NP, DK>(smem, i % (RT / GT) * GT + n, i / (RT / GT));
       return o;
     };
     auto tri = [&](int i) {    // rows 0 and 1, 2 and 3 of E's first half, 2 and 3 of its second
@@ -953,7 +954,8 @@ __global__ __launch_bounds__(kWalkBlock) void k_delta_states(DeltaShape s, Delta
     };
     float* Sg = kept.S + (slot * s.dvp + c0) * DK + t % kWave * 4;
     Tokens k0 = rows(0);
-    Op<3> so;
+    Op<3> so[2];
+    so[0] = operand<3>(S[0], S[1]);
 #pragma unroll
     for (int a = 0; a < RT; ++a) *reinterpret_cast<f32x4*>(Sg + 256 * a) = S[a];
     f32x4 R[4], bR[4];
@@ -961,35 +963,45 @@ __global__ __launch_bounds__(kWalkBlock) void k_delta_states(DeltaShape s, Delta
     for (int i = 0; i < 4; ++i) R[i] = f32x4{0, 0, 0, 0};
     Ops<3, 2> e0;
     pipe<KB * kSide>(k0, rows, [&](int i, const Tokens& o) {
-      if (i % kSide == 0) so = operand<3>(S[2 * (i / kSide)], S[2 * (i / kSide) + 1]);
-      mul_turns(R + i % kSide * GT, o.o, so);
+      // the next block is cut while this one is multiplied
+      if (i % kSide == 0 && i / kSide + 1 < KB)
+        so[(i / kSide + 1) % 2] = operand<3>(S[2 * (i / kSide) + 2], S[2 * (i / kSide) + 3]);
+      mul_turns(R + i % kSide * GT, o.o, so[i / kSide % 2]);
     }, [&] { e0 = tri(0); });
+    Op<3> n[2];
+    auto see = [&](int b) {   // R of tokens 32 b ..
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      R[i] = Values<T>::tile(smem + L::kV, wc, i) - quad(f.in, i) * R[i];
-      bR[i] = quad(f.beta, i) * R[i];
-    }
-    Op<3> n[2] = {operand<3>(bR[0], bR[1]), operand<3>(bR[2], bR[3])};
+      for (int i = 2 * b; i < 2 * b + 2; ++i) {
+        R[i] = Values<T>::tile(smem + L::kV, wc, i) - quad(f.in, i) * R[i];
+        bR[i] = quad(f.beta, i) * R[i];
+      }
+      n[b] = operand<3>(bR[2 * b], bR[2 * b + 1]);
+    };
+    see(0);
     float* Mg = kept.M + (slot * s.dvp + c0) * kChunk + t % kWave * 4;
     f32x4 x[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) x[i] = f32x4{0, 0, 0, 0};
     pipe<3>(e0, tri, [&](int i, const Ops<3, 2>& o) {
+      if (i == 0) see(1);
       mul_turns(x + (i ? 2 : 0), o.o, n[i / 2]);
     }, [&] { k0 = cols(0); });
+    auto correct = [&](int b) {   // M and exp(G_L - G) N of tokens 32 b ..
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      R[i] -= x[i];
-      *reinterpret_cast<f32x4*>(Mg + 256 * i) = R[i];
-      bR[i] = quad(f.out, i) * (quad(f.beta, i) * R[i]);
-    }
-    n[0] = operand<3>(bR[0], bR[1]);
-    n[1] = operand<3>(bR[2], bR[3]);
+      for (int i = 2 * b; i < 2 * b + 2; ++i) {
+        R[i] -= x[i];
+        *reinterpret_cast<f32x4*>(Mg + 256 * i) = R[i];
+        bR[i] = quad(f.out, i) * (quad(f.beta, i) * R[i]);
+      }
+      n[b] = operand<3>(bR[2 * b], bR[2 * b + 1]);
+    };
     const float all = f.all;
 #pragma unroll
     for (int a = 0; a < RT; ++a) S[a] *= all;
+    correct(0);
     pipe<RT / GT * 2>(k0, cols, [&](int i, const Tokens& o) {
-      mul_turns(S + i / 2 * GT, o.o, n[i % 2]);
+      if (i == 0) correct(1);
+      mul_turns(S + i % (RT / GT) * GT, o.o, n[i / (RT / GT)]);
     }, [] {});
   });
   if (send && live) store_state<DK>(S, send, s, head, c0);
@@ -1177,7 +1189,8 @@ __global__ __launch_bounds__(kWalkBlock) void k_delta_adjoint(
     auto cols = [&](const char* p, int i) {
       Tokens o;
 #pragma unroll
-      for (int n = 0; n < GT; ++n) o.o[n] = token_cols<NP, DK>(p, i / 2 * GT + n, i % 2);
+      for (int n = 0; n < GT; ++n)
+        o.o[n] = token_cols<NP, DK>(p, i % (RT / GT) * GT + n, i / (RT / GT));
       return o;
     };
     auto q_cols = [&](int i) { return cols(smem + L::kQ, i); };   // step i of q^T do
@@ -1193,7 +1206,8 @@ __global__ __launch_bounds__(kWalkBlock) void k_delta_adjoint(
     auto tri_e = [&](int i) { return tri_step(smem + L::kE, i); };
     float* Dg = dS + (slot * s.dvp + c0) * DK + t % kWave * 4;
     Tokens k0 = rows(0);
-    Op<3> so;
+    Op<3> so[2];
+    so[0] = operand<3>(D[0], D[1]);
 #pragma unroll
     for (int a = 0; a < RT; ++a) *reinterpret_cast<f32x4*>(Dg + 256 * a) = D[a];
     f32x4 Y[4], bY[4];
@@ -1201,8 +1215,9 @@ __global__ __launch_bounds__(kWalkBlock) void k_delta_adjoint(
     for (int i = 0; i < 4; ++i) Y[i] = f32x4{0, 0, 0, 0};
     Ops<3, 2> t0;
     pipe<KB * kSide>(k0, rows, [&](int i, const Tokens& o) {
-      if (i % kSide == 0) so = operand<3>(D[2 * (i / kSide)], D[2 * (i / kSide) + 1]);
-      mul_turns(Y + i % kSide * GT, o.o, so);
+      if (i % kSide == 0 && i / kSide + 1 < KB)
+        so[(i / kSide + 1) % 2] = operand<3>(D[2 * (i / kSide) + 2], D[2 * (i / kSide) + 3]);
+      mul_turns(Y + i % kSide * GT, o.o, so[i / kSide % 2]);
     }, [&] { t0 = tri_p(0); });
     auto out_grad = [&](int i) { return Values<T>::tile(smem + L::kO, wc, i); };
     const Op<NP> oo[2] = {operand_of<T>(out_grad(0), out_grad(1)),
@@ -1214,27 +1229,30 @@ __global__ __launch_bounds__(kWalkBlock) void k_delta_adjoint(
     }, [&] { k0 = q_cols(0); });
     {
       auto read_o = [&](int i) { return s.scale * quad(f.in, i) * out_grad(i); };
-      const Op<3> os[2] = {operand<3>(read_o(0), read_o(1)), operand<3>(read_o(2), read_o(3))};
+      Op<3> os[2];
+      os[0] = operand<3>(read_o(0), read_o(1));
       const float all = f.all;
 #pragma unroll
       for (int a = 0; a < RT; ++a) D[a] *= all;
       pipe<RT / GT * 2>(k0, q_cols, [&](int i, const Tokens& o) {
-        mul_turns(D + i / 2 * GT, o.o, os[i % 2]);
+        if (i == 0) os[1] = operand<3>(read_o(2), read_o(3));
+        mul_turns(D + i % (RT / GT) * GT, o.o, os[i / (RT / GT)]);
       }, [&] { t0 = tri_e(0); });
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) bY[i] = quad(f.beta, i) * Y[i];
-    Op<3> n[2] = {operand<3>(bY[0], bY[1]), operand<3>(bY[2], bY[3])};
+    Op<3> n[2];
+    n[1] = operand<3>(bY[2], bY[3]);
     float* Xg = X + (slot * s.dvp + c0) * kChunk + t % kWave * 4;
     T* const dvp = dv + ((p.tok + 4 * h) * s.hv + vh) * s.dv + c0 + l;
     f32x4 x[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) x[i] = f32x4{0, 0, 0, 0};
     pipe<3>(t0, tri_e, [&](int i, const Ops<3, 2>& o) {
+      if (i == 0) n[0] = operand<3>(bY[0], bY[1]);
       mul_turns(x + (i == 1 ? 2 : 0), o.o, n[i < 2]);
     }, [&] { k0 = k_cols(0); });
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    auto solved = [&](int i) {   // X and dv of tokens 16 i ..
       Y[i] -= x[i];
       *reinterpret_cast<f32x4*>(Xg + 256 * i) = Y[i];
       bY[i] = quad(f.beta, i) * Y[i];
@@ -1245,11 +1263,17 @@ __global__ __launch_bounds__(kWalkBlock) void k_delta_adjoint(
             dvp[int64_t(16 * i + r) * s.hv * s.dv] = T(bY[i][r]);
       }
       bY[i] *= -quad(f.in, i);
-    }
+    };
+    solved(0);
+    solved(1);
     n[0] = operand<3>(bY[0], bY[1]);
-    n[1] = operand<3>(bY[2], bY[3]);
     pipe<RT / GT * 2>(k0, k_cols, [&](int i, const Tokens& o) {
-      mul_turns(D + i / 2 * GT, o.o, n[i % 2]);
+      if (i == 0) {
+        solved(2);
+        solved(3);
+        n[1] = operand<3>(bY[2], bY[3]);
+      }
+      mul_turns(D + i % (RT / GT) * GT, o.o, n[i / (RT / GT)]);
     }, [] {});
   });
   if (ds0 && live) store_state<DK>(D, ds0, s, head, c0);
