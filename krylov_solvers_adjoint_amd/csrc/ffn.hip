@@ -24,7 +24,7 @@ constexpr int kFfnBlock = 256;
 // Bytes of k a step covers (64 bytes: 32 16-bit values or 16 fp32), and the
 // steps in LDS at a time.  Direct loads need the distance: with two steps of
 // 128 bytes (as many bytes in all) every step waited for memory: dx and dW of
-// 16384 x 1024 x 4096 took 316 and 330 us, and take 256 each.
+// 16384 x 1024 x 4096 took 316 and 330 us against 256 each.
 template <bool DIRECT>
 struct Ring {
   static constexpr int kStep = DIRECT ? 64 : 128, kDepth = DIRECT ? 4 : 2;
@@ -379,16 +379,13 @@ __device__ __forceinline__ void with_activation(const Product& g, F&& f) {
   else f(std::integral_constant<int, SLA_ACT_RELU>());
 }
 
-// Four columns of a row leave (d: dh there) at element `at` of C; the first
-// `have` of them exist.
+// What becomes of four columns of a row (d: dh there): u, and v for db.
 template <typename T, int EPI, int ACT>
-__device__ __forceinline__ void leave(const Product& g, int64_t at, const float (&d)[4],
-                                      int64_t have, int z, const f32x4& a, const f32x4& b) {
-  float u[4], v[4];
+__device__ __forceinline__ void result(const float (&d)[4], const f32x4& a, const f32x4& b,
+                                       float (&u)[4], float (&v)[4]) {
   if constexpr (EPI == EPI_STORE) {
 #pragma unroll
     for (int r = 0; r < 4; ++r) u[r] = a[r];
-    store_f32<4>((T*)(z ? g.C[1] : g.C[0]) + at, have, u);
   } else {
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
@@ -401,9 +398,39 @@ __device__ __forceinline__ void leave(const Product& g, int64_t at, const float 
         v[r] = d[r] * f;
       }
     }
-    store_f32<4>((T*)g.C[0] + at, have, u);
-    if constexpr (EPI == EPI_GATE_GRAD) store_f32<4>((T*)g.C[1] + at, have, v);
   }
+}
+// They leave at element `at` of C; the first `have` of them exist.
+template <typename T, int EPI, int ACT>
+__device__ __forceinline__ void leave(const Product& g, int64_t at, const float (&d)[4],
+                                      int64_t have, int z, const f32x4& a, const f32x4& b) {
+  float u[4], v[4];
+  result<T, EPI, ACT>(d, a, b, u, v);
+  store_f32<4>((T*)(EPI == EPI_STORE && z ? g.C[1] : g.C[0]) + at, have, u);
+  if constexpr (EPI == EPI_GATE_GRAD) store_f32<4>((T*)g.C[1] + at, have, v);
+}
+
+// Two neighbouring tiles' quads of 16-bit columns, x and y of lane (l, h), as
+// eight columns in a row: of tile h % 2, from 8 (h / 2) on, and back.  A store
+// then writes 64 bytes of each of 16 rows instead of 32: of 16384 x 1024 x 4096
+// bf16, da and db (0.4 GB beside the product) take 326 us instead of 363, h 286
+// instead of 295, dx and dW 248 and 245 instead of 253 and 256.
+typedef uint32_t Pair __attribute__((ext_vector_type(2)));
+typedef uint32_t Quads __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ Quads side_by_side(Pair x, Pair y) {
+  Quads q;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const auto s = __builtin_amdgcn_permlane16_swap(x[i], y[i], false, false);
+    q[i] = s[0];
+    q[2 + i] = s[1];
+  }
+  return q;
+}
+template <typename T>
+__device__ __forceinline__ Pair packed(const float (&u)[4]) {
+  typedef T V4 __attribute__((ext_vector_type(4)));
+  return __builtin_bit_cast(Pair, V4{T(u[0]), T(u[1]), T(u[2]), T(u[3])});
 }
 
 // Tiles of B x B in waves of WM x WN.  EPI_GATE*: the tile's columns are B / 2
@@ -418,7 +445,7 @@ __device__ __forceinline__ void leave(const Product& g, int64_t at, const float 
 //
 // Bound by the matrix cores at the card's power limit (the same products of
 // zeros take three quarters of the time) and, for tiles of 256, by the LDS
-// reads beside them: 8192 x 2048 x 2 x 8192 bf16 482 us, 1.14 PFLOP/s, where
+// reads beside them: 8192 x 2048 x 2 x 8192 bf16 478 us, 1.15 PFLOP/s, where
 // the instructions alone reach 1.8 on such data; fp32 85 % of its 0.154.
 template <typename T, int B, int WM, int WN, bool AT, bool BT, int EPI, bool DIRECT>
 __global__ __launch_bounds__(kWave* B* B / WM / WN, 2) void k_ffn_product(Product g) {
@@ -622,22 +649,79 @@ __global__ __launch_bounds__(kWave* B* B / WM / WN, 2) void k_ffn_product(Produc
                                      row0 * g.N + col0 : nullptr;
     constexpr int kQuads = kGate ? NJ / 2 : NJ;
     auto has = [&](int j) { return whole.value ? int64_t(4) : g.N - col0 - brow(j); };
+    // whole 16-bit tiles: two quads at a time
+    constexpr bool kWide = whole.value && sizeof(T) == 2 && kQuads % 2 == 0;
+    typedef typename std::conditional<sizeof(T) == 2, T, _Float16>::type Half;   // T, if kWide
+    typedef typename VecOf<Half, 8>::type Loose8;
+    const int wide = brow(h % 2) - brow(0) + 8 * (h / 2) - 4 * h;   // from the lane's first quad
     // dh of all rows is asked for before the first row leaves
     typename VecOf<T, 4>::type dh[EPI == EPI_GATE_GRAD ? NI : 1][kQuads];
     if constexpr (EPI == EPI_GATE_GRAD) {
       const T* p = (const T*)g.dh + row0 * g.lddh + col0;
+      if constexpr (kWide) {
+        Quads q[NI][kQuads / 2];
 #pragma unroll
-      for (int i = 0; i < NI; ++i, p += 16 * g.lddh)
+        for (int i = 0; i < NI; ++i, p += 16 * g.lddh)
 #pragma unroll
-        for (int j = 0; j < kQuads; ++j) {
-          const int64_t have = whole.value || row0 + 16 * i < g.M ? has(j) : 0;
-          if (have >= 4) {
-            dh[i][j] = *reinterpret_cast<const typename VecOf<T, 4>::type*>(p + brow(j));
-          } else {
-#pragma unroll
-            for (int r = 0; r < 4; ++r) dh[i][j][r] = r < have ? p[brow(j) + r] : T(0.f);
+          for (int j = 0; j < kQuads; j += 2) {
+            const Loose8 x = *reinterpret_cast<const Loose8*>(p + brow(j) + wide);
+            q[i][j / 2] = __builtin_bit_cast(Quads, x);
           }
-        }
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+#pragma unroll
+          for (int j = 0; j < kQuads; j += 2) {
+            const Quads x = q[i][j / 2], y = side_by_side(Pair{x[0], x[1]}, Pair{x[2], x[3]});
+            typedef Half V4 __attribute__((ext_vector_type(4)));
+            const V4 a = __builtin_bit_cast(V4, Pair{y[0], y[1]});
+            const V4 b = __builtin_bit_cast(V4, Pair{y[2], y[3]});
+#pragma unroll
+            for (int r = 0; r < 4; ++r) dh[i][j][r] = T(a[r]), dh[i][j + 1][r] = T(b[r]);
+          }
+      } else {
+#pragma unroll
+        for (int i = 0; i < NI; ++i, p += 16 * g.lddh)
+#pragma unroll
+          for (int j = 0; j < kQuads; ++j) {
+            const int64_t have = whole.value || row0 + 16 * i < g.M ? has(j) : 0;
+            if (have >= 4) {
+              dh[i][j] = *reinterpret_cast<const typename VecOf<T, 4>::type*>(p + brow(j));
+            } else {
+#pragma unroll
+              for (int r = 0; r < 4; ++r) dh[i][j][r] = r < have ? p[brow(j) + r] : T(0.f);
+            }
+          }
+      }
+    }
+    if constexpr (kWide) {
+      if (kGate || !part) {
+        T* c0 = (T*)(EPI == EPI_STORE && at.z ? g.C[1] : g.C[0]) + at_c + wide;
+        T* c1 = (T*)g.C[1] + at_c + wide;
+#pragma unroll
+        for (int i = 0; i < NI; ++i, c0 += 16 * g.ldc, c1 += 16 * g.ldc)
+#pragma unroll
+          for (int j = 0; j < kQuads; j += 2) {
+            Pair u2[2], v2[2];
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+              float d[4] = {0.f, 0.f, 0.f, 0.f}, u[4], v[4] = {0.f, 0.f, 0.f, 0.f};
+              if constexpr (EPI == EPI_GATE_GRAD) {
+#pragma unroll
+                for (int r = 0; r < 4; ++r) d[r] = float(dh[i][j + n][r]);
+              }
+              result<T, EPI, act.value>(d, acc[i][j + n], acc[i][kGate ? j + n + NJ / 2 : j + n],
+                                        u, v);
+              u2[n] = packed<Half>(u);
+              v2[n] = packed<Half>(v);
+            }
+            *reinterpret_cast<Loose8*>(c0 + brow(j)) =
+                __builtin_bit_cast(Loose8, side_by_side(u2[0], u2[1]));
+            if constexpr (EPI == EPI_GATE_GRAD)
+              *reinterpret_cast<Loose8*>(c1 + brow(j)) =
+                  __builtin_bit_cast(Loose8, side_by_side(v2[0], v2[1]));
+          }
+        return;
+      }
     }
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
