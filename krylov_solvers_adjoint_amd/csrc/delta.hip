@@ -29,7 +29,7 @@
 //   dq = scale exp(G) (do S^T) + dP k
 //   u  = - exp(G) B (X S^T) - dA k         w = dP^T q - dA^T k + exp(G_L - G) (N dS^T)
 //   dk = u + w       dG_i = q_i.dq_i + k_i.(u_i - w_i), and <S', dS> at the chunk's end
-//   dg = the sums of dG from each token to the chunk's end
+//   dg = the sums of dG from each token to the chunk's end (0 below kGateFloor)
 //
 // Work that does not depend on the state (k_delta_prepare, k_delta_out,
 // k_delta_grads) runs over all chunks at once; what does (k_delta_states,
@@ -46,7 +46,10 @@
 // average, 2^-21 at most.  (An infinite factor becomes NaN.)  Products
 // whose results are only rounded to 16 bits (o, dq, dk) take two parts of
 // their fp32 factors (2^-16 against the half step of 2^-9 or 2^-12).  G is
-// summed in fp64: its differences are exponents.
+// summed in fp64: its differences are exponents.  A gate that resets the state
+// (-infinity, a type's lowest value) would take the later gates' digits out of
+// that sum, or make its differences infinite less infinite: gates below
+// kGateFloor count as kGateFloor, whose exp is the same zero.
 //
 // An operand of the 16 x 16 x 32 instruction holds, in lane (l, h) = (lane %
 // 16, lane / 16), eight k of row (column) l; which eight is free as long as
@@ -69,6 +72,11 @@ constexpr int kDeltaBlock = 256;
 constexpr int kSlice = 32;              // columns of the state a parallel kernel takes at a time
 constexpr int kLdC = kChunk + 4;        // LDS row of 64 floats (padded against bank conflicts)
 constexpr int kWalk = 64;               // columns of the state per walking workgroup
+// exp() of a gate at the floor is 0 in fp32 (from -104 on), and stays 0 beside
+// any growth of a chunk's 63 other gates that exp() holds (88 each); 64 such
+// gates leave the fp64 sum 33 bits behind the point.
+constexpr float kGateFloor = -8192.f;
+__device__ __forceinline__ float floored(float g) { return g < kGateFloor ? kGateFloor : g; }  // NaN stays
 
 struct DeltaShape {
   int64_t total;      // tokens
@@ -592,7 +600,7 @@ __global__ __launch_bounds__(kDeltaBlock) void k_delta_prepare(DeltaShape s, Del
   }
   if (t < kChunk) {
     const int64_t at = (p.tok + t) * s.hv + vh;
-    double g = t < p.len ? double(in.g[at]) : 0.0;
+    double g = t < p.len ? double(floored(in.g[at])) : 0.0;
 #pragma unroll
     for (int d = 1; d < kWave; d <<= 1) {
       const double u = __shfl_up(g, d, kWave);
@@ -1567,7 +1575,11 @@ __global__ __launch_bounds__(kDeltaBlock, kParts<T> == 1 && !SHARED ? 2 : 1) voi
           const double u = __shfl_up(x, d, kWave);
           if (t >= d) x += u;
         }
-        if (row < p.len) dg[(p.tok + row) * s.hv + vh] = float(x);
+        if (row < p.len) {
+          // behind exp(g) = 0 nothing depends on g: not the sums' roundings either
+          const int64_t at = (p.tok + row) * s.hv + vh;
+          dg[at] = in.g[at] < kGateFloor ? 0.f : float(x);
+        }
       }
     }
   }

@@ -389,7 +389,8 @@ def gated_delta_rule(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch
 
     q, k [batch, tokens, heads, dk] (dk <= 128); v [batch, tokens, value_heads,
     dv], value_heads a multiple of heads (neighbouring value heads share a key
-    head); g (log decay, <= 0) and beta float32 [batch, tokens, value_heads].
+    head); g (log decay, <= 0; -inf or a type's lowest value begins the state
+    anew, with a gradient of 0) and beta float32 [batch, tokens, value_heads].
     scale defaults to 1 / sqrt(dk).  States are float32 [sequences,
     value_heads, dk, dv]; without an initial state they begin at zero.
 
