@@ -22,6 +22,7 @@ import functools
 import math
 
 import torch
+import torch.autograd.forward_ad as forward_ad
 from torch.autograd.function import once_differentiable
 
 from . import _I64, _check, _lib
@@ -109,9 +110,15 @@ def _ptr(t):
 
 
 def _wants(*tensors) -> bool:
+    """Whether a derivative is asked for: a gradient, or a tangent (which does
+    not require grad and passes no_grad; the autograd nodes refuse it)."""
     if torch.is_grad_enabled():
         for t in tensors:
             if t is not None and t.requires_grad:
+                return True
+    if forward_ad._current_level >= 0:
+        for t in tensors:
+            if t is not None and forward_ad.unpack_dual(t).tangent is not None:
                 return True
     return False
 
@@ -455,12 +462,14 @@ def gated_delta_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch
     q, k [sequences, heads, dk], v [sequences, value_heads, dv], g and beta
     float32 [sequences, value_heads], state float32 [sequences, value_heads,
     dk, dv], contiguous, as gated_delta_rule returns it.  For serving: it has
-    no gradient, and refuses inputs that ask for one."""
+    no derivative, and refuses inputs that ask for a gradient or carry a
+    tangent."""
     scale = _check_delta(q, k, v, g, beta, scale, 1)
     _tensor(state, "state", q, (torch.float32,))
     _sized(state, (q.shape[0], v.shape[1], q.shape[2], v.shape[2]), "state")
     if not state.is_contiguous():
         raise ValueError("state: expected a contiguous tensor (it is updated in place)")
     if _wants(q, k, v, g, beta, state):
-        raise ValueError("gated_delta_step has no gradient: use gated_delta_rule, or no_grad")
+        raise ValueError("gated_delta_step has no gradient (and no tangent): use "
+                         "gated_delta_rule, or no_grad and plain inputs")
     return sla_delta_step(q, k, v, g.contiguous(), beta.contiguous(), state, scale)

@@ -41,3 +41,33 @@ def test_a_gate_that_is_no_number_shows():
     o, s = K.gated_delta_rule(*(t.cuda() for t in ins[:5]), initial_state=ins[5].cuda(),
                               output_final_state=True)
     assert o[0, 30:].isnan().all() and s.isnan().all()
+
+
+# ---------------------------------------------------------------------------
+# Forward-mode derivatives
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("grad", [True, False])
+def test_tangents_are_refused(grad):
+    """They were dropped: a result without a tangent stands for a zero one."""
+    import krylov_solvers_adjoint_amd as K
+    import torch.autograd.forward_ad as fw
+    x = torch.randn(1, 5, 2, 16, device="cuda")
+    w = torch.randn(24, 16, device="cuda")
+    g = -torch.rand(1, 5, 2, device="cuda")
+    s = torch.zeros(1, 2, 16, 16, device="cuda")
+    with fw.dual_level(), torch.set_grad_enabled(grad):
+        d = fw.make_dual(x, torch.ones_like(x))
+        dg = fw.make_dual(g, torch.ones_like(g))
+        for call in (lambda: K.layer_norm(d), lambda: K.gated_ffn(d, w, w),
+                     lambda: K.gated_ffn(x, w, fw.make_dual(w, w)),
+                     lambda: K.gated_delta_rule(d, x, x, g, g),
+                     lambda: K.gated_delta_rule(x, x, x, dg, g)):
+            with pytest.raises(NotImplementedError):
+                call()
+        with pytest.raises(ValueError):
+            K.gated_delta_step(x[:, 0], x[:, 0], x[:, 0], dg[:, 0], g[:, 0], s)
+        assert not s.any()
+        # nothing that carries a tangent: as ever
+        assert torch.equal(K.layer_norm(x), K.layer_norm(x.clone()))
+    with pytest.raises(RuntimeError):
+        torch.func.jvp(lambda t: K.layer_norm(t), (x,), (x,))

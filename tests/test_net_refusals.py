@@ -156,3 +156,28 @@ def test_other_views_are_copied(make, tail):
     for n in t.shape[t.dim() - tail:]:
         width *= n
     assert ld == width
+
+
+def test_tangents_go_to_the_autograd_nodes_and_are_refused_there():
+    """A dual tensor does not require grad: called directly, a kernel would drop
+    its tangent in silence."""
+    import torch.autograd.forward_ad as fw
+    x = torch.randn(3, 4)
+    assert not net._wants(x, None)
+    with fw.dual_level():
+        d = fw.make_dual(x, torch.ones_like(x))
+        assert not net._wants(x, None)
+        assert net._wants(x, None, d)
+        with torch.no_grad():
+            assert net._wants(d)
+    y = x.clone()
+    with fw.dual_level(), pytest.MonkeyPatch.context() as m:
+        m.setattr(net, "sla_layer_norm", lambda *a, **k: (y, y))
+        m.setattr(net, "sla_gated_ffn", lambda *a, **k: y)
+        m.setattr(net, "sla_delta_rule", lambda *a, **k: (y, y, y))
+        d = fw.make_dual(x, torch.ones_like(x))
+        for call in (lambda: net._LayerNorm.apply(d, x, x, 1e-5),
+                     lambda: net._GatedFFN.apply(x, d, x, 0),
+                     lambda: net._DeltaRule.apply(x, x, x, d, x, None, None, 1, 1.0, True)):
+            with pytest.raises(NotImplementedError):
+                call()
