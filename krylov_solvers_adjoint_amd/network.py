@@ -8,7 +8,9 @@ As everywhere in this package a function marshals its arguments and calls the
 C ABI of the same name (``include/sla.h``); the autograd nodes stand on top.
 Work is enqueued on the current stream, workspaces come from PyTorch's
 allocator on that stream, nothing synchronises, and the same inputs give the
-same bits.
+same bits.  The sla_* functions take another stream too: everything they do
+then happens on it, so it has to be ordered behind the inputs, which live until
+it is done, and what is returned belongs to it.
 
 Inputs may be views whose last axis is contiguous and whose rows (tokens) are
 evenly spaced, such as the parts of one fused projection; any other layout is
@@ -19,6 +21,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import inspect
 import math
 
 import torch
@@ -55,12 +58,36 @@ def _tensor(t, name: str, like: torch.Tensor | None = None, dtypes=None) -> torc
     return t
 
 
-def _stream(stream, like: torch.Tensor) -> int:
-    """The raw stream: `stream`, or the current one of like's device.  (The
-    stream object of torch.cuda costs as much as a launch.)"""
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(like.get_device())
-    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+def _stream(like: torch.Tensor) -> int:
+    """The raw current stream of like's device.  (The stream object of
+    torch.cuda costs as much as a launch.)"""
+    return torch._C._cuda_getCurrentRawStream(like.get_device())
+
+
+def _takes_stream(f):
+    """f(..., stream=None): all of f on that stream (a torch stream or a raw
+    one), its copies and allocations included.  Memory of another stream's pool
+    would be given out again while the kernels still use it."""
+    signature = inspect.signature(f)
+    known = [*signature.parameters.values()]
+    extra = inspect.Parameter("stream", inspect.Parameter.POSITIONAL_OR_KEYWORD, default=None)
+
+    @functools.wraps(f)
+    def call(*args, **kwargs):
+        stream = kwargs.pop("stream", None)
+        if len(args) > len(known):
+            *args, stream = args
+        if stream is None:
+            return f(*args, **kwargs)
+        if not hasattr(stream, "cuda_stream"):
+            device = next(t for t in (*args, *kwargs.values())
+                          if isinstance(t, torch.Tensor)).device
+            stream = torch.cuda.ExternalStream(int(stream), device=device) if int(stream) \
+                else torch.cuda.default_stream(device)
+        with torch.cuda.stream(stream):
+            return f(*args, **kwargs)
+    call.__signature__ = signature.replace(parameters=[*known, extra])
+    return call
 
 
 @functools.lru_cache(maxsize=1024)
@@ -130,7 +157,8 @@ def _block(nbytes: int, like: torch.Tensor) -> torch.Tensor:
 # ---------------------------------------------------------------------------
 # Layer norm
 # ---------------------------------------------------------------------------
-def sla_layer_norm(x, weight, bias, eps: float, want_stats: bool = False, stream=None):
+@_takes_stream
+def sla_layer_norm(x, weight, bias, eps: float, want_stats: bool = False):
     """(y, stats): stats [rows, 2] = mean less the row's first element and
     1 / sqrt(var + eps), or None."""
     cols = x.shape[-1]
@@ -141,12 +169,13 @@ def sla_layer_norm(x, weight, bias, eps: float, want_stats: bool = False, stream
     par = weight if weight is not None else bias
     _check(_lib.sla_layer_norm(x.data_ptr(), ld, rows, cols, _TYPES[x.dtype], _ptr(weight),
                                _ptr(bias), _TYPES[par.dtype if par is not None else x.dtype],
-                               eps, y.data_ptr(), _ptr(stats), _stream(stream, x)))
+                               eps, y.data_ptr(), _ptr(stats), _stream(x)))
     return y, stats
 
 
+@_takes_stream
 def sla_layer_norm_grad(dy, x, weight, stats, want_x=True, want_weight=True, want_bias=True,
-                        wtype=None, stream=None):
+                        wtype=None):
     """(dx, dweight, dbias), None where not wanted."""
     cols = x.shape[-1]
     rows = x.numel() // cols
@@ -163,7 +192,7 @@ def sla_layer_norm_grad(dy, x, weight, stats, want_x=True, want_weight=True, wan
     _check(_lib.sla_layer_norm_grad(dy.data_ptr(), lddy, x.data_ptr(), ldx, rows, cols,
                                     _TYPES[x.dtype], _ptr(weight), _TYPES[wtype],
                                     stats.data_ptr(), _ptr(dx), _ptr(dw), _ptr(db), _ptr(work),
-                                    size, _stream(stream, x)))
+                                    size, _stream(x)))
     return dx, dw, db
 
 
@@ -213,18 +242,20 @@ def layer_norm(x: torch.Tensor, weight: torch.Tensor | None = None,
 # ---------------------------------------------------------------------------
 # The gated feed-forward unit
 # ---------------------------------------------------------------------------
-def sla_gated_ffn(x, w_gate, w_up, act: int, stream=None):
+@_takes_stream
+def sla_gated_ffn(x, w_gate, w_up, act: int):
     """h [..., outer] = f(x w_gate^T) * (x w_up^T)."""
     outer, inner = w_gate.shape
     x, ld = _rows(x, 1)
     h = torch.empty((*x.shape[:-1], outer), dtype=x.dtype, device=x.device)
     _check(_lib.sla_gated_ffn(x.data_ptr(), ld, w_gate.data_ptr(), w_up.data_ptr(),
                               x.numel() // inner, inner, outer, _TYPES[x.dtype], act,
-                              h.data_ptr(), _stream(stream, x)))
+                              h.data_ptr(), _stream(x)))
     return h
 
 
-def sla_gated_ffn_grad(dh, x, w_gate, w_up, act: int, want_x=True, want_w=True, stream=None):
+@_takes_stream
+def sla_gated_ffn_grad(dh, x, w_gate, w_up, act: int, want_x=True, want_w=True):
     """(dx, dw_gate, dw_up), None where not wanted."""
     outer, inner = w_gate.shape
     rows = x.numel() // inner
@@ -238,7 +269,7 @@ def sla_gated_ffn_grad(dh, x, w_gate, w_up, act: int, want_x=True, want_w=True, 
     _check(_lib.sla_gated_ffn_grad(dh.data_ptr(), lddh, x.data_ptr(), ldx, w_gate.data_ptr(),
                                    w_up.data_ptr(), rows, inner, outer, _TYPES[x.dtype], act,
                                    _ptr(dx), _ptr(dwg), _ptr(dwu), work.data_ptr(), size,
-                                   _stream(stream, x)))
+                                   _stream(x)))
     return dx, dwg, dwu
 
 
@@ -308,8 +339,9 @@ def _states(dims, like):
                        dtype=torch.float32, device=like.device)
 
 
+@_takes_stream
 def sla_delta_rule(q, k, v, g, beta, offsets, initial_state, sequences: int, scale: float,
-                   want_state: bool = True, stream=None):
+                   want_state: bool = True):
     """(o, final_state or None, kept): kept is what the gradient reads."""
     dims, at, size, _ = _delta_dims(q, v, sequences, scale, offsets is not None)
     (q, ldq), (k, ldk), (v, ldv) = _rows(q, 2), _rows(k, 2), _rows(v, 2)
@@ -319,12 +351,13 @@ def sla_delta_rule(q, k, v, g, beta, offsets, initial_state, sequences: int, sca
     _check(_lib.sla_delta_rule(at, q.data_ptr(), ldq, k.data_ptr(), ldk,
                                v.data_ptr(), ldv, g.data_ptr(), beta.data_ptr(), _ptr(offsets),
                                _ptr(initial_state), o.data_ptr(), _ptr(state), kept.data_ptr(),
-                               size, _stream(stream, q)))
+                               size, _stream(q)))
     return o, state, kept
 
 
+@_takes_stream
 def sla_delta_rule_grad(q, k, v, g, beta, kept, grad_o, grad_state, sequences: int, scale: float,
-                        packed: bool, want_initial: bool = True, stream=None):
+                        packed: bool, want_initial: bool = True):
     """(dq, dk, dv, dg, dbeta, grad of the initial state or None)."""
     dims, at, _, size = _delta_dims(q, v, sequences, scale, packed)
     (q, ldq), (k, ldk), (v, ldv) = _rows(q, 2), _rows(k, 2), _rows(v, 2)
@@ -337,7 +370,7 @@ def sla_delta_rule_grad(q, k, v, g, beta, kept, grad_o, grad_state, sequences: i
         at, q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv, g.data_ptr(),
         beta.data_ptr(), kept.data_ptr(), kept.numel(), grad_o.data_ptr(), ldo, _ptr(grad_state),
         dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), dg.data_ptr(), dbeta.data_ptr(), _ptr(ds0),
-        work.data_ptr(), size, _stream(stream, q)))
+        work.data_ptr(), size, _stream(q)))
     return dq, dk, dv, dg, dbeta, ds0
 
 
@@ -443,14 +476,15 @@ def gated_delta_rule(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch
                           bool(output_final_state))[:2]
 
 
-def sla_delta_step(q, k, v, g, beta, state, scale: float, stream=None):
+@_takes_stream
+def sla_delta_step(q, k, v, g, beta, state, scale: float):
     """o [sequences, value_heads, dv]; state is updated in place."""
     at = _delta_dims(q, v, q.shape[0], scale, False)[1]
     (q, ldq), (k, ldk), (v, ldv) = _rows(q, 2), _rows(k, 2), _rows(v, 2)
     o = torch.empty(v.shape, dtype=v.dtype, device=v.device)
     _check(_lib.sla_delta_step(at, q.data_ptr(), ldq, k.data_ptr(), ldk,
                                v.data_ptr(), ldv, g.data_ptr(), beta.data_ptr(),
-                               state.data_ptr(), o.data_ptr(), _stream(stream, q)))
+                               state.data_ptr(), o.data_ptr(), _stream(q)))
     return o
 
 

@@ -71,3 +71,74 @@ def test_tangents_are_refused(grad):
         assert torch.equal(K.layer_norm(x), K.layer_norm(x.clone()))
     with pytest.raises(RuntimeError):
         torch.func.jvp(lambda t: K.layer_norm(t), (x,), (x,))
+
+
+# ---------------------------------------------------------------------------
+# Another stream
+# ---------------------------------------------------------------------------
+def test_another_stream_gives_the_same_bits_and_owns_what_it_returns():
+    import krylov_solvers_adjoint_amd as K
+    from krylov_solvers_adjoint_amd import network as net
+    side = torch.cuda.Stream()
+
+    def pool(t):
+        for seg in torch.cuda.memory_snapshot():
+            if seg["address"] <= t.data_ptr() < seg["address"] + seg["total_size"]:
+                return seg["stream"]
+    base = torch.randn(200, 96, generator=R.gen(1)).cuda()
+    x, w = base[:, 3:67], torch.randn(128, 64, generator=R.gen(2)).cuda()
+    xt = torch.randn(64, 200, generator=R.gen(3)).cuda().t()      # copied
+    dh = torch.randn(200, 128, generator=R.gen(4)).cuda()
+    ins, do, ds = D.inputs(2, 100, 1, 2, 32, 48, torch.float32)
+    q, k, v, g, beta, s0 = (t.cuda() for t in ins)
+    do, ds = do.cuda(), ds.cuda()
+
+    def all_of(stream):
+        y, stats = net.sla_layer_norm(xt, None, None, 1e-5, True, stream=stream)
+        out = [y, *net.sla_layer_norm_grad(x, xt, None, stats, stream=stream)]
+        out.append(net.sla_gated_ffn(xt, w, w, 0, stream=stream))
+        out += net.sla_gated_ffn_grad(dh, x, w, w, 0, stream=stream)
+        o, s, kept = net.sla_delta_rule(q, k, v, g, beta, None, s0, 2, 0.2, stream=stream)
+        out += [o, s, *net.sla_delta_rule_grad(q, k, v, g, beta, kept, do, ds, 2, 0.2, False,
+                                               stream=stream)]
+        kept = s0.clone()
+        torch.cuda.synchronize()
+        out.append(net.sla_delta_step(q[:, 0], k[:, 0], v[:, 0], g[:, 0].contiguous(),
+                                      beta[:, 0].contiguous(), kept, 0.2, stream=stream))
+        torch.cuda.synchronize()
+        return [*out, kept]
+    want = all_of(None)
+    for stream in (side, side.cuda_stream, 0):
+        torch.cuda.synchronize()
+        got = all_of(stream)
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+        owner = 0 if stream == 0 else side.cuda_stream
+        assert all(pool(t) == owner for t in got[:-1])
+    torch.cuda.synchronize()
+
+
+def test_the_operators_on_a_side_stream_give_the_bits_of_the_default_one():
+    import krylov_solvers_adjoint_amd as K
+    x = torch.randn(300, 64, generator=R.gen(1)).cuda()
+    w = torch.randn(96, 64, generator=R.gen(2)).cuda()
+    ins, do, ds = D.inputs(1, 150, 1, 2, 32, 48, torch.bfloat16)
+    dev = [t.cuda() for t in ins]
+    do, ds = do.cuda(), ds.cuda()
+
+    def all_of():
+        a, b, c = (t.clone().requires_grad_() for t in (x, w, w))
+        n = K.layer_norm(a, b[0], c[0])
+        h = K.gated_ffn(n, b, c)
+        out = [n.detach(), h.detach(), *torch.autograd.grad(h.sum(), (a, b, c))]
+        leaves = [t.clone().requires_grad_() for t in dev]
+        o, s = K.gated_delta_rule(*leaves[:5], initial_state=leaves[5], output_final_state=True)
+        return [*out, o.detach(), s.detach(), *torch.autograd.grad((o, s), leaves, (do, ds))]
+    want = all_of()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = all_of()
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)

@@ -181,3 +181,72 @@ def test_tangents_go_to_the_autograd_nodes_and_are_refused_there():
                      lambda: net._DeltaRule.apply(x, x, x, d, x, None, None, 1, 1.0, True)):
             with pytest.raises(NotImplementedError):
                 call()
+
+
+def test_another_stream_gets_the_copies_and_the_memory_too(monkeypatch):
+    """With stream= everything of an sla_* call happens on that stream.  Memory
+    of the current stream's pool would go back to it on return, while the
+    kernels on the other stream still use it."""
+    import contextlib
+    import types
+    inside, seen = [None], []
+    other = types.SimpleNamespace(cuda_stream=77)
+
+    @contextlib.contextmanager
+    def on(stream):
+        inside[0] = stream.cuda_stream
+        yield
+        inside[0] = None
+    monkeypatch.setattr(torch.cuda, "stream", on)
+    monkeypatch.setattr(torch.cuda, "ExternalStream",
+                        lambda raw, device=None: types.SimpleNamespace(cuda_stream=raw))
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: inside[0] or 11,
+                        raising=False)
+    empty, empty_like = torch.empty, torch.empty_like
+
+    def allocate(make):
+        def call(*a, **k):
+            seen.append(("memory", inside[0]))
+            return make(*a, **k)
+        return call
+    monkeypatch.setattr(torch, "empty", allocate(empty))
+    monkeypatch.setattr(torch, "empty_like", allocate(empty_like))
+    rows = net._rows
+
+    def copied(t, tail):
+        seen.append(("copy", inside[0]))
+        return rows(t, tail)
+    monkeypatch.setattr(net, "_rows", copied)
+
+    def kernel(*args):
+        seen.append(("kernel", args[-1]))
+        return 0
+    names = ("sla_layer_norm", "sla_layer_norm_grad", "sla_gated_ffn", "sla_gated_ffn_grad",
+             "sla_delta_rule", "sla_delta_rule_grad", "sla_delta_step")
+    monkeypatch.setattr(net, "_lib", types.SimpleNamespace(**{n: kernel for n in names}))
+    monkeypatch.setattr(net, "_work_bytes", lambda *a: 64)
+    monkeypatch.setattr(net, "_delta_dims", lambda *a: (dims(), None, 64, 64))
+    x, w, stats = torch.zeros(8, 4).t(), torch.zeros(16, 8), torch.zeros(4, 2)
+    q = torch.zeros(2, 4, 2, 16)
+    v, gate = torch.zeros(2, 4, 4, 24), torch.zeros(2, 4, 4)
+    s = torch.zeros(2, 4, 16, 24)
+    calls = {
+        "sla_layer_norm": (x, None, None, 1e-5, True),
+        "sla_layer_norm_grad": (x, x, None, stats, True, True, True, None),
+        "sla_gated_ffn": (x, w, w, 0),
+        "sla_gated_ffn_grad": (torch.zeros(4, 16), x, w, w, 0, True, True),
+        "sla_delta_rule": (q, q, v, gate, gate, None, None, 2, 1.0, True),
+        "sla_delta_rule_grad": (q, q, v, gate, gate, s, v, None, 2, 1.0, False, True),
+        "sla_delta_step": (q[:, 0], q[:, 0], v[:, 0], gate[:, 0], gate[:, 0], s, 1.0),
+    }
+    for name in names:
+        f, args = getattr(net, name), calls[name]
+        for how in (lambda: f(*args, other), lambda: f(*args, stream=other),
+                    lambda: f(*args, stream=77)):
+            seen.clear()
+            how()
+            assert {what for what, _ in seen} == {"memory", "copy", "kernel"}
+            assert all(stream == 77 for _, stream in seen), (name, seen)
+        seen.clear()
+        f(*args)
+        assert all(stream in (None, 11) for _, stream in seen), (name, seen)
