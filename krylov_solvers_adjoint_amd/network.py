@@ -485,6 +485,7 @@ def sla_delta_step(q, k, v, g, beta, state, scale: float):
     _check(_lib.sla_delta_step(at, q.data_ptr(), ldq, k.data_ptr(), ldk,
                                v.data_ptr(), ldv, g.data_ptr(), beta.data_ptr(),
                                state.data_ptr(), o.data_ptr(), _stream(q)))
+    torch.autograd.graph.increment_version(state)  # a graph that saved it has to notice
     return o
 
 

@@ -142,3 +142,18 @@ def test_the_operators_on_a_side_stream_give_the_bits_of_the_default_one():
     torch.cuda.synchronize()
     for a, b in zip(got, want):
         assert torch.equal(a, b)
+
+
+# ---------------------------------------------------------------------------
+# A state that a graph has saved
+# ---------------------------------------------------------------------------
+def test_a_step_on_a_saved_state_is_noticed():
+    import krylov_solvers_adjoint_amd as K
+    ins, _, _ = D.inputs(1, 20, 1, 2, 16, 24, torch.float32)
+    leaves = [t.cuda().requires_grad_() for t in ins]
+    _, state = K.gated_delta_rule(*leaves[:5], initial_state=leaves[5], output_final_state=True)
+    loss = state.square().sum()
+    with torch.no_grad():
+        K.gated_delta_step(*(t[:, 0] for t in leaves[:5]), state.detach())
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()

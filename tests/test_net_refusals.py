@@ -250,3 +250,20 @@ def test_another_stream_gets_the_copies_and_the_memory_too(monkeypatch):
         seen.clear()
         f(*args)
         assert all(stream in (None, 11) for _, stream in seen), (name, seen)
+
+
+def test_a_step_counts_as_a_change_of_its_state(monkeypatch):
+    """The kernel writes through a pointer; autograd learns of it by the version."""
+    import types
+    monkeypatch.setattr(net, "_lib", types.SimpleNamespace(sla_delta_step=lambda *a: 0))
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: 0, raising=False)
+    q, gate = torch.zeros(2, 1, 4), torch.zeros(2, 1)
+    leaf = torch.randn(2, 1, 4, 4, requires_grad=True)
+    state = leaf.clone()
+    loss = state.square().sum()
+    net.sla_delta_step(q, q, q, gate, gate, state.detach(), 1.0)
+    assert state._version == 1
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+    with torch.inference_mode():
+        net.sla_delta_step(q, q, q, gate, gate, torch.zeros(2, 1, 4, 4), 1.0)
