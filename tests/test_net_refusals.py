@@ -256,6 +256,7 @@ def test_a_step_counts_as_a_change_of_its_state(monkeypatch):
     """The kernel writes through a pointer; autograd learns of it by the version."""
     import types
     monkeypatch.setattr(net, "_lib", types.SimpleNamespace(sla_delta_step=lambda *a: 0))
+    monkeypatch.setattr(net, "_delta_dims", lambda *a: (dims(), None, 64, 64))
     monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: 0, raising=False)
     q, gate = torch.zeros(2, 1, 4), torch.zeros(2, 1)
     leaf = torch.randn(2, 1, 4, 4, requires_grad=True)
