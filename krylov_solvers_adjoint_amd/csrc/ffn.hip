@@ -63,8 +63,8 @@ __device__ __forceinline__ void activation(float a, float& f, float& df) {
     f = a * c;
     df = c + a * (0.39894228040143268f * e);
   } else {
-    f = a > 0.f ? a : a * 0.f;  // NaN stays NaN
-    df = a > 0.f ? 1.f : 0.f;
+    f = a < 0.f ? 0.f : a;  // 0 at -inf; NaN stays NaN, the slope's too
+    df = a > 0.f ? 1.f : a <= 0.f ? 0.f : a;
   }
 }
 

@@ -157,3 +157,27 @@ def test_a_step_on_a_saved_state_is_noticed():
         K.gated_delta_step(*(t[:, 0] for t in leaves[:5]), state.detach())
     with pytest.raises(RuntimeError, match="modified by an inplace operation"):
         loss.backward()
+
+
+# ---------------------------------------------------------------------------
+# Activations
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("kind", ["fp32", "bf16"])
+@pytest.mark.parametrize("rows", [1, 80])
+def test_relu_of_minus_infinity_is_zero(kind, rows):
+    """a overflows to -inf where the definition has 0 and a slope of 0."""
+    import krylov_solvers_adjoint_amd as K
+    dtype = R.TYPES[kind]
+    x = torch.full((rows, 1), 3e38).to(dtype)
+    wg, wu = torch.tensor([[-3e38]]).to(dtype), torch.tensor([[1e-38]]).to(dtype)
+    leaves = [t.cuda().requires_grad_() for t in (x, wg, wu)]
+    h = K.gated_ffn(*leaves, "relu")
+    assert not h.any() and h.isfinite().all()
+    for t in torch.autograd.grad(h, leaves, torch.ones_like(h)):
+        assert not t.any() and t.isfinite().all()
+    # what is no number stays that, in h and in the gradients
+    leaves[0] = torch.full_like(leaves[0], math.nan).requires_grad_()
+    h = K.gated_ffn(*leaves, "relu")
+    assert h.isnan().all()
+    for t in torch.autograd.grad(h, leaves, torch.ones_like(h)):
+        assert t.isnan().all()
