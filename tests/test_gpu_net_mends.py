@@ -181,3 +181,24 @@ def test_relu_of_minus_infinity_is_zero(kind, rows):
     assert h.isnan().all()
     for t in torch.autograd.grad(h, leaves, torch.ones_like(h)):
         assert t.isnan().all()
+
+
+@pytest.mark.parametrize("kind", ["fp16", "bf16"])
+@pytest.mark.parametrize("few", [True, False])
+def test_gelu_keeps_its_relative_precision_in_the_tail(kind, few):
+    """f(a) b for single values of a (exact in the type), b = 2^15 so that fp16
+    holds f down to 2^-29: the output's rounding (half a step) and 2^-15 for
+    exp, its argument's rounding and the fit, all relative."""
+    import krylov_solvers_adjoint_amd as K
+    dtype = R.TYPES[kind]
+    a = torch.linspace(-12, 3, 4001).to(dtype)
+    x = torch.stack([a, torch.ones_like(a)], 1)
+    wg, wu = (torch.tensor([w]).to(dtype) for w in ([1.0, 0.0], [0.0, 2.0 ** 15]))
+    parts = x.cuda().split(50) if few else [x.cuda()]
+    h = torch.cat([K.gated_ffn(p, wg.cuda(), wu.cuda(), "gelu") for p in parts])[:, 0]
+    want = R.activation(a.double(), "gelu") * 2.0 ** 15
+    tol = (R.half_step(dtype) + 2.0 ** -15) * want.abs()
+    tol += 2.0 ** -25 if kind == "fp16" else 2.0 ** -126     # the type's smallest steps
+    held = want.abs() <= torch.finfo(dtype).max
+    bad = ((h.cpu().double() - want).abs() > tol) & held
+    assert not bad.any(), (a[bad], ((h.cpu().double() - want).abs() / want.abs())[bad].max())
