@@ -61,7 +61,7 @@ __device__ __forceinline__ void activation(float a, float& f, float& df) {
       c = a < 0.f ? c : 1.f - c;
     } else {
       e = expf(-0.5f * a * a);
-      c = 0.5f * (1.f + erff(a * 0.70710678118654752f));
+      c = 0.5f * erfcf(a * -0.70710678118654752f);   // 1 + erf() would cancel in the tail
     }
     f = a * c;
     df = c + a * (0.39894228040143268f * e);

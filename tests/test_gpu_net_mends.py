@@ -202,3 +202,19 @@ def test_gelu_keeps_its_relative_precision_in_the_tail(kind, few):
     held = want.abs() <= torch.finfo(dtype).max
     bad = ((h.cpu().double() - want).abs() > tol) & held
     assert not bad.any(), (a[bad], ((h.cpu().double() - want).abs() / want.abs())[bad].max())
+
+
+@pytest.mark.parametrize("few", [True, False])
+def test_gelu_keeps_its_relative_precision_in_fp32(few):
+    """f(a) by itself (b = 1): erfc's argument is rounded once, which its tail
+    multiplies by a^2; 32 roundings for erfc, the products and the output."""
+    import krylov_solvers_adjoint_amd as K
+    a = torch.linspace(-12, 6, 4001)
+    x = torch.stack([a, torch.ones_like(a)], 1)
+    wg, wu = torch.tensor([[1.0, 0.0]]), torch.tensor([[0.0, 1.0]])
+    parts = x.cuda().split(50) if few else [x.cuda()]
+    h = torch.cat([K.gated_ffn(p, wg.cuda(), wu.cuda(), "gelu") for p in parts])[:, 0]
+    a = a.double()
+    want = R.activation(a, "gelu")
+    bad = (h.cpu().double() - want).abs() > (2 * a * a + 32) * R.U32 * want.abs()
+    assert not bad.any(), (a[bad], ((h.cpu().double() - want).abs() / want.abs())[bad].max())
