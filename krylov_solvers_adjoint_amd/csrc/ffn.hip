@@ -11,7 +11,11 @@
 // than keep them.  da and db are rounded once to the inputs' type, the factors'
 // type of the products that follow: keeping fp32 would halve nothing and
 // double the bytes, and the 16-bit matrix instructions take 16-bit factors.
-// All sums are fp32.
+// That adds half a step to dx and dW (2.35e-3 instead of 1.7e-3 in bf16).
+// fp16 has not the range besides: products of a small dh fell below 2^-24, of
+// a large one passed 65504, where dx and dW are ordinary numbers.  Its da and
+// db are held times a power of two, taken from a bound on the largest of them
+// (k_ffn_bound), and dx and dW are multiplied back.  All sums are fp32.
 #include <type_traits>
 
 #include "net.h"
@@ -82,6 +86,7 @@ struct Product {
   const void* dh;    // EPI_GATE_GRAD [M][N]
   int64_t lddh;
   void* C[2];        // EPI_GATE: h; EPI_GATE_GRAD: da, db; EPI_STORE: one per output
+  const float* scale;   // fp16 gradients: {what da and db are held times, its inverse}
   int64_t ldc;
   int act;
   // filled by the launch
@@ -382,13 +387,20 @@ __device__ __forceinline__ void with_activation(const Product& g, F&& f) {
   else f(std::integral_constant<int, SLA_ACT_RELU>());
 }
 
+// What a product's results are multiplied with on their way out.
+template <typename T, int EPI>
+__device__ __forceinline__ float scale_of(const Product& g) {
+  if constexpr (std::is_same<T, _Float16>::value && EPI != EPI_GATE)
+    return g.scale ? g.scale[EPI == EPI_STORE] : 1.f;   // (no rows: none)
+  return 1.f;
+}
 // What becomes of four columns of a row (d: dh there): u, and v for db.
 template <typename T, int EPI, int ACT>
 __device__ __forceinline__ void result(const float (&d)[4], const f32x4& a, const f32x4& b,
-                                       float (&u)[4], float (&v)[4]) {
+                                       float scale, float (&u)[4], float (&v)[4]) {
   if constexpr (EPI == EPI_STORE) {
 #pragma unroll
-    for (int r = 0; r < 4; ++r) u[r] = a[r];
+    for (int r = 0; r < 4; ++r) u[r] = a[r] * scale;
   } else {
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
@@ -397,8 +409,9 @@ __device__ __forceinline__ void result(const float (&d)[4], const f32x4& a, cons
       if constexpr (EPI == EPI_GATE) {
         u[r] = f * b[r];
       } else {
-        u[r] = d[r] * b[r] * df;
-        v[r] = d[r] * f;
+        const float e = d[r] * scale;
+        u[r] = e * b[r] * df;
+        v[r] = e * f;
       }
     }
   }
@@ -408,7 +421,7 @@ template <typename T, int EPI, int ACT>
 __device__ __forceinline__ void leave(const Product& g, int64_t at, const float (&d)[4],
                                       int64_t have, int z, const f32x4& a, const f32x4& b) {
   float u[4], v[4];
-  result<T, EPI, ACT>(d, a, b, u, v);
+  result<T, EPI, ACT>(d, a, b, scale_of<T, EPI>(g), u, v);
   store_f32<4>((T*)(EPI == EPI_STORE && z ? g.C[1] : g.C[0]) + at, have, u);
   if constexpr (EPI == EPI_GATE_GRAD) store_f32<4>((T*)g.C[1] + at, have, v);
 }
@@ -700,6 +713,7 @@ __global__ __launch_bounds__(kWave* B* B / WM / WN, 2) void k_ffn_product(Produc
       if (kGate || !part) {
         T* c0 = (T*)(EPI == EPI_STORE && at.z ? g.C[1] : g.C[0]) + at_c + wide;
         T* c1 = (T*)g.C[1] + at_c + wide;
+        const float scale = scale_of<T, EPI>(g);
 #pragma unroll
         for (int i = 0; i < NI; ++i, c0 += 16 * g.ldc, c1 += 16 * g.ldc)
 #pragma unroll
@@ -713,7 +727,7 @@ __global__ __launch_bounds__(kWave* B* B / WM / WN, 2) void k_ffn_product(Produc
                 for (int r = 0; r < 4; ++r) d[r] = float(dh[i][j + n][r]);
               }
               result<T, EPI, act.value>(d, acc[i][j + n], acc[i][kGate ? j + n + NJ / 2 : j + n],
-                                        u, v);
+                                        scale, u, v);
               u2[n] = packed<Half>(u);
               v2[n] = packed<Half>(v);
             }
@@ -770,7 +784,82 @@ __global__ __launch_bounds__(kFfnBlock) void k_ffn_join(Product g) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) s[j] += u[j];
   }
+  const float scale = scale_of<T, EPI_STORE>(g);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) s[j] *= scale;
   store_f32<4>((T*)g.C[blockIdx.y] + i, size - i, s);
+}
+
+// fp16's da and db: |da| <= 1.13 |dh| |b| and |db| <= |dh| |a| (no activation is
+// steeper than 1.13 or larger than its argument), and |a|, |b| <= the norm of a
+// row of x times that of a row of the weights.  A wave takes a line of one of
+// the four arrays at a time; values that are not finite count nothing (what is
+// made of them is not finite either).  parts: three maxima a workgroup.  Reading
+// the arrays is the work: 46 us for the 184 MB of 16384 x 1024 x 4096 (4.0 TB/s),
+// of 1090 for the training step.
+constexpr int kBoundGroups = 1024;
+struct Lines {
+  const _Float16* p;
+  int64_t ld, count;
+  int width;
+};
+__device__ __forceinline__ float line_max(const Lines& s, int64_t line, bool square) {
+  const _Float16* p = s.p + line * s.ld;
+  float m = 0.f;
+  for (int64_t c = threadIdx.x % kWave * 8; c < s.width; c += kWave * 8) {
+    float v[8];
+    load_f32<8>(p + c, s.width - c, v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (square) m += v[i] * v[i];
+      else m = fmaxf(m, fabsf(v[i]) <= 65504.f ? fabsf(v[i]) : 0.f);
+    }
+  }
+#pragma unroll
+  for (int d = 1; d < kWave; d <<= 1) {
+    const float o = __shfl_xor(m, d, kWave);
+    m = square ? m + o : fmaxf(m, o);
+  }
+  return m < __builtin_inff() ? m : 0.f;
+}
+__global__ __launch_bounds__(kFfnBlock) void k_ffn_bound(Lines dh, Lines x, Lines wg, Lines wu,
+                                                         float* __restrict__ parts) {
+  constexpr int kWaves = kFfnBlock / kWave;
+  __shared__ float best[3][kWaves];
+  const int w = threadIdx.x / kWave;
+  const int64_t from = int64_t(blockIdx.x) * kWaves + w, step = int64_t(gridDim.x) * kWaves;
+  float m[3] = {0.f, 0.f, 0.f};
+  for (int64_t i = from; i < dh.count; i += step) m[0] = fmaxf(m[0], line_max(dh, i, false));
+  for (int64_t i = from; i < x.count; i += step) m[1] = fmaxf(m[1], line_max(x, i, true));
+  for (int64_t i = from; i < wg.count; i += step)
+    m[2] = fmaxf(m[2], fmaxf(line_max(wg, i, true), line_max(wu, i, true)));
+#pragma unroll
+  for (int k = 0; k < 3; ++k)
+    if (threadIdx.x % kWave == 0) best[k][w] = m[k];
+  __syncthreads();
+  if (threadIdx.x < 3) {
+    float v = 0.f;
+    for (int i = 0; i < kWaves; ++i) v = fmaxf(v, best[threadIdx.x][i]);
+    parts[3 * blockIdx.x + threadIdx.x] = v;
+  }
+}
+// The power of two that brings the bound to 2^14 .. 2^15, and its inverse.
+__global__ __launch_bounds__(kWave) void k_ffn_scale(const float* __restrict__ parts, int groups,
+                                                     float* __restrict__ scale) {
+  float m[3] = {0.f, 0.f, 0.f};
+  for (int i = threadIdx.x; i < groups; i += kWave)
+#pragma unroll
+    for (int k = 0; k < 3; ++k) m[k] = fmaxf(m[k], parts[3 * i + k]);
+#pragma unroll
+  for (int k = 0; k < 3; ++k)
+#pragma unroll
+    for (int d = 1; d < kWave; d <<= 1) m[k] = fmaxf(m[k], __shfl_xor(m[k], d, kWave));
+  if (threadIdx.x == 0) {
+    const float bound = 1.13f * m[0] * sqrtf(m[1]) * sqrtf(m[2]);
+    const int up = bound > 0.f ? 14 - ilogbf(bound) : 0;
+    scale[0] = ldexpf(1.f, up);
+    scale[1] = ldexpf(1.f, -up);
+  }
 }
 
 // The projections of few rows (at most 16 RT): reading the weights is the
@@ -999,15 +1088,17 @@ sla_status ffn_args(const char* who, int64_t rows, int64_t inner, int64_t outer,
   return SLA_OK;
 }
 
-// The workspace: da, db, then the sums of a split product (dx and the weights'
-// gradients use the same place one after the other).
+// The workspace: da, db, fp16's scale and what it comes from, then the sums of a
+// split product (dx and the weights' gradients use the same place one after the
+// other).
+constexpr int64_t kScaleBytes = 256 + kBoundGroups * 12;
 int64_t factor_bytes(int64_t rows, int64_t outer, int es) {
   return div_up(rows * outer * es, 256) * 256;
 }
 int64_t grad_bytes(int64_t rows, int64_t inner, int64_t outer, int es) {
   const int64_t x = split_bytes(rows, inner, outer, 2, 1, 1, es);
   const int64_t w = split_bytes(outer, inner, rows, 1, 2, 2, es);
-  return 2 * factor_bytes(rows, outer, es) + (x > w ? x : w);
+  return 2 * factor_bytes(rows, outer, es) + kScaleBytes + (x > w ? x : w);
 }
 
 template <typename F>
@@ -1093,8 +1184,23 @@ sla_status sla_gated_ffn_grad(const void* dh, int64_t lddh, const void* x, int64
     g.C[1] = (char*)work + size;
     g.ldc = outer;
     g.act = act;
+    float* scale = nullptr;
+    if (std::is_same<T, _Float16>::value && rows) {
+      scale = (float*)((char*)work + 2 * size);
+      const int64_t lines = rows > outer ? rows : outer;
+      const int groups = int(lines < 4 * kBoundGroups ? div_up(lines, 4) : kBoundGroups);
+      const Lines ld = {(const _Float16*)dh, lddh, rows, int(outer)};
+      const Lines lx = {(const _Float16*)x, ldx, rows, int(inner)};
+      const Lines lg = {(const _Float16*)w_gate, inner, outer, int(inner)};
+      const Lines lu = {(const _Float16*)w_up, inner, outer, int(inner)};
+      k_ffn_bound<<<groups, kFfnBlock, 0, stream>>>(ld, lx, lg, lu, scale + 64);
+      LAUNCH_CHECK();
+      k_ffn_scale<<<1, kWave, 0, stream>>>(scale + 64, groups, scale);
+      LAUNCH_CHECK();
+    }
+    g.scale = scale;
     SLA_TRY((launch_product<T, false, false, EPI_GATE_GRAD>(g, stream)));
-    float* part = (float*)((char*)work + 2 * size);
+    float* part = (float*)((char*)work + 2 * size + kScaleBytes);
     if (dx) {
       Product p{};
       p.A[0] = g.C[0], p.A[1] = g.C[1];
@@ -1102,6 +1208,7 @@ sla_status sla_gated_ffn_grad(const void* dh, int64_t lddh, const void* x, int64
       p.lda = outer, p.ldb = inner;
       p.M = rows, p.N = inner, p.K = outer, p.parts = 2, p.outputs = 1;
       p.part = part;
+      p.scale = scale;
       p.C[0] = dx;
       p.ldc = inner;
       SLA_TRY((launch_product<T, false, true, EPI_STORE>(p, stream)));
@@ -1113,6 +1220,7 @@ sla_status sla_gated_ffn_grad(const void* dh, int64_t lddh, const void* x, int64
       p.lda = outer, p.ldb = ldx;
       p.M = outer, p.N = inner, p.K = rows, p.parts = 1, p.outputs = 2;
       p.part = part;
+      p.scale = scale;
       p.C[0] = dw_gate, p.C[1] = dw_up;
       p.ldc = inner;
       SLA_TRY((launch_product<T, true, true, EPI_STORE>(p, stream)));

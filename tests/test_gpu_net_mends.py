@@ -6,6 +6,7 @@ import torch
 
 import net_refs as R
 import test_gpu_net_delta as D
+import test_gpu_net_ffn as F
 
 pytestmark = pytest.mark.gpu
 
@@ -200,7 +201,7 @@ def test_gelu_keeps_its_relative_precision_in_the_tail(kind, few):
     tol = (R.half_step(dtype) + 2.0 ** -15) * want.abs()
     tol += 2.0 ** -25 if kind == "fp16" else 2.0 ** -126     # the type's smallest steps
     held = want.abs() <= torch.finfo(dtype).max
-    bad = ((h.cpu().double() - want).abs() > tol) & held
+    bad = ~((h.cpu().double() - want).abs() <= tol) & held
     assert not bad.any(), (a[bad], ((h.cpu().double() - want).abs() / want.abs())[bad].max())
 
 
@@ -216,5 +217,67 @@ def test_gelu_keeps_its_relative_precision_in_fp32(few):
     h = torch.cat([K.gated_ffn(p, wg.cuda(), wu.cuda(), "gelu") for p in parts])[:, 0]
     a = a.double()
     want = R.activation(a, "gelu")
-    bad = (h.cpu().double() - want).abs() > (2 * a * a + 32) * R.U32 * want.abs()
+    bad = ~((h.cpu().double() - want).abs() <= (2 * a * a + 32) * R.U32 * want.abs())
     assert not bad.any(), (a[bad], ((h.cpu().double() - want).abs() / want.abs())[bad].max())
+
+
+# ---------------------------------------------------------------------------
+# fp16's range between the products of the feed-forward unit's gradient
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("rows, inner, outer", [(40, 64, 96), (300, 64, 96), (300, 65, 97),
+                                                (4096, 256, 2048)])
+@pytest.mark.parametrize("act", ["silu", "gelu", "relu"])
+@pytest.mark.parametrize("size", ["tiny", "small", "one", "large"])
+def test_fp16_gradients_hold_for_every_size_of_dh(rows, inner, outer, act, size):
+    """dx and dW are ordinary fp16 numbers, the products between them are not:
+    below 2^-24 (tiny: dh = 5 of fp16's smallest steps and less, large x and W)
+    or beyond 65504.  The bounds are the operator's own, beside 2^-38 of the
+    largest |da| or |db| that the norms allow (fp16's smallest half step at the
+    scale they are held) and half of fp16's smallest step in the output."""
+    import krylov_solvers_adjoint_amd as K
+    g = R.gen(rows + outer)
+    x = torch.rand(rows, inner, generator=g) - 0.25
+    wg = torch.randn(outer, inner, generator=g) / inner ** 0.5
+    wu = torch.randn(outer, inner, generator=g) / inner ** 0.5
+    dh = torch.rand(rows, outer, generator=g) - 0.25
+    sx, sg, su, sd = {"tiny": (1.0, 512.0, 0.5, 4e-7), "small": (64.0, 0.01, 0.01, 3e-5),
+                      "one": (1.0, 1.0, 1.0, 1.0), "large": (0.01, 0.01, 3e3, 4e3)}[size]
+    x, wg, wu, dh = ((t * s).half().cuda() for t, s in ((x, sx), (wg, sg), (wu, su), (dh, sd)))
+    leaves = [t.requires_grad_() for t in (x, wg, wu)]
+    got = torch.autograd.grad(K.gated_ffn(*leaves, act), leaves, dh)
+    x, wg, wu, dh = (t.detach().double() for t in (x, wg, wu, dh))
+    want = F.bounds(x, wg, wu, dh, act, R.half_step(torch.float16))
+    most = 1.13 * dh.abs().max() * x.norm(dim=1).max() * max(wg.norm(dim=1).max(),
+                                                              wu.norm(dim=1).max())
+    tiny = 2.0 ** -38 * most
+    more = {"dx": tiny * (wg.abs().sum(0) + wu.abs().sum(0)),
+            "dwg": tiny * x.abs().sum(0), "dwu": tiny * x.abs().sum(0)}
+    for name, t in zip(("dx", "dwg", "dwu"), got):
+        ref, tol = want[name]
+        tol = (tol + more[name]) * (1 + 2 ** -6) + 2.0 ** -25
+        t = t.double()
+        # of the largest case some results themselves lie beyond fp16: infinities
+        near = ((t - ref).abs() <= tol) | ((t == ref.sign() * math.inf) & (ref.abs() + tol >= 65520))
+        assert near.all(), (name, int((~near).sum()), t[~near][:4], ref[~near][:4])
+        assert size == "large" or t.isfinite().all()
+
+
+def test_fp16_gradients_beside_values_that_are_not_finite():
+    """A row of them leaves the other rows' dx as they are without it."""
+    import krylov_solvers_adjoint_amd as K
+    x, wg, wu, dh = (t.cuda() for t in F.inputs(100, 64, 96, torch.float16))
+
+    def dx_of(x, dh):
+        leaf = x.clone().requires_grad_()
+        return torch.autograd.grad(K.gated_ffn(leaf, wg, wu), leaf, dh)[0]
+    want = dx_of(x, dh)
+    x2, dh2 = x.clone(), dh.clone()
+    x2[3, 5], x2[70, 1], dh2[9, 9], dh2[60, 2] = math.inf, math.nan, math.inf, math.nan
+    got = dx_of(x2, dh2)
+    good = torch.ones(100, dtype=torch.bool)
+    good[[3, 70, 9, 60]] = False
+    # the scale may be another power of two: the same up to fp16's smallest steps
+    assert R.rel(got[good], want[good]) <= 2.0 ** -11
+    assert not got[~good].isfinite().all(1).any()
+    zero = dx_of(x, torch.zeros_like(dh))
+    assert not zero.any() and zero.isfinite().all()
