@@ -43,9 +43,10 @@
 // factor is cut into three bf16 parts of 8 bits each, which hold all its 24
 // (fp16 needs two, bf16 is one), and a product takes the pairs of parts whose
 // orders add up to at most 2: what is left out of a term is 2^-24 of it on
-// average, 2^-21 at most.  (An infinite factor becomes NaN.)  Products
-// whose results are only rounded to 16 bits (o, dq, dk) take two parts of
-// their fp32 factors (2^-16 against the half step of 2^-9 or 2^-12).  G is
+// average, 2^-21 at most.  (An infinite factor becomes NaN.)  That holds
+// for results that are rounded to 16 bits (o, dq, dk) too: they are sums of
+// terms that cancel, behind a token that erases above all, and terms of two
+// parts (cut off at 2^-16) had left 0.015 of a state of 1e3 in o.  G is
 // summed in fp64: its differences are exponents.  A gate that resets the state
 // (-infinity, a type's lowest value) would take the later gates' digits out of
 // that sum, or make its differences infinite less infinite: gates below
@@ -179,9 +180,6 @@ typedef __bf16 Frag __attribute__((ext_vector_type(8)));
 
 template <typename T>
 constexpr int kParts = sizeof(T) == 4 ? 3 : (std::is_same<T, _Float16>::value ? 2 : 1);
-// Parts of an fp32 factor whose product is rounded to T.
-template <typename T>
-constexpr int kRoundedParts = sizeof(T) == 4 ? 3 : 2;
 
 // The upper halves of two words, a's lowest.
 __device__ __forceinline__ uint32_t upper(uint32_t a, uint32_t b) {
@@ -1017,11 +1015,11 @@ __global__ __launch_bounds__(kWalkBlock) void k_delta_states(DeltaShape s, Delta
 
 // o = scale exp(G) (q S) + P N, a workgroup per chunk and value head, a slice
 // of the columns at a time; a wave has 16 tokens, its rows of q and P stay in
-// registers.  Bound by reading S and M (96 KB a chunk and head): 159 us for 4 x
-// 4096 tokens and 16 heads of 128, 2.9 TB/s.
+// registers.  Bound by reading S and M (96 KB a chunk and head): 162 us for 4 x
+// 4096 tokens and 16 heads of 128, 2.8 TB/s.
 template <typename T, int DK>
 struct OutLds {
-  static constexpr int NS = kRoundedParts<T>;
+  static constexpr int NS = 3;   // parts of the fp32 factors
   static constexpr int kSStride = 2 * DK + 8, kNStride = 136;
   static constexpr int kSPart = kSlice * kSStride, kNPart = kSlice * kNStride;
   static constexpr int kN = NS * kSPart, kFactors = kN + NS * kNPart;
@@ -1294,14 +1292,14 @@ __global__ __launch_bounds__(kWalkBlock) void k_delta_adjoint(
 // by element, whose row sums come from q.dq + k.u and column sums from k.w,
 //   dG_i = scale exp(G) q.(do S^T) - exp(G) beta k.(X S^T)
 //          - exp(G_L - G) k.(N dS^T) + rows of H - columns of H,
-// so only products of full precision enter dg, and dP and dA, which go on into
-// dq and dk, need no more parts than those are rounded to.  Two workgroups a CU
-// (bf16; 128 registers of sums a lane): 488 us for 4 x 4096 tokens and 16 heads
-// of 128, of which the reading of 0.8 GB is 160 and the matrix instructions 77;
+// so only products of the sums as they are enter dg, none of the cut dP and dA,
+// which go on into dq and dk.  Two workgroups a CU
+// (bf16; 128 registers of sums a lane): 467 us for 4 x 4096 tokens and 16 heads
+// of 128, of which the reading of 0.8 GB is 160;
 // the rest is waiting between the five barriers of a slice.
 template <typename T, int DK>
 struct GradsLds {
-  static constexpr int NS = kRoundedParts<T>;
+  static constexpr int NS = 3;   // parts of the fp32 factors
   // first over the columns of the state, a slice at a time: S (then dS) and
   // X and N, lines of a column each ...
   static constexpr int kSStride = 2 * DK + 32, kSPart = kSlice * kSStride;
@@ -1528,19 +1526,24 @@ __global__ __launch_bounds__(kDeltaBlock, kParts<T> == 1 && !SHARED ? 2 : 1) voi
     }
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
+      // (the empty blocks' operands are zero: a branch here would have the
+      // compiler move all sums about; dP's first, then dA's: all four operands
+      // at a time spill 53 registers instead of 23, 530 us instead of 467)
       const Op<NS> pr = upper_rows<NS>(smem + L::kdP, w, b);
-      const Op<NS> ar = upper_rows<NS>(smem + L::kdA, w, b);
       const Op<NS> pc = upper_turned<NS>(smem + L::kdP, w, b);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        mul(oS[n], pr, token_cols<NP, DK>(smem, n, b));
+        mul(xS[n], pc, token_cols<NP, DK>(smem + L::kQ, n, b));
+        if (n % 2) __builtin_amdgcn_sched_barrier(0);
+      }
+      const Op<NS> ar = upper_rows<NS>(smem + L::kdA, w, b);
       const Op<NS> ac = upper_turned<NS>(smem + L::kdA, w, b);
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         const Op<NP> kn = token_cols<NP, DK>(smem, n, b);
-        // (the empty blocks' operands are zero: a branch here would have the
-        // compiler move all sums about)
-        mul(oS[n], pr, kn);
         mul(xS[n], ar, kn);
         mul(xS[n], ac, kn);
-        mul(xS[n], pc, token_cols<NP, DK>(smem + L::kQ, n, b));
         if (n % 2) __builtin_amdgcn_sched_barrier(0);
       }
     }

@@ -281,3 +281,43 @@ def test_fp16_gradients_beside_values_that_are_not_finite():
     assert not got[~good].isfinite().all(1).any()
     zero = dx_of(x, torch.zeros_like(dh))
     assert not zero.any() and zero.isfinite().all()
+
+
+# ---------------------------------------------------------------------------
+# Results that cancel
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("kind", ["fp32", "fp16", "bf16"])
+@pytest.mark.parametrize("heads", [1, 2])
+def test_outputs_behind_erasing_tokens(kind, heads):
+    """Eight tokens erase eight rows of a state of 1e3 (beta = 1, keys of one
+    element, no decay) and write values of 1; every token asks for the mean of
+    those rows, and grad_o asks for one column.  What is left of 1e3 keeps
+    fp32's digits: 40 roundings of the terms before they cancel, then the
+    output's.  (Factors of two 8-bit parts, cut off at 2^-16, left 0.015.)"""
+    import krylov_solvers_adjoint_amd as K
+    dtype = R.TYPES[kind]
+    g = R.gen(8)
+    q, k = torch.zeros(1, 9, 1, 64), torch.zeros(1, 9, 1, 64)
+    k[0, range(8), 0, range(8)] = 1
+    q[..., :8] = 0.25
+    v = torch.randn(1, 9, heads, 64, generator=g)
+    beta, gate = torch.ones(1, 9, heads), torch.zeros(1, 9, heads)
+    s0 = 1e3 * torch.randn(1, heads, 64, 64, generator=g)
+    do = torch.zeros(1, 9, heads, 64)
+    for t in range(9):
+        do[0, t, :, 7 * t + 3] = 1
+    ins = [t.to(dtype) for t in (q, k, v)] + [gate, beta, s0]
+    leaves = [t.cuda().requires_grad_() for t in ins]
+    o, _ = K.gated_delta_rule(*leaves[:5], initial_state=leaves[5])
+    dq, dk = torch.autograd.grad(o, leaves[:2], do.to(dtype).cuda())
+    ref = [t.double().requires_grad_() for t in ins]
+    o64, _ = R.delta_rule(*ref, 1 / 8)
+    rq, rk = torch.autograd.grad(o64, ref[:2], do.double())
+    u = R.half_step(dtype)
+    size = s0.double().abs() + 4                                   # of the terms
+    tol = u * o64.detach().abs() + 40 * R.U32 / 8 * 0.25 * size[0, :, :8].sum(1)
+    assert ((o.detach().cpu().double() - o64.detach()).abs() <= tol).all()
+    each = torch.stack([size[0, :, :, 7 * t + 3].sum(0) for t in range(9)])[None, :, None]
+    near = (dq.cpu().double() - rq).abs() <= u * rq.abs() + 40 * R.U32 / 8 * each
+    assert near.all(), ((dq.cpu().double() - rq).abs() / each / R.U32).max()
+    assert R.rel(dk, rk) <= u + D.TOL
