@@ -284,30 +284,36 @@ __global__ __launch_bounds__(kNormBlock) void k_norm_columns(
 
 // dw and db from `slabs` partial rows each: 16 columns by 64 lines of
 // threads, so that a line reads 64 bytes and the longest chain of loads is
-// slabs / 64.
-constexpr int kJoinCols = 16, kJoinLines = 64;
+// slabs / 64.  A workgroup walks the columns: one for every 16 of them would be
+// a launch of 2^32 threads from 2^26 columns on, and the runtime starts such a
+// launch without its upper bits.
+constexpr int kJoinCols = 16, kJoinLines = 64, kJoinGroups = 1 << 16;
 template <typename W>
 __global__ __launch_bounds__(kJoinCols* kJoinLines) void k_norm_join(
     const float* __restrict__ part, int slabs, int64_t cols, W* __restrict__ dw,
     W* __restrict__ db) {
   __shared__ float s[kJoinLines][kJoinCols + 1];
   const int cc = threadIdx.x % kJoinCols, line = threadIdx.x / kJoinCols;
-  const int64_t c = int64_t(blockIdx.x) * kJoinCols + cc;
   const float* p = part + int64_t(blockIdx.y) * slabs * cols;
-  float v = 0.f;
-  if (c < cols) {
+  W* out = blockIdx.y ? db : dw;
+  for (int64_t c0 = int64_t(blockIdx.x) * kJoinCols; c0 < cols;
+       c0 += int64_t(gridDim.x) * kJoinCols) {
+    const int64_t c = c0 + cc;
+    float v = 0.f;
+    if (c < cols) {
 #pragma unroll 4
-    for (int i = line; i < slabs; i += kJoinLines) v += p[int64_t(i) * cols + c];
-  }
-  s[line][cc] = v;
-  __syncthreads();
+      for (int i = line; i < slabs; i += kJoinLines) v += p[int64_t(i) * cols + c];
+    }
+    s[line][cc] = v;
+    __syncthreads();
 #pragma unroll
-  for (int d = kJoinLines / 2; d > 0; d >>= 1) {
-    if (line < d) s[line][cc] += s[line + d][cc];
+    for (int d = kJoinLines / 2; d > 0; d >>= 1) {
+      if (line < d) s[line][cc] += s[line + d][cc];
+      __syncthreads();
+    }
+    if (line == 0 && c < cols && out) out[c] = W(s[0][cc]);
     __syncthreads();
   }
-  W* out = blockIdx.y ? db : dw;
-  if (line == 0 && c < cols && out) out[c] = W(s[0][cc]);
 }
 
 // The team for rows of `cols` elements: the smallest that holds a row in one
@@ -467,7 +473,9 @@ sla_status sla_layer_norm_grad(const void* dy, int64_t lddy, const void* x, int6
       }));
     }
     if (sums) {
-      k_norm_join<W><<<dim3(int(div_up(cols, kJoinCols)), 2), kJoinCols * kJoinLines, 0, stream>>>(
+      const int64_t want = div_up(cols, kJoinCols);
+      const int groups = int(want < kJoinGroups ? want : kJoinGroups);
+      k_norm_join<W><<<dim3(groups, 2), kJoinCols * kJoinLines, 0, stream>>>(
           part, slabs, cols, (W*)dweight, (W*)dbias);
       LAUNCH_CHECK();
     }

@@ -321,3 +321,20 @@ def test_outputs_behind_erasing_tokens(kind, heads):
     near = (dq.cpu().double() - rq).abs() <= u * rq.abs() + 40 * R.U32 / 8 * each
     assert near.all(), ((dq.cpu().double() - rq).abs() / each / R.U32).max()
     assert R.rel(dk, rk) <= u + D.TOL
+
+
+# ---------------------------------------------------------------------------
+# Launches of 2^32 threads
+# ---------------------------------------------------------------------------
+def test_weight_gradients_of_more_than_2_to_the_26_columns():
+    """All but 18 columns were never written: one row, so db is dy itself and dw
+    is dy times the normalised row, one rounding each."""
+    import krylov_solvers_adjoint_amd as K
+    n = (1 << 26) + 5
+    x = torch.rand(1, n, generator=torch.Generator("cuda").manual_seed(1), device="cuda")
+    w = torch.ones(n, device="cuda", requires_grad=True)
+    b = torch.zeros(n, device="cuda", requires_grad=True)
+    y = K.layer_norm(x, w, b)
+    dw, db = torch.autograd.grad(y, (w, b), x)
+    assert torch.equal(db, x[0])
+    assert ((dw - x[0] * y[0]).abs() <= 4 * R.U32 * dw.abs()).all()
