@@ -1599,12 +1599,12 @@ template <typename T, int NR>
 __global__ __launch_bounds__(kDeltaBlock) void k_delta_step(
     const T* __restrict__ q, int64_t ldq, const T* __restrict__ k, int64_t ldk,
     const T* __restrict__ v, int64_t ldv, const float* __restrict__ g,
-    const float* __restrict__ beta, float* __restrict__ state, T* __restrict__ o, int hk, int hv,
-    int dk, int dv, float scale) {
+    const float* __restrict__ beta, float* __restrict__ state, T* __restrict__ o, int64_t first,
+    int hk, int hv, int dk, int dv, float scale) {
   __shared__ f32x4 sk[4][8], sq[4][8];
   __shared__ float sqk[4];
   const int t = threadIdx.x, cl = t % 8, line = t / 8, w = t / kWave;
-  const int64_t sh = blockIdx.x;  // sequence * hv + head
+  const int64_t sh = first + blockIdx.x;  // sequence * hv + head
   const int vh = int(sh % hv);
   const int64_t seq = sh / hv;
   const int kh = vh / (hv / hk);
@@ -1673,6 +1673,9 @@ __global__ __launch_bounds__(kDeltaBlock) void k_delta_step(
 // Host side
 // ---------------------------------------------------------------------------
 constexpr int kMaxDk = 128;
+// Workgroups of 256 threads in a launch: the runtime starts a launch of 2^32
+// threads and more without its upper bits, and says nothing.
+constexpr int64_t kMostGroups = (int64_t(1) << 24) - 1;
 
 int pad_dk(int64_t dk) { return dk <= 64 ? 64 : 128; }
 int64_t pad_dv(int64_t dv) { return div_up(dv, kSlice) * kSlice; }
@@ -1702,7 +1705,7 @@ sla_status delta_sizes(const char* who, const sla_delta_dims* d, DeltaSizes& z) 
   const int64_t slots = z.chunks * d->value_heads;
   const int64_t dk = pad_dk(d->key_dim), dvp = pad_dv(d->value_dim);
   SLA_NET_REQUIRE(n * d->value_heads * (dvp / kSlice) < (int64_t(1) << 31) &&
-                      z.chunks < (int64_t(1) << 31),
+                      z.chunks <= kMostGroups,
                   "%s: too many sequences, heads or chunks", who);
   int64_t at = 0;
   auto take = [&at](int64_t bytes) {
@@ -1739,6 +1742,14 @@ DeltaShape delta_shape(const sla_delta_dims* d, const DeltaSizes& z, char* kept)
   s.tok = d->packed ? (const int32_t*)(kept + z.plan) : nullptr;
   s.first = d->packed ? s.tok + s.nseq + 1 : nullptr;
   return s;
+}
+
+// The walks' launch has to stay below 2^32 threads too.  (With a token each so
+// many sequences would keep 400 GB; without tokens the call copies states.)
+sla_status walk_groups(const char* who, const DeltaShape& s) {
+  SLA_NET_REQUIRE(int64_t(s.nseq) * s.hv * div_up(s.dvp, kWalk) <= kMostGroups / 2,
+                  "%s: too many sequences and heads", who);
+  return SLA_OK;
 }
 
 DeltaKept delta_kept(const DeltaSizes& z, char* kept) {
@@ -1818,6 +1829,7 @@ sla_status sla_delta_rule(const sla_delta_dims* dims, const void* q, int64_t ldq
                                                 (int32_t*)s.first, gaps);
     LAUNCH_CHECK();
   }
+  SLA_TRY(walk_groups("sla_delta_rule", s));
   return with_delta(dims, [&](auto te, auto width, auto whole) -> sla_status {
     using T = decltype(te);
     constexpr int DK = width.value;
@@ -1882,6 +1894,7 @@ sla_status sla_delta_rule_grad(const sla_delta_dims* dims, const void* q, int64_
     k_delta_gaps<<<1, kDeltaBlock, 0, stream>>>(s.tok, s.nseq, s.total, gaps);
     LAUNCH_CHECK();
   }
+  SLA_TRY(walk_groups("sla_delta_rule_grad", s));
   return with_delta(dims, [&](auto te, auto width, auto whole) -> sla_status {
     using T = decltype(te);
     constexpr int DK = width.value;
@@ -1924,12 +1937,17 @@ sla_status sla_delta_step(const sla_delta_dims* dims, const void* q, int64_t ldq
                   "sla_delta_step: a token stride is shorter than its heads");
   auto go = [&](auto te, auto nr) -> sla_status {
     using T = decltype(te);
-    const dim3 grid(int(dims->sequences * dims->value_heads), int(div_up(dims->value_dim, kSlice)));
-    k_delta_step<T, nr.value><<<grid, kDeltaBlock, 0, stream>>>(
-        (const T*)q, ldq, (const T*)k, ldk, (const T*)v, ldv, g, beta, state, (T*)o,
-        int(dims->key_heads), int(dims->value_heads), int(dims->key_dim), int(dims->value_dim),
-        float(dims->scale));
-    LAUNCH_CHECK();
+    const int64_t all = dims->sequences * dims->value_heads;
+    for (int64_t first = 0; first < all; first += kMostGroups) {
+      const int64_t left = all - first;
+      const dim3 grid(int(left < kMostGroups ? left : kMostGroups),
+                      int(div_up(dims->value_dim, kSlice)));
+      k_delta_step<T, nr.value><<<grid, kDeltaBlock, 0, stream>>>(
+          (const T*)q, ldq, (const T*)k, ldk, (const T*)v, ldv, g, beta, state, (T*)o, first,
+          int(dims->key_heads), int(dims->value_heads), int(dims->key_dim), int(dims->value_dim),
+          float(dims->scale));
+      LAUNCH_CHECK();
+    }
     return SLA_OK;
   };
   return with_delta(dims, [&](auto te, auto width, auto) {

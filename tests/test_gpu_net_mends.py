@@ -338,3 +338,14 @@ def test_weight_gradients_of_more_than_2_to_the_26_columns():
     dw, db = torch.autograd.grad(y, (w, b), x)
     assert torch.equal(db, x[0])
     assert ((dw - x[0] * y[0]).abs() <= 4 * R.U32 * dw.abs()).all()
+
+
+def test_steps_of_more_than_2_to_the_24_states():
+    """Half of the outputs and states were left as they were."""
+    import krylov_solvers_adjoint_amd as K
+    n = (1 << 24) - 1
+    one, two = torch.ones(n, 1, 1, device="cuda"), torch.ones(n, 2, 1, device="cuda")
+    v = torch.arange(2 * n, device="cuda").remainder(1 << 20).float().view(n, 2, 1)
+    s = torch.zeros(n, 2, 1, 1, device="cuda")
+    o = K.gated_delta_step(one, one, v, torch.zeros(n, 2, device="cuda"), two[..., 0], s)
+    assert torch.equal(o, v) and torch.equal(s[..., 0], v)

@@ -268,3 +268,16 @@ def test_a_step_counts_as_a_change_of_its_state(monkeypatch):
         loss.backward()
     with torch.inference_mode():
         net.sla_delta_step(q, q, q, gate, gate, torch.zeros(2, 1, 4, 4), 1.0)
+
+
+def test_walks_of_2_to_the_32_threads_are_refused():
+    """The runtime would start only a part of them (sequences without tokens:
+    with tokens what they keep would not fit the card)."""
+    d = dims(sequences=1 << 23, tokens=0, key_heads=1, value_heads=1)
+    assert lib.sla_delta_rule(ctypes.byref(d), None, 32, None, 32, None, 96, None, None, None, P,
+                              None, P, P, 1 << 50, None) == K.ERR_ARG
+    assert "too many" in last()
+    assert lib.sla_delta_rule_grad(ctypes.byref(d), None, 32, None, 32, None, 96, None, None, P,
+                                   1 << 50, None, 96, P, None, None, None, None, None, P, P,
+                                   1 << 50, None) == K.ERR_ARG
+    assert "too many" in last()
