@@ -649,8 +649,9 @@ typedef enum { SLA_F32 = 0, SLA_F16 = 1, SLA_BF16 = 2 } sla_type;
  * Layer norm over the last axis: y = (x - mean) / sqrt(var + eps) * weight +
  * bias, x [rows][cols].  weight and bias [cols] (either may be NULL: 1 and 0)
  * are of wtype: x's type or SLA_F32.  stats [rows][2] (may be NULL) receives
- * the mean less the row's first element and 1 / sqrt(var + eps), for the
- * gradient.
+ * what the gradient needs of a row: its mean less its first element and
+ * 1 / sqrt(var + eps), or, if that lies nearer to zero, its mean and
+ * -1 / sqrt(var + eps).
  */
 sla_status sla_layer_norm(const void* x, int64_t ldx, int64_t rows, int64_t cols, sla_type type,
                           const void* weight, const void* bias, sla_type wtype, double eps,

@@ -56,8 +56,8 @@ __device__ __forceinline__ void store_f32(T* __restrict__ p, int64_t have, const
 }
 
 // Sum over groups of W neighbouring lanes, in every lane of the group.
-template <int W>
-__device__ __forceinline__ float lane_sum(float v) {
+template <int W, typename V>
+__device__ __forceinline__ V lane_sum(V v) {
 #pragma unroll
   for (int d = 1; d < W; d <<= 1) v += __shfl_xor(v, d, kWave);
   return v;

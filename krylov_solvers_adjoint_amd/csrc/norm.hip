@@ -12,10 +12,18 @@
 // and both backward sums need no second read.  The forward pass keeps mean
 // and rstd (8 bytes a row).
 //
-// The sums run over x - x_0, x_0 the row's first element: exact for a row
-// that lies close to a far mean, and zero for a constant one, where the
-// rounding of a plain mean would pass for a deviation (constant rows of 1e18
-// came out as +-1).  The mean that is kept is less x_0 too.
+// The mean is found in two steps.  c = x_0 + mean(x - x_0), x_0 the row's first
+// element, lies next to the mean even if that is far from zero, but no closer
+// than the rounding of the largest |x - x_0|.  The differences d = x - c are
+// exact next to c, their own mean corrects it, and the variance is
+// mean(d^2) - mean(d)^2, whose second term is a rounding's square.  So a
+// constant row is exactly zero, a row close to a far mean keeps its digits, and
+// so does one whose first element is the outlier (differences to x_0 = 1e4
+// alone had left 4.5e-4 of the other 8191 elements).
+//
+// The gradient gets 1 / sqrt(var + eps) and the mean in one number: from x_0, or
+// from zero if that is nearer (the other number is negative then).  A mean far
+// from both belongs to a row whose deviations are of that size too.
 //
 // Measured: 10^6 x 64 fp32 forward 92 us (5.6 TB/s) and backward 152 + 5 (5.1
 // TB/s); 16384 x 1024 bf16 17 and 22 + 4.5 us.
@@ -36,19 +44,56 @@ constexpr int kNormBlock = 256;
 // a wave are the whole workgroup and go through LDS (`red`, one float per
 // wave; the caller alternates between two such arrays, so that one barrier
 // is enough).
-template <int TEAM>
-__device__ __forceinline__ float team_sum(float v, float* red) {
+template <int TEAM, typename V>
+__device__ __forceinline__ V team_sum(V v, V* red) {
   if constexpr (TEAM <= kWave) {
     return lane_sum<TEAM>(v);
   } else {
     v = lane_sum<kWave>(v);
     if (threadIdx.x % kWave == 0) red[threadIdx.x / kWave] = v;
     __syncthreads();
-    float s = 0.f;
+    V s = 0;
 #pragma unroll
     for (int i = 0; i < TEAM / kWave; ++i) s += red[i];
     return s;
   }
+}
+// Two sums behind one barrier.
+template <int TEAM>
+__device__ __forceinline__ float2 team_sums(float a, float b, float2* red) {
+  if constexpr (TEAM <= kWave) {
+    return make_float2(lane_sum<TEAM>(a), lane_sum<TEAM>(b));
+  } else {
+    a = lane_sum<kWave>(a);
+    b = lane_sum<kWave>(b);
+    if (threadIdx.x % kWave == 0) red[threadIdx.x / kWave] = make_float2(a, b);
+    __syncthreads();
+    float2 s = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < TEAM / kWave; ++i) s.x += red[i].x, s.y += red[i].y;
+    return s;
+  }
+}
+
+// A row's statistics as the gradient keeps them: the mean from x0 or from zero,
+// 1 / sqrt(var + eps), negative in the second case.
+__device__ __forceinline__ float2 pack_stats(double mean, float x0, float rstd) {
+  const double far = mean - double(x0);
+  return fabs(mean) < fabs(far) ? make_float2(float(mean), -rstd) : make_float2(float(far), rstd);
+}
+// The same for a mean c + more.
+__device__ __forceinline__ float2 pack_stats(float c, float more, float x0, float rstd) {
+  const float far = c - x0;
+  return fabsf(c) < fabsf(far) ? make_float2(c + more, -rstd) : make_float2(far + more, rstd);
+}
+struct Stats {
+  float from, mean, rstd;
+  __device__ __forceinline__ float normal(float x) const { return (x - from - mean) * rstd; }
+};
+template <typename T>
+__device__ __forceinline__ Stats row_stats(const float2& s, const T* x) {
+  const bool zero = __float_as_uint(s.y) >> 31;
+  return {zero ? 0.f : float(x[0]), s.x, zero ? -s.y : s.y};
 }
 
 template <typename T, typename W, int TEAM, int NV>
@@ -57,7 +102,8 @@ __global__ __launch_bounds__(kNormBlock) void k_layer_norm(
     const W* __restrict__ b, float eps, T* __restrict__ y, float2* __restrict__ stats) {
   constexpr int V = kVec<T>;
   constexpr int kTeams = kNormBlock / TEAM;
-  __shared__ float red[2][kNormBlock / kWave];
+  __shared__ float red[kNormBlock / kWave];
+  __shared__ float2 reds[kNormBlock / kWave];
   const int lane = threadIdx.x % TEAM;
   const float inv = 1.f / float(cols);
   float wv[NV][V], bv[NV][V];
@@ -90,31 +136,34 @@ __global__ __launch_bounds__(kNormBlock) void k_layer_norm(
     for (int j = 0; j < NV; ++j) {
       const int c = (j * TEAM + lane) * V;
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        v[j][i] -= x0;
-        if (c + i < cols) s += v[j][i];
-      }
+      for (int i = 0; i < V; ++i)
+        if (c + i < cols) s += v[j][i] - x0;
     }
-    const float mean = team_sum<TEAM>(s, red[0]) * inv;
-    float q = 0.f;
+    const float mid = x0 + team_sum<TEAM>(s, red) * inv;
+    float e = 0.f, q = 0.f;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int c = (j * TEAM + lane) * V;
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        v[j][i] -= mean;
-        if (c + i < cols) q += v[j][i] * v[j][i];
+        v[j][i] -= mid;
+        if (c + i < cols) {
+          e += v[j][i];
+          q += v[j][i] * v[j][i];
+        }
       }
     }
-    const float rstd = 1.f / sqrtf(team_sum<TEAM>(q, red[1]) * inv + eps);
+    const float2 eq = team_sums<TEAM>(e, q, reds);
+    const float more = eq.x * inv, var = eq.y * inv - more * more;
+    const float rstd = 1.f / sqrtf((var < 0.f ? 0.f : var) + eps);
     if (!on) continue;
-    if (stats && lane == 0) stats[r] = make_float2(mean, rstd);
+    if (stats && lane == 0) stats[r] = pack_stats(mid, more, x0, rstd);
     T* yr = y + r * cols;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int c = (j * TEAM + lane) * V;
 #pragma unroll
-      for (int i = 0; i < V; ++i) v[j][i] = v[j][i] * rstd * wv[j][i] + bv[j][i];
+      for (int i = 0; i < V; ++i) v[j][i] = (v[j][i] - more) * rstd * wv[j][i] + bv[j][i];
       store_f32<V>(yr + c, cols - c, v[j]);
     }
   }
@@ -148,8 +197,7 @@ __global__ __launch_bounds__(kNormBlock) void k_layer_norm_grad(
     const int64_t r = r0 + threadIdx.x / TEAM;
     const bool on = r < rows;
     const int64_t rr = on ? r : r0;
-    const float2 st = stats[rr];
-    const float x0 = float(x[rr * ldx]);
+    const Stats st = row_stats(stats[rr], x + rr * ldx);
     float n[NV][V], g[NV][V];
     float s1 = 0.f, s2 = 0.f;
 #pragma unroll
@@ -164,7 +212,7 @@ __global__ __launch_bounds__(kNormBlock) void k_layer_norm_grad(
       const int c = (j * TEAM + lane) * V;
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        n[j][i] = on && c + i < cols ? (n[j][i] - x0 - st.x) * st.y : 0.f;
+        n[j][i] = on && c + i < cols ? st.normal(n[j][i]) : 0.f;
         aw[j][i] += g[j][i] * n[j][i];
         ab[j][i] += g[j][i];
         g[j][i] *= wv[j][i];
@@ -180,7 +228,7 @@ __global__ __launch_bounds__(kNormBlock) void k_layer_norm_grad(
     for (int j = 0; j < NV; ++j) {
       const int c = (j * TEAM + lane) * V;
 #pragma unroll
-      for (int i = 0; i < V; ++i) g[j][i] = st.y * (g[j][i] - s1 - n[j][i] * s2);
+      for (int i = 0; i < V; ++i) g[j][i] = st.rstd * (g[j][i] - s1 - n[j][i] * s2);
       store_f32<V>(dx + r * cols + c, cols - c, g[j]);
     }
   }
@@ -217,27 +265,41 @@ __global__ __launch_bounds__(kNormBlock) void k_layer_norm_grad(
 
 // Rows wider than a workgroup's registers: the row is read again for each
 // pass (it comes from the cache), and the columns' sums are left to
-// k_norm_columns.
+// k_norm_columns.  A thread adds up cols / 256 values one after the other, so
+// these sums are fp64 (in fp32 2e7 columns were 3.8e-6 off).  The gradient sums
+// the mean again in place of the rounded one it gets: n is the same number in
+// both directions.
+template <typename T>
+__device__ __forceinline__ double wide_mean(const T* __restrict__ x, int64_t cols, double* red) {
+  double s = 0;
+#pragma unroll 8   // loads under way at a time
+  for (int64_t c = threadIdx.x; c < cols; c += kNormBlock) s += double(float(x[c]));
+  return team_sum<kNormBlock>(s, red) / double(cols);
+}
+template <typename T>
+__device__ __forceinline__ float wide_normal(T x, double mean, float rstd) {
+  return float(double(float(x)) - mean) * rstd;
+}
 template <typename T, typename W>
 __global__ __launch_bounds__(kNormBlock) void k_layer_norm_wide(
     const T* __restrict__ x, int64_t ldx, int64_t cols, const W* __restrict__ w,
     const W* __restrict__ b, float eps, T* __restrict__ y, float2* __restrict__ stats) {
-  __shared__ float red[2][kNormBlock / kWave];
+  __shared__ double red[2][kNormBlock / kWave];
   const int64_t r = blockIdx.x;
   const T* xr = x + r * ldx;
-  const float x0 = float(xr[0]);
-  float s = 0.f;
-  for (int64_t c = threadIdx.x; c < cols; c += kNormBlock) s += float(xr[c]) - x0;
-  const float mean = team_sum<kNormBlock>(s, red[0]) / float(cols);
-  float q = 0.f;
+  const double mean = wide_mean(xr, cols, red[0]);
+  double q = 0;
+#pragma unroll 8
   for (int64_t c = threadIdx.x; c < cols; c += kNormBlock) {
-    const float d = float(xr[c]) - x0 - mean;
+    const double d = double(float(xr[c])) - mean;
     q += d * d;
   }
-  const float rstd = 1.f / sqrtf(team_sum<kNormBlock>(q, red[1]) / float(cols) + eps);
-  if (stats && threadIdx.x == 0) stats[r] = make_float2(mean, rstd);
+  const double var = team_sum<kNormBlock>(q, red[1]) / double(cols);
+  const float rstd = float(1 / sqrt(var + double(eps)));
+  if (stats && threadIdx.x == 0) stats[r] = pack_stats(mean, float(xr[0]), rstd);
+#pragma unroll 8
   for (int64_t c = threadIdx.x; c < cols; c += kNormBlock)
-    y[r * cols + c] = T((float(xr[c]) - x0 - mean) * rstd * (w ? float(w[c]) : 1.f) +
+    y[r * cols + c] = T(wide_normal(xr[c], mean, rstd) * (w ? float(w[c]) : 1.f) +
                         (b ? float(b[c]) : 0.f));
 }
 
@@ -245,37 +307,47 @@ template <typename T, typename W>
 __global__ __launch_bounds__(kNormBlock) void k_layer_norm_grad_wide(
     const T* __restrict__ dy, int64_t lddy, const T* __restrict__ x, int64_t ldx, int64_t cols,
     const W* __restrict__ w, const float2* __restrict__ stats, T* __restrict__ dx) {
-  __shared__ float red[2][kNormBlock / kWave];
+  __shared__ double red[3][kNormBlock / kWave];
   const int64_t r = blockIdx.x;
-  const float2 st = stats[r];
-  const float x0 = float(x[r * ldx]);
-  float s1 = 0.f, s2 = 0.f;
+  const float rstd = fabsf(stats[r].y);
+  const double mean = wide_mean(x + r * ldx, cols, red[2]);
+  double a1 = 0, a2 = 0;
+#pragma unroll 8
   for (int64_t c = threadIdx.x; c < cols; c += kNormBlock) {
     const float t = float(dy[r * lddy + c]) * (w ? float(w[c]) : 1.f);
-    s1 += t;
-    s2 += t * ((float(x[r * ldx + c]) - x0 - st.x) * st.y);
+    a1 += double(t);
+    a2 += double(t * wide_normal(x[r * ldx + c], mean, rstd));
   }
-  s1 = team_sum<kNormBlock>(s1, red[0]) / float(cols);
-  s2 = team_sum<kNormBlock>(s2, red[1]) / float(cols);
+  const float s1 = float(team_sum<kNormBlock>(a1, red[0]) / double(cols));
+  const float s2 = float(team_sum<kNormBlock>(a2, red[1]) / double(cols));
+#pragma unroll 8
   for (int64_t c = threadIdx.x; c < cols; c += kNormBlock) {
     const float t = float(dy[r * lddy + c]) * (w ? float(w[c]) : 1.f);
-    const float n = (float(x[r * ldx + c]) - x0 - st.x) * st.y;
-    dx[r * cols + c] = T(st.y * (t - s1 - n * s2));
+    dx[r * cols + c] = T(rstd * (t - s1 - wide_normal(x[r * ldx + c], mean, rstd) * s2));
   }
 }
 
+// The wide rows' means for k_norm_columns.
+template <typename T>
+__global__ __launch_bounds__(kNormBlock) void k_norm_means(const T* __restrict__ x, int64_t ldx,
+                                                           int64_t cols, double* __restrict__ mean) {
+  __shared__ double red[kNormBlock / kWave];
+  const double m = wide_mean(x + blockIdx.x * ldx, cols, red);
+  if (threadIdx.x == 0) mean[blockIdx.x] = m;
+}
 // Column sums of the wide rows: a thread per column, a slab of rows per
 // workgroup row (the partials of k_layer_norm_grad's layout).
 template <typename T>
 __global__ __launch_bounds__(kNormBlock) void k_norm_columns(
     const T* __restrict__ dy, int64_t lddy, const T* __restrict__ x, int64_t ldx, int64_t rows,
-    int64_t cols, const float2* __restrict__ stats, float* __restrict__ part) {
+    int64_t cols, const float2* __restrict__ stats, const double* __restrict__ mean,
+    float* __restrict__ part) {
   const int64_t c = int64_t(blockIdx.x) * kNormBlock + threadIdx.x;
   if (c >= cols) return;
   float aw = 0.f, ab = 0.f;
   for (int64_t r = blockIdx.y; r < rows; r += gridDim.y) {
     const float g = float(dy[r * lddy + c]);
-    aw += g * ((float(x[r * ldx + c]) - float(x[r * ldx]) - stats[r].x) * stats[r].y);
+    aw += g * wide_normal(x[r * ldx + c], mean[r], fabsf(stats[r].y));
     ab += g;
   }
   part[int64_t(blockIdx.y) * cols + c] = aw;
@@ -348,6 +420,13 @@ int norm_slabs(int64_t rows, int64_t cols, int vec) {
   const NormPlan p = norm_plan(cols, vec);
   if (p.nv) return norm_grid(rows, p, kGradPerCu);
   return int(rows < kWideSlabs ? rows : kWideSlabs);
+}
+
+// The workspace: the partial sums, behind them the wide rows' means.
+int64_t slab_bytes(int slabs, int64_t cols) { return int64_t(slabs) * cols * 8; }
+int64_t norm_bytes(int64_t rows, int64_t cols, int vec) {
+  return slab_bytes(norm_slabs(rows, cols, vec), cols) +
+         (norm_plan(cols, vec).nv ? 0 : rows * int64_t(sizeof(double)));
 }
 
 template <typename F>
@@ -429,7 +508,7 @@ sla_status sla_layer_norm_work(int64_t rows, int64_t cols, sla_type type, int64_
   clear_error();
   SLA_TRY(norm_args("sla_layer_norm_work", rows, cols, cols, type, type));
   SLA_NET_REQUIRE(bytes_host, "sla_layer_norm_work: bytes_host is NULL");
-  *bytes_host = 2 * int64_t(norm_slabs(rows, cols, int(16 / type_size(type)))) * cols * 4;
+  *bytes_host = norm_bytes(rows, cols, int(16 / type_size(type)));
   return SLA_OK;
   SLA_NET_END
 }
@@ -447,7 +526,7 @@ sla_status sla_layer_norm_grad(const void* dy, int64_t lddy, const void* x, int6
     using T = decltype(te);
     using W = decltype(we);
     const int slabs = norm_slabs(rows, cols, kVec<T>);
-    SLA_NET_REQUIRE(!sums || slabs == 0 || (work && work_bytes >= int64_t(slabs) * cols * 8),
+    SLA_NET_REQUIRE(!sums || slabs == 0 || (work && work_bytes >= norm_bytes(rows, cols, kVec<T>)),
                     "sla_layer_norm_grad: workspace too small (sla_layer_norm_work)");
     float* part = sums ? (float*)work : nullptr;
     const NormPlan p = norm_plan(cols, kVec<T>);
@@ -459,8 +538,11 @@ sla_status sla_layer_norm_grad(const void* dy, int64_t lddy, const void* x, int6
         LAUNCH_CHECK();
       }
       if (sums) {
+        double* means = (double*)((char*)work + slab_bytes(slabs, cols));
+        k_norm_means<T><<<int(rows), kNormBlock, 0, stream>>>((const T*)x, ldx, cols, means);
+        LAUNCH_CHECK();
         k_norm_columns<T><<<dim3(int(div_up(cols, kNormBlock)), slabs), kNormBlock, 0, stream>>>(
-            (const T*)dy, lddy, (const T*)x, ldx, rows, cols, (const float2*)stats, part);
+            (const T*)dy, lddy, (const T*)x, ldx, rows, cols, (const float2*)stats, means, part);
         LAUNCH_CHECK();
       }
     } else if (rows) {

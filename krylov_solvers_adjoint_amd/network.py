@@ -160,7 +160,8 @@ def _block(nbytes: int, like: torch.Tensor) -> torch.Tensor:
 @_takes_stream
 def sla_layer_norm(x, weight, bias, eps: float, want_stats: bool = False):
     """(y, stats): stats [rows, 2] = mean less the row's first element and
-    1 / sqrt(var + eps), or None."""
+    1 / sqrt(var + eps), or mean and -1 / sqrt(var + eps) if that lies nearer to
+    zero; or None."""
     cols = x.shape[-1]
     rows = x.numel() // cols if cols else 0
     x, ld = _rows(x, 1)

@@ -349,3 +349,86 @@ def test_steps_of_more_than_2_to_the_24_states():
     s = torch.zeros(n, 2, 1, 1, device="cuda")
     o = K.gated_delta_step(one, one, v, torch.zeros(n, 2, device="cuda"), two[..., 0], s)
     assert torch.equal(o, v) and torch.equal(s[..., 0], v)
+
+
+# ---------------------------------------------------------------------------
+# Layer norm: rows with an outlier, far means, long rows
+# ---------------------------------------------------------------------------
+def norm_rows(cols, kind):
+    """Rows of N(0, 1) with one outlier (first, last), far means, and both."""
+    g = R.gen(cols)
+    top = {"fp32": 1e8, "bf16": 1e8, "fp16": 6e4}[kind]
+    far = {"fp32": 1e6, "bf16": 1e2, "fp16": 1e3}[kind]
+    x = torch.randn(9, cols, generator=g)
+    x[0, 0], x[1, 0], x[2, 0], x[3, -1] = 1e4, top / 50, -top, top
+    x[4] += far
+    x[5] += far
+    x[5, 0] = 0
+    x[6] += far
+    x[6, 0] = top
+    x[7] = x[7, 0]
+    return x.to(R.TYPES[kind])
+
+
+@pytest.mark.parametrize("cols", [2, 8, 40, 257, 1000, 2000, 4100, 8192, 8200, 20001])
+@pytest.mark.parametrize("kind", ["fp32", "fp16", "bf16"])
+def test_layer_norm_keeps_every_element_s_digits(cols, kind):
+    """Element by element, each at its own size: an element's deviation d carries
+    one rounding and the mean's, 40 (sums of 32 values a lane and the team's)
+    of the mean |d|; the statistic 1 / sqrt(var + eps) 60 relative ones.  The
+    gradient's deviation has the mean rounded once more, at its distance from
+    zero or the first element, whichever is nearer.  With differences to the
+    first element, its rounding was on every other one."""
+    import krylov_solvers_adjoint_amd as K
+    dtype = R.TYPES[kind]
+    x = norm_rows(cols, kind)
+    g = R.gen(1)
+    w = (1 + 0.1 * torch.randn(cols, generator=g)).to(dtype)
+    dy = torch.randn(x.shape, generator=g).to(dtype)
+    xd, wd = x.cuda().requires_grad_(), w.cuda().requires_grad_()
+    y = K.layer_norm(xd, wd)
+    dx, dw = torch.autograd.grad(y, (xd, wd), dy.cuda())
+    x64, w64 = x.double().requires_grad_(), w.double().requires_grad_()
+    y64 = R.layer_norm(x64, w64, None, 1e-5)
+    rx, rw = torch.autograd.grad(y64, (x64, w64), dy.double())
+    x64, w64, dy = x64.detach(), w64.detach(), dy.double()
+    U, u = R.U32, R.half_step(dtype)
+    mean = x64.mean(1, keepdim=True)
+    d = x64 - mean
+    rstd = 1 / (d.square().mean(1, keepdim=True) + 1e-5).sqrt()
+    n = d * rstd
+    base = 80 * d.abs().mean(1, keepdim=True)
+    en = U * (rstd * (2 * d.abs() + base) + 60 * n.abs())
+    tol = u * y64.detach().abs() + (en + 4 * U * n.abs()) * w64.abs()
+    near = (y.detach().cpu().double() - y64.detach()).abs() <= tol
+    assert near.all(), (near.logical_not().nonzero()[:5], (y.cpu().double() - y64)[~near][:5])
+    x0 = x64[:, :1]
+    zero = mean.abs() < (mean - x0).abs()
+    start, left = torch.where(zero, 0, x0), torch.where(zero, mean, mean - x0)
+    eb = en + U * rstd * ((x64 - start).abs() + 2 * left.abs())
+    t = dy * w64
+    s1, s2 = t.abs().mean(1, keepdim=True), (t * n).abs().mean(1, keepdim=True)
+    e2 = (t.abs() * eb).mean(1, keepdim=True) + 60 * U * s2
+    tol = u * rx.abs() + rstd * (60 * U * (t.abs() + s1 + n.abs() * s2)
+                                 + eb * (t * n).mean(1, keepdim=True).abs() + n.abs() * e2)
+    near = (dx.cpu().double() - rx).abs() <= tol * (1 + 2 ** -6) + (2.0 ** -25 if kind == "fp16" else 0)
+    assert near.all(), (near.logical_not().nonzero()[:5], (dx.cpu().double() - rx)[~near][:5])
+    tol = u * rw.abs() + (dy.abs() * eb).sum(0) + 60 * U * (dy * n).abs().sum(0)
+    assert ((dw.cpu().double() - rw).abs() <= tol * (1 + 2 ** -6)).all()
+    assert not y[7].any()      # a constant row
+
+
+def test_layer_norm_of_a_long_row():
+    """2e7 columns: 78125 values a thread, summed in fp64; what is left is the
+    rounding of a few elementwise steps."""
+    import krylov_solvers_adjoint_amd as K
+    x = 1 + torch.rand(1, 20_000_000, generator=torch.Generator("cuda").manual_seed(2),
+                       device="cuda")
+    dy = torch.randn(x.shape, generator=torch.Generator("cuda").manual_seed(3), device="cuda")
+    leaf = x.clone().requires_grad_()
+    y = K.layer_norm(leaf)
+    (dx,) = torch.autograd.grad(y, leaf, dy)
+    x64 = x.double().requires_grad_()
+    y64 = R.layer_norm(x64, None, None, 1e-5)
+    (rx,) = torch.autograd.grad(y64, x64, dy.double())
+    assert R.rel(y, y64) <= 8 * R.U32 and R.rel(dx, rx) <= 16 * R.U32
