@@ -671,7 +671,8 @@ sla_status sla_layer_norm_grad(const void* dy, int64_t lddy, const void* x, int6
 /*
  * Gated feed-forward unit: h = f(x w_gate^T) * (x w_up^T), x [rows][inner],
  * the weights [outer][inner] contiguous, h [rows][outer].  act: f(a) is
- * a / (1 + exp(-a)), a (1 + erf(a / sqrt 2)) / 2 or max(a, 0).
+ * a / (1 + exp(-a)), a (1 + erf(a / sqrt 2)) / 2 or max(a, 0).  rows is below
+ * 2^31, inner and outer below 2^22.
  */
 enum { SLA_ACT_SILU = 0, SLA_ACT_GELU = 1, SLA_ACT_RELU = 2 };
 sla_status sla_gated_ffn(const void* x, int64_t ldx, const void* w_gate, const void* w_up,

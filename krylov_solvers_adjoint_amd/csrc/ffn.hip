@@ -972,6 +972,10 @@ __global__ __launch_bounds__(kFfnBlock) void k_ffn_few(Product g) {
 struct ProductPlan {
   int tile, splits;
 };
+// Threads of a launch: the runtime starts one of 2^32 and more without its upper
+// bits.  Tiles of 64 columns or more stay below for every matrix that fits the
+// card; only long narrow ones have to take a larger tile for it.
+constexpr int64_t kMostThreads = (int64_t(1) << 32) - 1;
 ProductPlan plan_product(int64_t M, int64_t N, int64_t K, int parts, int outputs, bool gate,
                          int turned, int es, bool direct) {
   struct Kind {
@@ -989,7 +993,9 @@ ProductPlan plan_product(int64_t M, int64_t N, int64_t K, int parts, int outputs
   for (int i = es == 4 || !direct ? 1 : 0; i < 3; ++i) {
     const Kind& k = kinds[i];
     const int64_t tiles = div_up(M, k.tile) * div_up(N, gate ? k.tile / 2 : k.tile) * outputs;
+    const int64_t threads = k.tile == 256 ? 512 : 256;
     for (int s = 1; s <= (gate ? 1 : 32) && s <= (steps + 3) / 4; ++s) {
+      if (tiles * s * threads > kMostThreads) break;
       const int64_t n = div_up(tiles * s, cus);
       const double rounds = double(div_up(n, k.slots));
       const double wait = k.wait + (es == 4 ? 0.3 * turned : 0.0);
@@ -1027,8 +1033,8 @@ sla_status run_product(Product& g, hipStream_t stream) {
   constexpr int lds = Ring<DIRECT>::kDepth * (Tile<T, B, AT, kThreads, kStep, DIRECT>::kBytes +
                                               Tile<T, B, BT, kThreads, kStep, DIRECT>::kBytes);
   const int64_t gx = div_up(g.N, EPI == EPI_STORE ? B : B / 2), gy = div_up(g.M, B);
-  SLA_NET_REQUIRE(gx * gy * g.outputs * g.splits < (int64_t(1) << 31),
-                  "gated_ffn: a matrix is too large");
+  SLA_NET_REQUIRE(gx * gy * g.outputs * g.splits * kThreads <= kMostThreads,
+                  "sla_gated_ffn: a matrix is too large");
   g.gx = int(gx), g.gy = int(gy);
   auto* kernel = k_ffn_product<T, B, WM, WN, AT, BT, EPI, DIRECT>;
   if (lds > 65536)
@@ -1081,7 +1087,7 @@ sla_status ffn_args(const char* who, int64_t rows, int64_t inner, int64_t outer,
   SLA_NET_REQUIRE(valid_type(type), "%s: unknown type", who);
   SLA_NET_REQUIRE(act == SLA_ACT_SILU || act == SLA_ACT_GELU || act == SLA_ACT_RELU,
                   "%s: unknown activation", who);
-  SLA_NET_REQUIRE(rows >= 0 && rows < (int64_t(1) << 22), "%s: rows out of range", who);
+  SLA_NET_REQUIRE(rows >= 0 && rows < (int64_t(1) << 31), "%s: rows out of range", who);
   SLA_NET_REQUIRE(inner >= 1 && inner < (int64_t(1) << 22) && outer >= 1 &&
                       outer < (int64_t(1) << 22), "%s: inner or outer out of range", who);
   SLA_NET_REQUIRE(ldx >= inner, "%s: row stride below inner", who);

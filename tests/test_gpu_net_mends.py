@@ -432,3 +432,30 @@ def test_layer_norm_of_a_long_row():
     y64 = R.layer_norm(x64, None, None, 1e-5)
     (rx,) = torch.autograd.grad(y64, x64, dy.double())
     assert R.rel(y, y64) <= 8 * R.U32 and R.rel(dx, rx) <= 16 * R.U32
+
+
+# ---------------------------------------------------------------------------
+# The feed-forward unit: a row an unknown
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("rows, inner, outer, kind", [
+    ((1 << 22) + 77, 8, 16, "bf16"), ((1 << 22) + 77, 5, 3, "fp32"), (16_000_000, 16, 8, "fp16")])
+def test_more_than_2_to_the_22_rows(rows, inner, outer, kind):
+    """They were refused.  h and dx element by element; dW is a sum of `rows`
+    terms in fp32, whose roundings add up like a random walk."""
+    import krylov_solvers_adjoint_amd as K
+    dtype = R.TYPES[kind]
+    gen = torch.Generator("cuda").manual_seed(rows)
+    x, wg, wu, dh = (torch.randn(s, generator=gen, device="cuda") * c
+                     for s, c in (((rows, inner), 1), ((outer, inner), inner ** -0.5),
+                                  ((outer, inner), inner ** -0.5), ((rows, outer), 0.01)))
+    x, wg, wu, dh = (t.to(dtype) for t in (x, wg, wu, dh))
+    leaves = [t.requires_grad_() for t in (x, wg, wu)]
+    h = K.gated_ffn(*leaves)
+    got = dict(zip(("dx", "dwg", "dwu"), torch.autograd.grad(h, leaves, dh)), h=h)
+    want = F.bounds(*(t.detach().double() for t in (x, wg, wu, dh)), "silu", R.half_step(dtype))
+    for name in ("h", "dx"):
+        ref, tol = want[name]
+        tiny = 2.0 ** -25 if kind == "fp16" else 0
+        assert ((got[name].detach().double() - ref).abs() <= tol * (1 + 2 ** -6) + tiny).all(), name
+    for name in ("dwg", "dwu"):
+        assert R.rel(got[name], want[name][0]) <= 2 * R.half_step(dtype) + rows ** 0.5 * R.U32

@@ -281,3 +281,15 @@ def test_walks_of_2_to_the_32_threads_are_refused():
                                    1 << 50, None, 96, P, None, None, None, None, None, P, P,
                                    1 << 50, None) == K.ERR_ARG
     assert "too many" in last()
+
+
+def test_rows_of_the_feed_forward_unit():
+    """As many as layer norm's: a row an unknown, the framework's grids have 1.7e8."""
+    n = K._I64()
+    for rows in (1 << 22, 169_000_000, (1 << 31) - 1):
+        assert lib.sla_gated_ffn_work(rows, 8, 16, 2, ctypes.byref(n)) == K.OK, rows
+        assert n.value >= 2 * rows * 16 * 2
+    assert lib.sla_gated_ffn_work(1 << 31, 8, 16, 2, ctypes.byref(n)) == K.ERR_ARG
+    # no launch of 2^32 threads
+    assert lib.sla_gated_ffn(P, 8, P, P, (1 << 31) - 1, 8, 4096, 2, 0, P, None) == K.ERR_ARG
+    assert "too large" in last()
