@@ -263,8 +263,12 @@ __device__ __forceinline__ void send(const char* p, int at, char* lds) {
   const uint64_t q = reinterpret_cast<uint64_t>(p);
   const Words rsrc = {int(q), int(q >> 32) & 0xffff, 0x7fffffff, 0x00020000};
   const int m0 = int(reinterpret_cast<uintptr_t>((LdsPtr)lds));
+  // m0 is written: the compiler, which keeps it to itself, warns and takes note
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-               :: "s"(m0), "v"(at), "s"(rsrc) : "memory");
+               :: "s"(m0), "v"(at), "s"(rsrc) : "memory", "m0");
+#pragma clang diagnostic pop
 #endif
 }
 // Waits until at most N direct loads are under way and the wave's LDS reads

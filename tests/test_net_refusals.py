@@ -293,3 +293,17 @@ def test_rows_of_the_feed_forward_unit():
     # no launch of 2^32 threads
     assert lib.sla_gated_ffn(P, 8, P, P, (1 << 31) - 1, 8, 4096, 2, 0, P, None) == K.ERR_ARG
     assert "too large" in last()
+
+
+def test_assembly_names_the_registers_it_writes():
+    """m0 holds the LDS address of a direct load: the compiler uses it too."""
+    import os
+    import re
+    csrc = os.path.join(os.path.dirname(K.__file__), "csrc")
+    for name in sorted(os.listdir(csrc)):
+        if name.endswith((".hip", ".h")):
+            with open(os.path.join(csrc, name)) as f:
+                text = f.read()
+            for block in re.findall(r"asm volatile\((.*?)\);", text, re.S):
+                if re.search(r"s_mov_b32 m0", block):
+                    assert '"m0"' in block.rsplit(":", 1)[1], (name, block)
