@@ -7,10 +7,11 @@ trained through the solver's adjoint (``examples/coefficient_network.py``).
 As everywhere in this package a function marshals its arguments and calls the
 C ABI of the same name (``include/sla.h``); the autograd nodes stand on top.
 Work is enqueued on the current stream, workspaces come from PyTorch's
-allocator on that stream, nothing synchronises, and the same inputs give the
-same bits.  The sla_* functions take another stream too: everything they do
-then happens on it, so it has to be ordered behind the inputs, which live until
-it is done, and what is returned belongs to it.
+allocator on that stream, nothing synchronises (but offsets given on the host,
+which are copied), and the same inputs give the same bits.  The sla_* functions
+take another stream too: everything they do then happens on it, so it has to be
+ordered behind the inputs, which live until it is done, and what is returned
+belongs to it.
 
 Inputs may be views whose last axis is contiguous and whose rows (tokens) are
 evenly spaced, such as the parts of one fused projection; any other layout is
@@ -436,9 +437,9 @@ def gated_delta_rule(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch
     value_heads, dk, dv]; without an initial state they begin at zero.
 
     With cu_seqlens the batch is 1 and sequence i is the tokens cu_seqlens[i]
-    .. cu_seqlens[i+1] - 1: a list or CPU tensor is checked here; a GPU tensor
-    (int32 or int64) is read by the kernels alone, which raise falling offsets
-    and clamp those outside.  Tokens of no sequence get zeros.
+    .. cu_seqlens[i+1] - 1: a list or CPU tensor is checked here and copied to
+    the GPU, which waits for it; a GPU tensor (int32 or int64) is read by the
+    kernels alone, which raise falling offsets and clamp those outside.  Tokens of no sequence get zeros.
 
     One autograd node, with gradients for q, k, v, g, beta and the initial
     state; it keeps the state before every chunk of 64 tokens."""
@@ -450,11 +451,11 @@ def gated_delta_rule(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch
         if batch != 1:
             raise ValueError("cu_seqlens needs a batch of 1")
         if not isinstance(cu_seqlens, torch.Tensor):
-            cu_seqlens = torch.tensor(cu_seqlens, dtype=torch.int64)
-        if cu_seqlens.dtype not in (torch.int32, torch.int64):
-            raise TypeError(f"cu_seqlens: expected int32 or int64, got {cu_seqlens.dtype}")
+            cu_seqlens = torch.as_tensor(cu_seqlens)   # its own type: no rounding
         if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
             raise ValueError("cu_seqlens: expected [sequences + 1]")
+        if cu_seqlens.dtype not in (torch.int32, torch.int64):
+            raise TypeError(f"cu_seqlens: expected int32 or int64, got {cu_seqlens.dtype}")
         if not cu_seqlens.is_cuda:
             if bool((cu_seqlens.diff() < 0).any()) or int(cu_seqlens[0]) < 0 \
                     or int(cu_seqlens[-1]) > tokens:

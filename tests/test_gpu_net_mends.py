@@ -459,3 +459,23 @@ def test_more_than_2_to_the_22_rows(rows, inner, outer, kind):
         assert ((got[name].detach().double() - ref).abs() <= tol * (1 + 2 ** -6) + tiny).all(), name
     for name in ("dwg", "dwu"):
         assert R.rel(got[name], want[name][0]) <= 2 * R.half_step(dtype) + rows ** 0.5 * R.U32
+
+
+# ---------------------------------------------------------------------------
+# Offsets
+# ---------------------------------------------------------------------------
+def test_offsets_that_are_no_whole_numbers_are_refused():
+    """A list of them was cut off: 1.7 became 1."""
+    import numpy as np
+    import krylov_solvers_adjoint_amd as K
+    ins, _, _ = D.inputs(1, 6, 1, 1, 8, 8, torch.float32)
+    q, k, v, g, beta, _ = (t.cuda() for t in ins)
+    for bad in ([0, 1.7, 6], [0.0, 6.0], np.array([0.5, 6.0]), [True, True]):
+        with pytest.raises(TypeError):
+            K.gated_delta_rule(q, k, v, g, beta, cu_seqlens=bad)
+    with pytest.raises(ValueError):
+        K.gated_delta_rule(q, k, v, g, beta, cu_seqlens=[])
+    want = K.gated_delta_rule(q, k, v, g, beta, cu_seqlens=[0, 2, 6])[0]
+    for good in ((0, 2, 6), np.array([0, 2, 6]), np.array([0, 2, 6], dtype=np.int32),
+                 torch.tensor([0, 2, 6]), torch.tensor([0, 2, 6]).cuda()):
+        assert torch.equal(K.gated_delta_rule(q, k, v, g, beta, cu_seqlens=good)[0], want)
