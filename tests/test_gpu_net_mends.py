@@ -479,3 +479,57 @@ def test_offsets_that_are_no_whole_numbers_are_refused():
     for good in ((0, 2, 6), np.array([0, 2, 6]), np.array([0, 2, 6], dtype=np.int32),
                  torch.tensor([0, 2, 6]), torch.tensor([0, 2, 6]).cuda()):
         assert torch.equal(K.gated_delta_rule(q, k, v, g, beta, cu_seqlens=good)[0], want)
+
+
+# ---------------------------------------------------------------------------
+# What a comparison with ">" lets pass
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("kind", ["fp32", "fp16", "bf16"])
+def test_no_output_is_other_than_finite(kind):
+    """The element by element bounds of layer norm and the feed-forward unit ask
+    whether a difference is larger than its bound, which no NaN is."""
+    import krylov_solvers_adjoint_amd as K
+    import test_gpu_net_norm as N
+    dtype = R.TYPES[kind]
+    for rows, cols in N.CASES:
+        x, w, b, dy = (t.cuda() for t in N.inputs(rows, cols, dtype, dtype))
+        leaves = [t.requires_grad_() for t in (x, w, b)]
+        y = K.layer_norm(*leaves)
+        for t in (y, *torch.autograd.grad(y, leaves, dy)):
+            assert t.isfinite().all(), (rows, cols)
+    for rows, inner, outer in F.CASES + [(1030, 264, 520)]:
+        for act in ("silu", "gelu", "relu"):
+            x, wg, wu, dh = (t.cuda() for t in F.inputs(rows, inner, outer, dtype))
+            leaves = [t.requires_grad_() for t in (x, wg, wu)]
+            h = K.gated_ffn(*leaves, act)
+            for t in (h, *torch.autograd.grad(h, leaves, dh)):
+                assert t.isfinite().all(), (rows, inner, outer, act)
+
+
+def test_the_fp16_gradient_in_a_graph():
+    """Its scale is found anew in every replay, from that replay's inputs."""
+    import krylov_solvers_adjoint_amd as K
+    x, wg, wu, dh = (t.cuda() for t in F.inputs(300, 128, 256, torch.float16))
+
+    def step():
+        leaves = [t.detach().requires_grad_() for t in (x, wg, wu)]
+        h = K.gated_ffn(*leaves)
+        return (h.detach(), *torch.autograd.grad(h, leaves, dh))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(2):
+            step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    first = F.inputs(300, 128, 256, torch.float16)[3].cuda()
+    for size in (2.0 ** -14, 1.0, 2.0 ** 8, 2.0 ** -8):
+        dh.copy_(first * size)
+        graph.replay()
+        torch.cuda.synchronize()
+        again = step()
+        torch.cuda.synchronize()
+        for p, q in zip(out, again):
+            assert torch.equal(p, q) and p.isfinite().all()
