@@ -43,7 +43,9 @@
 // factor is cut into three bf16 parts of 8 bits each, which hold all its 24
 // (fp16 needs two, bf16 is one), and a product takes the pairs of parts whose
 // orders add up to at most 2: what is left out of a term is 2^-24 of it on
-// average, 2^-21 at most.  (An infinite factor becomes NaN.)  That holds
+// average, 2^-21 at most.  (An infinite factor becomes NaN, and what is not
+// finite reaches the earlier tokens of its chunk: zeros of the triangles meet it
+// in the products.)  That holds
 // for results that are rounded to 16 bits (o, dq, dk) too: they are sums of
 // terms that cancel, behind a token that erases above all, and terms of two
 // parts (cut off at 2^-16) had left 0.015 of a state of 1e3 in o.  G is
@@ -1295,7 +1297,7 @@ __global__ __launch_bounds__(kWalkBlock) void k_delta_adjoint(
 // so only products of the sums as they are enter dg, none of the cut dP and dA,
 // which go on into dq and dk.  Two workgroups a CU
 // (bf16; 128 registers of sums a lane): 467 us for 4 x 4096 tokens and 16 heads
-// of 128, of which the reading of 0.8 GB is 160;
+// of 128, of which the reading of 0.8 GB is 160 and the matrix instructions 85;
 // the rest is waiting between the five barriers of a slice.
 template <typename T, int DK>
 struct GradsLds {

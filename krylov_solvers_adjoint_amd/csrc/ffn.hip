@@ -869,7 +869,7 @@ __global__ __launch_bounds__(kWave) void k_ffn_scale(const float* __restrict__ p
 // The projections of few rows (at most 16 RT): reading the weights is the
 // work.  A workgroup has 16 columns of a and of b; its four waves take turns
 // along k, fragments straight from memory, and are joined through LDS.  4 x
-// 1024 x 2 x 4096 bf16: 5.4 us (16.8 MB), against 36 us with tiles of 128.
+// 1024 x 2 x 4096 bf16: 5.2 us (16.8 MB), against 36 us with tiles of 128.
 template <typename T, int RT, int EPI>
 __global__ __launch_bounds__(kFfnBlock) void k_ffn_few(Product g) {
   typedef typename Unit<T>::Vec Vec;

@@ -298,7 +298,9 @@ def gated_ffn(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor,
 
     x [..., inner], the weights [outer, inner], all of one type; activation f:
     "silu", "gelu" (with erf) or "relu".  One autograd node that keeps only
-    its inputs: backward computes both projections again."""
+    its inputs: backward computes both projections again, and rounds the
+    gradients of both to x's type (fp16: times a power of two that keeps them
+    in range) before the products that follow."""
     _tensor(x, "x")
     if activation not in ACTIVATIONS:
         raise ValueError(f"unknown activation {activation!r}")
@@ -442,7 +444,8 @@ def gated_delta_rule(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch
     kernels alone, which raise falling offsets and clamp those outside.  Tokens of no sequence get zeros.
 
     One autograd node, with gradients for q, k, v, g, beta and the initial
-    state; it keeps the state before every chunk of 64 tokens."""
+    state; it keeps the state before every chunk of 64 tokens.  A value that is
+    not finite spoils the earlier tokens of its chunk of 64 too."""
     scale = _check_delta(q, k, v, g, beta, scale, 2)
     batch, tokens = q.shape[0], q.shape[1]
     offsets = None
