@@ -699,8 +699,8 @@ sla_status sla_gated_ffn_grad(const void* dh, int64_t lddh, const void* x, int64
  * [value_dim], g and beta fp32 [tokens][value_heads].  Value head h reads key
  * head h / (value_heads / key_heads).  g <= 0 (a decay) is the meant range,
  * down to -infinity (the state begins anew; g's gradient is 0 there); growth
- * within a chunk of 64 tokens may overflow.  A value that is not finite spoils
- * the earlier tokens of its chunk too.
+ * within a chunk of 64 tokens may overflow.  A value that is not finite may
+ * spoil earlier tokens of its chunk too.
  * packed == 0: `tokens` are `sequences` sequences of equal length, one after
  * the other.  packed != 0: sequence i is the tokens offsets[i] ..
  * offsets[i+1] - 1 (offsets [sequences + 1], int32, device, not falling,

@@ -44,7 +44,7 @@
 // (fp16 needs two, bf16 is one), and a product takes the pairs of parts whose
 // orders add up to at most 2: what is left out of a term is 2^-24 of it on
 // average, 2^-21 at most.  (An infinite factor becomes NaN, and what is not
-// finite reaches the earlier tokens of its chunk: zeros of the triangles meet it
+// finite may reach earlier tokens of its chunk: zeros of the triangles meet it
 // in the products.)  That holds
 // for results that are rounded to 16 bits (o, dq, dk) too: they are sums of
 // terms that cancel, behind a token that erases above all, and terms of two

@@ -796,50 +796,59 @@ __global__ __launch_bounds__(kFfnBlock) void k_ffn_join(Product g) {
 
 // fp16's da and db: |da| <= 1.13 |dh| |b| and |db| <= |dh| |a| (no activation is
 // steeper than 1.13 or larger than its argument), and |a|, |b| <= the norm of a
-// row of x times that of a row of the weights.  A wave takes a line of one of
+// row of x times that of a row of the weights.  A wave takes lines of one of
 // the four arrays at a time; values that are not finite count nothing (what is
 // made of them is not finite either).  parts: three maxima a workgroup.  Reading
-// the arrays is the work: 46 us for the 184 MB of 16384 x 1024 x 4096 (4.0 TB/s),
-// of 1090 for the training step.
+// the arrays is the work: 49 us for the 184 MB of 16384 x 1024 x 4096 (3.8 TB/s),
+// of 1090 for the training step; 222 us for 1.6e7 rows of 16 and 16 (4.6 TB/s),
+// which a wave a line had made 6 ms.
 constexpr int kBoundGroups = 1024;
 struct Lines {
   const _Float16* p;
   int64_t ld, count;
   int width;
 };
-__device__ __forceinline__ float line_max(const Lines& s, int64_t line, bool square) {
-  const _Float16* p = s.p + line * s.ld;
-  float m = 0.f;
-  for (int64_t c = threadIdx.x % kWave * 8; c < s.width; c += kWave * 8) {
-    float v[8];
-    load_f32<8>(p + c, s.width - c, v);
+// The largest value (or sum of squares of a line) of the lines a wave walks, in
+// any of its lanes: teams of lanes, as many as hold a line in 16 bytes each.
+__device__ __forceinline__ float lines_max(const Lines& s, int64_t wave, int64_t waves,
+                                           bool square) {
+  const int lane = threadIdx.x % kWave;
+  int team = 1;
+  while (team < kWave && team * 8 < s.width) team *= 2;
+  const int per = kWave / team;
+  float best = 0.f;
+  for (int64_t i = wave * per + lane / team; i < s.count; i += waves * per) {
+    const _Float16* p = s.p + i * s.ld;
+    float m = 0.f;
+    for (int64_t c = lane % team * 8; c < s.width; c += team * 8) {
+      float v[8];
+      load_f32<8>(p + c, s.width - c, v);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (square) m += v[i] * v[i];
-      else m = fmaxf(m, fabsf(v[i]) <= 65504.f ? fabsf(v[i]) : 0.f);
+      for (int j = 0; j < 8; ++j) {
+        if (square) m += v[j] * v[j];
+        else m = fmaxf(m, fabsf(v[j]) <= 65504.f ? fabsf(v[j]) : 0.f);
+      }
     }
+    if (square)
+      for (int d = 1; d < team; d *= 2) m += __shfl_xor(m, d, kWave);
+    best = m < __builtin_inff() ? fmaxf(best, m) : best;
   }
-#pragma unroll
-  for (int d = 1; d < kWave; d <<= 1) {
-    const float o = __shfl_xor(m, d, kWave);
-    m = square ? m + o : fmaxf(m, o);
-  }
-  return m < __builtin_inff() ? m : 0.f;
+  return best;
 }
 __global__ __launch_bounds__(kFfnBlock) void k_ffn_bound(Lines dh, Lines x, Lines wg, Lines wu,
                                                          float* __restrict__ parts) {
   constexpr int kWaves = kFfnBlock / kWave;
   __shared__ float best[3][kWaves];
   const int w = threadIdx.x / kWave;
-  const int64_t from = int64_t(blockIdx.x) * kWaves + w, step = int64_t(gridDim.x) * kWaves;
-  float m[3] = {0.f, 0.f, 0.f};
-  for (int64_t i = from; i < dh.count; i += step) m[0] = fmaxf(m[0], line_max(dh, i, false));
-  for (int64_t i = from; i < x.count; i += step) m[1] = fmaxf(m[1], line_max(x, i, true));
-  for (int64_t i = from; i < wg.count; i += step)
-    m[2] = fmaxf(m[2], fmaxf(line_max(wg, i, true), line_max(wu, i, true)));
+  const int64_t wave = int64_t(blockIdx.x) * kWaves + w, waves = int64_t(gridDim.x) * kWaves;
+  float m[3] = {lines_max(dh, wave, waves, false), lines_max(x, wave, waves, true),
+                fmaxf(lines_max(wg, wave, waves, true), lines_max(wu, wave, waves, true))};
 #pragma unroll
-  for (int k = 0; k < 3; ++k)
+  for (int k = 0; k < 3; ++k) {
+#pragma unroll
+    for (int d = 1; d < kWave; d <<= 1) m[k] = fmaxf(m[k], __shfl_xor(m[k], d, kWave));
     if (threadIdx.x % kWave == 0) best[k][w] = m[k];
+  }
   __syncthreads();
   if (threadIdx.x < 3) {
     float v = 0.f;

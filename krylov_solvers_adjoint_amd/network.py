@@ -445,7 +445,7 @@ def gated_delta_rule(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch
 
     One autograd node, with gradients for q, k, v, g, beta and the initial
     state; it keeps the state before every chunk of 64 tokens.  A value that is
-    not finite spoils the earlier tokens of its chunk of 64 too."""
+    not finite may spoil earlier tokens of its chunk of 64 too."""
     scale = _check_delta(q, k, v, g, beta, scale, 2)
     batch, tokens = q.shape[0], q.shape[1]
     offsets = None
