@@ -28,8 +28,11 @@
 //   dP_ij = scale d_ij do_i.N_j            dA_ij = d_ij beta_i X_i.N_j
 //   dq = scale exp(G) (do S^T) + dP k
 //   u  = - exp(G) B (X S^T) - dA k         w = dP^T q - dA^T k + exp(G_L - G) (N dS^T)
-//   dk = u + w       dG_i = q_i.dq_i + k_i.(u_i - w_i), and <S', dS> at the chunk's end
-//   dg = the sums of dG from each token to the chunk's end (0 below kGateFloor)
+//   dk = u + w       dg_t = sum over i >= t > j of H_ij + sum over i >= t of a_i
+//                           + sum over j < t of b_j + exp(G_L) <S, dS>
+//   H_ij = do_i.N_j P_ij - beta_i X_i.N_j A_ij
+//   a_i  = scale exp(G_i) q_i.(do S^T)_i - exp(G_i) beta_i k_i.(X S^T)_i
+//   b_j  = exp(G_L - G_j) k_j.(N dS^T)_j
 //
 // Work that does not depend on the state (k_delta_prepare, k_delta_out,
 // k_delta_grads) runs over all chunks at once; what does (k_delta_states,
@@ -1290,13 +1293,14 @@ __global__ __launch_bounds__(kWalkBlock) void k_delta_adjoint(
 // All gradients of a chunk but the state's and v's, a workgroup per chunk and
 // key head, a wave 16 of its tokens: the value heads that share the key head
 // are walked one after the other, so the gradients of q and k are summed in
-// registers, in one order.  With H = (do N^T) P - (X N^T) (d beta k k^T) element
-// by element, whose row sums come from q.dq + k.u and column sums from k.w,
-//   dG_i = scale exp(G) q.(do S^T) - exp(G) beta k.(X S^T)
-//          - exp(G_L - G) k.(N dS^T) + rows of H - columns of H,
-// so only products of the sums as they are enter dg, none of the cut dP and dA,
-// which go on into dq and dk.  Two workgroups a CU
-// (bf16; 128 registers of sums a lane): 467 us for 4 x 4096 tokens and 16 heads
+// registers, in one order.  dg sums what crosses a token and nothing else: rows
+// less columns of H, from each token on, are 20 us less work, but what does not
+// cross cancels in them only up to its roundings, and behind gates of -10 that
+// was all dg consisted of (5e-3 off; at -20 noise).  H's off-diagonal blocks
+// need the sums of their rows and columns, the diagonal ones those of the rows
+// >= t and columns < t of their 16 x 16.  Only products of full precision enter
+// dg, none of the cut dP and dA, which go on into dq and dk.  Two workgroups a
+// CU (bf16; 128 registers of sums a lane): 486 us for 4 x 4096 tokens and 16 heads
 // of 128, of which the reading of 0.8 GB is 160 and the matrix instructions 85;
 // the rest is waiting between the five barriers of a slice.
 template <typename T, int DK>
@@ -1313,8 +1317,10 @@ struct GradsLds {
   static constexpr int kFactors = kFirst > kSecond ? kFirst : kSecond;
   struct Tail {
     Factors f;
-    double G[kChunk], dG[kChunk];
-    float cols[4][kChunk], part[8];
+    double G[kChunk];
+    // sums of H: rows of a block row's off-diagonal blocks, columns of each
+    // block, diagonal blocks; a and b
+    float rows[kChunk], cols[4][kChunk], own[kChunk], a[kChunk], b[kChunk], part[4];
   };
   static constexpr int kBytes = kFactors + int(sizeof(Tail));
 };
@@ -1472,7 +1478,7 @@ __global__ __launch_bounds__(kDeltaBlock, kParts<T> == 1 && !SHARED ? 2 : 1) voi
     }
     __syncthreads();
     const f32x4 fin = quad(z.f.in, w), fout = quad(z.f.out, w), fbe = quad(z.f.beta, w);
-    f32x4 row_h = {0, 0, 0, 0};   // the rows' sums of H, this lane's columns
+    f32x4 row_h = {0, 0, 0, 0}, own = {0, 0, 0, 0};   // H: rows' sums, the diagonal block
     const float* Pg = kept.P + slot * kChunk * kChunk;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -1491,8 +1497,12 @@ __global__ __launch_bounds__(kDeltaBlock, kParts<T> == 1 && !SHARED ? 2 : 1) voi
           dp[r] = s.scale * d * pp[j][r];
           da[r] = -bx;
           const float x = col <= row ? pp[j][r] * Pg[row * kChunk + col] - bx * kk[r] : 0.f;
-          row_h[r] += x;
-          col_h += x;
+          if (j < w) {
+            row_h[r] += x;
+            col_h += x;
+          } else {
+            own[r] = x;
+          }
         }
         // line 16 j + l, rows 16 w + 4 h .. of the turned triangle
         const float y[4] = {dp[0], dp[1], dp[2], dp[3]}, x[4] = {da[0], da[1], da[2], da[3]};
@@ -1510,9 +1520,27 @@ __global__ __launch_bounds__(kDeltaBlock, kParts<T> == 1 && !SHARED ? 2 : 1) voi
       col_h += __shfl_xor(col_h, 32, kWave);
       if (h == 0) z.cols[w][16 * j + l] = col_h;
     }
+    {
+      // rows >= 4 h + r of the diagonal block, then columns before it
+      float below = own[0] + own[1] + own[2] + own[3], above = 0.f;
+#pragma unroll
+      for (int d = 1; d < 4; ++d) {
+        const float u = __shfl(below, (t + 16 * d) % kWave, kWave);
+        if (h + d < 4) above += u;
+      }
+#pragma unroll
+      for (int r = 3; r >= 0; --r) {
+        above += own[r];
+        const float x = lane_sum<16>(l < 4 * h + r ? above : 0.f), y = lane_sum<16>(row_h[r]);
+        if (l == 0) {
+          z.own[16 * w + 4 * h + r] = x;
+          z.rows[16 * w + 4 * h + r] = y;
+        }
+      }
+    }
     __syncthreads();
     // dq = scale exp(G) (do S^T) + dP k and the like, the state's parts first
-    float end = 0.f;  // sum over the rows of k_i . exp(G_L - G_i) (N dS^T)_i
+    f32x4 a = {0, 0, 0, 0}, b = {0, 0, 0, 0};
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const f32x4 kv = token_tile<NP, DK>(smem, n, w), qv = token_tile<NP, DK>(smem + L::kQ, n, w);
@@ -1520,8 +1548,8 @@ __global__ __launch_bounds__(kDeltaBlock, kParts<T> == 1 && !SHARED ? 2 : 1) voi
       for (int r = 0; r < 4; ++r) {
         oS[n][r] *= s.scale * fin[r];
         const float u = fin[r] * fbe[r] * xS[n][r], y = fout[r] * nD[n][r];
-        row_h[r] += qv[r] * oS[n][r] - kv[r] * (u + y);
-        end += kv[r] * y;
+        a[r] += qv[r] * oS[n][r] - kv[r] * u;
+        b[r] += kv[r] * y;
         xS[n][r] = y - u;
       }
       __builtin_amdgcn_sched_barrier(0);
@@ -1530,7 +1558,7 @@ __global__ __launch_bounds__(kDeltaBlock, kParts<T> == 1 && !SHARED ? 2 : 1) voi
     for (int b = 0; b < 2; ++b) {
       // (the empty blocks' operands are zero: a branch here would have the
       // compiler move all sums about; dP's first, then dA's: all four operands
-      // at a time spill 53 registers instead of 23, 530 us instead of 467)
+      // at a time spill 53 registers instead of 23 and take 60 us more)
       const Op<NS> pr = upper_rows<NS>(smem + L::kdP, w, b);
       const Op<NS> pc = upper_turned<NS>(smem + L::kdP, w, b);
 #pragma unroll
@@ -1561,30 +1589,42 @@ __global__ __launch_bounds__(kDeltaBlock, kParts<T> == 1 && !SHARED ? 2 : 1) voi
     if (dg) {
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const float x = lane_sum<16>(row_h[r]);
-        if (l == 0) z.dG[16 * w + 4 * h + r] = double(x);
+        const float x = lane_sum<16>(a[r]), y = lane_sum<16>(b[r]);
+        if (l == 0) {
+          z.a[16 * w + 4 * h + r] = x;
+          z.b[16 * w + 4 * h + r] = y;
+        }
       }
-      end = lane_sum<kWave>(end);
-      if (t % kWave == 0) z.part[4 + w] = end;
       __syncthreads();
       if (t < kChunk) {
-        const int row = kChunk - 1 - t;
-        double x = z.dG[row] - ((double(z.cols[0][row]) + z.cols[1][row]) +
-                                (double(z.cols[2][row]) + z.cols[3][row]));
-        if (t == 0)
-          x += double(z.f.all) * ((double(z.part[0]) + z.part[1]) +
-                                  (double(z.part[2]) + z.part[3])) +
-               ((double(z.part[4]) + z.part[5]) + (double(z.part[6]) + z.part[7]));
+        const int row = kChunk - 1 - t, tile = row / 16;
+        // rows >= row: of all tokens (a), of its block row (H)
+        float sa = z.a[row], sr = z.rows[row];
+        // rows < row: of all tokens (b), of its block column (H)
+        float sb = row ? z.b[row - 1] : 0.f, sc = 0.f;
+#pragma unroll
+        for (int k = 1; k < 4; ++k)
+          if (row % 16 && k > tile) sc += z.cols[k][row - 1];
 #pragma unroll
         for (int d = 1; d < kWave; d <<= 1) {
-          const double u = __shfl_up(x, d, kWave);
-          if (t >= d) x += u;
+          const float u = __shfl_up(sa, d, kWave), v = __shfl_down(sb, d, kWave);
+          if (t >= d) sa += u;
+          if (t + d < kWave) sb += v;
         }
-        if (row < p.len) {
-          // behind exp(g) = 0 nothing depends on g: not the sums' roundings either
-          const int64_t at = (p.tok + row) * s.hv + vh;
-          dg[at] = in.g[at] < kGateFloor ? 0.f : float(x);
+#pragma unroll
+        for (int d = 1; d < 16; d <<= 1) {
+          const float u = __shfl_up(sr, d, kWave), v = __shfl_down(sc, d, kWave);
+          if (t % 16 >= d) sr += u;
+          if (t % 16 + d < 16) sc += v;
         }
+        // whole blocks below and before the tile's
+        const float f1 = lane_sum<kWave>(row < 16 ? z.cols[2][row] + z.cols[3][row] : 0.f);
+        const float f2 = lane_sum<kWave>(row < 32 ? z.cols[3][row] : 0.f);
+        const float full = tile == 1 ? f1 : tile == 2 ? f2 : 0.f;
+        const float kept_s = z.f.all * ((z.part[0] + z.part[1]) + (z.part[2] + z.part[3]));
+        if (row < p.len)
+          dg[(p.tok + row) * s.hv + vh] =
+              (sa + sb) + ((sr + sc) + (full + z.own[row])) + kept_s;
       }
     }
   }

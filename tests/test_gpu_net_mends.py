@@ -533,3 +533,38 @@ def test_the_fp16_gradient_in_a_graph():
         torch.cuda.synchronize()
         for p, q in zip(out, again):
             assert torch.equal(p, q) and p.isfinite().all()
+
+
+# ---------------------------------------------------------------------------
+# The gates' gradient behind strong decays
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("kind", ["fp32", "bf16"])
+@pytest.mark.parametrize("gate", [-2.0, -5.0, -10.0, -20.0, -60.0])
+def test_gradient_of_strong_gates(gate, kind):
+    """dg is as small as exp(g) then, and has the digits of every other gradient:
+    the operator's bound holds for it by itself.  (Sums of everything from a
+    token on, in which what does not cross the token cancels, had left 5e-3 at
+    -10 and noise of 1e9 times dg at -60.)"""
+    ins, do, ds = D.inputs(1, 150, 1, 2, 32, 48, R.TYPES[kind])
+    ins[3].fill_(gate)
+    D.compare(ins, do, ds)
+
+
+@pytest.mark.parametrize("shape", [(1, 300, 2, 2, 64, 64), (2, 130, 1, 3, 100, 40)])
+def test_gradient_of_strong_gates_among_weak_ones(shape):
+    """By the size of the gate: the strong ones' gradients are not lost beside
+    the weak ones'."""
+    import krylov_solvers_adjoint_amd as K
+    batch, tokens, hk, hv, dk, dv = shape
+    ins, do, ds = D.inputs(batch, tokens, hk, hv, dk, dv, torch.float32)
+    which = torch.randint(0, 4, ins[3].shape, generator=R.gen(3))
+    sizes = torch.tensor([-0.01, -1.0, -12.0, -40.0])
+    ins[3].copy_(sizes[which])
+    leaves = [t.cuda().requires_grad_() for t in ins]
+    out = K.gated_delta_rule(*leaves[:5], initial_state=leaves[5], output_final_state=True)
+    (dg,) = torch.autograd.grad(out, leaves[3], (do.cuda(), ds.cuda()))
+    ref = [t.double().requires_grad_() for t in ins]
+    out = R.delta_rule(*ref, dk ** -0.5)
+    (rg,) = torch.autograd.grad(out, ref[3], (do.double(), ds.double()))
+    for n in range(4):
+        assert R.rel(dg.cpu()[which == n], rg[which == n]) <= D.TOL, sizes[n]
