@@ -745,6 +745,101 @@ sla_status sla_delta_step(const sla_delta_dims* dims, const void* q, int64_t ldq
                           int64_t ldk, const void* v, int64_t ldv, const float* g,
                           const float* beta, float* state, void* o, hipStream_t stream);
 
+/*
+ * A projection with its epilogue: y = residual + f(x weight^T + bias), x
+ * [rows][inner], weight [outer][inner] contiguous, y [rows][outer].  bias
+ * [outer] (of btype: x's type or SLA_F32) and residual [rows][outer] may be
+ * NULL (zero); act: SLA_ACT_*, of which SLA_ACT_NONE is f(z) = z.  rows is
+ * below 2^31, inner and outer below 2^22.
+ */
+enum { SLA_ACT_NONE = 3 };
+sla_status sla_linear(const void* x, int64_t ldx, const void* weight, const void* bias,
+                      sla_type btype, const void* residual, int64_t ldr, int64_t rows,
+                      int64_t inner, int64_t outer, sla_type type, int act, void* y, void* work,
+                      int64_t work_bytes, hipStream_t stream);
+
+/* Workspace bytes of sla_linear (often 0) and of sla_linear_grad; either output
+ * may be NULL. */
+sla_status sla_linear_work(int64_t rows, int64_t inner, int64_t outer, sla_type type, int act,
+                           int64_t* forward_bytes_host, int64_t* grad_bytes_host);
+
+/* Gradients of sla_linear from dy [rows][outer] (which is the residual's own
+ * gradient); dx, dweight and dbias may each be NULL (not wanted).  bias is read
+ * with an activation only.  With no rows the weight's and bias's gradients are
+ * zero. */
+sla_status sla_linear_grad(const void* dy, int64_t lddy, const void* x, int64_t ldx,
+                           const void* weight, const void* bias, sla_type btype, int64_t rows,
+                           int64_t inner, int64_t outer, sla_type type, int act, void* dx,
+                           void* dweight, void* dbias, void* work, int64_t work_bytes,
+                           hipStream_t stream);
+
+/*
+ * Gated scan.  Every sequence and channel has a state h (fp32); token t turns
+ * it into
+ *   h <- exp(g_t) h + x_t
+ * and leaves it rounded to x's type.  x, g and h [tokens][channels]; g is of
+ * gate_type: x's type or SLA_F32.  g <= 0 (a decay) is the meant range, down to
+ * -infinity (the state begins anew); growth within a block of tokens (at most
+ * 256) may overflow.  What is not finite stays in its channel and its sequence,
+ * in the tokens behind it (gradients: before it).
+ * Sequences are laid out as sla_delta_rule's are: packed == 0, `tokens` are
+ * `sequences` of equal length; packed != 0, sequence i is the tokens offsets[i]
+ * .. offsets[i+1] - 1, falling offsets are raised, those outside clamped, and
+ * tokens of no sequence get zeros.
+ */
+typedef struct {
+  int64_t sequences, tokens, channels;
+  sla_type type, gate_type;
+  int packed;
+} sla_scan_dims;
+
+/* Bytes of the block that sla_gated_scan fills for its gradient, and of either's
+ * workspace; either output may be NULL. */
+sla_status sla_gated_scan_work(const sla_scan_dims* dims, int64_t* kept_bytes_host,
+                               int64_t* work_bytes_host);
+
+/* The scan over whole sequences.  initial_state and final_state [sequences]
+ * [channels] may be NULL (zeros; not wanted), and so may kept (no gradient will
+ * be asked for). */
+sla_status sla_gated_scan(const sla_scan_dims* dims, const void* x, int64_t ldx, const void* g,
+                          int64_t ldg, const int32_t* offsets, const float* initial_state,
+                          void* h, float* final_state, void* kept, int64_t kept_bytes, void* work,
+                          int64_t work_bytes, hipStream_t stream);
+
+/* Its gradients, from `kept` as the forward call left it.  grad_final_state may
+ * be NULL (zero), and so may every output (not wanted). */
+sla_status sla_gated_scan_grad(const sla_scan_dims* dims, const void* x, int64_t ldx,
+                               const void* g, int64_t ldg, const void* kept, int64_t kept_bytes,
+                               const void* dh, int64_t lddh, const float* grad_final_state,
+                               void* dx, void* dg, float* grad_initial_state, void* work,
+                               int64_t work_bytes, hipStream_t stream);
+
+/* One token of every sequence (tokens == sequences, packed == 0) against the
+ * kept states [sequences][channels], updated in place. */
+sla_status sla_gated_scan_step(const sla_scan_dims* dims, const void* x, int64_t ldx,
+                               const void* g, int64_t ldg, float* state, void* h,
+                               hipStream_t stream);
+
+/*
+ * Orthogonalised matrices: each of `count` matrices m [rows][cols] (one behind
+ * the other, rows ldm elements apart) becomes X = m / (|m|_F + eps), then
+ * `steps` times
+ *   X <- a X + (b A + c A A) X,   A = X X^T
+ * with a, b, c = coefficients[3 i ..] (on the host) of step i, so that its
+ * singular values s go to a s + b s^3 + c s^5.  x [count][rows][cols] is of m's
+ * type.  Entries of X have to stay below 16, of A and b A + c A A below 64 and
+ * 256 on the way: singular values up to 4, coefficients up to 64.  rows and
+ * cols are at most 65536, count at most 65535, steps at most 64.
+ */
+sla_status sla_orthogonalise(const void* m, int64_t ldm, int64_t count, int64_t rows,
+                             int64_t cols, sla_type type, int steps, const double* coefficients,
+                             double eps, void* x, void* work, int64_t work_bytes,
+                             hipStream_t stream);
+
+/* Workspace bytes of sla_orthogonalise. */
+sla_status sla_orthogonalise_work(int64_t count, int64_t rows, int64_t cols, sla_type type,
+                                  int64_t* bytes_host);
+
 /* Message of the last failed call on this thread ("" if none): the error
  * reporting of this boundary (not on the pages). */
 const char* sla_last_error(void);

@@ -35,6 +35,9 @@ __all__ = [
     "layer_norm", "gated_ffn", "gated_delta_rule", "gated_delta_step",
     "sla_layer_norm", "sla_layer_norm_grad", "sla_gated_ffn", "sla_gated_ffn_grad",
     "sla_delta_rule", "sla_delta_rule_grad", "sla_delta_step",
+    "linear", "gated_scan", "gated_scan_step", "orthogonalise",
+    "sla_linear", "sla_linear_grad", "sla_gated_scan", "sla_gated_scan_grad",
+    "sla_gated_scan_step", "sla_orthogonalise",
     "LIB_PATH", "EXPORTS",
 ]
 
@@ -66,6 +69,9 @@ EXPORTS = [
     "sla_layer_norm", "sla_layer_norm_work", "sla_layer_norm_grad",
     "sla_gated_ffn", "sla_gated_ffn_work", "sla_gated_ffn_grad",
     "sla_delta_rule_work", "sla_delta_rule", "sla_delta_rule_grad", "sla_delta_step",
+    "sla_linear", "sla_linear_work", "sla_linear_grad",
+    "sla_gated_scan_work", "sla_gated_scan", "sla_gated_scan_grad", "sla_gated_scan_step",
+    "sla_orthogonalise", "sla_orthogonalise_work",
     "sla_cg_solve_noalloc", "sla_last_error", "sla_status_string",
 ]
 
@@ -148,6 +154,18 @@ def _bind(lib):
         "sla_delta_rule_grad": [_P, _P, _I64, _P, _I64, _P, _I64, _P, _P, _P, _I64, _P, _I64,
                                 _P, _P, _P, _P, _P, _P, _P, _P, _I64, _P],
         "sla_delta_step": [_P, _P, _I64, _P, _I64, _P, _I64, _P, _P, _P, _P, _P],
+        "sla_linear": [_P, _I64, _P, _P, _S, _P, _I64, _I64, _I64, _I64, _S, _S, _P, _P, _I64,
+                       _P],
+        "sla_linear_work": [_I64, _I64, _I64, _S, _S, _P, _P],
+        "sla_linear_grad": [_P, _I64, _P, _I64, _P, _P, _S, _I64, _I64, _I64, _S, _S, _P, _P,
+                            _P, _P, _I64, _P],
+        "sla_gated_scan_work": [_P, _P, _P],
+        "sla_gated_scan": [_P, _P, _I64, _P, _I64, _P, _P, _P, _P, _P, _I64, _P, _I64, _P],
+        "sla_gated_scan_grad": [_P, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _P, _P, _P, _P,
+                                _I64, _P],
+        "sla_gated_scan_step": [_P, _P, _I64, _P, _I64, _P, _P, _P],
+        "sla_orthogonalise": [_P, _I64, _I64, _I64, _I64, _S, _S, _P, _D, _P, _P, _I64, _P],
+        "sla_orthogonalise_work": [_I64, _I64, _I64, _S, ctypes.POINTER(_I64)],
     }
     for name, args in sig.items():
         f = getattr(lib, name)
@@ -986,6 +1004,8 @@ def solve(A: SparseTensor, b: torch.Tensor, tol: float = 1e-10, maxit: int = 100
     return A.solve(b, tol, maxit, precond, method)
 
 
-from .network import (gated_delta_rule, gated_delta_step, gated_ffn, layer_norm,  # noqa: E402
-                      sla_delta_rule, sla_delta_rule_grad, sla_delta_step, sla_gated_ffn,
-                      sla_gated_ffn_grad, sla_layer_norm, sla_layer_norm_grad)
+from .network import (gated_delta_rule, gated_delta_step, gated_ffn, gated_scan,  # noqa: E402
+                      gated_scan_step, layer_norm, linear, orthogonalise, sla_delta_rule,
+                      sla_delta_rule_grad, sla_delta_step, sla_gated_ffn, sla_gated_ffn_grad,
+                      sla_gated_scan, sla_gated_scan_grad, sla_gated_scan_step, sla_layer_norm,
+                      sla_layer_norm_grad, sla_linear, sla_linear_grad, sla_orthogonalise)

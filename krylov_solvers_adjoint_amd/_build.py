@@ -16,7 +16,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libsla.so")
 SOURCES = ["api.hip", "csr_build.hip", "cg.hip", "lanczos.hip", "bicgstab.hip", "reorder.hip",
-           "noalloc.hip", "norm.hip", "ffn.hip", "delta.hip"]
+           "noalloc.hip", "norm.hip", "ffn.hip", "delta.hip", "linear.hip", "scan.hip",
+           "ortho.hip"]
 ARCH = os.environ.get("SLA_OFFLOAD_ARCH", "gfx950")
 
 HIPCC_FLAGS = [

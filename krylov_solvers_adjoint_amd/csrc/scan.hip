@@ -1,0 +1,763 @@
+// The gated scan: a linear recurrence with a decay of its own for every
+// channel and token, its gradients, and one token against a kept state.
+//
+//   a_t = exp(g_t)      h_t = a_t h_{t-1} + x_t
+//   l_t = dh_t + m_t    m_{t-1} = a_t l_t     (m_T: the final state's gradient)
+//   dx_t = l_t          dg_t = m_{t-1} h_{t-1}          ds0 = m_0
+//
+// Bound by memory: forward reads x and g and writes h, backward reads x, g and
+// dh and writes dx and dg, once each.  A span of tokens is a map h -> P h + H
+// with P the product of its decays (and, backwards, m -> P m + M): maps are
+// joined without a division, so a decay of zero or a product that underflows
+// is harmless.  A thread holds kSpan tokens of its channels in registers; the
+// spans of a workgroup's block of tokens are joined in the wave by shuffles and
+// over the waves through LDS, in a fixed order; then every thread walks its
+// tokens again from the state in front of them.  From block to block the state
+// is carried in registers, while the next block's loads travel.
+//
+// The forward pass keeps the state in front of every block (4 bytes a channel
+// and block), from which the backward pass makes h again: it needs x then
+// instead of h, as many bytes, and h in fp32 instead of rounded.
+//
+// Where sequences and channels do not fill the card a sequence is cut into
+// segments: k_scan_ends finds every segment's map first, the walks begin with
+// the maps of the segments on the way joined.  That reads two arrays again.
+#include <type_traits>
+
+#include "net.h"
+
+namespace sla {
+namespace net {
+namespace {
+
+constexpr int kSpan = 8;       // tokens a thread holds
+constexpr int kMostSegments = 64;
+constexpr int kFill = 512;     // workgroups wanted: two on each of the 256 CUs
+constexpr int64_t kMostGroups = int64_t(1) << 20;   // of a launch; they walk the items
+
+// exp(g) to 2 ulp: the instruction's exp2 with the product's rounding error put
+// right.  Below -200 and above 200 it is 0 and inf as it is; NaN stays.
+__device__ __forceinline__ float decay(float g) {
+  constexpr float kHi = 1.44269502f, kLo = 1.92596303e-08f;   // log2(e)
+  g = g < -200.f ? -200.f : g > 200.f ? 200.f : g;
+  const float t = g * kHi;
+  const float r = __builtin_fmaf(g, kLo, __builtin_fmaf(g, kHi, -t));
+  const float e = __builtin_amdgcn_exp2f(t);
+  return __builtin_fmaf(e, r * 0.693147182f, e);
+}
+
+struct ScanShape {
+  int64_t nseq, seqlen, total;   // seqlen: tokens of every sequence (no offsets)
+  int64_t channels;
+  const int32_t* tok;            // packed: first token of each sequence [nseq + 1]
+  int tiles;                     // of channels
+  int segments;
+  int64_t items;
+};
+
+// What a workgroup works on: a sequence's segment and a tile of its channels.
+struct Item {
+  int64_t seq;
+  int tile, seg;
+  int64_t from, len;      // the sequence's tokens
+  int64_t first;          // its first block among all blocks
+  int64_t b0, b1, blocks; // the segment's blocks, the sequence's
+};
+template <int BT>
+__device__ __forceinline__ Item item_of(const ScanShape& s, int64_t id) {
+  Item w;
+  w.tile = int(id % s.tiles);
+  id /= s.tiles;
+  w.seg = int(id % s.segments);
+  w.seq = id / s.segments;
+  if (w.seq >= s.nseq) return w;   // the tokens of no sequence
+  if (s.tok) {
+    w.from = s.tok[w.seq];
+    w.len = s.tok[w.seq + 1] - w.from;
+    w.first = w.from / BT + w.seq;
+  } else {
+    w.from = w.seq * s.seqlen;
+    w.len = s.seqlen;
+    w.first = w.seq * div_up(s.seqlen, BT);
+  }
+  w.blocks = (w.len + BT - 1) / BT;
+  const int64_t each = (w.blocks + s.segments - 1) / s.segments;
+  w.b0 = w.seg * each < w.blocks ? w.seg * each : w.blocks;
+  w.b1 = w.b0 + each < w.blocks ? w.b0 + each : w.blocks;
+  return w;
+}
+// Workgroups go to the 8 XCDs in turn: each gets a run of neighbouring items,
+// whose tiles share cache lines.
+__device__ __forceinline__ int64_t item_id(int64_t items) {
+  const int64_t total = gridDim.x, b = blockIdx.x;
+  if (total < items) return b;
+  const int64_t xcd = b % kXcds, q = total / kXcds, r = total % kXcds;
+  return xcd * q + (xcd < r ? xcd : r) + b / kXcds;
+}
+
+// A thread's place: CL lanes have the tile's channels, the others are further
+// spans of tokens.
+template <int CL, int WAVES, int V>
+struct Place {
+  static constexpr int kSlices = kWave / CL;            // spans of a wave
+  static constexpr int kBlock = WAVES * kSlices * kSpan;  // tokens of a block
+  int lane, slice, wave;
+  int64_t c;        // the thread's first channel to read
+  bool on;          // whether it is the thread's own (lanes behind the last read another's)
+  __device__ __forceinline__ Place(int tile, int64_t channels) {
+    const int t = threadIdx.x;
+    lane = t % CL;
+    slice = t % kWave / CL;
+    wave = __builtin_amdgcn_readfirstlane(t / kWave);
+    c = (int64_t(tile) * CL + lane) * V;
+    on = c < channels;
+    if (!on) c = channels - V;
+  }
+  __device__ __forceinline__ int64_t token(int64_t block) const {
+    return block * kBlock + (wave * kSlices + slice) * kSpan;
+  }
+};
+
+// The raw values of a thread's span; tokens behind the end read the last one.
+template <typename T, int V>
+struct Raw {
+  typename VecOf<T, V>::type v[kSpan];
+  __device__ __forceinline__ void load(const T* p, int64_t ld, int64_t t, int64_t len) {
+#pragma unroll
+    for (int j = 0; j < kSpan; ++j) {
+      const int64_t at = t + j < len ? t + j : len - 1;
+      v[j] = *reinterpret_cast<const typename VecOf<T, V>::type*>(p + at * ld);
+    }
+  }
+};
+
+// In-wave joins over the slices (CL lanes apart): inclusive from the first
+// slice on (UP), or from the last.
+template <int CL, int V, bool UP>
+__device__ __forceinline__ void join_slices(float (&P)[V], float (&H)[V], int slice) {
+#pragma unroll
+  for (int d = 1; d < kWave / CL; d <<= 1) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const float p = UP ? __shfl_up(P[v], d * CL, kWave) : __shfl_down(P[v], d * CL, kWave);
+      const float q = UP ? __shfl_up(H[v], d * CL, kWave) : __shfl_down(H[v], d * CL, kWave);
+      const bool has = UP ? slice >= d : slice + d < kWave / CL;
+      if (has) {
+        H[v] = P[v] * q + H[v];
+        P[v] *= p;
+      }
+    }
+  }
+}
+// ... and what lies before (behind) the own slice alone.
+template <int CL, int V, bool UP>
+__device__ __forceinline__ void shift_slices(float (&P)[V], float (&H)[V], int slice) {
+  if constexpr (CL == kWave) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) P[v] = 1.f, H[v] = 0.f;
+  } else {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const float p = UP ? __shfl_up(P[v], CL, kWave) : __shfl_down(P[v], CL, kWave);
+      const float q = UP ? __shfl_up(H[v], CL, kWave) : __shfl_down(H[v], CL, kWave);
+      const bool has = UP ? slice > 0 : slice < kWave / CL - 1;
+      P[v] = has ? p : 1.f;
+      H[v] = has ? q : 0.f;
+    }
+  }
+}
+
+// Rows of tokens of no sequence become zero.
+template <typename T, int CL, int WAVES, int V>
+__device__ __forceinline__ void clear_rows(const ScanShape& s, const Item& w, T* out) {
+  if (!out) return;
+  const Place<CL, WAVES, V> me(w.tile, s.channels);
+  const int64_t head = s.tok[0], tail = s.tok[s.nseq], rows = head + s.total - tail;
+  if (!me.on) return;
+  constexpr int kSlices = WAVES * Place<CL, WAVES, V>::kSlices;
+  for (int64_t i = int64_t(w.seg) * kSlices + threadIdx.x / CL; i < rows;
+       i += int64_t(s.segments) * kSlices) {
+    typename VecOf<T, V>::type z = {};
+    *reinterpret_cast<typename VecOf<T, V>::type*>(
+        out + (i < head ? i : tail + i - head) * s.channels + me.c) = z;
+  }
+}
+
+template <typename T, typename G, int CL, int WAVES, int V>
+__global__ __launch_bounds__(WAVES* kWave) void k_scan(
+    ScanShape s, const T* __restrict__ x, int64_t ldx, const G* __restrict__ g, int64_t ldg,
+    const float* __restrict__ s0, T* __restrict__ h, float* __restrict__ last,
+    float* __restrict__ kept, const float* __restrict__ ends) {
+  typedef Place<CL, WAVES, V> At;
+  constexpr int BT = At::kBlock;
+  __shared__ float2 agg[2][WAVES][CL * V];
+  int buf = 0;
+  for (int64_t id = item_id(s.items); id < s.items; id += gridDim.x) {
+    const Item w = item_of<BT>(s, id);
+    if (w.seq >= s.nseq) {
+      clear_rows<T, CL, WAVES, V>(s, w, h);
+      continue;
+    }
+    if (w.seg > 0 && w.b0 == w.b1) continue;
+    const At me(w.tile, s.channels);
+    float carry[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) carry[v] = s0 ? s0[w.seq * s.channels + me.c + v] : 0.f;
+    for (int k = 0; k < w.seg; ++k) {
+      const float* e = ends + ((w.seq * s.segments + k) * s.channels + me.c) * 2;
+#pragma unroll
+      for (int v = 0; v < V; ++v) carry[v] = e[2 * v] * carry[v] + e[2 * v + 1];
+    }
+    const T* px = x + w.from * ldx + me.c;
+    const G* pg = g + w.from * ldg + me.c;
+    Raw<T, V> rx;
+    Raw<G, V> rg;
+    if (w.b0 < w.b1) {
+      rx.load(px, ldx, me.token(w.b0), w.len);
+      rg.load(pg, ldg, me.token(w.b0), w.len);
+    }
+    for (int64_t b = w.b0; b < w.b1; ++b) {
+      const int64_t t0 = me.token(b);
+      float a[kSpan][V], u[kSpan][V], P[V], H[V];
+#pragma unroll
+      for (int v = 0; v < V; ++v) P[v] = 1.f, H[v] = 0.f;
+#pragma unroll
+      for (int j = 0; j < kSpan; ++j) {
+        const bool live = t0 + j < w.len;   // what lies behind the end changes nothing
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          a[j][v] = live ? decay(float(rg.v[j][v])) : 1.f;
+          u[j][v] = live ? float(rx.v[j][v]) : 0.f;
+          H[v] = a[j][v] * H[v] + u[j][v];
+          P[v] *= a[j][v];
+        }
+      }
+      if (b + 1 < w.b1) {
+        rx.load(px, ldx, me.token(b + 1), w.len);
+        rg.load(pg, ldg, me.token(b + 1), w.len);
+      }
+      join_slices<CL, V, true>(P, H, me.slice);
+      if (me.slice == At::kSlices - 1) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) agg[buf][me.wave][me.lane * V + v] = make_float2(P[v], H[v]);
+      }
+      shift_slices<CL, V, true>(P, H, me.slice);
+      __syncthreads();
+      if (kept && me.on && me.wave == 0 && me.slice == 0) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) kept[(w.first + b) * s.channels + me.c + v] = carry[v];
+      }
+      float state[V];
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        state[v] = carry[v];
+#pragma unroll
+        for (int k = 0; k < WAVES; ++k) {
+          if (k == me.wave) state[v] = carry[v];
+          const float2 m = agg[buf][k][me.lane * V + v];
+          carry[v] = m.x * carry[v] + m.y;
+        }
+        state[v] = P[v] * state[v] + H[v];
+      }
+      buf ^= 1;
+#pragma unroll
+      for (int j = 0; j < kSpan; ++j) {
+        typename VecOf<T, V>::type o;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          state[v] = a[j][v] * state[v] + u[j][v];
+          o[v] = T(state[v]);
+        }
+        if (me.on && t0 + j < w.len)
+          *reinterpret_cast<typename VecOf<T, V>::type*>(
+              h + (w.from + t0 + j) * s.channels + me.c) = o;
+      }
+    }
+    if (last && me.on && w.b1 == w.blocks && me.wave == 0 && me.slice == 0) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) last[w.seq * s.channels + me.c + v] = carry[v];
+    }
+  }
+}
+
+template <typename T, typename G, int CL, int WAVES, int V>
+__global__ __launch_bounds__(WAVES* kWave) void k_scan_grad(
+    ScanShape s, const T* __restrict__ x, int64_t ldx, const G* __restrict__ g, int64_t ldg,
+    const float* __restrict__ kept, const T* __restrict__ dh, int64_t lddh,
+    const float* __restrict__ dlast, T* __restrict__ dx, G* __restrict__ dg,
+    float* __restrict__ ds0, const float* __restrict__ ends) {
+  typedef Place<CL, WAVES, V> At;
+  constexpr int BT = At::kBlock;
+  __shared__ float2 fwd[2][WAVES][CL * V];
+  __shared__ float back[2][WAVES][CL * V];
+  int buf = 0;
+  for (int64_t id = item_id(s.items); id < s.items; id += gridDim.x) {
+    const Item w = item_of<BT>(s, id);
+    if (w.seq >= s.nseq) {
+      clear_rows<T, CL, WAVES, V>(s, w, dx);
+      clear_rows<G, CL, WAVES, V>(s, w, dg);
+      continue;
+    }
+    if (w.seg > 0 && w.b0 == w.b1) continue;
+    const At me(w.tile, s.channels);
+    float carry[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) carry[v] = dlast ? dlast[w.seq * s.channels + me.c + v] : 0.f;
+    for (int k = s.segments - 1; k > w.seg; --k) {
+      const float* e = ends + ((w.seq * s.segments + k) * s.channels + me.c) * 2;
+#pragma unroll
+      for (int v = 0; v < V; ++v) carry[v] = e[2 * v] * carry[v] + e[2 * v + 1];
+    }
+    const T* px = x + w.from * ldx + me.c;
+    const G* pg = g + w.from * ldg + me.c;
+    const T* pd = dh + w.from * lddh + me.c;
+    Raw<T, V> rx, rd;
+    Raw<G, V> rg;
+    auto load = [&](int64_t b) {
+      rx.load(px, ldx, me.token(b), w.len);
+      rg.load(pg, ldg, me.token(b), w.len);
+      rd.load(pd, lddh, me.token(b), w.len);
+    };
+    if (w.b0 < w.b1) load(w.b1 - 1);
+    for (int64_t b = w.b1; b-- > w.b0;) {
+      const int64_t t0 = me.token(b);
+      float start[V];
+#pragma unroll
+      for (int v = 0; v < V; ++v) start[v] = kept[(w.first + b) * s.channels + me.c + v];
+      float a[kSpan][V], u[kSpan][V], d[kSpan][V], P[V], H[V], Q[V], M[V];
+#pragma unroll
+      for (int v = 0; v < V; ++v) P[v] = 1.f, H[v] = 0.f, M[v] = 0.f;
+#pragma unroll
+      for (int j = 0; j < kSpan; ++j) {
+        const bool live = t0 + j < w.len;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          a[j][v] = live ? decay(float(rg.v[j][v])) : 1.f;
+          u[j][v] = live ? float(rx.v[j][v]) : 0.f;
+          d[j][v] = live ? float(rd.v[j][v]) : 0.f;
+          H[v] = a[j][v] * H[v] + u[j][v];
+          P[v] *= a[j][v];
+        }
+      }
+      if (b > w.b0) load(b - 1);
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+#pragma unroll
+        for (int j = kSpan - 1; j >= 0; --j) M[v] = a[j][v] * (d[j][v] + M[v]);
+        Q[v] = P[v];
+      }
+      join_slices<CL, V, true>(P, H, me.slice);
+      join_slices<CL, V, false>(Q, M, me.slice);
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        if (me.slice == At::kSlices - 1)
+          fwd[buf][me.wave][me.lane * V + v] = make_float2(P[v], H[v]);
+        if (me.slice == 0) back[buf][me.wave][me.lane * V + v] = M[v];
+      }
+      shift_slices<CL, V, true>(P, H, me.slice);
+      shift_slices<CL, V, false>(Q, M, me.slice);
+      __syncthreads();
+      float state[V], m[V];
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        state[v] = start[v];
+        m[v] = carry[v];
+#pragma unroll
+        for (int k = 0; k < WAVES; ++k) {
+          const float2 f = fwd[buf][k][me.lane * V + v];
+          if (k < me.wave) state[v] = f.x * state[v] + f.y;
+        }
+#pragma unroll
+        for (int k = WAVES - 1; k >= 0; --k) {
+          if (k == me.wave) m[v] = carry[v];
+          carry[v] = fwd[buf][k][me.lane * V + v].x * carry[v] + back[buf][k][me.lane * V + v];
+        }
+        state[v] = P[v] * state[v] + H[v];
+        m[v] = Q[v] * m[v] + M[v];
+      }
+      buf ^= 1;
+#pragma unroll
+      for (int j = 0; j < kSpan; ++j) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          const float next = a[j][v] * state[v] + u[j][v];
+          u[j][v] = state[v];
+          state[v] = next;
+        }
+      }
+#pragma unroll
+      for (int j = kSpan - 1; j >= 0; --j) {
+        typename VecOf<T, V>::type ox;
+        typename VecOf<G, V>::type og;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          const float l = d[j][v] + m[v];
+          m[v] = a[j][v] * l;
+          ox[v] = T(l);
+          og[v] = G(m[v] * u[j][v]);
+        }
+        if (me.on && t0 + j < w.len) {
+          const int64_t at = (w.from + t0 + j) * s.channels + me.c;
+          if (dx) *reinterpret_cast<typename VecOf<T, V>::type*>(dx + at) = ox;
+          if (dg) *reinterpret_cast<typename VecOf<G, V>::type*>(dg + at) = og;
+        }
+      }
+    }
+    if (ds0 && me.on && w.seg == 0 && me.wave == 0 && me.slice == 0) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) ds0[w.seq * s.channels + me.c + v] = carry[v];
+    }
+  }
+}
+
+// Every segment's map, forwards (u = x: from its first token to its last) or
+// backwards (u = dh).  Each span of threads walks a run of the segment's
+// tokens; one join at the end.
+template <typename T, typename G, int CL, int WAVES, int V, bool BACK>
+__global__ __launch_bounds__(WAVES* kWave) void k_scan_ends(
+    ScanShape s, const T* __restrict__ u, int64_t ldu, const G* __restrict__ g, int64_t ldg,
+    float* __restrict__ ends) {
+  typedef Place<CL, WAVES, V> At;
+  constexpr int BT = At::kBlock, kRuns = WAVES * At::kSlices;
+  __shared__ float2 agg[WAVES][CL * V];
+  for (int64_t id = item_id(s.items); id < s.items; id += gridDim.x) {
+    const Item w = item_of<BT>(s, id);
+    if (w.seq >= s.nseq) continue;
+    const At me(w.tile, s.channels);
+    const int64_t end = w.b1 * BT < w.len ? w.b1 * BT : w.len;
+    const int64_t begin = w.b0 * BT < end ? w.b0 * BT : end;
+    const int64_t each = (end - begin + kRuns - 1) / kRuns;
+    const int run = me.wave * At::kSlices + me.slice;
+    const int64_t lo = begin + run * each < end ? begin + run * each : end;
+    const int64_t hi = lo + each < end ? lo + each : end;
+    const T* pu = u + w.from * ldu + me.c;
+    const G* pg = g + w.from * ldg + me.c;
+    float P[V], H[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) P[v] = 1.f, H[v] = 0.f;
+    for (int64_t k = 0; k < each; k += kSpan) {
+      Raw<T, V> ru;
+      Raw<G, V> rg;
+      // backwards the walk begins at the end; tokens outside of the run change nothing
+      const int64_t t = BACK ? hi - kSpan - k : lo + k;
+#pragma unroll
+      for (int j = 0; j < kSpan; ++j) {
+        const int64_t q = t + j < 0 ? 0 : t + j < w.len ? t + j : w.len - 1;
+        ru.v[j] = *reinterpret_cast<const typename VecOf<T, V>::type*>(pu + q * ldu);
+        rg.v[j] = *reinterpret_cast<const typename VecOf<G, V>::type*>(pg + q * ldg);
+      }
+#pragma unroll
+      for (int i = 0; i < kSpan; ++i) {
+        const int j = BACK ? kSpan - 1 - i : i;
+        const bool live = t + j >= lo && t + j < hi;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          const float a = live ? decay(float(rg.v[j][v])) : 1.f;
+          const float y = live ? float(ru.v[j][v]) : 0.f;
+          H[v] = BACK ? a * (y + H[v]) : a * H[v] + y;
+          P[v] *= a;
+        }
+      }
+    }
+    join_slices<CL, V, !BACK>(P, H, me.slice);
+    __syncthreads();   // the item before has been read
+    if (me.slice == (BACK ? 0 : At::kSlices - 1)) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) agg[me.wave][me.lane * V + v] = make_float2(P[v], H[v]);
+    }
+    __syncthreads();
+    if (me.on && me.wave == 0 && me.slice == 0) {
+      float* e = ends + ((w.seq * s.segments + w.seg) * s.channels + me.c) * 2;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        float p = 1.f, q = 0.f;
+#pragma unroll
+        for (int i = 0; i < WAVES; ++i) {
+          const float2 m = agg[BACK ? WAVES - 1 - i : i][me.lane * V + v];
+          q = m.x * q + m.y;
+          p *= m.x;
+        }
+        e[2 * v] = p;
+        e[2 * v + 1] = q;
+      }
+    }
+  }
+}
+
+// The sequences' first tokens from the caller's offsets: each is the largest
+// of its predecessors and itself, clamped (they are on the device and cannot
+// be refused here), so that no kernel leaves the arrays.
+__global__ __launch_bounds__(kWave) void k_scan_plan(const int32_t* __restrict__ cu, int64_t nseq,
+                                                     int64_t total, int32_t* __restrict__ tok) {
+  int carry = 0;
+  for (int64_t b = 0; b <= nseq; b += kWave) {
+    const int64_t i = b + threadIdx.x;
+    int v = i <= nseq ? cu[i] : 0;
+    v = v < 0 ? 0 : (v > total ? int(total) : v);
+#pragma unroll
+    for (int d = 1; d < kWave; d <<= 1) {
+      const int u = __shfl_up(v, d, kWave);
+      if (int(threadIdx.x) >= d && u > v) v = u;
+    }
+    v = v > carry ? v : carry;
+    if (i <= nseq) tok[i] = v;
+    carry = __shfl(v, kWave - 1, kWave);
+  }
+}
+
+// One token of every sequence; a thread has V channels of a row.
+template <typename T, typename G, int V>
+__global__ __launch_bounds__(256) void k_scan_step(const T* __restrict__ x, int64_t ldx,
+                                                   const G* __restrict__ g, int64_t ldg,
+                                                   int64_t rows, int64_t channels,
+                                                   float* __restrict__ state, T* __restrict__ h) {
+  const int64_t per = (channels + V - 1) / V, all = rows * per;
+  for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < all;
+       i += int64_t(gridDim.x) * 256) {
+    const int64_t r = all < (int64_t(1) << 32) ? int64_t(uint32_t(i) / uint32_t(per)) : i / per;
+    const int64_t c = (i - r * per) * V, have = channels - c;
+    float xv[V], gv[V], sv[V];
+    load_f32<V>(x + r * ldx + c, have, xv);
+    load_f32<V>(g + r * ldg + c, have, gv);
+    load_f32<V>(state + r * channels + c, have, sv);
+#pragma unroll
+    for (int v = 0; v < V; ++v) sv[v] = decay(gv[v]) * sv[v] + xv[v];
+    store_f32<V>(state + r * channels + c, have, sv);
+    store_f32<V>(h + r * channels + c, have, sv);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+
+// Lanes along the channels and waves of a workgroup, and the segments of a
+// sequence.  The sizes alone decide (what the forward pass keeps is laid out by
+// them).
+struct ScanPlan {
+  int cl, waves, v, segments;
+  int64_t tiles, blocks, block_tokens;   // blocks: of all sequences (packed: at most)
+};
+ScanPlan scan_plan(const sla_scan_dims* d) {
+  ScanPlan p;
+  p.v = d->type != SLA_F32 && d->channels % 2 == 0 ? 2 : 1;
+  const int64_t lanes = d->channels / p.v, n = d->sequences ? d->sequences : 1;
+  const int64_t mean = div_up(d->tokens, n);
+  p.cl = 64;
+  while (p.cl > 16 && (lanes <= p.cl / 2 || n * div_up(lanes, p.cl) < kFill)) p.cl /= 2;
+  p.waves = mean <= 4 * kSpan * (kWave / p.cl) ? 1 : 8;
+  p.tiles = div_up(lanes, p.cl);
+  p.block_tokens = int64_t(p.waves) * (kWave / p.cl) * kSpan;
+  const int64_t groups = n * p.tiles, blocks = div_up(mean, p.block_tokens);
+  int64_t s = groups >= kFill / 2 ? 1 : div_up(kFill, groups);
+  s = s < blocks / 2 ? s : blocks / 2;
+  p.segments = int(s < 1 ? 1 : s < kMostSegments ? s : kMostSegments);
+  p.blocks = d->packed ? d->tokens / p.block_tokens + n : n * blocks;
+  return p;
+}
+
+int64_t up256(int64_t n) { return div_up(n, 256) * 256; }
+
+struct ScanSizes {
+  ScanPlan plan;
+  int64_t tok, kept, work;   // bytes: the offsets', all that is kept, the workspace
+};
+sla_status scan_sizes(const char* who, const sla_scan_dims* d, ScanSizes& z) {
+  SLA_NET_REQUIRE(d, "%s: dims is NULL", who);
+  SLA_NET_REQUIRE(valid_type(d->type) && (d->gate_type == d->type || d->gate_type == SLA_F32),
+                  "%s: unknown or mixed types", who);
+  SLA_NET_REQUIRE(d->sequences >= 0 && d->sequences < (int64_t(1) << 31) && d->tokens >= 0 &&
+                      d->tokens < (int64_t(1) << 40), "%s: sequences or tokens out of range", who);
+  SLA_NET_REQUIRE(d->channels >= 1 && d->channels < (int64_t(1) << 31),
+                  "%s: channels out of range", who);
+  if (d->packed) {
+    SLA_NET_REQUIRE(d->tokens < (int64_t(1) << 31), "%s: too many tokens for 32-bit offsets", who);
+    SLA_NET_REQUIRE(d->sequences > 0 || d->tokens == 0, "%s: tokens without a sequence", who);
+  } else {
+    SLA_NET_REQUIRE(d->sequences ? d->tokens % d->sequences == 0 : d->tokens == 0,
+                    "%s: %lld tokens are not %lld equal sequences", who, (long long)d->tokens,
+                    (long long)d->sequences);
+  }
+  z.plan = scan_plan(d);
+  // no product of sizes below passes 63 bits: nothing larger fits a card
+  const double all = double(z.plan.blocks + d->tokens + d->sequences * kMostSegments) *
+                     double(d->channels);
+  SLA_NET_REQUIRE(all < 1e15, "%s: too large", who);
+  z.tok = d->packed ? up256((d->sequences + 1) * 4) : 0;
+  z.kept = z.tok + up256(z.plan.blocks * d->channels * 4);
+  z.work = z.tok + (z.plan.segments > 1
+                        ? up256(d->sequences * z.plan.segments * d->channels * 8) : 0);
+  return SLA_OK;
+}
+
+template <typename F>
+sla_status with_scan(const sla_scan_dims* d, const ScanPlan& p, F&& f) {
+  auto shape = [&](auto te, auto ge, auto v) -> sla_status {
+    using std::integral_constant;
+    auto waves = [&](auto cl) -> sla_status {
+      if (p.waves == 1) return f(te, ge, cl, integral_constant<int, 1>(), v);
+      return f(te, ge, cl, integral_constant<int, 8>(), v);
+    };
+    if (p.cl == 64) return waves(integral_constant<int, 64>());
+    if (p.cl == 32) return waves(integral_constant<int, 32>());
+    return waves(integral_constant<int, 16>());
+  };
+  auto width = [&](auto te, auto ge) -> sla_status {
+    if constexpr (sizeof(te) == 2)
+      if (p.v == 2) return shape(te, ge, std::integral_constant<int, 2>());
+    return shape(te, ge, std::integral_constant<int, 1>());
+  };
+  const bool wide = d->gate_type == SLA_F32;
+  if (d->type == SLA_F32) return width(float(), float());
+  if (d->type == SLA_F16) return wide ? width(_Float16(), float()) : width(_Float16(), _Float16());
+  return wide ? width(__bf16(), float()) : width(__bf16(), __bf16());
+}
+
+ScanShape scan_shape(const sla_scan_dims* d, const ScanPlan& p, const int32_t* tok) {
+  ScanShape s{};
+  s.nseq = d->sequences;
+  s.seqlen = d->sequences && !d->packed ? d->tokens / d->sequences : 0;
+  s.total = d->tokens;
+  s.channels = d->channels;
+  s.tok = tok;
+  s.tiles = int(p.tiles);
+  s.segments = p.segments;
+  s.items = (s.nseq + (tok ? 1 : 0)) * p.tiles * p.segments;
+  return s;
+}
+int scan_grid(const ScanShape& s) { return int(s.items < kMostGroups ? s.items : kMostGroups); }
+
+}  // namespace
+}  // namespace net
+}  // namespace sla
+
+using namespace sla;
+using namespace sla::net;
+
+extern "C" {
+
+sla_status sla_gated_scan_work(const sla_scan_dims* dims, int64_t* kept_bytes_host,
+                               int64_t* work_bytes_host) {
+  SLA_NET_BEGIN
+  clear_error();
+  ScanSizes z;
+  SLA_TRY(scan_sizes("sla_gated_scan_work", dims, z));
+  if (kept_bytes_host) *kept_bytes_host = z.kept;
+  if (work_bytes_host) *work_bytes_host = z.work;
+  return SLA_OK;
+  SLA_NET_END
+}
+
+sla_status sla_gated_scan(const sla_scan_dims* dims, const void* x, int64_t ldx, const void* g,
+                          int64_t ldg, const int32_t* offsets, const float* initial_state,
+                          void* h, float* final_state, void* kept, int64_t kept_bytes, void* work,
+                          int64_t work_bytes, hipStream_t stream) {
+  SLA_NET_BEGIN
+  clear_error();
+  ScanSizes z;
+  SLA_TRY(scan_sizes("sla_gated_scan", dims, z));
+  if (dims->sequences == 0) return SLA_OK;
+  SLA_NET_REQUIRE(dims->tokens == 0 || (x && g && h), "sla_gated_scan: an argument is NULL");
+  SLA_NET_REQUIRE(!dims->packed || offsets, "sla_gated_scan: offsets is NULL");
+  SLA_NET_REQUIRE(ldx >= dims->channels && ldg >= dims->channels,
+                  "sla_gated_scan: a token stride is below channels");
+  SLA_NET_REQUIRE(!kept || kept_bytes >= z.kept,
+                  "sla_gated_scan: kept block too small (sla_gated_scan_work)");
+  SLA_NET_REQUIRE(z.work == 0 || (work && work_bytes >= z.work),
+                  "sla_gated_scan: workspace too small (sla_gated_scan_work)");
+  int32_t* tok = dims->packed ? (int32_t*)(kept ? kept : work) : nullptr;
+  float* states = kept ? (float*)((char*)kept + z.tok) : nullptr;
+  float* ends = (float*)((char*)work + z.tok);
+  if (tok) {
+    k_scan_plan<<<1, kWave, 0, stream>>>(offsets, dims->sequences, dims->tokens, tok);
+    LAUNCH_CHECK();
+  }
+  const ScanShape s = scan_shape(dims, z.plan, tok);
+  return with_scan(dims, z.plan, [&](auto te, auto ge, auto cl, auto waves, auto v) -> sla_status {
+    using T = decltype(te);
+    using G = decltype(ge);
+    const int grid = scan_grid(s);
+    if (s.segments > 1) {
+      k_scan_ends<T, G, cl.value, waves.value, v.value, false>
+          <<<grid, waves.value * kWave, 0, stream>>>(s, (const T*)x, ldx, (const G*)g, ldg, ends);
+      LAUNCH_CHECK();
+    }
+    k_scan<T, G, cl.value, waves.value, v.value><<<grid, waves.value * kWave, 0, stream>>>(
+        s, (const T*)x, ldx, (const G*)g, ldg, initial_state, (T*)h, final_state, states, ends);
+    LAUNCH_CHECK();
+    return SLA_OK;
+  });
+  SLA_NET_END
+}
+
+sla_status sla_gated_scan_grad(const sla_scan_dims* dims, const void* x, int64_t ldx,
+                               const void* g, int64_t ldg, const void* kept, int64_t kept_bytes,
+                               const void* dh, int64_t lddh, const float* grad_final_state,
+                               void* dx, void* dg, float* grad_initial_state, void* work,
+                               int64_t work_bytes, hipStream_t stream) {
+  SLA_NET_BEGIN
+  clear_error();
+  ScanSizes z;
+  SLA_TRY(scan_sizes("sla_gated_scan_grad", dims, z));
+  if (dims->sequences == 0) return SLA_OK;
+  SLA_NET_REQUIRE(dims->tokens == 0 || (x && g && dh), "sla_gated_scan_grad: an argument is NULL");
+  SLA_NET_REQUIRE(ldx >= dims->channels && ldg >= dims->channels && lddh >= dims->channels,
+                  "sla_gated_scan_grad: a token stride is below channels");
+  SLA_NET_REQUIRE(z.kept == 0 || (kept && kept_bytes >= z.kept),
+                  "sla_gated_scan_grad: kept block too small (sla_gated_scan_work)");
+  SLA_NET_REQUIRE(z.work == 0 || (work && work_bytes >= z.work),
+                  "sla_gated_scan_grad: workspace too small (sla_gated_scan_work)");
+  const int32_t* tok = dims->packed ? (const int32_t*)kept : nullptr;
+  const float* states = (const float*)((const char*)kept + z.tok);
+  float* ends = (float*)((char*)work + z.tok);
+  const ScanShape s = scan_shape(dims, z.plan, tok);
+  return with_scan(dims, z.plan, [&](auto te, auto ge, auto cl, auto waves, auto v) -> sla_status {
+    using T = decltype(te);
+    using G = decltype(ge);
+    const int grid = scan_grid(s);
+    if (s.segments > 1) {
+      k_scan_ends<T, G, cl.value, waves.value, v.value, true>
+          <<<grid, waves.value * kWave, 0, stream>>>(s, (const T*)dh, lddh, (const G*)g, ldg,
+                                                     ends);
+      LAUNCH_CHECK();
+    }
+    k_scan_grad<T, G, cl.value, waves.value, v.value><<<grid, waves.value * kWave, 0, stream>>>(
+        s, (const T*)x, ldx, (const G*)g, ldg, states, (const T*)dh, lddh, grad_final_state,
+        (T*)dx, (G*)dg, grad_initial_state, ends);
+    LAUNCH_CHECK();
+    return SLA_OK;
+  });
+  SLA_NET_END
+}
+
+sla_status sla_gated_scan_step(const sla_scan_dims* dims, const void* x, int64_t ldx,
+                               const void* g, int64_t ldg, float* state, void* h,
+                               hipStream_t stream) {
+  SLA_NET_BEGIN
+  clear_error();
+  ScanSizes z;
+  SLA_TRY(scan_sizes("sla_gated_scan_step", dims, z));
+  SLA_NET_REQUIRE(!dims->packed && dims->tokens == dims->sequences,
+                  "sla_gated_scan_step: one token of every sequence");
+  if (dims->sequences == 0) return SLA_OK;
+  SLA_NET_REQUIRE(x && g && state && h, "sla_gated_scan_step: an argument is NULL");
+  SLA_NET_REQUIRE(ldx >= dims->channels && ldg >= dims->channels,
+                  "sla_gated_scan_step: a token stride is below channels");
+  const bool wide = dims->gate_type == SLA_F32;
+  auto run = [&](auto te, auto ge) -> sla_status {
+    using T = decltype(te);
+    using G = decltype(ge);
+    constexpr int V = 4;
+    const int64_t groups = div_up(dims->sequences * div_up(dims->channels, V), 256);
+    k_scan_step<T, G, V><<<int(groups < kMostGroups ? groups : kMostGroups), 256, 0, stream>>>(
+        (const T*)x, ldx, (const G*)g, ldg, dims->sequences, dims->channels, state, (T*)h);
+    LAUNCH_CHECK();
+    return SLA_OK;
+  };
+  if (dims->type == SLA_F32) return run(float(), float());
+  if (dims->type == SLA_F16) return wide ? run(_Float16(), float()) : run(_Float16(), _Float16());
+  return wide ? run(__bf16(), float()) : run(__bf16(), __bf16());
+  SLA_NET_END
+}
+
+}  // extern "C"

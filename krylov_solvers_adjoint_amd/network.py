@@ -1,6 +1,7 @@
 """Network operators on the library's kernels: layer norm, the gated
-feed-forward unit, and the gated delta rule (whole sequences, and single
-tokens against a kept state).
+feed-forward unit, the projection with bias, activation and residual, the
+gated delta rule and the gated scan (whole sequences, and single tokens against
+a kept state), and the orthogonalised update of a weight.
 
 They are the parts of a network that predicts a system's coefficients and is
 trained through the solver's adjoint (``examples/coefficient_network.py``).
@@ -34,12 +35,18 @@ from . import _I64, _check, _lib
 F32, F16, BF16 = 0, 1, 2
 _TYPES = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
 ACTIVATIONS = {"silu": 0, "gelu": 1, "relu": 2}
+_NO_ACTIVATION = 3
 
 
 class _DeltaDims(ctypes.Structure):
     _fields_ = [("sequences", _I64), ("tokens", _I64), ("key_heads", _I64),
                 ("value_heads", _I64), ("key_dim", _I64), ("value_dim", _I64),
                 ("scale", ctypes.c_double), ("type", ctypes.c_int), ("packed", ctypes.c_int)]
+
+
+class _ScanDims(ctypes.Structure):
+    _fields_ = [("sequences", _I64), ("tokens", _I64), ("channels", _I64), ("type", ctypes.c_int),
+                ("gate_type", ctypes.c_int), ("packed", ctypes.c_int)]
 
 
 def _tensor(t, name: str, like: torch.Tensor | None = None, dtypes=None) -> torch.Tensor:
@@ -153,6 +160,26 @@ def _wants(*tensors) -> bool:
 
 def _block(nbytes: int, like: torch.Tensor) -> torch.Tensor:
     return torch.empty(max(nbytes, 1), dtype=torch.uint8, device=like.device)
+
+
+def _offsets(cu_seqlens, tokens: int, like: torch.Tensor):
+    """(offsets as the kernels read them, the number of sequences)"""
+    if not isinstance(cu_seqlens, torch.Tensor):
+        cu_seqlens = torch.as_tensor(cu_seqlens)   # its own type: no rounding
+    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
+        raise ValueError("cu_seqlens: expected [sequences + 1]")
+    if cu_seqlens.dtype not in (torch.int32, torch.int64):
+        raise TypeError(f"cu_seqlens: expected int32 or int64, got {cu_seqlens.dtype}")
+    if not cu_seqlens.is_cuda:
+        if bool((cu_seqlens.diff() < 0).any()) or int(cu_seqlens[0]) < 0 \
+                or int(cu_seqlens[-1]) > tokens:
+            raise ValueError(f"cu_seqlens: offsets must not fall and lie in 0..{tokens}")
+    elif cu_seqlens.device != like.device:
+        raise ValueError(f"cu_seqlens: is on {cu_seqlens.device}, the tokens on {like.device}")
+    sequences = cu_seqlens.numel() - 1
+    if cu_seqlens.dtype == torch.int64:  # clamped first: narrowing would wrap
+        cu_seqlens = cu_seqlens.clamp(0, tokens)
+    return cu_seqlens.to(device=like.device, dtype=torch.int32).contiguous(), sequences
 
 
 # ---------------------------------------------------------------------------
@@ -453,22 +480,7 @@ def gated_delta_rule(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch
     if cu_seqlens is not None:
         if batch != 1:
             raise ValueError("cu_seqlens needs a batch of 1")
-        if not isinstance(cu_seqlens, torch.Tensor):
-            cu_seqlens = torch.as_tensor(cu_seqlens)   # its own type: no rounding
-        if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
-            raise ValueError("cu_seqlens: expected [sequences + 1]")
-        if cu_seqlens.dtype not in (torch.int32, torch.int64):
-            raise TypeError(f"cu_seqlens: expected int32 or int64, got {cu_seqlens.dtype}")
-        if not cu_seqlens.is_cuda:
-            if bool((cu_seqlens.diff() < 0).any()) or int(cu_seqlens[0]) < 0 \
-                    or int(cu_seqlens[-1]) > tokens:
-                raise ValueError(f"cu_seqlens: offsets must not fall and lie in 0..{tokens}")
-        elif cu_seqlens.device != q.device:
-            raise ValueError(f"cu_seqlens: is on {cu_seqlens.device}, q on {q.device}")
-        sequences = cu_seqlens.numel() - 1
-        if cu_seqlens.dtype == torch.int64:  # clamped first: narrowing would wrap
-            cu_seqlens = cu_seqlens.clamp(0, tokens)
-        offsets = cu_seqlens.to(device=q.device, dtype=torch.int32).contiguous()
+        offsets, sequences = _offsets(cu_seqlens, tokens, q)
     if initial_state is not None:
         _tensor(initial_state, "initial_state", q, (torch.float32,))
         _sized(initial_state, (sequences, v.shape[2], q.shape[3], v.shape[3]), "initial_state")
@@ -513,3 +525,309 @@ def gated_delta_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch
         raise ValueError("gated_delta_step has no gradient (and no tangent): use "
                          "gated_delta_rule, or no_grad and plain inputs")
     return sla_delta_step(q, k, v, g.contiguous(), beta.contiguous(), state, scale)
+
+
+# ---------------------------------------------------------------------------
+# The projection with its epilogue
+# ---------------------------------------------------------------------------
+@functools.lru_cache(maxsize=1024)
+def _linear_bytes(*args):
+    """Workspace bytes of (sla_linear, sla_linear_grad)"""
+    forward, grad = _I64(), _I64()
+    _check(_lib.sla_linear_work(*args, ctypes.byref(forward), ctypes.byref(grad)))
+    return forward.value, grad.value
+
+
+@_takes_stream
+def sla_linear(x, weight, bias, residual, act: int):
+    """y [..., outer] = residual + f(x weight^T + bias); bias and residual may be None."""
+    outer, inner = weight.shape
+    rows = x.numel() // inner
+    kind = _TYPES[x.dtype]
+    x, ldx = _rows(x, 1)
+    ldr = outer
+    if residual is not None:
+        residual, ldr = _rows(residual, 1)
+    size = _linear_bytes(rows, inner, outer, kind, act)[0]
+    work = _block(size, x) if size else None
+    y = torch.empty((*x.shape[:-1], outer), dtype=x.dtype, device=x.device)
+    _check(_lib.sla_linear(x.data_ptr(), ldx, weight.data_ptr(), _ptr(bias),
+                           kind if bias is None else _TYPES[bias.dtype], _ptr(residual), ldr,
+                           rows, inner, outer, kind, act, y.data_ptr(), _ptr(work), size,
+                           _stream(x)))
+    return y
+
+
+@_takes_stream
+def sla_linear_grad(dy, x, weight, bias, act: int, want_x=True, want_weight=True, want_bias=True,
+                    btype=None):
+    """(dx, dweight, dbias), None where not wanted; bias is read with an activation only."""
+    outer, inner = weight.shape
+    rows = x.numel() // inner
+    kind = _TYPES[x.dtype]
+    x, ldx = _rows(x, 1)
+    dy, lddy = _rows(dy, 1)
+    btype = btype or (x.dtype if bias is None else bias.dtype)
+    dx = torch.empty(x.shape, dtype=x.dtype, device=x.device) if want_x else None
+    dw = torch.empty_like(weight) if want_weight else None
+    db = torch.empty(outer, dtype=btype, device=x.device) if want_bias else None
+    size = _linear_bytes(rows, inner, outer, kind, act)[1]
+    work = _block(size, x)
+    _check(_lib.sla_linear_grad(dy.data_ptr(), lddy, x.data_ptr(), ldx, weight.data_ptr(),
+                                _ptr(bias), _TYPES[btype], rows, inner, outer, kind, act,
+                                _ptr(dx), _ptr(dw), _ptr(db), work.data_ptr(), size, _stream(x)))
+    return dx, dw, db
+
+
+class _Linear(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, residual, act):
+        ctx.act = act
+        ctx.btype = None if bias is None else bias.dtype
+        ctx.save_for_backward(x, weight, bias if act != _NO_ACTIVATION else None)
+        return sla_linear(x, weight, bias, residual, act)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        x, weight, bias = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        grads = (None, None, None)
+        if need[0] or need[1] or need[2]:
+            grads = sla_linear_grad(dy, x, weight, bias, ctx.act, *need[:3], ctx.btype)
+        return (*grads, dy if need[3] else None, None)
+
+
+def linear(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = None,
+           activation: str | None = None, residual: torch.Tensor | None = None) -> torch.Tensor:
+    """A projection with its epilogue: residual + f(x weight^T + bias).
+
+    x [..., inner] and weight [outer, inner] of one type; bias [outer] of x's
+    type or float32, residual [..., outer] of x's type, either may be None;
+    activation f: None, "silu", "gelu" (with erf) or "relu".  One autograd node
+    that keeps only its inputs; with an activation backward computes the
+    projection again and rounds its gradient to x's type (fp16: times a power
+    of two that keeps it in range) before the products that follow.  The
+    residual's gradient is the output's."""
+    _tensor(x, "x")
+    if activation is not None and activation not in ACTIVATIONS:
+        raise ValueError(f"unknown activation {activation!r}")
+    _tensor(weight, "weight", x, (x.dtype,))
+    if weight.dim() != 2 or weight.shape[0] < 1 or weight.shape[1] < 1:
+        raise ValueError("weight: expected [outer, inner]")
+    if x.dim() < 1 or x.shape[-1] != weight.shape[1]:
+        raise ValueError(f"x: expected [..., {weight.shape[1]}], got {tuple(x.shape)}")
+    if bias is not None:
+        _tensor(bias, "bias", x, (x.dtype, torch.float32))
+        _sized(bias, weight.shape[:1], "bias")
+        bias = bias.contiguous()
+    if residual is not None:
+        _tensor(residual, "residual", x, (x.dtype,))
+        _sized(residual, (*x.shape[:-1], weight.shape[0]), "residual")
+    act = _NO_ACTIVATION if activation is None else ACTIVATIONS[activation]
+    weight = weight.contiguous()
+    if _wants(x, weight, bias, residual):
+        return _Linear.apply(x, weight, bias, residual, act)
+    return sla_linear(x, weight, bias, residual, act)
+
+
+# ---------------------------------------------------------------------------
+# The gated scan
+# ---------------------------------------------------------------------------
+@functools.lru_cache(maxsize=1024)
+def _scan_plan(*args):
+    """(the C structure, its address, the bytes that sla_gated_scan_work says)"""
+    d = _ScanDims(*args)
+    kept, work = _I64(), _I64()
+    _check(_lib.sla_gated_scan_work(ctypes.byref(d), ctypes.byref(kept), ctypes.byref(work)))
+    return d, ctypes.byref(d), kept.value, work.value
+
+
+def _scan_dims(x, g, sequences, packed):
+    channels = x.shape[-1]
+    return _scan_plan(sequences, x.numel() // channels, channels, _TYPES[x.dtype],
+                      _TYPES[g.dtype], int(packed))
+
+
+@_takes_stream
+def sla_gated_scan(x, g, offsets, initial_state, sequences: int, want_state: bool = True,
+                   want_kept: bool = False):
+    """(h, final_state or None, kept or None): kept is what the gradient reads."""
+    dims, at, ksize, wsize = _scan_dims(x, g, sequences, offsets is not None)
+    (x, ldx), (g, ldg) = _rows(x, 1), _rows(g, 1)
+    kept = _block(ksize, x) if want_kept else None
+    work = _block(wsize, x) if wsize else None
+    h = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    state = torch.empty(sequences, dims.channels, dtype=torch.float32, device=x.device) \
+        if want_state else None
+    _check(_lib.sla_gated_scan(at, x.data_ptr(), ldx, g.data_ptr(), ldg, _ptr(offsets),
+                               _ptr(initial_state), h.data_ptr(), _ptr(state), _ptr(kept), ksize,
+                               _ptr(work), wsize, _stream(x)))
+    return h, state, kept
+
+
+@_takes_stream
+def sla_gated_scan_grad(x, g, kept, grad_h, grad_state, sequences: int, packed: bool,
+                        want_x=True, want_g=True, want_initial=True):
+    """(dx, dg, grad of the initial state), None where not wanted."""
+    dims, at, ksize, wsize = _scan_dims(x, g, sequences, packed)
+    (x, ldx), (g, ldg), (grad_h, ldh) = _rows(x, 1), _rows(g, 1), _rows(grad_h, 1)
+    work = _block(wsize, x) if wsize else None
+    dx = torch.empty(x.shape, dtype=x.dtype, device=x.device) if want_x else None
+    dg = torch.empty(g.shape, dtype=g.dtype, device=g.device) if want_g else None
+    ds0 = torch.empty(sequences, dims.channels, dtype=torch.float32, device=x.device) \
+        if want_initial else None
+    _check(_lib.sla_gated_scan_grad(at, x.data_ptr(), ldx, g.data_ptr(), ldg, kept.data_ptr(),
+                                    kept.numel(), grad_h.data_ptr(), ldh, _ptr(grad_state),
+                                    _ptr(dx), _ptr(dg), _ptr(ds0), _ptr(work), wsize, _stream(x)))
+    return dx, dg, ds0
+
+
+class _GatedScan(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, g, initial_state, offsets, sequences, want_state):
+        h, state, kept = sla_gated_scan(x, g, offsets, initial_state, sequences, want_state, True)
+        ctx.sequences, ctx.packed = sequences, offsets is not None
+        ctx.save_for_backward(x, g, kept)
+        ctx.set_materialize_grads(False)
+        return h, state
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, grad_h, grad_state):
+        x, g, kept = ctx.saved_tensors
+        if grad_h is None:
+            grad_h = torch.zeros(x.shape, dtype=x.dtype, device=x.device)
+        if grad_state is not None:
+            grad_state = grad_state.contiguous()
+        grads = sla_gated_scan_grad(x, g, kept, grad_h, grad_state, ctx.sequences, ctx.packed,
+                                    *ctx.needs_input_grad[:3])
+        return (*grads, None, None, None)
+
+
+def _check_scan(x, g, lead: int):
+    _tensor(x, "x")
+    if x.dim() != lead + 1 or x.shape[-1] < 1:
+        raise ValueError(f"x: expected {lead + 1} axes, the last of 1 channel or more")
+    _tensor(g, "g", x, (x.dtype, torch.float32))
+    _sized(g, x.shape, "g")
+
+
+def gated_scan(x: torch.Tensor, g: torch.Tensor, initial_state: torch.Tensor | None = None,
+               output_final_state: bool = False, cu_seqlens=None):
+    """A gated linear recurrence over whole sequences: (h, final state or None).
+
+    Per channel h_t = exp(g_t) h_{t-1} + x_t, with the state in float32; h is
+    rounded to x's type on its way out.
+
+    x and h [batch, tokens, channels]; g (log decay, <= 0; -inf or a type's
+    lowest value begins the state anew) of the same shape and of x's type or
+    float32.  States are float32 [sequences, channels]; without an initial state
+    they begin at zero.  cu_seqlens as in gated_delta_rule: the batch is 1 and
+    sequence i is the tokens cu_seqlens[i] .. cu_seqlens[i+1] - 1; tokens of no
+    sequence get zeros.
+
+    One autograd node, with gradients for x, g and the initial state; it keeps
+    its inputs and the state before every block of 8 to 256 tokens."""
+    _check_scan(x, g, 2)
+    batch, tokens = x.shape[0], x.shape[1]
+    offsets, sequences = None, batch
+    if cu_seqlens is not None:
+        if batch != 1:
+            raise ValueError("cu_seqlens needs a batch of 1")
+        offsets, sequences = _offsets(cu_seqlens, tokens, x)
+    if initial_state is not None:
+        _tensor(initial_state, "initial_state", x, (torch.float32,))
+        _sized(initial_state, (sequences, x.shape[2]), "initial_state")
+        initial_state = initial_state.contiguous()
+    if _wants(x, g, initial_state):
+        return _GatedScan.apply(x, g, initial_state, offsets, sequences, bool(output_final_state))
+    return sla_gated_scan(x, g, offsets, initial_state, sequences, bool(output_final_state))[:2]
+
+
+@_takes_stream
+def sla_gated_scan_step(x, g, state):
+    """h [sequences, channels]; state is updated in place."""
+    at = _scan_dims(x, g, x.shape[0], False)[1]
+    (x, ldx), (g, ldg) = _rows(x, 1), _rows(g, 1)
+    h = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    _check(_lib.sla_gated_scan_step(at, x.data_ptr(), ldx, g.data_ptr(), ldg, state.data_ptr(),
+                                    h.data_ptr(), _stream(x)))
+    torch.autograd.graph.increment_version(state)  # a graph that saved it has to notice
+    return h
+
+
+def gated_scan_step(x: torch.Tensor, g: torch.Tensor, state: torch.Tensor) -> torch.Tensor:
+    """One token of every sequence: h, with ``state`` updated in place.
+
+    x [sequences, channels], g of the same shape and of x's type or float32,
+    state float32 [sequences, channels], contiguous, as gated_scan returns it.
+    For serving: it has no derivative, and refuses inputs that ask for a
+    gradient or carry a tangent."""
+    _check_scan(x, g, 1)
+    _tensor(state, "state", x, (torch.float32,))
+    _sized(state, x.shape, "state")
+    if not state.is_contiguous():
+        raise ValueError("state: expected a contiguous tensor (it is updated in place)")
+    if _wants(x, g, state):
+        raise ValueError("gated_scan_step has no gradient (and no tangent): use gated_scan, or "
+                         "no_grad and plain inputs")
+    return sla_gated_scan_step(x, g, state)
+
+
+# ---------------------------------------------------------------------------
+# Orthogonalised updates
+# ---------------------------------------------------------------------------
+@functools.lru_cache(maxsize=64)
+def _coefficients(steps: int, coefficients: tuple):
+    """The C array of a triple a step."""
+    flat = [float(v) for t in coefficients for v in t]
+    return (ctypes.c_double * max(len(flat), 1))(*flat)
+
+
+@_takes_stream
+def sla_orthogonalise(m, steps: int, coefficients: tuple, eps: float):
+    """x of m's shape [..., rows, cols]; coefficients: a triple for each step."""
+    rows, cols = m.shape[-2:]
+    count = m.numel() // (rows * cols)
+    m, ld = _rows(m, 1)
+    x = torch.empty(m.shape, dtype=m.dtype, device=m.device)
+    size = _work_bytes("sla_orthogonalise_work", count, rows, cols, _TYPES[m.dtype])
+    work = _block(size, m)
+    _check(_lib.sla_orthogonalise(m.data_ptr(), ld, count, rows, cols, _TYPES[m.dtype], steps,
+                                  _coefficients(steps, coefficients), eps, x.data_ptr(),
+                                  work.data_ptr(), size, _stream(m)))
+    return x
+
+
+def orthogonalise(m: torch.Tensor, steps: int = 5, coefficients=(3.4445, -4.775, 2.0315),
+                  eps: float = 1e-7) -> torch.Tensor:
+    """Newton-Schulz steps towards the nearest matrix with orthonormal rows (or columns).
+
+    m [..., rows, cols], each matrix by itself: X = m / (|m|_F + eps), then
+    `steps` times X <- a X + (b A + c A A) X with A = X X^T, which takes the
+    singular values s to a s + b s^3 + c s^5 and keeps the singular vectors.
+    coefficients: one triple (a, b, c) for all steps, or one for each.  The
+    default brings singular values from 1e-2 on to between 0.7 and 1.2 in five
+    steps, for a weight's update.  The result has m's type; the products hold
+    22 bits of their factors and sum in float32, and take singular values up to
+    4 on the way.  It has no derivative, and refuses inputs that ask for a
+    gradient or carry a tangent."""
+    _tensor(m, "m")
+    if m.dim() < 2:
+        raise ValueError("m: expected [..., rows, cols]")
+    if isinstance(steps, bool) or not isinstance(steps, int) or not 0 <= steps <= 64:
+        raise ValueError("steps: expected a whole number from 0 to 64")
+    triples = tuple(tuple(t) if isinstance(t, (tuple, list)) else t for t in coefficients)
+    if len(triples) == 3 and not any(isinstance(t, tuple) for t in triples):
+        triples = (triples,) * steps
+    if len(triples) != steps or any(not isinstance(t, tuple) or len(t) != 3 for t in triples):
+        raise ValueError("coefficients: expected one triple, or one for each step")
+    if not eps >= 0:
+        raise ValueError("eps must not be negative")
+    if _wants(m):
+        raise ValueError("orthogonalise has no gradient (and no tangent): use no_grad and plain "
+                         "inputs")
+    if m.numel() == 0:
+        return torch.empty(m.shape, dtype=m.dtype, device=m.device)
+    return sla_orthogonalise(m, steps, triples, float(eps))

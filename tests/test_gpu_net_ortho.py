@@ -1,0 +1,187 @@
+"""The orthogonalised update on the GPU against its 64-bit form.
+
+Bound, in the Frobenius norm (`bound`): a step's products carry 2^-21 of their
+absolute terms (factors of 22 bits, lo lo left out) and (3 K + 4) U32 for their
+sums; what X carries into a step leaves it times the step's largest slope (and
+p(s) / s, the other eigenvalues of its derivative) over the singular values that
+there are.  Beside that worst case the roundings are independent, so five steps
+of the default coefficients leave at most 4/3 4^4 2^-22 of the norm of the
+result: 2^-13.6, the second test's tolerance."""
+import pytest
+import torch
+
+import net_refs as R
+
+pytestmark = pytest.mark.gpu
+
+TRIPLE = (3.4445, -4.775, 2.0315)
+CASES = [(1, 1), (1, 9), (9, 1), (2, 3), (16, 16), (31, 33), (33, 31), (64, 128), (128, 64),
+         (65, 190), (200, 70), (130, 130), (257, 40), (300, 515)]
+
+
+def matrices(count, rows, cols, dtype, seed=0):
+    g = R.gen(seed + rows * 3 + cols)
+    r = max(1, min(rows, cols) // 4)
+    m = torch.randn(count, rows, r, generator=g) @ torch.randn(count, r, cols, generator=g)
+    return (0.01 * (m / r ** 0.5 + 0.2 * torch.randn(count, rows, cols, generator=g))).to(dtype)
+
+
+def reference(m, triples, eps=1e-7):
+    """(X, bound) of one matrix in 64 bits."""
+    x = m.double()
+    x = x / (x.norm() + eps)
+    if x.shape[0] > x.shape[1]:
+        y, e = reference(m.t(), triples, eps)
+        return y.t(), e
+    err = 2.0 ** -23 * x.norm()
+    for a, b, c in triples:
+        rows, cols = x.shape
+        A = x @ x.t()
+        B = b * A + c * (A @ A)
+        s = torch.linalg.svdvals(x)
+        s = torch.linspace(0, 1.01 * float(s.max()) + 1e-3, 500, dtype=torch.float64)
+        slope = max(float((a + 3 * b * s ** 2 + 5 * c * s ** 4).abs().max()),
+                    float((a + b * s ** 2 + c * s ** 4).abs().max()))
+        nx, na = torch.linalg.matrix_norm(x, 2), torch.linalg.matrix_norm(A, 2)
+
+        def product(p, q):
+            k = p.shape[1]
+            return (2.0 ** -21 + (3 * k + 4) * R.U32) * (p.abs() @ q.abs()).norm()
+        ea = product(x, x.t()) + 2.0 ** -22 * A.norm()
+        eb = abs(b) * ea + abs(c) * (2 * na * ea + product(A, A)) + 2.0 ** -22 * (
+            abs(b) * A.norm() + B.norm())
+        err = slope * err + nx * eb + product(B, x) + 2.0 ** -22 * (abs(a) * x.norm())
+        x = a * x + B @ x
+        err = err + 2.0 ** -22 * x.norm()
+    return x, float(err)
+
+
+def check(m, got, triples, eps=1e-7, scale=1.01):
+    for i in range(m.shape[0]):
+        want, err = reference(m[i], triples, eps)
+        d = (got[i].double().cpu() - want).norm()
+        u = R.half_step(m.dtype)
+        tiny = 2.0 ** -25 * want.numel() ** 0.5 if m.dtype == torch.float16 else 0
+        assert d <= scale * err + u * want.norm() + tiny, (i, float(d), err, float(want.norm()))
+
+
+@pytest.mark.parametrize("rows, cols", CASES)
+@pytest.mark.parametrize("kind", ["fp32", "fp16", "bf16"])
+def test_orthogonalise(rows, cols, kind):
+    import krylov_solvers_adjoint_amd as K
+    dtype = R.TYPES[kind]
+    for count in (1, 3):
+        m = matrices(count, rows, cols, dtype)
+        got = K.orthogonalise(m.cuda())
+        assert got.dtype == dtype and got.shape == m.shape
+        check(m, got, [TRIPLE] * 5)
+        assert torch.equal(K.orthogonalise(m.cuda()), got)
+
+
+@pytest.mark.parametrize("rows, cols", [(64, 128), (200, 70), (300, 515), (512, 512)])
+def test_precision_of_five_steps(rows, cols):
+    import krylov_solvers_adjoint_amd as K
+    m = matrices(2, rows, cols, torch.float32)
+    got = K.orthogonalise(m.cuda())
+    for i in range(2):
+        assert R.rel(got[i], reference(m[i], [TRIPLE] * 5)[0]) < 2.0 ** -13.6
+
+
+def test_singular_values_come_near_one_and_the_vectors_stay():
+    import krylov_solvers_adjoint_amd as K
+    g = R.gen(2)
+    u, _ = torch.linalg.qr(torch.randn(90, 60, generator=g, dtype=torch.float64))
+    v, _ = torch.linalg.qr(torch.randn(60, 60, generator=g, dtype=torch.float64))
+    s = torch.logspace(-1.5, 0, 60, dtype=torch.float64)
+    got = K.orthogonalise((u * s @ v.t()).float().cuda(), steps=8).double().cpu()
+    mid = u.t() @ got @ v
+    values = mid.diagonal()
+    assert values.min() > 0.6 and values.max() < 1.3
+    assert (mid - torch.diag(values)).norm() < 1e-3
+    # the cubic steps converge to one
+    got = K.orthogonalise((u * s @ v.t()).float().cuda(), 20, (1.5, -0.5, 0.0)).double().cpu()
+    # 20 steps of 22 bits, each multiplied by at most 1.5 on the way and contracted at the end
+    assert (got.t() @ got - torch.eye(60, dtype=torch.float64)).norm() < 60 * 2.0 ** -18
+
+
+def test_steps_coefficients_and_eps():
+    import krylov_solvers_adjoint_amd as K
+    m = matrices(2, 40, 70, torch.float32)
+    triples = [(3.0, -3.5, 1.4), (2.0, -1.5, 0.5), (1.875, -1.25, 0.375)]
+    check(m, K.orthogonalise(m.cuda(), 3, triples), triples)
+    check(m, K.orthogonalise(m.cuda(), 1, TRIPLE), [TRIPLE])
+    check(m, K.orthogonalise(m.cuda(), 0), [])
+    check(m, K.orthogonalise(m.cuda(), eps=0.5), [TRIPLE] * 5, 0.5)
+    for kind in ("fp32", "fp16", "bf16"):
+        dtype = R.TYPES[kind]
+        assert not K.orthogonalise(torch.zeros(2, 30, 20, dtype=dtype).cuda()).any()
+        # far from one: the norm is a sum in 64 bits
+        for scale in (1e-30, 1e30) if kind != "fp16" else (1e-4, 1e4):
+            far = (matrices(1, 30, 50, torch.float32) * 20 * scale).to(dtype)
+            check(far, K.orthogonalise(far.cuda(), eps=0.0), [TRIPLE] * 5, 0.0)
+    assert K.orthogonalise(torch.zeros(0, 3, 4).cuda()).shape == (0, 3, 4)
+    assert K.orthogonalise(torch.zeros(3, 0).cuda()).shape == (3, 0)
+
+
+def test_a_matrix_that_is_not_finite_leaves_the_others():
+    import krylov_solvers_adjoint_amd as K
+    m = matrices(3, 40, 50, torch.float32).cuda()
+    want = K.orthogonalise(m)
+    for bad in (float("nan"), float("inf")):
+        m2 = m.clone()
+        m2[1, 3, 4] = bad
+        got = K.orthogonalise(m2)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[2], want[2])
+        assert got[1].isnan().all()
+
+
+def test_views():
+    import krylov_solvers_adjoint_amd as K
+    base = matrices(4, 60, 90, torch.bfloat16).cuda()
+    for v in (base[:, :, 7:51], base[1, 3:40, 1:], base.transpose(1, 2), base[::2, 5:],
+              base.unflatten(0, (2, 2)), base[0].expand(3, 60, 90)):
+        got = K.orthogonalise(v)
+        assert got.shape == v.shape and torch.equal(got, K.orthogonalise(v.contiguous()))
+
+
+def test_refusals():
+    import krylov_solvers_adjoint_amd as K
+    m = matrices(1, 8, 9, torch.float32).cuda()
+    for call in (lambda: K.orthogonalise(m[0, 0]), lambda: K.orthogonalise(m, -1),
+                 lambda: K.orthogonalise(m, 65), lambda: K.orthogonalise(m, 2.0),
+                 lambda: K.orthogonalise(m, 2, (1.0, 2.0)),
+                 lambda: K.orthogonalise(m, 2, [TRIPLE] * 3), lambda: K.orthogonalise(m, eps=-1),
+                 lambda: K.orthogonalise(m.clone().requires_grad_()),
+                 lambda: K.orthogonalise(m.cpu())):
+        with pytest.raises(ValueError):
+            call()
+    with pytest.raises(TypeError):
+        K.orthogonalise(m.double())
+    with pytest.raises(K.SlaError):
+        K.orthogonalise(m, 5, (1.0, float("nan"), 0.0))
+    with torch.no_grad():
+        K.orthogonalise(m.clone().requires_grad_())
+
+
+def test_graph_replays_and_two_streams():
+    import krylov_solvers_adjoint_amd as K
+    m = matrices(2, 150, 260, torch.bfloat16).cuda()
+    other = matrices(2, 260, 150, torch.bfloat16).cuda()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(2):
+            K.orthogonalise(m)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = K.orthogonalise(m)
+    want = K.orthogonalise(other)
+    for k in range(3):
+        m.copy_(matrices(2, 150, 260, torch.bfloat16, seed=k + 1))
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            beside = K.orthogonalise(other)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, K.orthogonalise(m)) and torch.equal(beside, want)

@@ -1,0 +1,326 @@
+"""The gated scan on the GPU against its 64-bit form.
+
+Bounds, element by element.  With S_t = a_t S_{t-1} + |x_t| the sum of the
+absolute terms of h_t, and D_t = a_t (D_{t-1} + S_{t-1}) the same terms, each
+times the tokens that it has come through: a term carries 8 U32 for every such
+token (4 for its decay's exp, one for the product, up to three where the maps of
+spans are joined), and 16 at its own (the joins over waves, blocks and
+segments).  The backward recurrence is bounded the same way; dg is a product,
+whose factors' bounds add.  Outputs add half a step of their type."""
+import pytest
+import torch
+
+import net_refs as R
+
+pytestmark = pytest.mark.gpu
+
+# batch, tokens, channels: one token to many blocks and segments, odd widths
+CASES = [
+    (1, 1, 1), (2, 1, 5), (3, 7, 16), (1, 8, 33), (2, 9, 64), (1, 31, 130), (1, 64, 31),
+    (2, 65, 128), (1, 129, 100), (1, 300, 17), (5, 33, 48), (1, 1000, 3), (1, 2048, 32),
+    (1, 4097, 20), (3, 513, 66), (40, 5, 24), (2, 0, 8), (0, 4, 8), (70, 70, 512),
+]
+KINDS = [("fp32", "fp32"), ("fp16", "fp16"), ("bf16", "bf16"), ("bf16", "fp32"), ("fp16", "fp32")]
+
+
+def inputs(batch, tokens, channels, dtype, gtype, sequences=None, seed=0):
+    g = R.gen(seed + 31 * tokens + channels)
+    n = batch if sequences is None else sequences
+    x = torch.randn(batch, tokens, channels, generator=g)
+    rate = torch.exp(1.0 - 7.0 * torch.rand(channels, generator=g))
+    gate = -rate * torch.rand(batch, tokens, channels, generator=g) * 2
+    s0 = torch.randn(n, channels, generator=g)
+    dh = torch.randn(batch, tokens, channels, generator=g)
+    ds = torch.randn(n, channels, generator=g)
+    return x.to(dtype), gate.to(gtype), s0, dh.to(dtype), ds
+
+
+def one(x, g, s0, dh, ds):
+    """One sequence [T, C] in 64 bits: {name: (value, bound without the type's half step)}"""
+    T, a, eps = x.shape[0], g.exp(), R.U32
+    h, S, D = s0, s0.abs(), torch.zeros_like(s0)
+    hs, Ss, Ds = [h], [S], [D]
+    for t in range(T):
+        D = a[t] * (D + S)
+        S = a[t] * S + x[t].abs()
+        h = a[t] * h + x[t]
+        hs.append(h), Ss.append(S), Ds.append(D)
+    eh = [eps * (8 * d + 16 * s) for d, s in zip(Ds, Ss)]
+    m, M, N = ds, ds.abs(), torch.zeros_like(ds)
+    dx, edx, dg, edg = [None] * T, [None] * T, [None] * T, [None] * T
+    for t in reversed(range(T)):
+        lam, L = dh[t] + m, dh[t].abs() + M
+        dx[t], edx[t] = lam, eps * (8 * N + 16 * L)
+        N = a[t] * (N + L)
+        m, M = a[t] * lam, a[t] * L
+        dg[t] = m * hs[t]
+        edg[t] = eps * (8 * N + 16 * M) * Ss[t] + M * eh[t] + 2 * eps * M * Ss[t]
+
+    def stack(parts):
+        return torch.stack(parts) if parts else x.new_zeros(x.shape)
+    return {"h": (stack(hs[1:]), stack(eh[1:])), "state": (hs[-1], eh[-1]),
+            "dx": (stack(dx), stack(edx)), "dg": (stack(dg), stack(edg)),
+            "ds0": (m, eps * (8 * N + 16 * M))}
+
+
+def wanted(x, g, s0, dh, ds, edges=None):
+    x, g, s0, dh, ds = (t.double() for t in (x, g, s0, dh, ds))
+    if edges is None:
+        parts = [one(x[i], g[i], s0[i], dh[i], ds[i]) for i in range(x.shape[0])]
+        return {n: [torch.stack([p[n][k] for p in parts]) for k in (0, 1)] for n in parts[0]} \
+            if parts else {}
+    parts = [one(x[0, a:b], g[0, a:b], s0[i], dh[0, a:b], ds[i])
+             for i, (a, b) in enumerate(zip(edges, edges[1:]))]
+    out = {n: [torch.stack([p[n][k] for p in parts]) for k in (0, 1)] for n in ("state", "ds0")}
+    gap = [x.new_zeros(edges[0], x.shape[2]), x.new_zeros(x.shape[1] - edges[-1], x.shape[2])]
+    for n in ("h", "dx", "dg"):
+        out[n] = [torch.cat([gap[0], *[p[n][k] for p in parts], gap[1]])[None] for k in (0, 1)]
+    return out
+
+
+def close(got, want, what):
+    value, tol = want
+    u = R.half_step(got.dtype)
+    tiny = 2.0 ** -25 if got.dtype == torch.float16 else 2.0 ** -120
+    d = (got.detach().double().cpu() - value).abs()
+    bad = ~(d <= (tol * (1 + u) + u * value.abs()) * (1 + 2 ** -6) + tiny)
+    assert not bad.any(), (what, d[bad].max().item(), tol[bad].max().item(), int(bad.sum()))
+
+
+def run(x, g, s0, dh, ds, cu=None):
+    import krylov_solvers_adjoint_amd as K
+    leaves = [t.cuda().requires_grad_() for t in (x, g, s0)]
+    h, state = K.gated_scan(*leaves[:2], leaves[2], True, cu)
+    grads = torch.autograd.grad((h, state), leaves, (dh.cuda(), ds.cuda()))
+    with torch.no_grad():
+        again = K.gated_scan(*leaves[:2], leaves[2], True, cu)
+    assert torch.equal(again[0], h.detach()) and torch.equal(again[1], state.detach())
+    return {"h": h, "state": state, "dx": grads[0], "dg": grads[1], "ds0": grads[2]}
+
+
+@pytest.mark.parametrize("batch, tokens, channels", CASES)
+@pytest.mark.parametrize("kind, gkind", KINDS)
+def test_scan_and_gradients(batch, tokens, channels, kind, gkind):
+    args = inputs(batch, tokens, channels, R.TYPES[kind], R.TYPES[gkind])
+    got = run(*args)
+    assert got["h"].dtype == got["dx"].dtype == args[0].dtype and got["dg"].dtype == args[1].dtype
+    assert got["state"].dtype == got["ds0"].dtype == torch.float32
+    want = wanted(*args)
+    for n in want:
+        close(got[n], want[n], n)
+    if tokens == 0:
+        assert torch.equal(got["state"].cpu(), args[2]) and torch.equal(got["ds0"].cpu(), args[4])
+
+
+PACKED = [  # offsets, tokens
+    ([0, 5], 5), ([0, 0, 1, 1, 9], 9), ([0, 63, 64, 65, 200], 200), ([3, 10, 10, 40], 50),
+    ([0, 700, 701, 1500], 1500), ([0, 1, 2, 3, 4, 5, 6, 7, 8], 8), ([7, 7], 20),
+    ([0, 3000, 3100], 3100), (list(range(0, 1001, 10)), 1000),
+]
+
+
+@pytest.mark.parametrize("edges, tokens", PACKED)
+@pytest.mark.parametrize("kind, gkind, channels", [("fp32", "fp32", 20), ("bf16", "bf16", 66),
+                                                   ("fp16", "fp32", 7)])
+def test_packed_sequences(edges, tokens, kind, gkind, channels):
+    args = inputs(1, tokens, channels, R.TYPES[kind], R.TYPES[gkind], len(edges) - 1)
+    want = wanted(*args, edges=edges)
+    outs = []
+    for cu in (edges, torch.tensor(edges, dtype=torch.int32).cuda(),
+               torch.tensor(edges, dtype=torch.int64).cuda()):
+        got = run(*args, cu=cu)
+        for n in want:
+            close(got[n], want[n], n)
+        outs.append(got)
+    for n in want:
+        assert torch.equal(outs[0][n], outs[1][n]) and torch.equal(outs[0][n], outs[2][n])
+    for n in ("h", "dx", "dg"):
+        assert not outs[0][n][0, :edges[0]].any() and not outs[0][n][0, edges[-1]:].any()
+
+
+def test_offsets_on_the_device_are_raised_and_clamped():
+    import krylov_solvers_adjoint_amd as K
+    x, g, s0, dh, ds = inputs(1, 100, 12, torch.float32, torch.float32, 4)
+    bad = torch.tensor([-5, 40, 20, 90, 1000], dtype=torch.int32)
+    good = [0, 40, 40, 90, 100]
+    got, want = run(x, g, s0, dh, ds, bad.cuda()), run(x, g, s0, dh, ds, good)
+    for n in want:
+        assert torch.equal(got[n], want[n]), n
+    for cu in ([0, 5, 3, 100], [0, 101], [-1, 100]):
+        with pytest.raises(ValueError):
+            K.gated_scan(x.cuda(), g.cuda(), cu_seqlens=cu)
+
+
+def test_gates_that_reset():
+    """-inf and a type's lowest value begin the state anew; a gate of zero keeps it."""
+    for kind, gkind in KINDS:
+        dtype, gtype = R.TYPES[kind], R.TYPES[gkind]
+        x, g, s0, dh, ds = inputs(2, 90, 20, dtype, gtype)
+        g[:, 10], g[0, 40, 3], g[1, 70:75] = -float("inf"), -float("inf"), torch.finfo(gtype).min
+        g[:, 20:30] = 0
+        got = run(x, g, s0, dh, ds)
+        want = wanted(x, g.double().clamp(min=-2000), s0, dh, ds)
+        for n in want:
+            assert got[n].isfinite().all()
+            close(got[n], want[n], n)
+        assert not got["dg"][:, 10].any()
+
+
+def test_what_is_not_finite_stays_in_its_channel():
+    import krylov_solvers_adjoint_amd as K
+    x, g, s0, dh, ds = (t.cuda() for t in inputs(2, 400, 40, torch.float32, torch.float32))
+    for where, value in ((x, float("nan")), (x, float("inf")), (g, float("nan"))):
+        clean = K.gated_scan(x, g, s0, True)
+        keep = where[0, 150, 7].clone()
+        where[0, 150, 7] = value
+        h, state = K.gated_scan(x, g, s0, True)
+        where[0, 150, 7] = keep
+        assert torch.equal(h[1], clean[0][1]) and torch.equal(h[0, :150], clean[0][0, :150])
+        other = [c for c in range(40) if c != 7]
+        assert torch.equal(h[0][:, other], clean[0][0][:, other])
+        assert not h[0, 150, 7].isfinite()
+
+
+def test_optional_states_and_gradients():
+    import krylov_solvers_adjoint_amd as K
+    x, g, s0, dh, ds = (t.cuda() for t in inputs(2, 77, 24, torch.float32, torch.float32))
+    zero = torch.zeros_like(s0)
+    h, state = K.gated_scan(x, g)
+    assert state is None and torch.equal(h, K.gated_scan(x, g, zero)[0])
+    full = [t.clone().requires_grad_() for t in (x, g, s0)]
+    want = torch.autograd.grad(K.gated_scan(*full)[0], full, dh)
+    for keep in range(3):
+        some = [t.clone().requires_grad_(i == keep) for i, t in enumerate((x, g, s0))]
+        (got,) = torch.autograd.grad(K.gated_scan(*some)[0], some[keep], dh)
+        assert torch.equal(got, want[keep])
+    # the final state alone
+    leaf = [t.clone().requires_grad_() for t in (x, g, s0)]
+    _, state = K.gated_scan(*leaf, True)
+    got = torch.autograd.grad(state, leaf, ds)
+    ref = wanted(*(t.cpu() for t in (x, g, s0)), torch.zeros(2, 77, 24), ds.cpu())
+    for n, t in zip(("dx", "dg", "ds0"), got):
+        close(t, ref[n], n)
+
+
+def test_views():
+    import krylov_solvers_adjoint_amd as K
+    g0 = R.gen(4)
+    for dtype in (torch.float32, torch.bfloat16):
+        base = torch.randn(2, 150, 130, generator=g0).to(dtype).cuda()
+        gate = -torch.rand(2, 150, 120, generator=g0).to(dtype).cuda()
+        for x, g in ((base[..., 3:45], gate[..., 11:53]), (base[:, ::2, 1:43], gate[:, ::2, :42]),
+                     (base.transpose(1, 2)[:, :, :60], gate.transpose(1, 2)[:, :, :60][:, :130]),
+                     (base[:1, :, :41].expand(2, 150, 41), gate[:, :1, :41].expand(2, 150, 41))):
+            n = min(x.shape[1], g.shape[1])
+            x, g = x[:, :n], g[:, :n]
+            leaves = [t.detach().requires_grad_() for t in (x, g)]
+            h, _ = K.gated_scan(*leaves)
+            dh = torch.ones(1, device="cuda", dtype=dtype).expand_as(h)
+            got = torch.autograd.grad(h, leaves, dh)
+            whole = [t.detach().contiguous().requires_grad_() for t in (x, g)]
+            hw, _ = K.gated_scan(*whole)
+            want = torch.autograd.grad(hw, whole, torch.ones_like(hw))
+            assert torch.equal(h, hw)
+            for p, q in zip(got, want):
+                assert torch.equal(p, q)
+
+
+@pytest.mark.parametrize("kind, gkind", KINDS)
+@pytest.mark.parametrize("n, channels", [(1, 1), (3, 7), (1, 2048), (130, 65), (17, 300)])
+def test_steps_give_what_the_sequence_gives(n, channels, kind, gkind):
+    import krylov_solvers_adjoint_amd as K
+    x, g, s0, dh, ds = inputs(n, 6, channels, R.TYPES[kind], R.TYPES[gkind])
+    want = wanted(x, g, s0, dh, ds)
+    state = s0.cuda()
+    for t in range(6):
+        h = K.gated_scan_step(x.cuda()[:, t], g.cuda()[:, t], state)
+        close(h, [w[:, t] for w in want["h"]], t)
+    close(state, want["state"], "state")
+
+
+def test_refusals():
+    import krylov_solvers_adjoint_amd as K
+    x, g, s0, dh, ds = (t.cuda() for t in inputs(2, 9, 8, torch.float32, torch.float32))
+    for call in (lambda: K.gated_scan(x, g[:1]), lambda: K.gated_scan(x, g, s0[:1]),
+                 lambda: K.gated_scan(x[0], g[0]), lambda: K.gated_scan(x, g, cu_seqlens=[0, 9]),
+                 lambda: K.gated_scan(x[:1], g[:1], cu_seqlens=[0]),
+                 lambda: K.gated_scan(x[..., :0], g[..., :0]),
+                 lambda: K.gated_scan(x, g.cpu()), lambda: K.gated_scan_step(x, g, s0),
+                 lambda: K.gated_scan_step(x[:, 0], g[:, 0], s0.t().contiguous().t()),
+                 lambda: K.gated_scan_step(x[:, 0], g[:, 0], s0.clone().requires_grad_())):
+        with pytest.raises(ValueError):
+            call()
+    for call in (lambda: K.gated_scan(x, g.half()), lambda: K.gated_scan(x.double(), g),
+                 lambda: K.gated_scan(x, g, s0.half()),
+                 lambda: K.gated_scan(x[:1], g[:1], cu_seqlens=[0.0, 9.0]),
+                 lambda: K.gated_scan_step(x[:, 0], g[:, 0], s0.half())):
+        with pytest.raises(TypeError):
+            call()
+
+
+def test_against_differences():
+    import krylov_solvers_adjoint_amd as K
+    x, g, s0, dh, ds = (t.cuda() for t in inputs(2, 333, 30, torch.float32, torch.float32))
+    leaves = [t.clone().requires_grad_() for t in (x, g, s0)]
+    h, state = K.gated_scan(*leaves, True)
+    grads = torch.autograd.grad((h, state), leaves, (dh, ds))
+    step = [torch.randn(t.shape, generator=R.gen(9)).cuda() * 1e-3 * t.std() for t in (x, g, s0)]
+    ends = []
+    for s in (-1, 1):
+        p, q = K.gated_scan(*[t + s * d for t, d in zip((x, g, s0), step)], True)
+        ends.append((p.double() * dh).sum().item() + (q.double() * ds).sum().item())
+    num = (ends[1] - ends[0]) / 2
+    ana = sum((p.double() * d.double()).sum().item() for p, d in zip(grads, step))
+    size = sum((p.double() * d.double()).norm().item() for p, d in zip(grads, step))
+    # a step of 1e-3: 1e-6 of third derivatives (times tokens remembered), fp32's rounding of h
+    assert abs(num - ana) < 1e-2 * size, (num, ana, size)
+
+
+@pytest.mark.parametrize("tokens, channels", [(300, 64), (3000, 16)])
+def test_graph_replays(tokens, channels):
+    import krylov_solvers_adjoint_amd as K
+    x, g, s0, dh, ds = (t.cuda() for t in inputs(1, tokens, channels, torch.bfloat16,
+                                                 torch.float32, 3))
+    cu = torch.tensor([0, tokens // 3, tokens // 2, tokens - 5], dtype=torch.int32).cuda()
+    state = s0.clone()
+
+    def step():
+        leaves = [t.detach().requires_grad_() for t in (x, g, s0)]
+        h, last = K.gated_scan(*leaves, True, cu)
+        grads = torch.autograd.grad((h, last), leaves, (dh, ds))
+        return (h.detach(), last.detach(), *grads,
+                K.gated_scan_step(x[0, :3], g[0, :3], state))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(2):
+            step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for k in range(3):
+        x.copy_(torch.randn(1, tokens, channels, generator=R.gen(20 + k)))
+        state.copy_(s0)
+        graph.replay()
+        torch.cuda.synchronize()
+        state.copy_(s0)
+        again = step()
+        torch.cuda.synchronize()
+        for p, q in zip(out, again):
+            assert torch.equal(p, q)
+
+
+def test_two_streams_at_once():
+    sets = [inputs(2, 3000, 24, torch.float32, torch.float32, seed=s) for s in (1, 2)]
+    want = [run(*s) for s in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    got = [None, None]
+    for i, st in enumerate(streams):
+        with torch.cuda.stream(st):
+            got[i] = run(*sets[i])
+    torch.cuda.synchronize()
+    for p, q in zip(got, want):
+        for n in q:
+            assert torch.equal(p[n], q[n])
