@@ -26,8 +26,7 @@ struct Ring {
 // there is one):
 //   GATE f(a) b   GATE_GRAD d b f'(a) and d f(a)   STORE a
 //   LINEAR d + f(a + bias)   SLOPE d f'(a + bias)
-//   POLY alpha D + beta a, cut into two fp16 planes, or rounded to the last type
-enum { EPI_GATE, EPI_GATE_GRAD, EPI_STORE, EPI_LINEAR, EPI_SLOPE, EPI_POLY };
+enum { EPI_GATE, EPI_GATE_GRAD, EPI_STORE, EPI_LINEAR, EPI_SLOPE };
 constexpr int kActNone = 3;   // beside the SLA_ACT_* (LINEAR alone)
 constexpr bool two_weights(int epi) { return epi == EPI_GATE || epi == EPI_GATE_GRAD; }
 constexpr bool takes_d(int epi) {
@@ -80,7 +79,7 @@ __device__ __forceinline__ void activation(float a, float& f, float& df) {
 // AT: A is stored [k][row] (lda elements from one k to the next) instead of
 // [row][k]; BT: likewise.
 struct Product {
-  const void *A[3], *B[3];
+  const void *A[2], *B[2];
   int64_t lda, ldb;
   int64_t M, N, K;
   int parts, outputs;
@@ -92,13 +91,6 @@ struct Product {
   const float* scale;   // fp16 gradients: {what is held times it, its inverse}
   int64_t ldc;
   int act;
-  // EPI_POLY: `outputs` matrices, so many elements apart
-  int64_t za, zb, zc;
-  const _Float16* D[2];   // planes laid out as C; may be none
-  float alpha, beta;
-  void* last;        // where the result leaves rounded, [outputs][last_rows][last_cols]
-  int last_type;
-  int64_t last_rows, last_cols;
   const char* who;   // the entry, for its errors
   // filled by the launch
   int splits;        // of the steps; > 1: fp32 sums go to part [output][split][M][N]
@@ -397,7 +389,6 @@ __device__ __forceinline__ Where find_tile(const Product& g) {
 // f(ACT) with the product's activation as a constant.
 template <int EPI, typename F>
 __device__ __forceinline__ void with_activation(const Product& g, F&& f) {
-  if constexpr (EPI == EPI_POLY) return f(std::integral_constant<int, SLA_ACT_SILU>());
   if (EPI == EPI_LINEAR && g.act == kActNone) f(std::integral_constant<int, kActNone>());
   else if (EPI == EPI_STORE || g.act == SLA_ACT_SILU) f(std::integral_constant<int, SLA_ACT_SILU>());
   else if (g.act == SLA_ACT_GELU) f(std::integral_constant<int, SLA_ACT_GELU>());
@@ -461,38 +452,6 @@ __device__ __forceinline__ void leave(const Product& g, int64_t at, const float 
   if constexpr (EPI == EPI_GATE_GRAD) store_f32<4>((T*)g.C[1] + at, have, v);
 }
 
-// EPI_POLY: what becomes of four columns of a row, of which `have` exist.
-template <typename T>
-__device__ __forceinline__ void leave_rounded(const Product& g, int64_t row, int64_t col, int z,
-                                              const float (&u)[4]) {
-  store_f32<4>((T*)g.last + (z * g.last_rows + row) * g.last_cols + col, g.last_cols - col, u);
-}
-__device__ __forceinline__ void leave_poly(const Product& g, int64_t row, int64_t col,
-                                           int64_t have, int z, const f32x4& a) {
-  const int64_t at = z * g.zc + row * g.ldc + col;
-  float u[4], hi[4] = {0, 0, 0, 0}, lo[4] = {0, 0, 0, 0};
-  if (g.D[0]) {
-    load_f32<4>(g.D[0] + at, have, hi);
-    load_f32<4>(g.D[1] + at, have, lo);
-  }
-#pragma unroll
-  for (int r = 0; r < 4; ++r) u[r] = g.alpha * hi[r] + (g.alpha * lo[r] + g.beta * a[r]);
-  if (g.last) {
-    if (row >= g.last_rows || col >= g.last_cols) return;
-    if (g.last_type == SLA_F32) leave_rounded<float>(g, row, col, z, u);
-    else if (g.last_type == SLA_F16) leave_rounded<_Float16>(g, row, col, z, u);
-    else leave_rounded<__bf16>(g, row, col, z, u);
-    return;
-  }
-#pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    hi[r] = float(_Float16(u[r]));
-    lo[r] = u[r] - hi[r];
-  }
-  store_f32<4>((_Float16*)g.C[0] + at, have, hi);
-  store_f32<4>((_Float16*)g.C[1] + at, have, lo);
-}
-
 // Two neighbouring tiles' quads of 16-bit columns, x and y of lane (l, h), as
 // eight columns in a row: of tile h % 2, from 8 (h / 2) on, and back.  A store
 // then writes 64 bytes of each of 16 rows instead of 32: of 16384 x 1024 x 4096
@@ -532,7 +491,7 @@ __device__ __forceinline__ Pair packed(const float (&u)[4]) {
 // the instructions alone reach 1.8 on such data; fp32 85 % of its 0.154.
 template <typename T, int B, int WM, int WN, bool AT, bool BT, int EPI, bool DIRECT>
 __global__ __launch_bounds__(kWave* B* B / WM / WN, 2) void k_product(Product g) {
-  constexpr bool kGate = two_weights(EPI), kPoly = EPI == EPI_POLY;
+  constexpr bool kGate = two_weights(EPI);
   constexpr int kThreads = kWave * (B / WM) * (B / WN);
   constexpr int NI = WM / 16, NJ = WN / 16, kCols = kGate ? B / 2 : B;
   constexpr int kStep = Ring<DIRECT>::kStep, kDepth = Ring<DIRECT>::kDepth;
@@ -556,19 +515,17 @@ __global__ __launch_bounds__(kWave* B* B / WM / WN, 2) void k_product(Product g)
     for (int j = 0; j < NJ; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
 
   auto source_a = [&](int it) {
-    const int seg = (it >= steps) + (kPoly && it >= 2 * steps);
+    const int seg = it >= steps;
     const int64_t k0 = int64_t(it - seg * steps) * TA::kSteps;
-    const void* base = kPoly ? (const T*)(seg == 2 ? g.A[2] : seg ? g.A[1] : g.A[0]) + at.z * g.za
-                       : kGate || !(seg + at.z) ? g.A[0] : g.A[1];
-    const T* p = (const T*)base + (AT ? k0 * g.lda + m0 : m0 * g.lda + k0);
+    const T* p = (const T*)(kGate || !(seg + at.z) ? g.A[0] : g.A[1]) +
+                 (AT ? k0 * g.lda + m0 : m0 * g.lda + k0);
     return Source{(const char*)p, g.lda, g.M - m0, g.K - k0, AT ? g.M : g.K};
   };
   auto source_b = [&](int it, int which) {
-    const int seg = (it >= steps) + (kPoly && it >= 2 * steps);
+    const int seg = it >= steps;
     const int64_t k0 = int64_t(it - seg * steps) * TB::kSteps;
-    const void* base = kPoly ? (const T*)(seg == 2 ? g.B[2] : seg ? g.B[1] : g.B[0]) + at.z * g.zb
-                       : (kGate ? which : seg) ? g.B[1] : g.B[0];
-    const T* p = (const T*)base + (BT ? k0 * g.ldb + n0 : n0 * g.ldb + k0);
+    const T* p = (const T*)((kGate ? which : seg) ? g.B[1] : g.B[0]) +
+                 (BT ? k0 * g.ldb + n0 : n0 * g.ldb + k0);
     return Source{(const char*)p, g.ldb, g.N - n0, g.K - k0, BT ? g.N : g.K};
   };
   // the wave's rows of the B tile: column tile j
@@ -735,7 +692,7 @@ __global__ __launch_bounds__(kWave* B* B / WM / WN, 2) void k_product(Product g)
     constexpr int kQuads = kGate ? NJ / 2 : NJ;
     auto has = [&](int j) { return whole.value ? int64_t(4) : g.N - col0 - brow(j); };
     // whole 16-bit tiles: two quads at a time
-    constexpr bool kWide = whole.value && sizeof(T) == 2 && kQuads % 2 == 0 && !kPoly;
+    constexpr bool kWide = whole.value && sizeof(T) == 2 && kQuads % 2 == 0;
     typedef typename std::conditional<sizeof(T) == 2, T, _Float16>::type Half;   // T, if kWide
     typedef typename VecOf<Half, 8>::type Loose8;
     const int wide = brow(h % 2) - brow(0) + 8 * (h / 2) - 4 * h;   // from the lane's first quad
@@ -843,9 +800,7 @@ __global__ __launch_bounds__(kWave* B* B / WM / WN, 2) void k_product(Product g)
           } else {
 #pragma unroll
             for (int r = 0; r < 4; ++r) u[r] = takes_d(EPI) ? float(dh[i][j][r]) : 0.f;
-            if constexpr (kPoly)
-              leave_poly(g, row0 + 16 * i, col0 + brow(j), have, at.z, acc[i][j]);
-            else if constexpr (EPI == EPI_LINEAR || EPI == EPI_SLOPE)
+            if constexpr (EPI == EPI_LINEAR || EPI == EPI_SLOPE)
               leave<T, EPI, act.value>(g, at_c + brow(j), u, have, at.z, acc[i][j], bias[j]);
             else
               leave<T, EPI, act.value>(g, at_c + brow(j), u, have, at.z, acc[i][j],
@@ -881,9 +836,6 @@ __global__ __launch_bounds__(kProductBlock) void k_join(Product g) {
   if constexpr (EPI == EPI_STORE) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) s[j] *= scale;
-  } else if constexpr (EPI == EPI_POLY) {   // N is a multiple of 4
-    leave_poly(g, i / g.N, i % g.N, size - i, blockIdx.y, f32x4{s[0], s[1], s[2], s[3]});
-    return;
   } else {
     with_activation<EPI>(g, [&](auto act) {
 #pragma unroll
@@ -1199,19 +1151,19 @@ sla_status launch_product(Product& g, hipStream_t stream) {
   constexpr bool kGate = two_weights(EPI);
   constexpr int es = int(sizeof(T));
   if (g.M == 0 || g.N == 0) return SLA_OK;
-  if constexpr (EPI != EPI_STORE && EPI != EPI_POLY)
+  if constexpr (EPI != EPI_STORE)
     if (g.M <= kFewRows) return launch_few<T, EPI>(g, stream);
   const int64_t ka = AT ? g.M : g.K, kb = BT ? g.N : g.K;
   const bool direct =
       es == 2 && whole_units(g.A[0], g.lda, ka, es) && whole_units(g.B[0], g.ldb, kb, es) &&
-      EPI != EPI_POLY && (!g.A[1] || whole_units(g.A[1], g.lda, ka, es)) &&
+      (!g.A[1] || whole_units(g.A[1], g.lda, ka, es)) &&
       (!g.B[1] || whole_units(g.B[1], g.ldb, kb, es));
   const ProductPlan p = plan_product(g.M, g.N, g.K, g.parts, g.outputs, kGate, int(AT) + int(BT),
                                      es, direct);
   g.splits = p.splits;
   if (p.tile == 64) SLA_TRY((run_product<T, 64, 32, 32, AT, BT, EPI, false>(g, stream)));
   if (p.tile == 128) SLA_TRY((run_product<T, 128, 64, 64, AT, BT, EPI, false>(g, stream)));
-  if constexpr (es == 2 && EPI != EPI_POLY)
+  if constexpr (es == 2)
     if (p.tile == 256) SLA_TRY((run_product<T, 256, 128, 64, AT, BT, EPI, true>(g, stream)));
   if (g.splits > 1) {
     k_join<T, EPI><<<dim3(int(div_up(g.M * g.N, 4 * kProductBlock)), g.outputs), kProductBlock, 0,

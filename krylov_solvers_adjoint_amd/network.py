@@ -793,10 +793,10 @@ def sla_orthogonalise(m, steps: int, coefficients: tuple, eps: float):
     m, ld = _rows(m, 1)
     x = torch.empty(m.shape, dtype=m.dtype, device=m.device)
     size = _work_bytes("sla_orthogonalise_work", count, rows, cols, _TYPES[m.dtype])
-    work = _block(size, m)
+    work = _block(size, m) if size else None
     _check(_lib.sla_orthogonalise(m.data_ptr(), ld, count, rows, cols, _TYPES[m.dtype], steps,
                                   _coefficients(steps, coefficients), eps, x.data_ptr(),
-                                  work.data_ptr(), size, _stream(m)))
+                                  _ptr(work), size, _stream(m)))
     return x
 
 

@@ -16,7 +16,8 @@ pytestmark = pytest.mark.gpu
 
 TRIPLE = (3.4445, -4.775, 2.0315)
 CASES = [(1, 1), (1, 9), (9, 1), (2, 3), (16, 16), (31, 33), (33, 31), (64, 128), (128, 64),
-         (65, 190), (200, 70), (130, 130), (257, 40), (300, 515)]
+         (65, 190), (200, 70), (130, 130), (257, 40), (300, 515), (64, 512), (513, 64), (128, 128),
+         (100, 127), (20, 400), (64, 65)]
 
 
 def matrices(count, rows, cols, dtype, seed=0):
@@ -111,6 +112,9 @@ def test_steps_coefficients_and_eps():
     check(m, K.orthogonalise(m.cuda(), 3, triples), triples)
     check(m, K.orthogonalise(m.cuda(), 1, TRIPLE), [TRIPLE])
     check(m, K.orthogonalise(m.cuda(), 0), [])
+    far = matrices(2, 140, 170, torch.float32)
+    check(far, K.orthogonalise(far.cuda(), 0), [])
+    check(far, K.orthogonalise(far.cuda(), 2, triples[:2]), triples[:2])
     check(m, K.orthogonalise(m.cuda(), eps=0.5), [TRIPLE] * 5, 0.5)
     for kind in ("fp32", "fp16", "bf16"):
         dtype = R.TYPES[kind]

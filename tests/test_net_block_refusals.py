@@ -95,13 +95,14 @@ def test_orthogonalise_refusals():
     n = K._I64()
     refused("sla_orthogonalise_work", [2, 8, 9, 0, ctypes.byref(n)],
             [(0, -1), (0, 65536), (1, 0), (1, 65537), (2, 0), (2, 65537), (3, 3), (4, None)])
-    assert lib.sla_orthogonalise_work(2, 8, 9, 0, ctypes.byref(n)) == K.OK
+    assert lib.sla_orthogonalise_work(2, 8, 9, 0, ctypes.byref(n)) == K.OK and n.value == 0
+    assert lib.sla_orthogonalise_work(2, 200, 300, 0, ctypes.byref(n)) == K.OK and n.value > 0
     c = (ctypes.c_double * 3)(1.5, -0.5, 0.0)
     nan = (ctypes.c_double * 3)(1.5, float("nan"), 0.0)
     big = (ctypes.c_double * 3)(1.5, -65.0, 0.0)
-    good = [P, 9, 2, 8, 9, 0, 1, c, 1e-7, P, P, n.value, None]
+    good = [P, 300, 2, 200, 300, 0, 1, c, 1e-7, P, P, n.value, None]
     refused("sla_orthogonalise", good,
-            [(0, None), (1, 8), (2, -1), (3, 0), (4, 0), (5, 4), (6, -1), (6, 65), (7, None),
+            [(0, None), (1, 299), (2, -1), (3, 0), (4, 0), (5, 4), (6, -1), (6, 65), (7, None),
              (7, nan), (7, big), (8, -1.0), (8, float("nan")), (9, None), (10, None),
              (11, n.value - 1)])
     good[2] = 0
