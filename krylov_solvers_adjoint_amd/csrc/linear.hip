@@ -16,66 +16,93 @@ namespace sla {
 namespace net {
 namespace {
 
-// Column sums of dz: a workgroup has 64 lanes of 16 bytes of a row, its four
-// waves (and the slabs of rows) take rows in turn; the slabs' sums are joined in
-// order.
-constexpr int kColumnSlabs = 256;
-template <typename T>
+// Column sums of dz: a team of lanes has 16 bytes a lane of a row, the other
+// teams of the workgroup and the slabs of rows take rows in turn; teams and slabs
+// are joined in order.
+constexpr int kColumnSlabs = 512;
+template <typename T, int TEAM>
 __global__ __launch_bounds__(256) void k_column_sums(const T* __restrict__ dz, int64_t ld,
                                                      int64_t rows, int64_t cols,
                                                      float* __restrict__ part) {
-  constexpr int V = kVec<T>;
-  __shared__ float join[3][V][kWave];
-  const int lane = threadIdx.x % kWave, w = threadIdx.x / kWave;
-  const int64_t c = (int64_t(blockIdx.x) * kWave + lane) * V, have = cols - c;
+  constexpr int V = kVec<T>, kTeams = 256 / TEAM;
+  __shared__ float join[kTeams][V][TEAM];
+  const int lane = threadIdx.x % TEAM, team = threadIdx.x / TEAM;
+  const int64_t c = (int64_t(blockIdx.x) * TEAM + lane) * V, have = cols - c;
   float s[V];
 #pragma unroll
   for (int j = 0; j < V; ++j) s[j] = 0.f;
   if (have > 0) {
-#pragma unroll 4
-    for (int64_t r = int64_t(blockIdx.y) * 4 + w; r < rows; r += int64_t(gridDim.y) * 4) {
+    const int64_t turn = int64_t(gridDim.y) * kTeams;
+    int64_t r = int64_t(blockIdx.y) * kTeams + team;
+    for (; r + 3 * turn < rows; r += 4 * turn) {   // four rows' loads travel at once
+      float v[4][V];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) load_f32<V>(dz + (r + k * turn) * ld + c, have, v[k]);
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int j = 0; j < V; ++j) s[j] += v[k][j];
+    }
+    for (; r < rows; r += turn) {
       float v[V];
       load_f32<V>(dz + r * ld + c, have, v);
 #pragma unroll
       for (int j = 0; j < V; ++j) s[j] += v[j];
     }
   }
-  if (w) {
 #pragma unroll
-    for (int j = 0; j < V; ++j) join[w - 1][j][lane] = s[j];
-  }
+  for (int j = 0; j < V; ++j) join[team][j][lane] = s[j];
   __syncthreads();
-  if (w == 0 && have > 0) {
+  if (team == 0 && have > 0) {
 #pragma unroll
-    for (int j = 0; j < V; ++j) s[j] = (s[j] + join[0][j][lane]) + (join[1][j][lane] + join[2][j][lane]);
+    for (int j = 0; j < V; ++j) {
+      s[j] = 0.f;
+      for (int k = 0; k < kTeams; ++k) s[j] += join[k][j][lane];
+    }
     store_f32<V>(part + int64_t(blockIdx.y) * cols + c, have, s);
   }
 }
+constexpr int kJoinLines = 16;
 template <typename W>
-__global__ __launch_bounds__(256) void k_column_join(const float* __restrict__ part, int slabs,
-                                                     int64_t cols,
-                                                     const float* __restrict__ scale,
-                                                     W* __restrict__ out) {
-  __shared__ float join[4][kWave];
+__global__ __launch_bounds__(kWave* kJoinLines) void k_column_join(
+    const float* __restrict__ part, int slabs, int64_t cols, const float* __restrict__ scale,
+    W* __restrict__ out) {
+  __shared__ float join[kJoinLines][kWave];
   const int lane = threadIdx.x % kWave, w = threadIdx.x / kWave;
   const int64_t c = int64_t(blockIdx.x) * kWave + lane;
   float s = 0.f;
   if (c < cols) {
 #pragma unroll 8
-    for (int i = w; i < slabs; i += 4) s += part[int64_t(i) * cols + c];
+    for (int i = w; i < slabs; i += kJoinLines) s += part[int64_t(i) * cols + c];
   }
   join[w][lane] = s;
   __syncthreads();
   if (w == 0 && c < cols) {
-    s = (join[0][lane] + join[1][lane]) + (join[2][lane] + join[3][lane]);
+    s = 0.f;
+    for (int k = 0; k < kJoinLines; ++k) s += join[k][lane];
     out[c] = W(scale ? s * scale[1] : s);
   }
 }
 
+int column_team(int64_t cols, int es) {
+  const int64_t lanes = div_up(cols, 16 / es);
+  return lanes <= 4 ? 4 : lanes <= 16 ? 16 : 64;
+}
 int column_slabs(int64_t rows, int64_t cols, int es) {
-  const int64_t tiles = div_up(cols, kWave * 16 / es), want = div_up(1024, tiles);
-  const int64_t most = div_up(rows, 16) < want ? div_up(rows, 16) : want;
+  const int team = column_team(cols, es);
+  const int64_t tiles = div_up(cols, team * 16 / es), want = div_up(2048, tiles);
+  const int64_t least = div_up(rows, 4 * (256 / team));   // four rows a team
+  const int64_t most = least < want ? least : want;
   return int(most < 1 ? 1 : most < kColumnSlabs ? most : kColumnSlabs);
+}
+template <typename T>
+void start_column_sums(const T* dz, int64_t ld, int64_t rows, int64_t cols, float* part,
+                       hipStream_t stream) {
+  const int team = column_team(cols, int(sizeof(T)));
+  const dim3 grid(int(div_up(cols, team * kVec<T>)), column_slabs(rows, cols, int(sizeof(T))));
+  if (team == 4) k_column_sums<T, 4><<<grid, 256, 0, stream>>>(dz, ld, rows, cols, part);
+  else if (team == 16) k_column_sums<T, 16><<<grid, 256, 0, stream>>>(dz, ld, rows, cols, part);
+  else k_column_sums<T, 64><<<grid, 256, 0, stream>>>(dz, ld, rows, cols, part);
 }
 
 sla_status linear_args(const char* who, int64_t rows, int64_t inner, int64_t outer, int64_t ldx,
@@ -91,6 +118,9 @@ sla_status linear_args(const char* who, int64_t rows, int64_t inner, int64_t out
   return SLA_OK;
 }
 
+// Splits of dW's sums at most: one workgroup's share of a million rows would
+// take a millisecond.
+constexpr int kWeightSplits = 1024;
 int64_t up256(int64_t n) { return div_up(n, 256) * 256; }
 
 // The gradient's workspace: dz (with an activation), fp16's scale and what it
@@ -106,7 +136,7 @@ LinearSizes linear_sizes(int64_t rows, int64_t inner, int64_t outer, sla_type ty
   z.scale = act != SLA_ACT_NONE && type == SLA_F16 ? 256 + up256(kBoundGroups * 12) : 0;
   z.columns = up256(column_slabs(rows, outer, es) * outer * 4);
   const int64_t x = split_bytes(rows, inner, outer, 1, 1, 1, es);
-  const int64_t w = split_bytes(outer, inner, rows, 1, 1, 2, es);
+  const int64_t w = split_bytes(outer, inner, rows, 1, 1, 2, es, kWeightSplits);
   z.sums = x > w ? x : w;
   if (act != SLA_ACT_NONE && z.forward > z.sums) z.sums = z.forward;
   z.grad = z.dz + z.scale + z.columns + z.sums;
@@ -236,20 +266,20 @@ sla_status sla_linear_grad(const void* dy, int64_t lddy, const void* x, int64_t 
       p.M = outer, p.N = inner, p.K = rows, p.parts = p.outputs = 1;
       p.part = sums;
       p.scale = scale;
+      p.most = kWeightSplits;
       p.C[0] = dweight;
       p.ldc = inner;
       SLA_TRY((launch_product<T, true, true, EPI_STORE>(p, stream)));
     }
     if (dbias) {
       const int slabs = column_slabs(rows, outer, int(sizeof(T)));
-      k_column_sums<T><<<dim3(int(div_up(outer, kWave * kVec<T>)), slabs), 256, 0, stream>>>(
-          (const T*)dz, lddz, rows, outer, columns);
+      start_column_sums<T>((const T*)dz, lddz, rows, outer, columns, stream);
       LAUNCH_CHECK();
       const int grid = int(div_up(outer, kWave));
       if (btype == SLA_F32)
-        k_column_join<float><<<grid, 256, 0, stream>>>(columns, slabs, outer, scale, (float*)dbias);
+        k_column_join<float><<<grid, kWave * kJoinLines, 0, stream>>>(columns, slabs, outer, scale, (float*)dbias);
       else
-        k_column_join<T><<<grid, 256, 0, stream>>>(columns, slabs, outer, scale, (T*)dbias);
+        k_column_join<T><<<grid, kWave * kJoinLines, 0, stream>>>(columns, slabs, outer, scale, (T*)dbias);
       LAUNCH_CHECK();
     }
     return SLA_OK;

@@ -96,7 +96,9 @@ struct Product {
   int splits;        // of the steps; > 1: fp32 sums go to part [output][split][M][N]
   float* part;
   int gx, gy;        // tiles along N and M
+  int most;          // splits at most (0: kMostSplits)
 };
+constexpr int kMostSplits = 32;
 
 // 16 bytes of an operand: a lane's factor of one matrix instruction (8 16-bit
 // values of 32 k) or of four (4 fp32 values of 16 k).
@@ -819,18 +821,35 @@ __global__ __launch_bounds__(kWave* B* B / WM / WN, 2) void k_product(Product g)
 }
 
 // The sums of a split product, in the order of the splits, rounded once.
-template <typename T, int EPI>
+// LINES > 1: for many splits of few sums; a line of threads takes every
+// LINES-th split, the first line joins them.
+template <typename T, int EPI, int LINES>
 __global__ __launch_bounds__(kProductBlock) void k_join(Product g) {
+  constexpr int kWidth = kProductBlock / LINES;
+  __shared__ f32x4 lines[LINES > 1 ? LINES : 1][LINES > 1 ? kWidth : 1];
+  const int at = threadIdx.x % kWidth, line = threadIdx.x / kWidth;
   const int64_t size = g.M * g.N, quads = div_up(size, 4);
-  const int64_t i = (int64_t(blockIdx.x) * kProductBlock + threadIdx.x) * 4;
-  if (i >= quads * 4) return;
-  const float* p = g.part + int64_t(blockIdx.y) * g.splits * size + i;
-  float s[4], u[4];
-  load_f32<4>(p, size - i, s);
-  for (int k = 1; k < g.splits; ++k) {
-    load_f32<4>(p + k * size, size - i, u);
+  const int64_t i = (int64_t(blockIdx.x) * kWidth + at) * 4;
+  if (LINES == 1 && i >= quads * 4) return;
+  float s[4] = {0.f, 0.f, 0.f, 0.f}, u[4];
+  if (i < size) {
+    const float* p = g.part + int64_t(blockIdx.y) * g.splits * size + i;
+    if (line < g.splits) load_f32<4>(p + line * size, size - i, s);
+#pragma unroll 4
+    for (int k = line + LINES; k < g.splits; k += LINES) {
+      load_f32<4>(p + k * size, size - i, u);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) s[j] += u[j];
+      for (int j = 0; j < 4; ++j) s[j] += u[j];
+    }
+  }
+  if constexpr (LINES > 1) {
+    lines[line][at] = f32x4{s[0], s[1], s[2], s[3]};
+    __syncthreads();
+    if (line || i >= size) return;
+#pragma unroll
+    for (int k = 1; k < LINES; ++k)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) s[j] += lines[k][at][j];
   }
   const float scale = scale_of<T, EPI>(g);
   if constexpr (EPI == EPI_STORE) {
@@ -1061,7 +1080,7 @@ struct ProductPlan {
 // card; only long narrow ones have to take a larger tile for it.
 constexpr int64_t kMostThreads = (int64_t(1) << 32) - 1;
 ProductPlan plan_product(int64_t M, int64_t N, int64_t K, int parts, int outputs, bool gate,
-                         int turned, int es, bool direct) {
+                         int turned, int es, bool direct, int most = 0) {
   struct Kind {
     int tile, slots;
     double wait, share, start;   // us; start: before and behind the steps
@@ -1078,7 +1097,8 @@ ProductPlan plan_product(int64_t M, int64_t N, int64_t K, int parts, int outputs
     const Kind& k = kinds[i];
     const int64_t tiles = div_up(M, k.tile) * div_up(N, gate ? k.tile / 2 : k.tile) * outputs;
     const int64_t threads = k.tile == 256 ? 512 : 256;
-    for (int s = 1; s <= (gate ? 1 : 32) && s <= (steps + 3) / 4; ++s) {
+    for (int s = 1; s <= (gate ? 1 : most ? most : kMostSplits) && s <= (steps + 3) / 4;
+         s += s < kMostSplits ? 1 : s / 8) {
       if (tiles * s * threads > kMostThreads) break;
       const int64_t n = div_up(tiles * s, cus);
       const double rounds = double(div_up(n, k.slots));
@@ -1092,10 +1112,11 @@ ProductPlan plan_product(int64_t M, int64_t N, int64_t K, int parts, int outputs
   return best;
 }
 
-int64_t split_bytes(int64_t M, int64_t N, int64_t K, int parts, int outputs, int turned, int es) {
+int64_t split_bytes(int64_t M, int64_t N, int64_t K, int parts, int outputs, int turned, int es,
+                    int limit = 0) {
   int64_t most = 0;
   for (int direct = 0; direct < 2; ++direct) {
-    const ProductPlan p = plan_product(M, N, K, parts, outputs, false, turned, es, direct);
+    const ProductPlan p = plan_product(M, N, K, parts, outputs, false, turned, es, direct, limit);
     const int64_t b = p.splits > 1 ? p.splits * outputs * M * N * 4 : 0;
     if (b > most) most = b;
   }
@@ -1159,15 +1180,19 @@ sla_status launch_product(Product& g, hipStream_t stream) {
       (!g.A[1] || whole_units(g.A[1], g.lda, ka, es)) &&
       (!g.B[1] || whole_units(g.B[1], g.ldb, kb, es));
   const ProductPlan p = plan_product(g.M, g.N, g.K, g.parts, g.outputs, kGate, int(AT) + int(BT),
-                                     es, direct);
+                                     es, direct, g.most);
   g.splits = p.splits;
   if (p.tile == 64) SLA_TRY((run_product<T, 64, 32, 32, AT, BT, EPI, false>(g, stream)));
   if (p.tile == 128) SLA_TRY((run_product<T, 128, 64, 64, AT, BT, EPI, false>(g, stream)));
   if constexpr (es == 2)
     if (p.tile == 256) SLA_TRY((run_product<T, 256, 128, 64, AT, BT, EPI, true>(g, stream)));
   if (g.splits > 1) {
-    k_join<T, EPI><<<dim3(int(div_up(g.M * g.N, 4 * kProductBlock)), g.outputs), kProductBlock, 0,
-                    stream>>>(g);
+    if (g.splits > kMostSplits)
+      k_join<T, EPI, 16><<<dim3(int(div_up(g.M * g.N, 4 * kProductBlock / 16)), g.outputs),
+                           kProductBlock, 0, stream>>>(g);
+    else
+      k_join<T, EPI, 1><<<dim3(int(div_up(g.M * g.N, 4 * kProductBlock)), g.outputs),
+                          kProductBlock, 0, stream>>>(g);
     LAUNCH_CHECK();
   }
   return SLA_OK;
