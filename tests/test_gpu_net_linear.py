@@ -26,6 +26,8 @@ CASES = [  # rows, inner, outer
     (1, 1, 1), (1, 64, 64), (4, 96, 40), (3, 7, 130), (33, 100, 65), (128, 64, 128), (65, 64, 1),
     (130, 33, 67), (65, 515, 140), (257, 128, 256), (300, 72, 200), (16, 2048, 128), (17, 64, 96),
     (0, 32, 48), (512, 256, 384), (64, 1500, 33), (5000, 16, 24), (90, 4096, 72),
+    (4096, 64, 64), (4097, 5, 64), (4110, 64, 1), (6001, 33, 17), (4500, 32, 32), (20011, 61, 50),
+    (5001, 64, 32),
 ]
 
 
@@ -120,6 +122,16 @@ def test_values_that_are_not_finite_stay_where_they_are():
     import krylov_solvers_adjoint_amd as K
     for kind in ("fp32", "fp16", "bf16"):
         dtype = R.TYPES[kind]
+        # many narrow rows: no other row's products see one that is not finite
+        x, w, b, _, dy = (t.cuda() for t in inputs(5003, 40, 60, dtype, dtype))
+        bad = x.clone()
+        bad[5002], bad[17] = float("inf"), float("nan")
+        full = [t.clone().requires_grad_() for t in (bad, w, b)]
+        clean = [t.clone().requires_grad_() for t in (x, w, b)]
+        got = torch.autograd.grad(K.linear(*full, "silu"), full, dy)[0]
+        want = torch.autograd.grad(K.linear(*clean, "silu"), clean, dy)[0]
+        rest = [i for i in range(5003) if i not in (17, 5002)]
+        assert torch.equal(got[rest], want[rest])
         x, w, b, r, dy = (t.cuda() for t in inputs(70, 40, 90, dtype, dtype))
         for act in (None, "silu", "gelu", "relu"):
             want = K.linear(x, w, b, act, r)
@@ -240,7 +252,8 @@ def test_against_differences():
         assert abs(num - ana) < 1e-3 * ((hi - lo).norm() * dy.double().norm()).item() / 2
 
 
-@pytest.mark.parametrize("rows, inner, outer", [(300, 128, 256), (3, 2048, 64), (70, 4096, 64)])
+@pytest.mark.parametrize("rows, inner, outer", [(300, 128, 256), (3, 2048, 64), (70, 4096, 64),
+                                                (5000, 60, 64)])
 def test_graph_replays(rows, inner, outer):
     import krylov_solvers_adjoint_amd as K
     for dtype in (torch.bfloat16, torch.float16):
