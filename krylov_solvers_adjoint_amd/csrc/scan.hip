@@ -35,10 +35,15 @@ constexpr int kMostSegments = 64;
 constexpr int kFill = 512;     // workgroups wanted: two on each of the 256 CUs
 constexpr int64_t kMostGroups = int64_t(1) << 20;   // of a launch; they walk the items
 
-// exp(g) to 2 ulp: the instruction's exp2 with the product's rounding error put
-// right.  Below -200 and above 200 it is 0 and inf as it is; NaN stays.
-__device__ __forceinline__ float decay(float g) {
+// exp(g).  fp32 gates: to 2 ulp, the instruction's exp2 with the product's
+// rounding error put right; below -200 and above 200 it is 0 and inf as it is; NaN
+// stays.  16-bit gates: without that, off by |g| 2^-23.5 of itself, far below
+// their own half step (and a |g| is 0.4 at most, so the state is as good).
+template <typename G>
+__device__ __forceinline__ float decay(G gate) {
   constexpr float kHi = 1.44269502f, kLo = 1.92596303e-08f;   // log2(e)
+  float g = float(gate);
+  if constexpr (sizeof(G) == 2) return __builtin_amdgcn_exp2f(g * kHi);
   g = g < -200.f ? -200.f : g > 200.f ? 200.f : g;
   const float t = g * kHi;
   const float r = __builtin_fmaf(g, kLo, __builtin_fmaf(g, kHi, -t));
@@ -81,7 +86,9 @@ __device__ __forceinline__ Item item_of(const ScanShape& s, int64_t id) {
     w.first = w.seq * div_up(s.seqlen, BT);
   }
   w.blocks = (w.len + BT - 1) / BT;
-  const int64_t each = (w.blocks + s.segments - 1) / s.segments;
+  // an odd number of blocks: segments that begin at multiples of a large power
+  // of two would all begin in the same memory channels
+  const int64_t each = (w.blocks + s.segments - 1) / s.segments | (s.segments > 1);
   w.b0 = w.seg * each < w.blocks ? w.seg * each : w.blocks;
   w.b1 = w.b0 + each < w.blocks ? w.b0 + each : w.blocks;
   return w;
@@ -102,19 +109,47 @@ struct Place {
   static constexpr int kSlices = kWave / CL;            // spans of a wave
   static constexpr int kBlock = WAVES * kSlices * kSpan;  // tokens of a block
   int lane, slice, wave;
-  int64_t c;        // the thread's first channel to read
+  int64_t tile;     // the tile's first channel
+  int in;           // the thread's first channel to read, from there on
   bool on;          // whether it is the thread's own (lanes behind the last read another's)
-  __device__ __forceinline__ Place(int tile, int64_t channels) {
+  __device__ __forceinline__ Place(int which, int64_t channels) {
     const int t = threadIdx.x;
     lane = t % CL;
     slice = t % kWave / CL;
     wave = __builtin_amdgcn_readfirstlane(t / kWave);
-    c = (int64_t(tile) * CL + lane) * V;
-    on = c < channels;
-    if (!on) c = channels - V;
+    tile = int64_t(which) * CL * V;
+    const int64_t left = channels - tile;
+    on = lane * V < left;
+    in = on ? lane * V : int(left) - V;
   }
+  __device__ __forceinline__ int64_t channel() const { return tile + in; }
+  // the thread's first token of a block
   __device__ __forceinline__ int64_t token(int64_t block) const {
     return block * kBlock + (wave * kSlices + slice) * kSpan;
+  }
+};
+
+// One array's part of a sequence's tile: where a wave's block begins (in scalar
+// registers) and the thread's place behind that, in bytes (31 bits: spans of a
+// wave lie less than 2^24 elements apart, or there is one).
+template <typename T, int V, typename At>
+struct Lane {
+  typedef typename VecOf<typename std::remove_const<T>::type, V>::type Value;
+  typedef typename std::conditional<std::is_const<T>::value, const Value, Value>::type Vec;
+  T* p;            // the sequence's first token, the tile's first channel
+  int64_t ld;
+  int at;
+  __device__ __forceinline__ Lane(T* first, int64_t ld_, const At& me)
+      : p(first), ld(ld_), at(int((me.slice * kSpan * ld_ + me.in) * int64_t(sizeof(T)))) {}
+  __device__ __forceinline__ T* block(int64_t b, int wave) const {
+    const uint64_t q = reinterpret_cast<uint64_t>(
+        p + (b * At::kBlock + wave * At::kSlices * kSpan) * ld);
+    return reinterpret_cast<T*>(
+        uint64_t(uint32_t(__builtin_amdgcn_readfirstlane(int(q >> 32)))) << 32 |
+        uint32_t(__builtin_amdgcn_readfirstlane(int(q))));
+  }
+  __device__ __forceinline__ Vec* token(T* block, int j) const {
+    return reinterpret_cast<Vec*>(reinterpret_cast<uintptr_t>(block + j * ld) + uint32_t(at));
   }
 };
 
@@ -122,11 +157,20 @@ struct Place {
 template <typename T, int V>
 struct Raw {
   typename VecOf<T, V>::type v[kSpan];
-  __device__ __forceinline__ void load(const T* p, int64_t ld, int64_t t, int64_t len) {
+  template <typename At>
+  __device__ __forceinline__ void load(const Lane<const T, V, At>& from, int64_t b, int64_t len,
+                                       const At& me) {
+    if ((b + 1) * At::kBlock <= len) {
+      const T* q = from.block(b, me.wave);
 #pragma unroll
-    for (int j = 0; j < kSpan; ++j) {
-      const int64_t at = t + j < len ? t + j : len - 1;
-      v[j] = *reinterpret_cast<const typename VecOf<T, V>::type*>(p + at * ld);
+      for (int j = 0; j < kSpan; ++j) v[j] = *from.token(q, j);
+    } else {
+      const int64_t t = me.token(b);
+#pragma unroll
+      for (int j = 0; j < kSpan; ++j) {
+        const int64_t at = t + j < len ? t + j : len - 1;
+        v[j] = *reinterpret_cast<const typename VecOf<T, V>::type*>(from.p + at * from.ld + me.in);
+      }
     }
   }
 };
@@ -167,6 +211,27 @@ __device__ __forceinline__ void shift_slices(float (&P)[V], float (&H)[V], int s
   }
 }
 
+// A state through `count` segments' maps, forwards or backwards; eight maps'
+// loads travel at once (one by one 63 of them took longer than the walk).
+template <int V, int STEP>
+__device__ __forceinline__ void through(float (&state)[V], const float* ends, int64_t ld,
+                                        int count) {
+  for (int k = 0; k < count; k += 8) {
+    float e[8][2 * V];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float* p = ends + STEP * (k + i < count ? k + i : k) * ld;
+#pragma unroll
+      for (int v = 0; v < 2 * V; ++v) e[i][v] = p[v];
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        state[v] = k + i < count ? e[i][2 * v] * state[v] + e[i][2 * v + 1] : state[v];
+  }
+}
+
 // Rows of tokens of no sequence become zero.
 template <typename T, int CL, int WAVES, int V>
 __device__ __forceinline__ void clear_rows(const ScanShape& s, const Item& w, T* out) {
@@ -179,12 +244,12 @@ __device__ __forceinline__ void clear_rows(const ScanShape& s, const Item& w, T*
        i += int64_t(s.segments) * kSlices) {
     typename VecOf<T, V>::type z = {};
     *reinterpret_cast<typename VecOf<T, V>::type*>(
-        out + (i < head ? i : tail + i - head) * s.channels + me.c) = z;
+        out + (i < head ? i : tail + i - head) * s.channels + me.channel()) = z;
   }
 }
 
 template <typename T, typename G, int CL, int WAVES, int V>
-__global__ __launch_bounds__(WAVES* kWave) void k_scan(
+__global__ __launch_bounds__(WAVES* kWave, 4) void k_scan(
     ScanShape s, const T* __restrict__ x, int64_t ldx, const G* __restrict__ g, int64_t ldg,
     const float* __restrict__ s0, T* __restrict__ h, float* __restrict__ last,
     float* __restrict__ kept, const float* __restrict__ ends) {
@@ -200,41 +265,53 @@ __global__ __launch_bounds__(WAVES* kWave) void k_scan(
     }
     if (w.seg > 0 && w.b0 == w.b1) continue;
     const At me(w.tile, s.channels);
+    const int64_t ch = me.channel();
     float carry[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) carry[v] = s0 ? s0[w.seq * s.channels + me.c + v] : 0.f;
-    for (int k = 0; k < w.seg; ++k) {
-      const float* e = ends + ((w.seq * s.segments + k) * s.channels + me.c) * 2;
-#pragma unroll
-      for (int v = 0; v < V; ++v) carry[v] = e[2 * v] * carry[v] + e[2 * v + 1];
-    }
-    const T* px = x + w.from * ldx + me.c;
-    const G* pg = g + w.from * ldg + me.c;
+    for (int v = 0; v < V; ++v) carry[v] = s0 ? s0[w.seq * s.channels + ch + v] : 0.f;
+    through<V, 1>(carry, ends + (w.seq * s.segments * s.channels + ch) * 2, s.channels * 2, w.seg);
+    const Lane<const T, V, At> fx(x + w.from * ldx + me.tile, ldx, me);
+    const Lane<const G, V, At> fg(g + w.from * ldg + me.tile, ldg, me);
+    const Lane<T, V, At> fh(h + w.from * s.channels + me.tile, s.channels, me);
     Raw<T, V> rx;
     Raw<G, V> rg;
     if (w.b0 < w.b1) {
-      rx.load(px, ldx, me.token(w.b0), w.len);
-      rg.load(pg, ldg, me.token(w.b0), w.len);
+      rx.load(fx, w.b0, w.len, me);
+      rg.load(fg, w.b0, w.len, me);
     }
     for (int64_t b = w.b0; b < w.b1; ++b) {
-      const int64_t t0 = me.token(b);
+      const bool whole = (b + 1) * BT <= w.len;
+      const int left = whole ? kSpan : int(w.len - me.token(b) < kSpan ? w.len - me.token(b) : kSpan);
       float a[kSpan][V], u[kSpan][V], P[V], H[V];
 #pragma unroll
-      for (int v = 0; v < V; ++v) P[v] = 1.f, H[v] = 0.f;
-#pragma unroll
-      for (int j = 0; j < kSpan; ++j) {
-        const bool live = t0 + j < w.len;   // what lies behind the end changes nothing
+      for (int j = 0; j < kSpan; ++j)
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-          a[j][v] = live ? decay(float(rg.v[j][v])) : 1.f;
-          u[j][v] = live ? float(rx.v[j][v]) : 0.f;
+          a[j][v] = decay(rg.v[j][v]);
+          u[j][v] = float(rx.v[j][v]);
+        }
+      if (!whole) {   // what lies behind the end changes nothing
+#pragma unroll
+        for (int j = 0; j < kSpan; ++j)
+#pragma unroll
+          for (int v = 0; v < V; ++v) {
+            a[j][v] = j < left ? a[j][v] : 1.f;
+            u[j][v] = j < left ? u[j][v] : 0.f;
+          }
+      }
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        P[v] = a[0][v];
+        H[v] = u[0][v];
+#pragma unroll
+        for (int j = 1; j < kSpan; ++j) {
           H[v] = a[j][v] * H[v] + u[j][v];
           P[v] *= a[j][v];
         }
       }
       if (b + 1 < w.b1) {
-        rx.load(px, ldx, me.token(b + 1), w.len);
-        rg.load(pg, ldg, me.token(b + 1), w.len);
+        rx.load(fx, b + 1, w.len, me);
+        rg.load(fg, b + 1, w.len, me);
       }
       join_slices<CL, V, true>(P, H, me.slice);
       if (me.slice == At::kSlices - 1) {
@@ -245,7 +322,7 @@ __global__ __launch_bounds__(WAVES* kWave) void k_scan(
       __syncthreads();
       if (kept && me.on && me.wave == 0 && me.slice == 0) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) kept[(w.first + b) * s.channels + me.c + v] = carry[v];
+        for (int v = 0; v < V; ++v) kept[(w.first + b) * s.channels + ch + v] = carry[v];
       }
       float state[V];
 #pragma unroll
@@ -260,6 +337,7 @@ __global__ __launch_bounds__(WAVES* kWave) void k_scan(
         state[v] = P[v] * state[v] + H[v];
       }
       buf ^= 1;
+      T* const to = fh.block(b, me.wave);
 #pragma unroll
       for (int j = 0; j < kSpan; ++j) {
         typename VecOf<T, V>::type o;
@@ -268,14 +346,12 @@ __global__ __launch_bounds__(WAVES* kWave) void k_scan(
           state[v] = a[j][v] * state[v] + u[j][v];
           o[v] = T(state[v]);
         }
-        if (me.on && t0 + j < w.len)
-          *reinterpret_cast<typename VecOf<T, V>::type*>(
-              h + (w.from + t0 + j) * s.channels + me.c) = o;
+        if (me.on && j < left) *fh.token(to, j) = o;
       }
     }
     if (last && me.on && w.b1 == w.blocks && me.wave == 0 && me.slice == 0) {
 #pragma unroll
-      for (int v = 0; v < V; ++v) last[w.seq * s.channels + me.c + v] = carry[v];
+      for (int v = 0; v < V; ++v) last[w.seq * s.channels + ch + v] = carry[v];
     }
   }
 }
@@ -300,50 +376,67 @@ __global__ __launch_bounds__(WAVES* kWave) void k_scan_grad(
     }
     if (w.seg > 0 && w.b0 == w.b1) continue;
     const At me(w.tile, s.channels);
+    const int64_t ch = me.channel();
     float carry[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) carry[v] = dlast ? dlast[w.seq * s.channels + me.c + v] : 0.f;
-    for (int k = s.segments - 1; k > w.seg; --k) {
-      const float* e = ends + ((w.seq * s.segments + k) * s.channels + me.c) * 2;
-#pragma unroll
-      for (int v = 0; v < V; ++v) carry[v] = e[2 * v] * carry[v] + e[2 * v + 1];
-    }
-    const T* px = x + w.from * ldx + me.c;
-    const G* pg = g + w.from * ldg + me.c;
-    const T* pd = dh + w.from * lddh + me.c;
+    for (int v = 0; v < V; ++v) carry[v] = dlast ? dlast[w.seq * s.channels + ch + v] : 0.f;
+    through<V, -1>(carry,
+                   ends + (((w.seq + 1) * s.segments - 1) * s.channels + ch) * 2, s.channels * 2,
+                   s.segments - 1 - w.seg);
+    const Lane<const T, V, At> fx(x + w.from * ldx + me.tile, ldx, me);
+    const Lane<const G, V, At> fg(g + w.from * ldg + me.tile, ldg, me);
+    const Lane<const T, V, At> fd(dh + w.from * lddh + me.tile, lddh, me);
+    const int64_t out = w.from * s.channels + me.tile;
+    const Lane<T, V, At> tx(dx + (dx ? out : 0), s.channels, me);
+    const Lane<G, V, At> tg(dg + (dg ? out : 0), s.channels, me);
     Raw<T, V> rx, rd;
     Raw<G, V> rg;
+    float next[V];   // the state in front of the block that is loaded
     auto load = [&](int64_t b) {
-      rx.load(px, ldx, me.token(b), w.len);
-      rg.load(pg, ldg, me.token(b), w.len);
-      rd.load(pd, lddh, me.token(b), w.len);
+      rx.load(fx, b, w.len, me);
+      rg.load(fg, b, w.len, me);
+      rd.load(fd, b, w.len, me);
+#pragma unroll
+      for (int v = 0; v < V; ++v) next[v] = kept[(w.first + b) * s.channels + ch + v];
     };
     if (w.b0 < w.b1) load(w.b1 - 1);
     for (int64_t b = w.b1; b-- > w.b0;) {
-      const int64_t t0 = me.token(b);
-      float start[V];
+      const bool whole = (b + 1) * BT <= w.len;
+      const int left = whole ? kSpan : int(w.len - me.token(b) < kSpan ? w.len - me.token(b) : kSpan);
+      float a[kSpan][V], u[kSpan][V], d[kSpan][V], P[V], H[V], Q[V], M[V], state[V], m[V];
 #pragma unroll
-      for (int v = 0; v < V; ++v) start[v] = kept[(w.first + b) * s.channels + me.c + v];
-      float a[kSpan][V], u[kSpan][V], d[kSpan][V], P[V], H[V], Q[V], M[V];
+      for (int v = 0; v < V; ++v) state[v] = next[v];
 #pragma unroll
-      for (int v = 0; v < V; ++v) P[v] = 1.f, H[v] = 0.f, M[v] = 0.f;
-#pragma unroll
-      for (int j = 0; j < kSpan; ++j) {
-        const bool live = t0 + j < w.len;
+      for (int j = 0; j < kSpan; ++j)
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-          a[j][v] = live ? decay(float(rg.v[j][v])) : 1.f;
-          u[j][v] = live ? float(rx.v[j][v]) : 0.f;
-          d[j][v] = live ? float(rd.v[j][v]) : 0.f;
-          H[v] = a[j][v] * H[v] + u[j][v];
-          P[v] *= a[j][v];
+          a[j][v] = decay(rg.v[j][v]);
+          u[j][v] = float(rx.v[j][v]);
+          d[j][v] = float(rd.v[j][v]);
         }
+      if (!whole) {
+#pragma unroll
+        for (int j = 0; j < kSpan; ++j)
+#pragma unroll
+          for (int v = 0; v < V; ++v) {
+            a[j][v] = j < left ? a[j][v] : 1.f;
+            u[j][v] = j < left ? u[j][v] : 0.f;
+            d[j][v] = j < left ? d[j][v] : 0.f;
+          }
       }
       if (b > w.b0) load(b - 1);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
+        P[v] = a[0][v];
+        H[v] = u[0][v];
 #pragma unroll
-        for (int j = kSpan - 1; j >= 0; --j) M[v] = a[j][v] * (d[j][v] + M[v]);
+        for (int j = 1; j < kSpan; ++j) {
+          H[v] = a[j][v] * H[v] + u[j][v];
+          P[v] *= a[j][v];
+        }
+        M[v] = a[kSpan - 1][v] * d[kSpan - 1][v];
+#pragma unroll
+        for (int j = kSpan - 2; j >= 0; --j) M[v] = a[j][v] * (d[j][v] + M[v]);
         Q[v] = P[v];
       }
       join_slices<CL, V, true>(P, H, me.slice);
@@ -357,20 +450,19 @@ __global__ __launch_bounds__(WAVES* kWave) void k_scan_grad(
       shift_slices<CL, V, true>(P, H, me.slice);
       shift_slices<CL, V, false>(Q, M, me.slice);
       __syncthreads();
-      float state[V], m[V];
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        state[v] = start[v];
         m[v] = carry[v];
+        float2 f[WAVES];
 #pragma unroll
         for (int k = 0; k < WAVES; ++k) {
-          const float2 f = fwd[buf][k][me.lane * V + v];
-          if (k < me.wave) state[v] = f.x * state[v] + f.y;
+          f[k] = fwd[buf][k][me.lane * V + v];
+          if (k < me.wave) state[v] = f[k].x * state[v] + f[k].y;
         }
 #pragma unroll
         for (int k = WAVES - 1; k >= 0; --k) {
           if (k == me.wave) m[v] = carry[v];
-          carry[v] = fwd[buf][k][me.lane * V + v].x * carry[v] + back[buf][k][me.lane * V + v];
+          carry[v] = f[k].x * carry[v] + back[buf][k][me.lane * V + v];
         }
         state[v] = P[v] * state[v] + H[v];
         m[v] = Q[v] * m[v] + M[v];
@@ -380,32 +472,33 @@ __global__ __launch_bounds__(WAVES* kWave) void k_scan_grad(
       for (int j = 0; j < kSpan; ++j) {
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-          const float next = a[j][v] * state[v] + u[j][v];
+          const float after = a[j][v] * state[v] + u[j][v];
           u[j][v] = state[v];
-          state[v] = next;
+          state[v] = after;
         }
       }
+      T* const ox = tx.block(b, me.wave);
+      G* const og = tg.block(b, me.wave);
 #pragma unroll
       for (int j = kSpan - 1; j >= 0; --j) {
-        typename VecOf<T, V>::type ox;
-        typename VecOf<G, V>::type og;
+        typename VecOf<T, V>::type vx;
+        typename VecOf<G, V>::type vg;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
           const float l = d[j][v] + m[v];
           m[v] = a[j][v] * l;
-          ox[v] = T(l);
-          og[v] = G(m[v] * u[j][v]);
+          vx[v] = T(l);
+          vg[v] = G(m[v] * u[j][v]);
         }
-        if (me.on && t0 + j < w.len) {
-          const int64_t at = (w.from + t0 + j) * s.channels + me.c;
-          if (dx) *reinterpret_cast<typename VecOf<T, V>::type*>(dx + at) = ox;
-          if (dg) *reinterpret_cast<typename VecOf<G, V>::type*>(dg + at) = og;
+        if (me.on && j < left) {
+          if (dx) *tx.token(ox, j) = vx;
+          if (dg) *tg.token(og, j) = vg;
         }
       }
     }
     if (ds0 && me.on && w.seg == 0 && me.wave == 0 && me.slice == 0) {
 #pragma unroll
-      for (int v = 0; v < V; ++v) ds0[w.seq * s.channels + me.c + v] = carry[v];
+      for (int v = 0; v < V; ++v) ds0[w.seq * s.channels + ch + v] = carry[v];
     }
   }
 }
@@ -430,8 +523,8 @@ __global__ __launch_bounds__(WAVES* kWave) void k_scan_ends(
     const int run = me.wave * At::kSlices + me.slice;
     const int64_t lo = begin + run * each < end ? begin + run * each : end;
     const int64_t hi = lo + each < end ? lo + each : end;
-    const T* pu = u + w.from * ldu + me.c;
-    const G* pg = g + w.from * ldg + me.c;
+    const T* pu = u + w.from * ldu + me.channel();
+    const G* pg = g + w.from * ldg + me.channel();
     float P[V], H[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) P[v] = 1.f, H[v] = 0.f;
@@ -452,7 +545,7 @@ __global__ __launch_bounds__(WAVES* kWave) void k_scan_ends(
         const bool live = t + j >= lo && t + j < hi;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-          const float a = live ? decay(float(rg.v[j][v])) : 1.f;
+          const float a = live ? decay(rg.v[j][v]) : 1.f;
           const float y = live ? float(ru.v[j][v]) : 0.f;
           H[v] = BACK ? a * (y + H[v]) : a * H[v] + y;
           P[v] *= a;
@@ -467,7 +560,7 @@ __global__ __launch_bounds__(WAVES* kWave) void k_scan_ends(
     }
     __syncthreads();
     if (me.on && me.wave == 0 && me.slice == 0) {
-      float* e = ends + ((w.seq * s.segments + w.seg) * s.channels + me.c) * 2;
+      float* e = ends + ((w.seq * s.segments + w.seg) * s.channels + me.channel()) * 2;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         float p = 1.f, q = 0.f;
@@ -516,12 +609,21 @@ __global__ __launch_bounds__(256) void k_scan_step(const T* __restrict__ x, int6
        i += int64_t(gridDim.x) * 256) {
     const int64_t r = all < (int64_t(1) << 32) ? int64_t(uint32_t(i) / uint32_t(per)) : i / per;
     const int64_t c = (i - r * per) * V, have = channels - c;
-    float xv[V], gv[V], sv[V];
+    float xv[V], sv[V];
     load_f32<V>(x + r * ldx + c, have, xv);
-    load_f32<V>(g + r * ldg + c, have, gv);
+    G gate[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) gate[v] = G(0.f);
+    if (have >= V) {
+      const auto q = *reinterpret_cast<const typename VecOf<G, V>::type*>(g + r * ldg + c);
+#pragma unroll
+      for (int v = 0; v < V; ++v) gate[v] = q[v];
+    } else {
+      for (int v = 0; v < have; ++v) gate[v] = g[r * ldg + c + v];
+    }
     load_f32<V>(state + r * channels + c, have, sv);
 #pragma unroll
-    for (int v = 0; v < V; ++v) sv[v] = decay(gv[v]) * sv[v] + xv[v];
+    for (int v = 0; v < V; ++v) sv[v] = decay(gate[v]) * sv[v] + xv[v];
     store_f32<V>(state + r * channels + c, have, sv);
     store_f32<V>(h + r * channels + c, have, sv);
   }
@@ -545,15 +647,22 @@ ScanPlan scan_plan(const sla_scan_dims* d) {
   const int64_t mean = div_up(d->tokens, n);
   p.cl = 64;
   while (p.cl > 16 && (lanes <= p.cl / 2 || n * div_up(lanes, p.cl) < kFill)) p.cl /= 2;
-  p.waves = mean <= 4 * kSpan * (kWave / p.cl) ? 1 : 8;
   p.tiles = div_up(lanes, p.cl);
+  const int64_t groups = n * p.tiles;
+  const bool one_each = groups >= kFill / 2 && groups < kFill;   // a workgroup a CU: 8 waves
+  p.waves = mean <= 4 * kSpan * (kWave / p.cl) ? 1 : one_each ? 8 : 4;
   p.block_tokens = int64_t(p.waves) * (kWave / p.cl) * kSpan;
-  const int64_t groups = n * p.tiles, blocks = div_up(mean, p.block_tokens);
+  const int64_t blocks = div_up(mean, p.block_tokens);
   int64_t s = groups >= kFill / 2 ? 1 : div_up(kFill, groups);
   s = s < blocks / 2 ? s : blocks / 2;
   p.segments = int(s < 1 ? 1 : s < kMostSegments ? s : kMostSegments);
   p.blocks = d->packed ? d->tokens / p.block_tokens + n : n * blocks;
   return p;
+}
+
+// Whether a thread's place in a wave's tokens fits 31 bits.
+bool scan_stride(const ScanPlan& p, int64_t ld) {
+  return p.cl == kWave || ld < (int64_t(1) << 24);
 }
 
 int64_t up256(int64_t n) { return div_up(n, 256) * 256; }
@@ -596,6 +705,7 @@ sla_status with_scan(const sla_scan_dims* d, const ScanPlan& p, F&& f) {
     using std::integral_constant;
     auto waves = [&](auto cl) -> sla_status {
       if (p.waves == 1) return f(te, ge, cl, integral_constant<int, 1>(), v);
+      if (p.waves == 4) return f(te, ge, cl, integral_constant<int, 4>(), v);
       return f(te, ge, cl, integral_constant<int, 8>(), v);
     };
     if (p.cl == 64) return waves(integral_constant<int, 64>());
@@ -661,6 +771,8 @@ sla_status sla_gated_scan(const sla_scan_dims* dims, const void* x, int64_t ldx,
   SLA_NET_REQUIRE(!dims->packed || offsets, "sla_gated_scan: offsets is NULL");
   SLA_NET_REQUIRE(ldx >= dims->channels && ldg >= dims->channels,
                   "sla_gated_scan: a token stride is below channels");
+  SLA_NET_REQUIRE(scan_stride(z.plan, ldx) && scan_stride(z.plan, ldg),
+                  "sla_gated_scan: a token stride of 2^24 or more");
   SLA_NET_REQUIRE(!kept || kept_bytes >= z.kept,
                   "sla_gated_scan: kept block too small (sla_gated_scan_work)");
   SLA_NET_REQUIRE(z.work == 0 || (work && work_bytes >= z.work),
@@ -703,6 +815,9 @@ sla_status sla_gated_scan_grad(const sla_scan_dims* dims, const void* x, int64_t
   SLA_NET_REQUIRE(dims->tokens == 0 || (x && g && dh), "sla_gated_scan_grad: an argument is NULL");
   SLA_NET_REQUIRE(ldx >= dims->channels && ldg >= dims->channels && lddh >= dims->channels,
                   "sla_gated_scan_grad: a token stride is below channels");
+  SLA_NET_REQUIRE(scan_stride(z.plan, ldx) && scan_stride(z.plan, ldg) &&
+                      scan_stride(z.plan, lddh),
+                  "sla_gated_scan_grad: a token stride of 2^24 or more");
   SLA_NET_REQUIRE(z.kept == 0 || (kept && kept_bytes >= z.kept),
                   "sla_gated_scan_grad: kept block too small (sla_gated_scan_work)");
   SLA_NET_REQUIRE(z.work == 0 || (work && work_bytes >= z.work),
