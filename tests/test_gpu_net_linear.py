@@ -252,8 +252,36 @@ def test_against_differences():
         assert abs(num - ana) < 1e-3 * ((hi - lo).norm() * dy.double().norm()).item() / 2
 
 
+@pytest.mark.parametrize("rows, inner, outer", [
+    (5000, 771, 1403), (4096, 515, 1000), (1100, 1021, 1024), (70, 8001, 2000), (2100, 4096, 520),
+    (16400, 264, 520), (300000, 96, 40), (40000, 64, 48), (16384, 512, 512)])
+@pytest.mark.parametrize("kind", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("act", [None, "gelu"])
+def test_large(rows, inner, outer, kind, act):
+    """Large tiles, padded copies, split sums, one-pass gradients: against 64 bits on the GPU."""
+    import krylov_solvers_adjoint_amd as K
+    dtype = R.TYPES[kind]
+    x, w, b, r, dy = (t.cuda() for t in inputs(rows, inner, outer, dtype, dtype))
+    leaves = [t.requires_grad_() for t in (x, w, b, r)]
+    y = K.linear(*leaves[:3], act, leaves[3])
+    got = (y, *torch.autograd.grad(y, leaves, dy))
+    want = bounds(*(t.detach().double() for t in (x, w, b, r, dy)), act, dtype, dtype)
+    tiny = 2.0 ** -25 if kind == "fp16" else 0.0
+    for name, t in zip(("y", "dx", "dw", "db"), got):
+        ref, tol = want[name]
+        bad = ~((t.detach().double() - ref).abs() <= (tol + tiny) * (1 + 2 ** -6))
+        assert not bad.any(), (name, int(bad.sum()))
+    # the whole: half a step of every value, and dz's rounding beside it
+    u = R.half_step(dtype)
+    for name, t in zip(("y", "dx", "dw", "db"), got):
+        assert R.rel(t, want[name][0]) <= 1.5 * u + 200 * R.U32, name
+    again = torch.autograd.grad(K.linear(*leaves[:3], act, leaves[3]), leaves, dy)
+    for p, q in zip(got[1:], again):
+        assert torch.equal(p, q)
+
+
 @pytest.mark.parametrize("rows, inner, outer", [(300, 128, 256), (3, 2048, 64), (70, 4096, 64),
-                                                (5000, 60, 64)])
+                                                (5000, 60, 64), (1500, 771, 901)])
 def test_graph_replays(rows, inner, outer):
     import krylov_solvers_adjoint_amd as K
     for dtype in (torch.bfloat16, torch.float16):
