@@ -643,6 +643,15 @@ def _scan_plan(*args):
     return d, ctypes.byref(d), kept.value, work.value
 
 
+def _tokens(t: torch.Tensor):
+    """_rows of single tokens; rows 2^24 elements apart or more are copied."""
+    t, ld = _rows(t, 1)
+    if ld >= 1 << 24:
+        t = t.contiguous()
+        ld = t.shape[-1]
+    return t, ld
+
+
 def _scan_dims(x, g, sequences, packed):
     channels = x.shape[-1]
     return _scan_plan(sequences, x.numel() // channels, channels, _TYPES[x.dtype],
@@ -654,7 +663,7 @@ def sla_gated_scan(x, g, offsets, initial_state, sequences: int, want_state: boo
                    want_kept: bool = False):
     """(h, final_state or None, kept or None): kept is what the gradient reads."""
     dims, at, ksize, wsize = _scan_dims(x, g, sequences, offsets is not None)
-    (x, ldx), (g, ldg) = _rows(x, 1), _rows(g, 1)
+    (x, ldx), (g, ldg) = _tokens(x), _tokens(g)
     kept = _block(ksize, x) if want_kept else None
     work = _block(wsize, x) if wsize else None
     h = torch.empty(x.shape, dtype=x.dtype, device=x.device)
@@ -671,7 +680,7 @@ def sla_gated_scan_grad(x, g, kept, grad_h, grad_state, sequences: int, packed: 
                         want_x=True, want_g=True, want_initial=True):
     """(dx, dg, grad of the initial state), None where not wanted."""
     dims, at, ksize, wsize = _scan_dims(x, g, sequences, packed)
-    (x, ldx), (g, ldg), (grad_h, ldh) = _rows(x, 1), _rows(g, 1), _rows(grad_h, 1)
+    (x, ldx), (g, ldg), (grad_h, ldh) = _tokens(x), _tokens(g), _tokens(grad_h)
     work = _block(wsize, x) if wsize else None
     dx = torch.empty(x.shape, dtype=x.dtype, device=x.device) if want_x else None
     dg = torch.empty(g.shape, dtype=g.dtype, device=g.device) if want_g else None
@@ -781,7 +790,7 @@ def gated_scan_step(x: torch.Tensor, g: torch.Tensor, state: torch.Tensor) -> to
 @functools.lru_cache(maxsize=64)
 def _coefficients(steps: int, coefficients: tuple):
     """The C array of a triple a step."""
-    flat = [float(v) for t in coefficients for v in t]
+    flat = [v for t in coefficients for v in t]
     return (ctypes.c_double * max(len(flat), 1))(*flat)
 
 
@@ -818,7 +827,8 @@ def orthogonalise(m: torch.Tensor, steps: int = 5, coefficients=(3.4445, -4.775,
         raise ValueError("m: expected [..., rows, cols]")
     if isinstance(steps, bool) or not isinstance(steps, int) or not 0 <= steps <= 64:
         raise ValueError("steps: expected a whole number from 0 to 64")
-    triples = tuple(tuple(t) if isinstance(t, (tuple, list)) else t for t in coefficients)
+    triples = tuple(tuple(map(float, t)) if isinstance(t, (tuple, list)) else float(t)
+                    for t in coefficients)
     if len(triples) == 3 and not any(isinstance(t, tuple) for t in triples):
         triples = (triples,) * steps
     if len(triples) != steps or any(not isinstance(t, tuple) or len(t) != 3 for t in triples):

@@ -331,3 +331,23 @@ def test_two_streams_at_once():
         for p, q in zip(got, want):
             for a, b in zip(p, q):
                 assert torch.equal(a, b)
+
+
+def test_more_than_2_to_the_31_elements():
+    """Rows behind the 2^31st element are what they are by themselves."""
+    import krylov_solvers_adjoint_amd as K
+    g = torch.Generator(device="cuda").manual_seed(1)
+    for rows, inner, outer, act in ((34_000_000, 64, 64, "silu"), (1_100_000, 2000, 1024, None)):
+        assert rows * inner > 1 << 31
+        dtype = torch.bfloat16
+        x = torch.randn(rows, inner, generator=g, device="cuda", dtype=dtype).requires_grad_()
+        w = (torch.randn(outer, inner, generator=g, device="cuda") / inner ** 0.5).to(dtype)
+        b = torch.randn(outer, generator=g, device="cuda", dtype=dtype)
+        y = K.linear(x, w, b, act)
+        (dx,) = torch.autograd.grad(y, x, y.detach())
+        tail = x[-5000:].detach().clone().requires_grad_()
+        yt = K.linear(tail, w, b, act)
+        (dt,) = torch.autograd.grad(yt, tail, yt.detach())
+        # other tiles: sums in another order, rounded to the other side here and there
+        assert R.rel(y[-5000:], yt) < R.half_step(dtype) / 4
+        assert R.rel(dx[-5000:], dt) < R.half_step(dtype)

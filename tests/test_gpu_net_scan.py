@@ -115,7 +115,7 @@ def test_scan_and_gradients(batch, tokens, channels, kind, gkind):
 PACKED = [  # offsets, tokens
     ([0, 5], 5), ([0, 0, 1, 1, 9], 9), ([0, 63, 64, 65, 200], 200), ([3, 10, 10, 40], 50),
     ([0, 700, 701, 1500], 1500), ([0, 1, 2, 3, 4, 5, 6, 7, 8], 8), ([7, 7], 20),
-    ([0, 3000, 3100], 3100), (list(range(0, 1001, 10)), 1000),
+    ([0, 3000, 3100], 3100), (list(range(0, 1001, 10)), 1000), ([0, 0], 0), ([0, 0, 0, 0], 5),
 ]
 
 
@@ -324,3 +324,34 @@ def test_two_streams_at_once():
     for p, q in zip(got, want):
         for n in q:
             assert torch.equal(p[n], q[n])
+
+
+def test_more_than_2_to_the_31_elements():
+    """Tokens and channels behind the 2^31st element: the last channels of the last sequence
+    are what they are by themselves."""
+    import krylov_solvers_adjoint_amd as K
+    n, tokens, channels = 2, 8200, 131200
+    assert n * tokens * channels > 1 << 31
+    g0 = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randn(n, tokens, channels, generator=g0, device="cuda", dtype=torch.bfloat16)
+    g = -torch.rand(n, tokens, channels, generator=g0, device="cuda", dtype=torch.bfloat16)
+    xl, gl = x.requires_grad_(), g.requires_grad_()
+    h, state = K.gated_scan(xl, gl, None, True)
+    dx, dg = torch.autograd.grad((h, state), (xl, gl), (h.detach(), state.detach()))
+    part = [t[1:, :, -64:].detach().contiguous().requires_grad_() for t in (x, g)]
+    hp, sp = K.gated_scan(*part, None, True)
+    dxp, dgp = torch.autograd.grad((hp, sp), part, (hp.detach(), sp.detach()))
+    for whole, alone in ((h, hp), (dx, dxp), (dg, dgp)):
+        # the same sums joined in other places: a step of bf16 where they fall on either side
+        assert R.rel(whole[1:, :, -64:], alone) < R.half_step(torch.bfloat16) / 4
+    assert R.rel(state[1:, -64:], sp) < 64 * R.U32
+
+
+def test_tokens_far_apart_are_copied():
+    import krylov_solvers_adjoint_amd as K
+    base = torch.randn(3, (1 << 24) + 8, device="cuda")[None, :, :20]
+    gate = -torch.rand(1, 3, 20, device="cuda")
+    h, _ = K.gated_scan(base, gate)
+    assert torch.equal(h, K.gated_scan(base.contiguous(), gate)[0])
+    state = torch.zeros(3, 20, device="cuda")
+    assert torch.equal(K.gated_scan_step(base[0], gate[0], state), base[0])
