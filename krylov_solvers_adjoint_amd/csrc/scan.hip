@@ -22,6 +22,8 @@
 // Where sequences and channels do not fill the card a sequence is cut into
 // segments: k_scan_ends finds every segment's map first, the walks begin with
 // the maps of the segments on the way joined.  That reads two arrays again.
+// Packed sequences, whose lengths the host does not know, are cut by length: a
+// table on the device says which workgroup has which segment.
 #include <type_traits>
 
 #include "net.h"
@@ -56,14 +58,20 @@ struct ScanShape {
   int64_t channels;
   const int32_t* tok;            // packed: first token of each sequence [nseq + 1]
   int tiles;                     // of channels
-  int segments;
+  int segments;                  // of every sequence (no table)
+  // packed sequences of which the long ones are cut: {sequence, segment, its map's
+  // number} of up to `parts` segments of `each` blocks, sequence -1 behind the last
+  const int4* table;
+  int64_t parts, each;
   int64_t items;
 };
+constexpr int kGapItems = 8;     // workgroups (of a tile) for the tokens of no sequence
 
 // What a workgroup works on: a sequence's segment and a tile of its channels.
 struct Item {
   int64_t seq;
-  int tile, seg;
+  int tile, seg, segs;    // segs: the sequence's
+  int64_t map;            // where the segment's map lies
   int64_t from, len;      // the sequence's tokens
   int64_t first;          // its first block among all blocks
   int64_t b0, b1, blocks; // the segment's blocks, the sequence's
@@ -73,9 +81,23 @@ __device__ __forceinline__ Item item_of(const ScanShape& s, int64_t id) {
   Item w;
   w.tile = int(id % s.tiles);
   id /= s.tiles;
-  w.seg = int(id % s.segments);
-  w.seq = id / s.segments;
-  if (w.seq >= s.nseq) return w;   // the tokens of no sequence
+  const int64_t all = s.table ? s.parts : s.nseq * s.segments;
+  w.map = id;
+  if (id >= all) {   // the tokens of no sequence
+    w.seq = s.nseq;
+    w.seg = int(id - all);
+    return w;
+  }
+  if (s.table) {
+    const int4 e = s.table[id];
+    w.seq = e.x;
+    w.seg = e.y;
+    w.map = e.z;
+    if (w.seq < 0) return w;
+  } else {
+    w.seg = int(id % s.segments);
+    w.seq = id / s.segments;
+  }
   if (s.tok) {
     w.from = s.tok[w.seq];
     w.len = s.tok[w.seq + 1] - w.from;
@@ -88,18 +110,21 @@ __device__ __forceinline__ Item item_of(const ScanShape& s, int64_t id) {
   w.blocks = (w.len + BT - 1) / BT;
   // an odd number of blocks: segments that begin at multiples of a large power
   // of two would all begin in the same memory channels
-  const int64_t each = (w.blocks + s.segments - 1) / s.segments | (s.segments > 1);
+  const int64_t each =
+      s.table ? s.each : (w.blocks + s.segments - 1) / s.segments | (s.segments > 1);
+  w.segs = s.table ? int((w.blocks + each - 1) / each) : s.segments;
   w.b0 = w.seg * each < w.blocks ? w.seg * each : w.blocks;
   w.b1 = w.b0 + each < w.blocks ? w.b0 + each : w.blocks;
   return w;
 }
-// Workgroups go to the 8 XCDs in turn: each gets a run of neighbouring items,
-// whose tiles share cache lines.
+// Workgroups go to the 8 XCDs in turn: each gets runs of 16 neighbouring items,
+// whose tiles share cache lines.  (One long run each would leave the XCDs idle
+// that have the short sequences, or nothing but the tokens of none.)
 __device__ __forceinline__ int64_t item_id(int64_t items) {
+  constexpr int kRun = 16, kTurn = kRun * kXcds;
   const int64_t total = gridDim.x, b = blockIdx.x;
-  if (total < items) return b;
-  const int64_t xcd = b % kXcds, q = total / kXcds, r = total % kXcds;
-  return xcd * q + (xcd < r ? xcd : r) + b / kXcds;
+  if (total < items || b >= total / kTurn * kTurn) return b;
+  return b / kTurn * kTurn + b % kXcds * kRun + b / kXcds % kRun;
 }
 
 // A thread's place: CL lanes have the tile's channels, the others are further
@@ -241,7 +266,7 @@ __device__ __forceinline__ void clear_rows(const ScanShape& s, const Item& w, T*
   if (!me.on) return;
   constexpr int kSlices = WAVES * Place<CL, WAVES, V>::kSlices;
   for (int64_t i = int64_t(w.seg) * kSlices + threadIdx.x / CL; i < rows;
-       i += int64_t(s.segments) * kSlices) {
+       i += int64_t(kGapItems) * kSlices) {
     typename VecOf<T, V>::type z = {};
     *reinterpret_cast<typename VecOf<T, V>::type*>(
         out + (i < head ? i : tail + i - head) * s.channels + me.channel()) = z;
@@ -259,6 +284,7 @@ __global__ __launch_bounds__(WAVES* kWave, 4) void k_scan(
   int buf = 0;
   for (int64_t id = item_id(s.items); id < s.items; id += gridDim.x) {
     const Item w = item_of<BT>(s, id);
+    if (w.seq < 0) continue;
     if (w.seq >= s.nseq) {
       clear_rows<T, CL, WAVES, V>(s, w, h);
       continue;
@@ -269,7 +295,7 @@ __global__ __launch_bounds__(WAVES* kWave, 4) void k_scan(
     float carry[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) carry[v] = s0 ? s0[w.seq * s.channels + ch + v] : 0.f;
-    through<V, 1>(carry, ends + (w.seq * s.segments * s.channels + ch) * 2, s.channels * 2, w.seg);
+    through<V, 1>(carry, ends + ((w.map - w.seg) * s.channels + ch) * 2, s.channels * 2, w.seg);
     const Lane<const T, V, At> fx(x + w.from * ldx + me.tile, ldx, me);
     const Lane<const G, V, At> fg(g + w.from * ldg + me.tile, ldg, me);
     const Lane<T, V, At> fh(h + w.from * s.channels + me.tile, s.channels, me);
@@ -369,6 +395,7 @@ __global__ __launch_bounds__(WAVES* kWave) void k_scan_grad(
   int buf = 0;
   for (int64_t id = item_id(s.items); id < s.items; id += gridDim.x) {
     const Item w = item_of<BT>(s, id);
+    if (w.seq < 0) continue;
     if (w.seq >= s.nseq) {
       clear_rows<T, CL, WAVES, V>(s, w, dx);
       clear_rows<G, CL, WAVES, V>(s, w, dg);
@@ -380,9 +407,9 @@ __global__ __launch_bounds__(WAVES* kWave) void k_scan_grad(
     float carry[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) carry[v] = dlast ? dlast[w.seq * s.channels + ch + v] : 0.f;
-    through<V, -1>(carry,
-                   ends + (((w.seq + 1) * s.segments - 1) * s.channels + ch) * 2, s.channels * 2,
-                   s.segments - 1 - w.seg);
+    if (w.segs > 1)
+      through<V, -1>(carry, ends + ((w.map - w.seg + w.segs - 1) * s.channels + ch) * 2,
+                     s.channels * 2, w.segs - 1 - w.seg);
     const Lane<const T, V, At> fx(x + w.from * ldx + me.tile, ldx, me);
     const Lane<const G, V, At> fg(g + w.from * ldg + me.tile, ldg, me);
     const Lane<const T, V, At> fd(dh + w.from * lddh + me.tile, lddh, me);
@@ -515,7 +542,7 @@ __global__ __launch_bounds__(WAVES* kWave) void k_scan_ends(
   __shared__ float2 agg[WAVES][CL * V];
   for (int64_t id = item_id(s.items); id < s.items; id += gridDim.x) {
     const Item w = item_of<BT>(s, id);
-    if (w.seq >= s.nseq) continue;
+    if (w.seq < 0 || w.seq >= s.nseq || w.segs < 2) continue;
     const At me(w.tile, s.channels);
     const int64_t end = w.b1 * BT < w.len ? w.b1 * BT : w.len;
     const int64_t begin = w.b0 * BT < end ? w.b0 * BT : end;
@@ -560,7 +587,7 @@ __global__ __launch_bounds__(WAVES* kWave) void k_scan_ends(
     }
     __syncthreads();
     if (me.on && me.wave == 0 && me.slice == 0) {
-      float* e = ends + ((w.seq * s.segments + w.seg) * s.channels + me.channel()) * 2;
+      float* e = ends + (w.map * s.channels + me.channel()) * 2;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         float p = 1.f, q = 0.f;
@@ -580,22 +607,65 @@ __global__ __launch_bounds__(WAVES* kWave) void k_scan_ends(
 // The sequences' first tokens from the caller's offsets: each is the largest
 // of its predecessors and itself, clamped (they are on the device and cannot
 // be refused here), so that no kernel leaves the arrays.
-__global__ __launch_bounds__(kWave) void k_scan_plan(const int32_t* __restrict__ cu, int64_t nseq,
-                                                     int64_t total, int32_t* __restrict__ tok) {
-  int carry = 0;
-  for (int64_t b = 0; b <= nseq; b += kWave) {
+// With a table the segments of up to `each` blocks of BT tokens follow.
+constexpr int kPlanBlock = 1024;
+__global__ __launch_bounds__(kPlanBlock) void k_scan_plan(const int32_t* __restrict__ cu,
+                                                          int64_t nseq, int64_t total,
+                                                          int32_t* __restrict__ tok,
+                                                          int64_t block_tokens, int64_t each,
+                                                          int4* __restrict__ table,
+                                                          int64_t parts) {
+  constexpr int kWaves = kPlanBlock / kWave;
+  __shared__ int tops[kWaves];
+  __shared__ int2 sums[kWaves];
+  const int lane = threadIdx.x % kWave, w = threadIdx.x / kWave;
+  int carry = 0;          // the largest offset so far
+  int64_t used = 0, maps = 0;   // entries so far, maps of cut sequences
+  for (int64_t b = 0; b <= nseq; b += kPlanBlock) {
     const int64_t i = b + threadIdx.x;
     int v = i <= nseq ? cu[i] : 0;
     v = v < 0 ? 0 : (v > total ? int(total) : v);
 #pragma unroll
     for (int d = 1; d < kWave; d <<= 1) {
       const int u = __shfl_up(v, d, kWave);
-      if (int(threadIdx.x) >= d && u > v) v = u;
+      if (lane >= d && u > v) v = u;
     }
-    v = v > carry ? v : carry;
+    if (lane == kWave - 1) tops[w] = v;
+    __syncthreads();
+    int before = carry;
+    for (int k = 0; k < kWaves; ++k) {
+      if (k < w && tops[k] > before) before = tops[k];
+      if (tops[k] > carry) carry = tops[k];
+    }
+    v = v > before ? v : before;
     if (i <= nseq) tok[i] = v;
-    carry = __shfl(v, kWave - 1, kWave);
+    if (table) {
+      int prev = __shfl_up(v, 1, kWave);
+      if (lane == 0) prev = before;
+      const int64_t blocks = (int64_t(v) - prev + block_tokens - 1) / block_tokens;
+      const int64_t cut = (blocks + each - 1) / each;
+      const int mine = i >= 1 && i <= nseq ? int(cut < 1 ? 1 : cut) : 0;   // of sequence i - 1
+      int2 at = make_int2(mine, mine > 1 ? mine : 0);
+#pragma unroll
+      for (int d = 1; d < kWave; d <<= 1) {
+        const int p = __shfl_up(at.x, d, kWave), q = __shfl_up(at.y, d, kWave);
+        if (lane >= d) at.x += p, at.y += q;
+      }
+      if (lane == kWave - 1) sums[w] = at;
+      __syncthreads();
+      int64_t first = used + at.x - mine, map = maps + at.y - mine;
+      for (int k = 0; k < kWaves; ++k) {
+        if (k < w) first += sums[k].x, map += sums[k].y;
+        used += sums[k].x;
+        maps += sums[k].y;
+      }
+      for (int k = 0; k < mine; ++k)
+        if (first + k < parts) table[first + k] = make_int4(int(i - 1), k, int(map + k), 0);
+    }
+    __syncthreads();
   }
+  if (table)
+    for (int64_t k = used + threadIdx.x; k < parts; k += kPlanBlock) table[k] = make_int4(-1, 0, 0, 0);
 }
 
 // One token of every sequence; a thread has V channels of a row.
@@ -639,9 +709,14 @@ __global__ __launch_bounds__(256) void k_scan_step(const T* __restrict__ x, int6
 struct ScanPlan {
   int cl, waves, v, segments;
   int64_t tiles, blocks, block_tokens;   // blocks: of all sequences (packed: at most)
+  int64_t each, parts, maps;   // packed, with a table: blocks of a segment, segments and
+                               // segments of cut sequences at most
 };
+// Blocks of all packed sequences up to which the long ones are not cut: a
+// workgroup walks them in about a millisecond.
+constexpr int64_t kUncutBlocks = 1024;
 ScanPlan scan_plan(const sla_scan_dims* d) {
-  ScanPlan p;
+  ScanPlan p{};
   p.v = d->type != SLA_F32 && d->channels % 2 == 0 ? 2 : 1;
   const int64_t lanes = d->channels / p.v, n = d->sequences ? d->sequences : 1;
   const int64_t mean = div_up(d->tokens, n);
@@ -657,6 +732,18 @@ ScanPlan scan_plan(const sla_scan_dims* d) {
   s = s < blocks / 2 ? s : blocks / 2;
   p.segments = int(s < 1 ? 1 : s < kMostSegments ? s : kMostSegments);
   p.blocks = d->packed ? d->tokens / p.block_tokens + n : n * blocks;
+  if (d->packed) {
+    p.segments = 1;
+    const bool few = groups < kFill / 2;
+    int64_t each = few ? div_up(p.blocks * p.tiles, kFill) : 4 * blocks;
+    if (!few && each < 256) each = 256;
+    each = (each < 2 ? 2 : each) | 1;
+    if (p.blocks > (few ? 4 : kUncutBlocks) && each < p.blocks) {
+      p.each = each;
+      p.parts = n + p.blocks / each + 1;
+      p.maps = 2 * (p.blocks / each + 1);   // a cut sequence is longer than `each`
+    }
+  }
   return p;
 }
 
@@ -669,7 +756,8 @@ int64_t up256(int64_t n) { return div_up(n, 256) * 256; }
 
 struct ScanSizes {
   ScanPlan plan;
-  int64_t tok, kept, work;   // bytes: the offsets', all that is kept, the workspace
+  int64_t tok, kept, work;   // bytes: the offsets and the table, all that is kept, the workspace
+  int64_t table;             // where the table begins
 };
 sla_status scan_sizes(const char* who, const sla_scan_dims* d, ScanSizes& z) {
   SLA_NET_REQUIRE(d, "%s: dims is NULL", who);
@@ -692,10 +780,11 @@ sla_status scan_sizes(const char* who, const sla_scan_dims* d, ScanSizes& z) {
   const double all = double(z.plan.blocks + d->tokens + d->sequences * kMostSegments) *
                      double(d->channels);
   SLA_NET_REQUIRE(all < 1e15, "%s: too large", who);
-  z.tok = d->packed ? up256((d->sequences + 1) * 4) : 0;
+  z.table = d->packed ? up256((d->sequences + 1) * 4) : 0;
+  z.tok = z.table + up256(z.plan.parts * 16);
   z.kept = z.tok + up256(z.plan.blocks * d->channels * 4);
-  z.work = z.tok + (z.plan.segments > 1
-                        ? up256(d->sequences * z.plan.segments * d->channels * 8) : 0);
+  const int64_t maps = z.plan.segments > 1 ? d->sequences * z.plan.segments : z.plan.maps;
+  z.work = z.tok + up256(maps * d->channels * 8);
   return SLA_OK;
 }
 
@@ -723,7 +812,8 @@ sla_status with_scan(const sla_scan_dims* d, const ScanPlan& p, F&& f) {
   return wide ? width(__bf16(), float()) : width(__bf16(), __bf16());
 }
 
-ScanShape scan_shape(const sla_scan_dims* d, const ScanPlan& p, const int32_t* tok) {
+ScanShape scan_shape(const sla_scan_dims* d, const ScanSizes& z, const int32_t* tok) {
+  const ScanPlan& p = z.plan;
   ScanShape s{};
   s.nseq = d->sequences;
   s.seqlen = d->sequences && !d->packed ? d->tokens / d->sequences : 0;
@@ -732,7 +822,12 @@ ScanShape scan_shape(const sla_scan_dims* d, const ScanPlan& p, const int32_t* t
   s.tok = tok;
   s.tiles = int(p.tiles);
   s.segments = p.segments;
-  s.items = (s.nseq + (tok ? 1 : 0)) * p.tiles * p.segments;
+  if (p.parts) {
+    s.table = (const int4*)((const char*)tok + z.table);
+    s.parts = p.parts;
+    s.each = p.each;
+  }
+  s.items = ((p.parts ? p.parts : s.nseq * p.segments) + (tok ? kGapItems : 0)) * p.tiles;
   return s;
 }
 int scan_grid(const ScanShape& s) { return int(s.items < kMostGroups ? s.items : kMostGroups); }
@@ -781,15 +876,17 @@ sla_status sla_gated_scan(const sla_scan_dims* dims, const void* x, int64_t ldx,
   float* states = kept ? (float*)((char*)kept + z.tok) : nullptr;
   float* ends = (float*)((char*)work + z.tok);
   if (tok) {
-    k_scan_plan<<<1, kWave, 0, stream>>>(offsets, dims->sequences, dims->tokens, tok);
+    k_scan_plan<<<1, kPlanBlock, 0, stream>>>(
+        offsets, dims->sequences, dims->tokens, tok, z.plan.block_tokens, z.plan.each,
+        z.plan.parts ? (int4*)((char*)tok + z.table) : nullptr, z.plan.parts);
     LAUNCH_CHECK();
   }
-  const ScanShape s = scan_shape(dims, z.plan, tok);
+  const ScanShape s = scan_shape(dims, z, tok);
   return with_scan(dims, z.plan, [&](auto te, auto ge, auto cl, auto waves, auto v) -> sla_status {
     using T = decltype(te);
     using G = decltype(ge);
     const int grid = scan_grid(s);
-    if (s.segments > 1) {
+    if (s.segments > 1 || s.table) {
       k_scan_ends<T, G, cl.value, waves.value, v.value, false>
           <<<grid, waves.value * kWave, 0, stream>>>(s, (const T*)x, ldx, (const G*)g, ldg, ends);
       LAUNCH_CHECK();
@@ -825,12 +922,12 @@ sla_status sla_gated_scan_grad(const sla_scan_dims* dims, const void* x, int64_t
   const int32_t* tok = dims->packed ? (const int32_t*)kept : nullptr;
   const float* states = (const float*)((const char*)kept + z.tok);
   float* ends = (float*)((char*)work + z.tok);
-  const ScanShape s = scan_shape(dims, z.plan, tok);
+  const ScanShape s = scan_shape(dims, z, tok);
   return with_scan(dims, z.plan, [&](auto te, auto ge, auto cl, auto waves, auto v) -> sla_status {
     using T = decltype(te);
     using G = decltype(ge);
     const int grid = scan_grid(s);
-    if (s.segments > 1) {
+    if (s.segments > 1 || s.table) {
       k_scan_ends<T, G, cl.value, waves.value, v.value, true>
           <<<grid, waves.value * kWave, 0, stream>>>(s, (const T*)dh, lddh, (const G*)g, ldg,
                                                      ends);

@@ -138,12 +138,53 @@ def test_packed_sequences(edges, tokens, kind, gkind, channels):
         assert not outs[0][n][0, :edges[0]].any() and not outs[0][n][0, edges[-1]:].any()
 
 
+def long_among_short(n, long, short):
+    edges = [0]
+    for i in range(n):
+        edges.append(edges[-1] + (long if i == n // 2 else i % (2 * short)))
+    return edges
+
+
+@pytest.mark.parametrize("n, long, short, channels", [
+    (5, 9000, 30, 24), (2000, 24000, 20, 16), (300, 20000, 200, 130), (1, 5000, 1, 64),
+    (40, 5000, 400, 500)])
+@pytest.mark.parametrize("kind, gkind", [("fp32", "fp32"), ("bf16", "bf16")])
+def test_one_long_sequence_among_short_ones(n, long, short, channels, kind, gkind):
+    """Long sequences of a packed call are cut; the whole against the sequence by itself, whose
+    sums are joined in other places (bounds of the recurrence in 64 bits, on the GPU)."""
+    edges = long_among_short(n, long, short)
+    tokens = edges[-1] + 3
+    args = inputs(1, tokens, channels, R.TYPES[kind], R.TYPES[gkind], n)
+    got = run(*args, cu=torch.tensor(edges, dtype=torch.int32).cuda())
+    x, g, s0, dh, ds = (t.cuda().double() for t in args)
+    for i in sorted({0, n // 2, n // 3, n - 1}):
+        a, b = edges[i], edges[i + 1]
+        parts = [t[0, a:b].contiguous() for t in (x, g)] + [s0[i], dh[0, a:b], ds[i]]
+        want = one(*parts)
+        for name in want:
+            t = got[name][i] if name in ("state", "ds0") else got[name][0, a:b]
+            close(t, [v.cpu() for v in want[name]], (name, i))
+    for name in ("h", "dx", "dg"):
+        assert not got[name][0, edges[-1]:].any()
+
+
 def test_offsets_on_the_device_are_raised_and_clamped():
     import krylov_solvers_adjoint_amd as K
     x, g, s0, dh, ds = inputs(1, 100, 12, torch.float32, torch.float32, 4)
     bad = torch.tensor([-5, 40, 20, 90, 1000], dtype=torch.int32)
     good = [0, 40, 40, 90, 100]
     got, want = run(x, g, s0, dh, ds, bad.cuda()), run(x, g, s0, dh, ds, good)
+    for n in want:
+        assert torch.equal(got[n], want[n]), n
+    # more sequences than a workgroup has threads, some of them cut
+    edges = torch.tensor(long_among_short(3000, 20000, 10))
+    total = int(edges[-1])
+    args = inputs(1, total, 8, torch.float32, torch.float32, 3000)
+    bad = edges.clone()
+    bad[1700:1720] = -7
+    bad[-3:] = total + 1000
+    good = torch.cummax(bad.clamp(0, total), 0).values
+    got, want = run(*args, bad.int().cuda()), run(*args, good.int().cuda())
     for n in want:
         assert torch.equal(got[n], want[n]), n
     for cu in ([0, 5, 3, 100], [0, 101], [-1, 100]):
