@@ -16,7 +16,7 @@
 // square), and lo's last bit lies 2^-36, 2^-34 and 2^-32 below one.
 //
 // Planes are padded to multiples of 32 with zeros, which every product keeps.
-#include "product.h"
+#include "mfma.h"
 
 namespace sla {
 namespace net {
@@ -620,7 +620,6 @@ __global__ __launch_bounds__(kSmallBlock) void k_ortho_small(const T* __restrict
       const int tile = w + 16 * n, i = tile / (S / 16), j = tile % (S / 16);
       f32x4 acc[3] = {};
       if (i < squares && j < squares)
-#pragma unroll 4
         for (int k = 0; k < 16 * tiles; k += 32) {
           Vec a[2], b[2];
 #pragma unroll
@@ -639,7 +638,6 @@ __global__ __launch_bounds__(kSmallBlock) void k_ortho_small(const T* __restrict
       const int tile = w + 16 * n, i = tile / (S / 16), j = tile % (S / 16);
       f32x4 acc[3] = {};
       if (i < squares && j < squares)
-#pragma unroll 2
         for (int k = 0; k < ks; k += 32) {
           Vec a[2], b[2];
 #pragma unroll
@@ -668,7 +666,6 @@ __global__ __launch_bounds__(kSmallBlock) void k_ortho_small(const T* __restrict
       const int tile = w + 16 * n, i = tile % (S / 16), j = tile / (S / 16);
       f32x4 acc[3] = {};
       if (i < squares && j < tiles)
-#pragma unroll 2
         for (int k = 0; k < ks; k += 32) {
           Vec a[2], b[2];
 #pragma unroll
