@@ -16,8 +16,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libsla.so")
 SOURCES = ["api.hip", "csr_build.hip", "cg.hip", "lanczos.hip", "bicgstab.hip", "reorder.hip",
-           "noalloc.hip", "norm.hip", "ffn.hip", "delta.hip", "linear.hip", "scan.hip",
-           "ortho.hip"]
+           "noalloc.hip", "norm.hip", "ffn.hip", "delta.hip", "linear.hip", "linear_narrow.hip",
+           "scan.hip", "ortho.hip"]
 ARCH = os.environ.get("SLA_OFFLOAD_ARCH", "gfx950")
 
 HIPCC_FLAGS = [
@@ -53,7 +53,7 @@ def build(verbose: bool = True) -> str:
             print(" ".join(cmd), flush=True)
         subprocess.run(cmd, check=True)
 
-    with ThreadPoolExecutor(min(4, os.cpu_count() or 1)) as pool:
+    with ThreadPoolExecutor(min(6, os.cpu_count() or 1)) as pool:
         list(pool.map(compile_one, SOURCES, objs))
     tmp = LIB + ".tmp"
     cmd = [hipcc(), "-shared", "-fPIC", f"--offload-arch={ARCH}", *objs, "-o", tmp]

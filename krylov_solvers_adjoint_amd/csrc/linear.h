@@ -1,0 +1,39 @@
+// The projection's gradients in one pass over x and dy, for narrow projections of
+// many rows (linear_narrow.hip).
+#pragma once
+
+#include "net.h"
+
+namespace sla {
+namespace net {
+
+struct NarrowGrad {
+  const void *x, *dy, *w, *bias;   // the weight and bias as sla_linear takes them
+  int64_t ldx, lddy, rows;
+  int inner, outer, bias_f32, act, want_w;
+  const float* scale;
+  void* dx;
+  void *dw, *db;   // may be none, each
+  float* part;     // the workgroups' sums; none if neither dw nor db is wanted
+};
+
+// Where one pass pays: the tiles of the general products read x and dy three
+// times.
+constexpr int64_t kNarrow = 64, kNarrowRows = 4096;
+constexpr int kNarrowGroups = 512;
+inline bool narrow(int64_t rows, int64_t inner, int64_t outer) {
+  return inner <= kNarrow && outer <= kNarrow && rows >= kNarrowRows;
+}
+inline int narrow_pad(int64_t n) { return n <= 32 ? 32 : 64; }
+inline int narrow_groups(int64_t rows) {
+  const int64_t n = div_up(rows, 128);
+  return int(n < kNarrowGroups ? n : kNarrowGroups);
+}
+inline int64_t narrow_bytes(int64_t rows, int64_t inner, int64_t outer) {
+  const int64_t np = narrow_pad(outer), kp = narrow_pad(inner);
+  return narrow_groups(rows) * (np * kp + np) * 4;
+}
+sla_status launch_narrow(const NarrowGrad& g, sla_type type, hipStream_t stream);
+
+}  // namespace net
+}  // namespace sla
