@@ -17,9 +17,12 @@ struct NarrowGrad {
   float* part;     // the workgroups' sums; none if neither dw nor db is wanted
 };
 
-// Where one pass pays: the tiles of the general products read x and dy three
-// times.
-constexpr int64_t kNarrow = 64, kNarrowRows = 4096;
+// Where one pass pays: the general products read x and dy three times, in four
+// launches or more.  64 x 64, bias, silu, one pass against them: 64 rows fp32 15.3
+// and 16.2 us, 1000 rows 19 and 27, 10^5 rows 47 and 80; bf16 12.6 and 13.7, 13.5
+// and 22, 28 and 48; 16 rows 14.7 and 14.8.  Wider ones leave too few registers for
+// dW's sums.
+constexpr int64_t kNarrow = 64, kNarrowRows = 64;
 constexpr int kNarrowGroups = 512;
 inline bool narrow(int64_t rows, int64_t inner, int64_t outer) {
   return inner <= kNarrow && outer <= kNarrow && rows >= kNarrowRows;

@@ -10,6 +10,12 @@
 // products that follow, which adds half a step to dx and dW; fp16's is held
 // times a power of two that the largest |dy| gives, for its range (no activation
 // is steeper than 1.13).  All sums are fp32.
+//
+// Measured: 16384 x 4096 x 1024 bf16 with a residual 124 us forward (1.1 PFLOP/s),
+// dx 135, dW 124 + 12 (two splits); 5000 x 771 x 1403 fp16 40 to 45 us a product:
+// the sizes ask for 128 tiles (440 of them, 26 us at widths that are multiples of
+// 8), whose stores of odd rows take 7 us more; padded copies of the operands
+// changed nothing.  4 x 4096 x 1024 bf16: 8 us, 64 workgroups that read 8.4 MB.
 #include "linear.h"
 #include "product.h"
 
@@ -19,7 +25,8 @@ namespace {
 
 // Column sums of dz: a team of lanes has 16 bytes a lane of a row, the other
 // teams of the workgroup and the slabs of rows take rows in turn; teams and slabs
-// are joined in order.
+// are joined in order.  10^6 x 64 fp32: 40 us (6.4 TB/s); lanes of one row a wave
+// had left 48 of 64 idle, 312 us.
 constexpr int kColumnSlabs = 512;
 template <typename T, int TEAM>
 __global__ __launch_bounds__(256) void k_column_sums(const T* __restrict__ dz, int64_t ld,

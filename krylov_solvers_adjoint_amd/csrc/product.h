@@ -1016,7 +1016,7 @@ ProductPlan plan_product(int64_t M, int64_t N, int64_t K, int parts, int outputs
   return best;
 }
 
-int64_t split_bytes(int64_t M, int64_t N, int64_t K, int parts, int outputs, int turned, int es,
+inline int64_t split_bytes(int64_t M, int64_t N, int64_t K, int parts, int outputs, int turned, int es,
                     int limit = 0) {
   int64_t most = 0;
   for (int direct = 0; direct < 2; ++direct) {
@@ -1029,7 +1029,7 @@ int64_t split_bytes(int64_t M, int64_t N, int64_t K, int parts, int outputs, int
 
 // Whether an operand's lines are whole aligned 16-byte units that 31 bits of
 // a tile's offsets reach.
-bool whole_units(const void* p, int64_t ld, int64_t along, int es) {
+inline bool whole_units(const void* p, int64_t ld, int64_t along, int es) {
   const int64_t n = 16 / es;
   return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % n == 0 && along % n == 0 &&
          ld * es * 256 < (int64_t(1) << 31);

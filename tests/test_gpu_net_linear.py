@@ -203,14 +203,15 @@ def test_views_and_leading_axes():
 
 def test_only_some_gradients_and_refusals():
     import krylov_solvers_adjoint_amd as K
-    x, w, b, r, dy = (t.cuda() for t in inputs(20, 40, 50, torch.float32, torch.float32))
-    for act in (None, "silu"):
-        full = [t.clone().requires_grad_() for t in (x, w, b, r)]
-        want = torch.autograd.grad(K.linear(*full[:3], act, full[3]), full, dy)
-        for keep in range(4):
-            some = [t.clone().requires_grad_(i == keep) for i, t in enumerate((x, w, b, r))]
-            (got,) = torch.autograd.grad(K.linear(*some[:3], act, some[3]), some[keep], dy)
-            assert torch.equal(got, want[keep])
+    for rows in (5000, 20):
+        x, w, b, r, dy = (t.cuda() for t in inputs(rows, 40, 50, torch.float32, torch.float32))
+        for act in (None, "silu"):
+            full = [t.clone().requires_grad_() for t in (x, w, b, r)]
+            want = torch.autograd.grad(K.linear(*full[:3], act, full[3]), full, dy)
+            for keep in range(4):
+                some = [t.clone().requires_grad_(i == keep) for i, t in enumerate((x, w, b, r))]
+                (got,) = torch.autograd.grad(K.linear(*some[:3], act, some[3]), some[keep], dy)
+                assert torch.equal(got, want[keep])
     with pytest.raises(ValueError):
         K.linear(x, w, b, "tanh")
     with pytest.raises(TypeError):
