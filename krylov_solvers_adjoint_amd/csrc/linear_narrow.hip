@@ -147,6 +147,8 @@ __global__ __launch_bounds__(256, 2) void k_narrow_grad(NarrowGrad g) {
             activation<act.value, L::kHalf>(z[j][r], f, df);
             const float e = float(dy[i][j][r]);
             dz[i][j][r] = T(act.value == kActNone ? e : e * up * df);
+            // z of a column that does not exist is NaN where x is not finite
+            if (!WHOLE && 16 * j + 4 * h + r >= g.outer) dz[i][j][r] = T(0.f);
           }
       };
       if (g.act == SLA_ACT_SILU) make(std::integral_constant<int, SLA_ACT_SILU>());

@@ -148,6 +148,26 @@ def test_values_that_are_not_finite_stay_where_they_are():
             assert torch.equal(got[:7], want[:7]) and torch.equal(got[8:], want[8:])
 
 
+@pytest.mark.parametrize("kind", ["fp32", "fp16", "bf16"])
+@pytest.mark.parametrize("rows, inner, outer", [(300, 40, 60), (300, 64, 64), (300, 100, 60),
+                                                (20, 33, 7)])
+def test_infinite_inputs_have_the_gradients_that_they_have(rows, inner, outer, kind):
+    """relu's slope at z = inf is 1: dx of such a row is finite, whatever the sizes are padded to."""
+    import krylov_solvers_adjoint_amd as K
+    dtype = R.TYPES[kind]
+    x, w, b, r, dy = inputs(rows, inner, outer, dtype, dtype)
+    x[5, 3], x[rows - 1, inner - 1] = float("inf"), -float("inf")
+    leaves = [t.cuda().requires_grad_() for t in (x, w, b)]
+    dx, dw, db = torch.autograd.grad(K.linear(*leaves, "relu"), leaves, dy.cuda())
+    want = bounds(x.double(), w.double(), b.double(), None, dy.double(), "relu", dtype, dtype)
+    assert torch.equal(dx.isfinite().cpu(), want["dx"][0].isfinite())
+    assert torch.equal(db.isfinite().cpu(), want["db"][0].isfinite())
+    assert torch.equal(dw.isfinite().cpu(), want["dw"][0].isfinite())
+    for row in (5, rows - 1):
+        dz = dy.double()[row] * ((x.double() @ w.double().t() + b.double())[row] > 0)
+        assert R.rel(dx[row], dz @ w.double()) <= 4 * R.half_step(dtype) + 200 * R.U32
+
+
 def test_small_and_large_gradients_in_fp16():
     """dz of fp16 keeps its digits where dy is near the ends of the range."""
     import krylov_solvers_adjoint_amd as K
