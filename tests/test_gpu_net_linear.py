@@ -27,7 +27,7 @@ CASES = [  # rows, inner, outer
     (130, 33, 67), (65, 515, 140), (257, 128, 256), (300, 72, 200), (16, 2048, 128), (17, 64, 96),
     (0, 32, 48), (512, 256, 384), (64, 1500, 33), (5000, 16, 24), (90, 4096, 72),
     (4096, 64, 64), (4097, 5, 64), (4110, 64, 1), (6001, 33, 17), (4500, 32, 32), (20011, 61, 50),
-    (5001, 64, 32), (4200, 128, 64), (4111, 100, 64), (4097, 64, 128), (5005, 13, 99),
+    (5001, 64, 32), (4300, 32, 64), (300, 9, 64), (4200, 128, 64), (4111, 100, 64), (4097, 64, 128), (5005, 13, 99),
 ]
 
 
