@@ -808,8 +808,10 @@ sla_status with_scan(const sla_scan_dims* d, const ScanPlan& p, F&& f) {
     using std::integral_constant;
     auto waves = [&](auto cl) -> sla_status {
       if (p.waves == 1) return f(te, ge, cl, integral_constant<int, 1>(), v);
-      if (p.waves == 4) return f(te, ge, cl, integral_constant<int, 4>(), v);
-      return f(te, ge, cl, integral_constant<int, 8>(), v);
+      // (eight waves: less than kFill workgroups, so the fewest lanes)
+      if constexpr (cl.value == 16)
+        if (p.waves == 8) return f(te, ge, cl, integral_constant<int, 8>(), v);
+      return f(te, ge, cl, integral_constant<int, 4>(), v);
     };
     if (p.cl == 64) return waves(integral_constant<int, 64>());
     if (p.cl == 32) return waves(integral_constant<int, 32>());

@@ -277,7 +277,7 @@ def test_against_differences():
     (5000, 771, 1403), (4096, 515, 1000), (1100, 1021, 1024), (70, 8001, 2000), (2100, 4096, 520),
     (16400, 264, 520), (300000, 96, 40), (40000, 64, 48), (16384, 512, 512)])
 @pytest.mark.parametrize("kind", ["bf16", "fp16", "fp32"])
-@pytest.mark.parametrize("act", [None, "gelu"])
+@pytest.mark.parametrize("act", [None, "silu", "gelu", "relu"])
 def test_large(rows, inner, outer, kind, act):
     """Large tiles, padded copies, split sums, one-pass gradients: against 64 bits on the GPU."""
     import krylov_solvers_adjoint_amd as K
@@ -292,9 +292,12 @@ def test_large(rows, inner, outer, kind, act):
         ref, tol = want[name]
         bad = ~((t.detach().double() - ref).abs() <= (tol + tiny) * (1 + 2 ** -6))
         assert not bad.any(), (name, int(bad.sum()))
-    # the whole: half a step of every value, and dz's rounding beside it
+    # the whole: half a step of every value, and dz's rounding beside it.  relu's gradients are
+    # left to the bounds above: where z is within its error of 0, for some 4e-7 of 8.5e6 values
+    # (density 0.4 times 1e-6), the slope may be the other one, and dz changes by all of dy:
+    # sqrt(4e-7) = 6e-4 of the norm
     u = R.half_step(dtype)
-    for name, t in zip(("y", "dx", "dw", "db"), got):
+    for name, t in zip(("y", "dx", "dw", "db"), got[:1] if act == "relu" else got):
         assert R.rel(t, want[name][0]) <= 1.5 * u + 200 * R.U32, name
     again = torch.autograd.grad(K.linear(*leaves[:3], act, leaves[3]), leaves, dy)
     for p, q in zip(got[1:], again):

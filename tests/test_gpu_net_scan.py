@@ -112,6 +112,27 @@ def test_scan_and_gradients(batch, tokens, channels, kind, gkind):
         assert torch.equal(got["state"].cpu(), args[2]) and torch.equal(got["ds0"].cpu(), args[4])
 
 
+@pytest.mark.parametrize("batch, tokens, channels", [
+    (600, 10, 64), (600, 70, 128), (300, 20, 128), (300, 130, 64), (80, 300, 128), (130, 200, 128),
+    (300, 40, 65), (90, 290, 47)])
+@pytest.mark.parametrize("kind, gkind", KINDS)
+def test_many_sequences(batch, tokens, channels, kind, gkind):
+    """Workgroups of every width and number of waves (all sequences side by side in 64 bits)."""
+    args = inputs(batch, tokens, channels, R.TYPES[kind], R.TYPES[gkind])
+    got = run(*args)
+    x, g, s0, dh, ds = (t.double() for t in args)
+
+    def beside(t):
+        return t.transpose(0, 1).reshape(tokens, batch * channels)
+    want = one(beside(x), beside(g), s0.reshape(-1), beside(dh), ds.reshape(-1))
+    for n, parts in want.items():
+        shape = (batch, channels) if n in ("state", "ds0") else (tokens, batch, channels)
+        parts = [p.reshape(shape) for p in parts]
+        if len(shape) == 3:
+            parts = [p.transpose(0, 1) for p in parts]
+        close(got[n], parts, n)
+
+
 PACKED = [  # offsets, tokens
     ([0, 5], 5), ([0, 0, 1, 1, 9], 9), ([0, 63, 64, 65, 200], 200), ([3, 10, 10, 40], 50),
     ([0, 700, 701, 1500], 1500), ([0, 1, 2, 3, 4, 5, 6, 7, 8], 8), ([7, 7], 20),
