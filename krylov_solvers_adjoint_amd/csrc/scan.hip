@@ -44,8 +44,9 @@ constexpr int kFill = 512;     // workgroups wanted: two on each of the 256 CUs
 constexpr int64_t kMostGroups = int64_t(1) << 20;   // of a launch; they walk the items
 
 // exp(g).  fp32 gates: to 2 ulp, the instruction's exp2 with the product's
-// rounding error put right; below -200 and above 200 it is 0 and inf as it is; NaN
-// stays.  16-bit gates: without that, off by |g| 2^-23.5 of itself, far below
+// rounding error put right; below -200 and above 200 it is 0 and inf as it is, and
+// where exp2 has left the range nothing is put right (inf with an error of 0 or below
+// would be NaN); NaN stays.  16-bit gates: without that, off by |g| 2^-23.5 of itself, far below
 // their own half step (and a |g| is 0.4 at most, so the state is as good).
 template <typename G>
 __device__ __forceinline__ float decay(G gate) {
@@ -56,7 +57,7 @@ __device__ __forceinline__ float decay(G gate) {
   const float t = g * kHi;
   const float r = __builtin_fmaf(g, kLo, __builtin_fmaf(g, kHi, -t));
   const float e = __builtin_amdgcn_exp2f(t);
-  return __builtin_fmaf(e, r * 0.693147182f, e);
+  return e == __builtin_inff() ? e : __builtin_fmaf(e, r * 0.693147182f, e);
 }
 
 struct ScanShape {
