@@ -41,7 +41,11 @@ __device__ __forceinline__ typename VecOf<T, N>::type some(const T* p, int have)
   for (int j = 0; j < N; ++j) v[j] = j < have ? p[j] : T(0.f);
   return v;
 }
-template <typename T, int NP, int KP, bool WHOLE>
+// SLOPE: there is an activation.  A kernel of its own for dz = dy: as a fourth way
+// of the branch over the activations, one that hands dy's registers on untouched, it
+// has made the compiler (-O3) leave out the copies to dz on one of the two edges that
+// lead to it (seen in the assembly of a 64 x 64 fp16 kernel, whose dx was wrong).
+template <typename T, int NP, int KP, bool WHOLE, bool SLOPE>
 __global__ __launch_bounds__(256, 2) void k_narrow_grad(NarrowGrad g) {
   typedef Narrow<T, NP, KP> L;
   typedef typename Unit<T>::Vec Vec;
@@ -54,8 +58,7 @@ __global__ __launch_bounds__(256, 2) void k_narrow_grad(NarrowGrad g) {
   T* const tz = (T*)(smem + 2 * L::kWeight + w * L::kTurn);
   T* const tx = tz + L::kRows * L::kLineN;
   const T* W = (const T*)g.w;
-  const bool slope = g.act != SLA_ACT_NONE;
-  for (int i = w; i < NJ * KS; i += 4) {
+  for (int i = w; SLOPE && i < NJ * KS; i += 4) {
     const int n = i / KS * 16 + l, k = i % KS * L::kUnit + h * kN;
     Vec v;
 #pragma unroll
@@ -75,7 +78,7 @@ __global__ __launch_bounds__(256, 2) void k_narrow_grad(NarrowGrad g) {
   }
   f32x4 bias[NJ];
   Product p{};
-  p.bias = slope ? g.bias : nullptr;
+  p.bias = SLOPE ? g.bias : nullptr;
   p.bias_f32 = g.bias_f32;
 #pragma unroll
   for (int j = 0; j < NJ; ++j) bias[j] = bias_of<T>(p, 16 * j + 4 * h, g.outer - 16 * j - 4 * h);
@@ -127,9 +130,9 @@ __global__ __launch_bounds__(256, 2) void k_narrow_grad(NarrowGrad g) {
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
       f32x4 z[NJ];
+      if constexpr (SLOPE) {
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) z[j] = bias[j];
-      if (slope) {
+        for (int j = 0; j < NJ; ++j) z[j] = bias[j];
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
           Vec b[NJ];
@@ -143,18 +146,21 @@ __global__ __launch_bounds__(256, 2) void k_narrow_grad(NarrowGrad g) {
         for (int j = 0; j < NJ; ++j)
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            float f, df;
-            activation<act.value, L::kHalf>(z[j][r], f, df);
-            const float e = float(dy[i][j][r]);
-            dz[i][j][r] = T(act.value == kActNone ? e : e * up * df);
+            float v = float(dy[i][j][r]);
+            if constexpr (act.value != kActNone) {
+              float f, df;
+              activation<act.value, L::kHalf>(z[j][r], f, df);
+              v = v * up * df;
+            }
             // z of a column that does not exist is NaN where x is not finite
-            if (!WHOLE && 16 * j + 4 * h + r >= g.outer) dz[i][j][r] = T(0.f);
+            if (!WHOLE && 16 * j + 4 * h + r >= g.outer) v = 0.f;
+            dz[i][j][r] = T(v);
           }
       };
-      if (g.act == SLA_ACT_SILU) make(std::integral_constant<int, SLA_ACT_SILU>());
+      if constexpr (!SLOPE) make(std::integral_constant<int, kActNone>());
+      else if (g.act == SLA_ACT_SILU) make(std::integral_constant<int, SLA_ACT_SILU>());
       else if (g.act == SLA_ACT_GELU) make(std::integral_constant<int, SLA_ACT_GELU>());
-      else if (g.act == SLA_ACT_RELU) make(std::integral_constant<int, SLA_ACT_RELU>());
-      else make(std::integral_constant<int, kActNone>());
+      else make(std::integral_constant<int, SLA_ACT_RELU>());
 #pragma unroll
       for (int j = 0; j < NJ; ++j)
 #pragma unroll
@@ -285,8 +291,11 @@ __global__ __launch_bounds__(kWave* kJoinLines) void k_narrow_join(
 template <typename T, int NP, int KP>
 sla_status start_narrow(const NarrowGrad& g, hipStream_t stream) {
   constexpr int lds = Narrow<T, NP, KP>::kBytes;
-  const bool whole = g.outer == NP && g.inner == KP;
-  auto* kernel = whole ? k_narrow_grad<T, NP, KP, true> : k_narrow_grad<T, NP, KP, false>;
+  const bool whole = g.outer == NP && g.inner == KP, slope = g.act != SLA_ACT_NONE;
+  auto* kernel = whole ? (slope ? k_narrow_grad<T, NP, KP, true, true>
+                                : k_narrow_grad<T, NP, KP, true, false>)
+                       : (slope ? k_narrow_grad<T, NP, KP, false, true>
+                                : k_narrow_grad<T, NP, KP, false, false>);
   SLA_TRY_HIP(hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
                                   hipFuncAttributeMaxDynamicSharedMemorySize, lds));
   kernel<<<narrow_groups(g.rows), 256, lds, stream>>>(g);
