@@ -155,16 +155,15 @@ __global__ __launch_bounds__(256, 2) void k_narrow_grad(NarrowGrad g) {
             // z of a column that does not exist is NaN where x is not finite
             if (!WHOLE && 16 * j + 4 * h + r >= g.outer) v = 0.f;
             dz[i][j][r] = T(v);
+            db[j][r] += v;   // (not rounded to T)
+            // summed here: behind the branch all of v would have to wait in registers
+            asm volatile("" : "+v"(db[j][r]));
           }
       };
       if constexpr (!SLOPE) make(std::integral_constant<int, kActNone>());
       else if (g.act == SLA_ACT_SILU) make(std::integral_constant<int, SLA_ACT_SILU>());
       else if (g.act == SLA_ACT_GELU) make(std::integral_constant<int, SLA_ACT_GELU>());
       else make(std::integral_constant<int, SLA_ACT_RELU>());
-#pragma unroll
-      for (int j = 0; j < NJ; ++j)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) db[j][r] += float(dz[i][j][r]);
     }
     if (g.want_w) {   // turned by way of LDS (the wave's own: no barrier)
 #pragma unroll

@@ -6,6 +6,7 @@ import pytest
 import torch
 
 import net_refs as R
+import test_gpu_net_linear as L
 
 pytestmark = pytest.mark.gpu
 
@@ -42,3 +43,37 @@ def test_a_gate_whose_exp_leaves_the_range_gives_infinity(kind, gkind):
     nan = torch.full((1, n), math.nan, dtype=gtype).cuda()
     K.gated_scan_step(zero, nan, state)
     assert state.isnan().all()
+
+
+# ---------------------------------------------------------------------------
+# The bias's gradient
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("rows, inner, outer", [(64, 32, 32), (65, 64, 64), (300, 9, 64),
+                                                (130, 61, 50), (100, 33, 17), (257, 64, 32),
+                                                (4096, 64, 64)])
+@pytest.mark.parametrize("kind", ["fp16", "bf16"])
+@pytest.mark.parametrize("act", ["silu", "gelu", "relu"])
+def test_a_wide_bias_gradient_of_narrow_projections_is_summed_unrounded(rows, inner, outer, kind,
+                                                                        act):
+    """A bias in fp32 has a gradient whose terms were never rounded to 16 bits: the linear tests'
+    bound of db without u |dz|."""
+    import krylov_solvers_adjoint_amd as K
+    dtype = R.TYPES[kind]
+    x, w, b, r, dy = L.inputs(rows, inner, outer, dtype, torch.float32)
+    leaves = [t.cuda().requires_grad_() for t in (x, w, b)]
+    db = torch.autograd.grad(K.linear(*leaves, act), leaves, dy.cuda())[2]
+    x, w, b, dy = (t.double() for t in (x, w, b, dy))
+    z = x @ w.t() + b
+    ez = (inner + 3) * R.U32 * (x.abs() @ w.abs().t() + b.abs())
+    z.requires_grad_()
+    (slope,) = torch.autograd.grad(R.activation(z, act).sum(), z)
+    z = z.detach()
+    near = 16 * R.U32 * (z.abs() + 1) + (1.2e-5 * (z.abs() + 1) if act == "gelu" else 0)
+    jump = (z.abs() <= ez).double() if act == "relu" else ez
+    dz = dy * slope
+    tol = R.U32 * dz.sum(0).abs() + (dy.abs() * (jump + near)).sum(0) \
+        + (rows + 2) * R.U32 * dz.abs().sum(0)
+    if act == "relu":   # the slopes are exact: fp32's sums are all that is rounded
+        tol = R.U32 * dz.sum(0).abs() + (dy.abs() * jump).sum(0) \
+            + (rows + 2) * R.U32 * dz.abs().sum(0)
+    L.close(db, dz.sum(0), tol, "db")
