@@ -140,7 +140,8 @@ struct LinearSizes {
 LinearSizes linear_sizes(int64_t rows, int64_t inner, int64_t outer, sla_type type, int act) {
   const int es = int(type_size(type));
   LinearSizes z{};
-  z.forward = split_bytes(rows, outer, inner, 1, 1, 0, es);
+  // (few rows: one launch that keeps its sums on the chip)
+  z.forward = rows <= kFewRows ? 0 : split_bytes(rows, outer, inner, 1, 1, 0, es);
   z.scale = act != SLA_ACT_NONE && type == SLA_F16 ? 256 + up256(kBoundGroups * 12) : 0;
   if (narrow(rows, inner, outer)) {
     z.sums = narrow_bytes(rows, inner, outer);
