@@ -864,13 +864,15 @@ __global__ __launch_bounds__(kWave) void k_scale(const float* __restrict__ parts
 // The projections of few rows (at most 16 RT): reading the weights is the
 // work.  A workgroup has 16 columns of each weight; its waves take turns
 // along k, fragments straight from memory, and are joined through LDS.  4 x
-// 1024 x 2 x 4096 bf16: 5.2 us (16.8 MB), against 36 us with tiles of 128.
-template <typename T, int RT, int EPI, int WAVES>
-__global__ __launch_bounds__(kWave* WAVES) void k_few(Product g) {
+// 1024 x 2 x 4096 bf16: 5.2 us (16.8 MB), against 36 us with tiles of 128; 4 x 4096 x
+// 1024 with one weight 8.0 us (8.4 MB), 64 workgroups (of 16 waves each: 8.4).
+constexpr int kFewWaves = 4;
+template <typename T, int RT, int EPI>
+__global__ __launch_bounds__(kWave* kFewWaves) void k_few(Product g) {
   constexpr int NB = two_weights(EPI) ? 2 : 1;
   typedef typename Unit<T>::Vec Vec;
   constexpr int kN = Unit<T>::kN, kSpan = 4 * kN;   // k of one fragment
-  __shared__ f32x4 sums[WAVES][RT][NB][kWave];
+  __shared__ f32x4 sums[kFewWaves][RT][NB][kWave];
   const int t = threadIdx.x, w = t / kWave, l = t % 16, h = t % kWave / 16;
   const int64_t n0 = int64_t(blockIdx.x) * 16;
   auto line = [](const void* p, int64_t ld, int64_t row, int64_t rows) {
@@ -917,7 +919,7 @@ __global__ __launch_bounds__(kWave* WAVES) void k_few(Product g) {
         if constexpr (NB == 2) mma16(acc[i][1], x[s][i], u[s][1]);
       }
   };
-  constexpr int kStep = 2 * kSpan, kTurn = WAVES * kStep;
+  constexpr int kStep = 2 * kSpan, kTurn = kFewWaves * kStep;
   int k = kStep * w;
   for (; k + 3 * kTurn + kStep <= K; k += 4 * kTurn) {  // four turns' loads travel at once
     Vec u[4][2][NB], x[4][2][RT];
@@ -938,20 +940,14 @@ __global__ __launch_bounds__(kWave* WAVES) void k_few(Product g) {
     if constexpr (NB == 2) sums[w][i][1][t % kWave] = acc[i][1];
   }
   __syncthreads();
-  for (int i = w; i < RT; i += WAVES) {
+  for (int i = w; i < RT; i += kFewWaves) {
     const int64_t row = 16 * i + l, col = n0 + 4 * h;
     if (row >= g.M || col >= g.N) continue;
     f32x4 s[2];
 #pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      s[b] = f32x4{0, 0, 0, 0};
-#pragma unroll
-      for (int k = 0; k < WAVES; k += 4) {
-        const f32x4 q = (sums[k][i][b][t % kWave] + sums[k + 1][i][b][t % kWave]) +
-                        (sums[k + 2][i][b][t % kWave] + sums[k + 3][i][b][t % kWave]);
-        s[b] = k ? s[b] + q : q;
-      }
-    }
+    for (int b = 0; b < NB; ++b)
+      s[b] = (sums[0][i][b][t % kWave] + sums[1][i][b][t % kWave]) +
+             (sums[2][i][b][t % kWave] + sums[3][i][b][t % kWave]);
     if constexpr (NB == 1) s[1] = bias_of<T>(g, col, g.N - col);
     float d[4] = {0.f, 0.f, 0.f, 0.f};
     if (takes_d(EPI) && (EPI != EPI_LINEAR || g.dh))
@@ -1055,18 +1051,12 @@ sla_status run_product(Product& g, hipStream_t stream) {
 }
 
 constexpr int64_t kFewRows = 64;
-// Four waves where the columns fill the card with workgroups; 16 along k where
-// they do not.
-template <typename T, int EPI, int WAVES>
-void start_few(const Product& g, hipStream_t stream) {
-  const int grid = int(div_up(g.N, 16));
-  if (g.M <= 16) k_few<T, 1, EPI, WAVES><<<grid, kWave * WAVES, 0, stream>>>(g);
-  else if (g.M <= 32) k_few<T, 2, EPI, WAVES><<<grid, kWave * WAVES, 0, stream>>>(g);
-  else k_few<T, 4, EPI, WAVES><<<grid, kWave * WAVES, 0, stream>>>(g);
-}
 template <typename T, int EPI>
 sla_status launch_few(const Product& g, hipStream_t stream) {
-  start_few<T, EPI, 4>(g, stream);
+  const int grid = int(div_up(g.N, 16));
+  if (g.M <= 16) k_few<T, 1, EPI><<<grid, kWave * kFewWaves, 0, stream>>>(g);
+  else if (g.M <= 32) k_few<T, 2, EPI><<<grid, kWave * kFewWaves, 0, stream>>>(g);
+  else k_few<T, 4, EPI><<<grid, kWave * kFewWaves, 0, stream>>>(g);
   LAUNCH_CHECK();
   return SLA_OK;
 }
