@@ -749,8 +749,8 @@ sla_status sla_delta_step(const sla_delta_dims* dims, const void* q, int64_t ldq
  * A projection with its epilogue: y = residual + f(x weight^T + bias), x
  * [rows][inner], weight [outer][inner] contiguous, y [rows][outer].  bias
  * [outer] (of btype: x's type or SLA_F32) and residual [rows][outer] may be
- * NULL (zero); act: SLA_ACT_*, of which SLA_ACT_NONE is f(z) = z.  rows is
- * below 2^31, inner and outer below 2^22.
+ * NULL (zero); act: SLA_ACT_*, of which SLA_ACT_NONE is f(z) = z.  rows is at
+ * most 2^31 - 128, inner and outer are below 2^22.
  */
 enum { SLA_ACT_NONE = 3 };
 sla_status sla_linear(const void* x, int64_t ldx, const void* weight, const void* bias,

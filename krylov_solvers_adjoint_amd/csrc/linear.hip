@@ -120,7 +120,8 @@ sla_status linear_args(const char* who, int64_t rows, int64_t inner, int64_t out
                   "%s: unknown or mixed types", who);
   SLA_NET_REQUIRE(act == SLA_ACT_SILU || act == SLA_ACT_GELU || act == SLA_ACT_RELU ||
                       act == SLA_ACT_NONE, "%s: unknown activation", who);
-  SLA_NET_REQUIRE(rows >= 0 && rows < (int64_t(1) << 31), "%s: rows out of range", who);
+  // more would be 2^32 threads in tiles of 128 rows
+  SLA_NET_REQUIRE(rows >= 0 && rows <= (int64_t(1) << 31) - 128, "%s: rows out of range", who);
   SLA_NET_REQUIRE(inner >= 1 && inner < (int64_t(1) << 22) && outer >= 1 &&
                       outer < (int64_t(1) << 22), "%s: inner or outer out of range", who);
   SLA_NET_REQUIRE(ldx >= inner, "%s: row stride below inner", who);
