@@ -779,9 +779,13 @@ sla_status sla_linear_grad(const void* dy, int64_t lddy, const void* x, int64_t 
  *   h <- exp(g_t) h + x_t
  * and leaves it rounded to x's type.  x, g and h [tokens][channels]; g is of
  * gate_type: x's type or SLA_F32.  g <= 0 (a decay) is the meant range, down to
- * -infinity (the state begins anew); growth within a block of tokens (at most
- * 256) may overflow.  What is not finite stays in its channel and its sequence,
- * in the tokens behind it (gradients: before it).
+ * -infinity (the state begins anew).  Gates that grow may overflow also where the
+ * state does not: where the product of exp(g) over a stretch of tokens leaves fp32's
+ * range, what follows may be infinite or NaN.  A stretch is a block (at most 256
+ * tokens) or, where few sequences or a long one among short ones are cut to fill
+ * the card, a segment of many blocks.  What is not finite stays in its channel and
+ * its sequence: in the tokens behind it, going backwards in those before it (g's
+ * gradient takes part in both).
  * Sequences are laid out as sla_delta_rule's are: packed == 0, `tokens` are
  * `sequences` of equal length; packed != 0, sequence i is the tokens offsets[i]
  * .. offsets[i+1] - 1, falling offsets are raised, those outside clamped, and

@@ -731,7 +731,9 @@ def gated_scan(x: torch.Tensor, g: torch.Tensor, initial_state: torch.Tensor | N
 
     x and h [batch, tokens, channels]; g (log decay, <= 0; -inf or a type's
     lowest value begins the state anew) of the same shape and of x's type or
-    float32.  States are float32 [sequences, channels]; without an initial state
+    float32.  Gates above zero are computed, but may overflow also where the
+    state does not, if the product of exp(g) over a block or a segment of a long
+    sequence leaves float32's range.  States are float32 [sequences, channels]; without an initial state
     they begin at zero.  cu_seqlens as in gated_delta_rule: the batch is 1 and
     sequence i is the tokens cu_seqlens[i] .. cu_seqlens[i+1] - 1; tokens of no
     sequence get zeros.
