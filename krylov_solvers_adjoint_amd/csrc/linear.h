@@ -20,8 +20,10 @@ struct NarrowGrad {
 // Where one pass pays: the general products read x and dy three times, in four
 // launches or more.  64 x 64, bias, silu, one pass against them: 64 rows fp32 15.3
 // and 16.2 us, 1000 rows 19 and 27, 10^5 rows 47 and 80; bf16 12.6 and 13.7, 13.5
-// and 22, 28 and 48; 16 rows 14.7 and 14.8.  Wider ones leave too few registers for
-// dW's sums.
+// and 22, 28 and 48; 16 rows 14.7 and 14.8.  Up to 64 x 128 and 128 x 64 one pass was
+// faster too (10^6 rows fp32 414 us against 495 and 354 against 484, bf16 274 against
+// 263 and 192 against 273), but its kernels took 100 s more to compile: left out for
+// that alone.
 constexpr int64_t kNarrow = 64, kNarrowRows = 64;
 constexpr int kNarrowGroups = 512;
 inline bool narrow(int64_t rows, int64_t inner, int64_t outer) {

@@ -13,7 +13,7 @@
 // its range (no activation is steeper than 1.13).  All sums are fp32.
 //
 // Measured: 16384 x 4096 x 1024 bf16 with a residual 124 us forward (1.1 PFLOP/s),
-// dx 135, dW 124 + 12 (two splits); 5000 x 771 x 1403 fp16 40 to 45 us a product:
+// dx 135, dW 124 + 12 (two splits); 5000 x 771 x 1403 fp16 41 to 48 us a product:
 // the sizes ask for 128 tiles (440 of them, 26 us at widths that are multiples of
 // 8), whose stores of odd rows take 7 us more; padded copies of the operands
 // changed nothing.  4 x 4096 x 1024 bf16: 8 us, 64 workgroups that read 8.4 MB.

@@ -15,8 +15,8 @@ namespace {
 // without leaving the registers.  For dW dz and x are turned by way of LDS.
 //
 // Bound by the fp32 matrix instructions (10^6 x 64 x 64 with silu: 25 Gflop, 160 us
-// at their rate, beside 768 MB, 154 us): 250 to 280 us, where the four general
-// kernels took 490; bf16 112 us for 384 MB (3.4 TB/s).
+// at their rate, beside 768 MB, 154 us): 275 to 290 us, where the four general
+// kernels took 490; bf16 98 us for 384 MB (3.9 TB/s); without an activation 164 and 95.
 template <typename T, int NP, int KP>
 struct Narrow {
   static constexpr bool kHalf = sizeof(T) == 2;

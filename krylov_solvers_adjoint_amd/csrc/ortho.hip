@@ -17,8 +17,8 @@
 //
 // Lines are padded to multiples of 32 with zeros, which every product keeps.
 //
-// Measured, five steps: 1024 x 4096 325 us (A 18 + 6 in seven splits, B 12, X 27 a
-// step; 70 Gflop, three times that for the parts: 0.65 PFLOP/s), 4096 x 4096 4.07 ms
+// Measured, five steps: 1024 x 4096 321 to 347 us on four machines (A 18 + 6 in seven
+// splits, B 12, X 27 a step; 70 Gflop, three times that for the parts: 0.65 PFLOP/s), 4096 x 4096 4.07 ms
 // (1.0 PFLOP/s), 1403 x 515 169 us.  X of 1024 x 4096 without its parts, timed in a
 // copy: products alone 17 us (10 at the instructions' rate, launch and first loads
 // the rest), loads and LDS reads beside them 6, the way out 4.  Short products are
@@ -710,7 +710,7 @@ __global__ __launch_bounds__(kSmallBlock) void k_ortho_small(const T* __restrict
 // Host side
 // ---------------------------------------------------------------------------
 // Tiles of 128 where they fill the card: 1024 x 4096 in all 342 us instead of 401
-// with 64, 2048 x 2048 795 instead of 905, 4096 x 4096 4.07 ms instead of 5.8.  Fewer
+// with 64 (one machine, side by side), 2048 x 2048 795 instead of 905, 4096 x 4096 4.07 ms instead of 5.8.  Fewer
 // long sums are split (A of 1024 x 4096: 18 + 6 us instead of 34 in tiles of 64), short
 // ones not (K = 1024: 14 + 6 instead of 12).
 constexpr int64_t kTilesFor128 = 200, kTilesToSplit = 24, kLongSums = 2048;
